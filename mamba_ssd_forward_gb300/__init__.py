@@ -8,6 +8,9 @@ in the library's CUDA kernels; there is no CPU or PyTorch fallback.
 Tensor layouts (all contiguous, on one CUDA device):
     x [b, L, nh, P], dt [b, L, nh], B/C [b, L, ng, S] -- float32 or bfloat16
     A [nh], D [nh], h0 [b, nh, P, S]                   -- float32
+
+The operators around the scan in a layer (causal_conv*, selective_scan*,
+gated_norm*, clip_grad_norm) are in layer.py and exported here.
 """
 from __future__ import annotations
 
@@ -17,10 +20,29 @@ import torch
 
 from . import _abi
 from ._abi import SSD_BF16, SSD_F32, SsdError  # noqa: F401
+from .layer import (  # noqa: F401
+    causal_conv,
+    causal_conv_backward,
+    causal_conv_forward,
+    causal_conv_step,
+    clip_grad_norm,
+    gated_norm,
+    gated_norm_backward,
+    gated_norm_forward,
+    selective_scan,
+    selective_scan_backward,
+    selective_scan_forward,
+    selective_scan_step,
+    selective_scan_workspace_size,
+)
 
 __all__ = ["forward", "chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
            "decode_step", "workspace_size", "new_workspace", "workspace_error", "dims_of",
            "backward", "backward_workspace_size", "ssd",
+           "causal_conv", "causal_conv_forward", "causal_conv_backward", "causal_conv_step",
+           "selective_scan", "selective_scan_forward", "selective_scan_backward",
+           "selective_scan_step", "selective_scan_workspace_size",
+           "gated_norm", "gated_norm_forward", "gated_norm_backward", "clip_grad_norm",
            "SsdError"]
 
 

@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI declared in include/ssd.h (libssd_gb300.so).
+"""ctypes view of the C ABI declared in include/ssd.h and include/ssd_layer.h
+(libssd_gb300.so).
 
 Marshalling only: every step of the forward pass runs in the library's CUDA
 kernels.  If the library has not been built, loading fails loudly; there is
@@ -20,7 +21,7 @@ SSD_NOALLOC_SCRATCH_BYTES = 32 << 20
 # Workspace header holding a call's device error word (SSD_WS_HEADER_BYTES).
 SSD_WS_HEADER_BYTES = 256
 
-# Every symbol include/ssd.h declares.
+# Every symbol include/ssd.h and include/ssd_layer.h declare.
 EXPORTS = (
     "ssd_status_string",
     "ssd_forward_workspace_size",
@@ -46,7 +47,24 @@ EXPORTS = (
     "ssd_backward_workspace_size",
     "ssd_backward",
     "ssd_backward_profiled",
+    "ssd_causal_conv",
+    "ssd_causal_conv_backward_workspace_size",
+    "ssd_causal_conv_backward",
+    "ssd_causal_conv_step",
+    "ssd_selective_scan_workspace_size",
+    "ssd_selective_scan",
+    "ssd_selective_scan_backward_workspace_size",
+    "ssd_selective_scan_backward",
+    "ssd_selective_scan_step",
+    "ssd_gated_norm",
+    "ssd_gated_norm_backward_workspace_size",
+    "ssd_gated_norm_backward",
+    "ssd_clip_grad_norm_workspace_size",
+    "ssd_clip_grad_norm",
 )
+
+SSD_ACT_NONE, SSD_ACT_SILU = 0, 1
+SSD_GATE_NONE, SSD_GATE_INPUT, SSD_GATE_OUTPUT = 0, 1, 2
 
 
 class SsdDims(ctypes.Structure):
@@ -60,6 +78,37 @@ class SsdPlan(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
+
+
+class SsdSeq(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class SsdConvDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "width")] + \
+        [("activation", ctypes.c_int32)]
+
+
+class SsdScanDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "channels", "dstate", "ngroups")] + \
+        [("dt_softplus", ctypes.c_int32)]
+
+
+class SsdScanGrads(ctypes.Structure):
+    _fields_ = [(n, SsdSeq) for n in ("du", "ddt", "dz", "dB", "dC")] + \
+        [(n, ctypes.c_void_p) for n in ("dA", "dD", "ddt_bias", "dh0")]
+
+
+class SsdNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "ngroups")] + \
+        [("eps", ctypes.c_float), ("gate", ctypes.c_int32), ("center", ctypes.c_int32)]
+
+
+class SsdGrad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 class SsdError(RuntimeError):
@@ -135,6 +184,32 @@ def load(path: str | None = None):
     lib.ssd_backward_profiled.restype = i32
     lib.ssd_backward_profiled.argtypes = ([dims_p, i32] + [vp] * 17 +
                                           [sz, vp, vp, i32, ctypes.POINTER(ctypes.c_int)])
+    P = ctypes.POINTER
+    seq, conv, scan, norm = P(SsdSeq), P(SsdConvDims), P(SsdScanDims), P(SsdNormDims)
+    f32 = ctypes.c_float
+    for name, res, args in (
+            ("ssd_causal_conv", i32, [conv, i32, seq, vp, vp, vp, vp, seq, vp, vp]),
+            ("ssd_causal_conv_backward_workspace_size", sz, [conv, i32]),
+            ("ssd_causal_conv_backward", i32,
+             [conv, i32, seq, vp, vp, vp, seq, vp, vp, seq, vp, vp, vp, vp, sz, vp]),
+            ("ssd_causal_conv_step", i32, [conv, i32, seq, vp, vp, vp, seq, vp]),
+            ("ssd_selective_scan_workspace_size", sz, [scan, i32]),
+            ("ssd_selective_scan", i32,
+             [scan, i32, seq, seq, vp, seq, seq, vp, seq, vp, vp, vp, seq, vp, vp, sz, vp]),
+            ("ssd_selective_scan_backward_workspace_size", sz, [scan, i32]),
+            ("ssd_selective_scan_backward", i32,
+             [scan, i32, seq, seq, vp, seq, seq, vp, seq, vp, vp, seq, vp, vp, P(SsdScanGrads),
+              vp, sz, vp]),
+            ("ssd_selective_scan_step", i32,
+             [scan, i32, seq, seq, vp, seq, seq, vp, seq, vp, vp, seq, vp]),
+            ("ssd_gated_norm", i32, [norm, i32, seq, vp, vp, seq, seq, vp]),
+            ("ssd_gated_norm_backward_workspace_size", sz, [norm, i32]),
+            ("ssd_gated_norm_backward", i32,
+             [norm, i32, seq, vp, vp, seq, seq, seq, seq, vp, vp, vp, sz, vp]),
+            ("ssd_clip_grad_norm_workspace_size", sz, [P(SsdGrad), i32]),
+            ("ssd_clip_grad_norm", i32, [P(SsdGrad), i32, f32, f32, vp, vp, sz, vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
     if path is None:
         _lib = lib
     return lib

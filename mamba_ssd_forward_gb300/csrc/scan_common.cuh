@@ -1,0 +1,91 @@
+// Shared by the selective scan's kernels.  A channel's N states lie on NL
+// neighbouring lanes (a power of two), four to a lane; states N and up of the
+// last lanes are kept at zero.
+#pragma once
+
+#include <type_traits>
+
+#include "layer.cuh"
+
+namespace ssd {
+namespace scan {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The step of a token: v = dt + bias, or log(1 + exp(v)) in the form that
+// neither overflows nor loses small values.
+__device__ __forceinline__ float step_of(float v, bool softplus) {
+  return softplus ? fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v))) : v;
+}
+
+// The four states of a lane: loads of a row of N floats or I/O elements from
+// index n0 on, zero past N.
+template <typename T>
+__device__ __forceinline__ void load4_tail(const T *row, int n0, int N, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n0 + i < N ? ld_io(row + n0 + i) : 0.f;
+}
+__device__ __forceinline__ void store4_tail(float *row, int n0, int N, const float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n0 + i < N) row[n0 + i] = v[i];
+}
+
+// Sum over the NL lanes of a channel, in every lane.
+template <int NL>
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+  for (int off = NL / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+template <typename T>
+struct tag {
+  using type = T;
+};
+
+// Lanes per channel: the least power of two with four states to a lane.
+inline int lanes_of(int64_t N) {
+  int nl = 1;
+  while (nl * 4 < N) nl *= 2;
+  return nl;
+}
+
+template <typename F>
+cudaError_t dispatch(ssd_dtype io, int64_t N, F f) {
+  auto by_lanes = [&](auto io_c) {
+    switch (lanes_of(N)) {
+      case 1: return f(io_c, std::integral_constant<int, 1>{});
+      case 2: return f(io_c, std::integral_constant<int, 2>{});
+      case 4: return f(io_c, std::integral_constant<int, 4>{});
+      case 8: return f(io_c, std::integral_constant<int, 8>{});
+      default: return f(io_c, std::integral_constant<int, 16>{});
+    }
+  };
+  return io == SSD_BF16 ? by_lanes(tag<__nv_bfloat16>{}) : by_lanes(tag<float>{});
+}
+
+// The inputs of the forward recurrence, as the kernels take them.
+template <typename IO>
+struct In {
+  SeqView<const IO> u, dt, B, C, z;
+  const float *A, *Dskip, *dt_bias, *h0;
+  const int32_t *lengths;
+  int64_t nb, L, D;
+  int N, per_group;  // states, channels per group
+  bool softplus;
+};
+template <typename IO>
+In<IO> in_of(const ScanArgs &a) {
+  In<IO> i;
+  i.u = view_of<const IO>(a.u), i.dt = view_of<const IO>(a.dt);
+  i.B = view_of<const IO>(a.B), i.C = view_of<const IO>(a.C), i.z = view_of<const IO>(a.z);
+  i.A = a.A, i.Dskip = a.Dskip, i.dt_bias = a.dt_bias, i.h0 = a.h0;
+  i.lengths = a.lengths;
+  i.nb = a.b, i.L = a.L, i.D = a.D, i.N = (int)a.N, i.per_group = (int)(a.D / a.G);
+  i.softplus = a.softplus;
+  return i;
+}
+
+}  // namespace scan
+}  // namespace ssd

@@ -1,0 +1,474 @@
+"""The operators around a state space scan in a layer (include/ssd_layer.h):
+the short causal convolution, the selective scan, the gated group norm and
+the global gradient norm with clipping.
+
+As in the rest of the package, the functions here check types and shapes,
+allocate outputs and workspaces on the current CUDA stream and pass pointers;
+all arithmetic runs in the library's kernels.
+
+Activations ([b, L, D] and the like) may be views with any strides between
+sequences and tokens as long as the last axis is dense, such as slices of a
+wider projection; other views are refused.  `lengths` (int32 [b] on the
+device, or None) gives the real tokens of each padded sequence.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _abi
+from ._abi import SsdSeq
+
+_GATES = {"none": _abi.SSD_GATE_NONE, "input": _abi.SSD_GATE_INPUT,
+          "output": _abi.SSD_GATE_OUTPUT}
+_ACTS = {None: _abi.SSD_ACT_NONE, "silu": _abi.SSD_ACT_SILU}
+_IO = {torch.float32: _abi.SSD_F32, torch.bfloat16: _abi.SSD_BF16}
+
+
+def _io(t, name):
+    try:
+        return _IO[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}") from None
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _check(t, name, shape, dtype, like):
+    """A tensor of exactly this shape and type on the device of `like`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the same device as the input")
+
+
+def _dense(t, name, shape, dtype, like):
+    """Address of a dense tensor (None stays None)."""
+    if t is None:
+        return None
+    _check(t, name, shape, dtype, like)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _seq(t, name, shape, dtype, like):
+    """View of an activation [b, L, D], [b, D] (one token each) or, with the
+    last two axes groups and states, one axis more; None stays None."""
+    if t is None:
+        return None
+    _check(t, name, shape, dtype, like)
+    st, sh = t.stride(), t.shape
+    lead = len(sh)
+    step = 1
+    while lead > len(shape) - _inner(shape):
+        lead -= 1
+        if sh[lead] != 1 and st[lead] != step:
+            raise ValueError(f"{name} must be dense along its last axes")
+        step *= sh[lead]
+    return SsdSeq(t.data_ptr(), st[0] if sh[0] > 1 else 0,
+                  st[1] if lead == 2 and sh[1] > 1 else 0)
+
+
+class _Shape(tuple):
+    """A shape whose last `inner` axes are dense."""
+    inner = 1
+
+
+def _inner(shape):
+    return getattr(shape, "inner", 1)
+
+
+def _grouped(*dims):
+    s = _Shape(dims)
+    s.inner = 2
+    return s
+
+
+def _sized(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _workspace(need, workspace, like, fn):
+    """(tensor kept alive, address, bytes) of a workspace of `need` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _sized(need, like.device)
+    elif workspace.dtype != torch.uint8 or workspace.device != like.device:
+        raise ValueError(f"{fn}: workspace must be a uint8 tensor on the inputs' device")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _lengths(lengths, b, like):
+    return _dense(lengths, "lengths", (b,), torch.int32, like)
+
+
+def _out(t, name, shape, dtype, like):
+    """A given output, checked, or a new dense one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return t
+
+
+# ------------------------------------------------------ causal convolution
+
+def _conv_dims(x, weight, activation, step=False):
+    if activation not in _ACTS:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    if x.dim() != (2 if step else 3) or weight.dim() != 2:
+        raise ValueError("x must be [b, D] and weight [D, W]" if step else
+                         "x must be [b, L, D] and weight [D, W]")
+    b, D = x.shape[0], x.shape[-1]
+    return _abi.SsdConvDims(b, 1 if step else x.shape[1], D, weight.shape[1], _ACTS[activation])
+
+
+def causal_conv_forward(x, weight, bias=None, state=None, lengths=None, activation="silu",
+                        y=None, final_state=None, return_final_state: bool = True):
+    """y [b, L, D], final_state [b, W - 1, D] = the causal convolution of each
+    channel with its W (2 to 4) weights and SiLU (ssd_causal_conv).
+
+    x [b, L, D] and state [b, W - 1, D] (the inputs before the first token,
+    oldest first; None = zeros) in the I/O type, weight [D, W] and bias [D]
+    float32.  final_state holds the last W - 1 inputs, for a later call or
+    causal_conv_step."""
+    d = _conv_dims(x, weight, activation)
+    io, b, L, D, W = _io(x, "x"), d.batch, d.seqlen, d.channels, d.width
+    y = _out(y, "y", (b, L, D), x.dtype, x)
+    keep = (b, W - 1, D)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(keep, dtype=x.dtype, device=x.device)
+    _abi.check("ssd_causal_conv", _abi.load().ssd_causal_conv(
+        d, io, _seq(x, "x", (b, L, D), x.dtype, x),
+        _dense(weight, "weight", (D, W), torch.float32, x),
+        _dense(bias, "bias", (D,), torch.float32, x), _dense(state, "state", keep, x.dtype, x),
+        _lengths(lengths, b, x), _seq(y, "y", (b, L, D), x.dtype, x),
+        _dense(final_state, "final_state", keep, x.dtype, x), _stream()))
+    return y, final_state
+
+
+def causal_conv_backward(x, weight, bias=None, state=None, gy=None, gfinal=None, lengths=None,
+                         activation="silu", workspace=None) -> dict:
+    """Gradients through causal_conv_forward given gy = dL/dy and gfinal =
+    dL/dfinal_state (None = 0), by ssd_causal_conv_backward: a dict of dx (I/O
+    type), dweight, dbias (float32; dbias None without a bias) and dstate (None
+    without a state)."""
+    if gy is None:
+        raise ValueError("gy (dL/dy) is required")
+    d = _conv_dims(x, weight, activation)
+    io, b, L, D, W = _io(x, "x"), d.batch, d.seqlen, d.channels, d.width
+    lib, keep = _abi.load(), (b, W - 1, D)
+    ws, wp, wn = _workspace(lib.ssd_causal_conv_backward_workspace_size(d, io), workspace, x,
+                            "causal_conv_backward")
+    dx = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
+    dw = torch.empty((D, W), dtype=torch.float32, device=x.device)
+    db = None if bias is None else torch.empty((D,), dtype=torch.float32, device=x.device)
+    ds = None if state is None else torch.empty(keep, dtype=x.dtype, device=x.device)
+    _abi.check("ssd_causal_conv_backward", lib.ssd_causal_conv_backward(
+        d, io, _seq(x, "x", (b, L, D), x.dtype, x),
+        _dense(weight, "weight", (D, W), torch.float32, x),
+        _dense(bias, "bias", (D,), torch.float32, x), _dense(state, "state", keep, x.dtype, x),
+        _seq(gy, "gy", (b, L, D), x.dtype, x), _dense(gfinal, "gfinal", keep, x.dtype, x),
+        _lengths(lengths, b, x), _seq(dx, "dx", (b, L, D), x.dtype, x), dw.data_ptr(),
+        None if db is None else db.data_ptr(), None if ds is None else ds.data_ptr(), wp, wn,
+        _stream()))
+    return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
+
+
+def causal_conv_step(x, weight, bias, state, activation="silu", y=None):
+    """y [b, D] = one token of the convolution for every sequence
+    (ssd_causal_conv_step).  state [b, W - 1, D] is updated in place."""
+    d = _conv_dims(x, weight, activation, step=True)
+    b, D, W = d.batch, d.channels, d.width
+    y = _out(y, "y", (b, D), x.dtype, x)
+    if state is None:
+        raise ValueError("state is required")
+    _abi.check("ssd_causal_conv_step", _abi.load().ssd_causal_conv_step(
+        d, _io(x, "x"), _seq(x, "x", (b, D), x.dtype, x),
+        _dense(weight, "weight", (D, W), torch.float32, x),
+        _dense(bias, "bias", (D,), torch.float32, x),
+        _dense(state, "state", (b, W - 1, D), x.dtype, x), _seq(y, "y", (b, D), x.dtype, x),
+        _stream()))
+    return y
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, lengths, activation):
+        y, final_state = causal_conv_forward(x, weight, bias, state, lengths, activation)
+        ctx.save_for_backward(x, weight, bias, state, lengths)
+        ctx.activation = activation
+        return y, final_state
+
+    @staticmethod
+    def backward(ctx, gy, gfinal):
+        x, weight, bias, state, lengths = ctx.saved_tensors
+        g = causal_conv_backward(x, weight, bias, state, gy.contiguous(), gfinal.contiguous(),
+                                 lengths, ctx.activation)
+        return g["dx"], g["dweight"], g["dbias"], g["dstate"], None, None
+
+
+def causal_conv(x, weight, bias=None, state=None, lengths=None, activation="silu"):
+    """y, final_state = causal_conv_forward, differentiable with respect to x,
+    weight, bias and state."""
+    return _CausalConv.apply(x, weight, bias, state, lengths, activation)
+
+
+# ----------------------------------------------------------- selective scan
+
+def _scan_dims(u, A, B, dt_softplus, step=False):
+    if u.dim() != (2 if step else 3) or A.dim() != 2 or B.dim() != u.dim() + 1:
+        raise ValueError("u must be [b, D], A [D, N] and B, C [b, G, N]" if step else
+                         "u must be [b, L, D], A [D, N] and B, C [b, L, G, N]")
+    b, D = u.shape[0], u.shape[-1]
+    return _abi.SsdScanDims(b, 1 if step else u.shape[1], D, A.shape[1], B.shape[-2],
+                            1 if dt_softplus else 0)
+
+
+def _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias, step=False):
+    """The leading arguments of the scan's calls, checked."""
+    lead = (d.batch,) if step else (d.batch, d.seqlen)
+    row, grp = lead + (d.channels,), _grouped(*lead, d.ngroups, d.dstate)
+    io = u.dtype
+    return [d, _io(u, "u"), _seq(u, "u", row, io, u), _seq(dt, "dt", row, io, u),
+            _dense(A, "A", (d.channels, d.dstate), torch.float32, u),
+            _seq(B, "B", grp, io, u), _seq(C, "C", grp, io, u),
+            _dense(D, "D", (d.channels,), torch.float32, u), _seq(z, "z", row, io, u),
+            _dense(dt_bias, "dt_bias", (d.channels,), torch.float32, u)]
+
+
+def selective_scan_workspace_size(u, A, B) -> int:
+    d = _scan_dims(u, A, B, False)
+    return int(_abi.load().ssd_selective_scan_workspace_size(d, _io(u, "u")))
+
+
+def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None,
+                           dt_softplus: bool = False, y=None, final_state=None,
+                           return_final_state: bool = True, workspace=None):
+    """y [b, L, D], final_state [b, D, N] = the scan whose decay is
+    exp(s A[d, n]) per channel and state, with the step s = dt + dt_bias or
+    softplus of it (ssd_selective_scan).
+
+    u, dt, z [b, L, D] and B, C [b, L, G, N] in the I/O type (G groups of
+    channels share B and C, N <= 64); A [D, N], D [D], dt_bias [D] and h0
+    [b, D, N] float32.  With z, y is multiplied by silu(z)."""
+    d = _scan_dims(u, A, B, dt_softplus)
+    lib, b, L, nd = _abi.load(), d.batch, d.seqlen, d.channels
+    args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias)
+    keep = (b, nd, d.dstate)
+    y = _out(y, "y", (b, L, nd), u.dtype, u)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(keep, dtype=torch.float32, device=u.device)
+    ws, wp, wn = _workspace(lib.ssd_selective_scan_workspace_size(d, args[1]), workspace, u,
+                            "selective_scan_forward")
+    _abi.check("ssd_selective_scan", lib.ssd_selective_scan(
+        *args, _dense(h0, "h0", keep, torch.float32, u), _lengths(lengths, b, u),
+        _seq(y, "y", (b, L, nd), u.dtype, u),
+        _dense(final_state, "final_state", keep, torch.float32, u), wp, wn, _stream()))
+    return y, final_state
+
+
+def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, gy=None,
+                            gfinal=None, lengths=None, dt_softplus: bool = False,
+                            workspace=None) -> dict:
+    """Gradients through selective_scan_forward given gy = dL/dy and gfinal =
+    dL/dfinal_state (None = 0), by ssd_selective_scan_backward: a dict of du,
+    ddt, dB, dC, dz (I/O type), dA, dD, ddt_bias, dh0 (float32); those of
+    absent inputs are None."""
+    if gy is None:
+        raise ValueError("gy (dL/dy) is required")
+    d = _scan_dims(u, A, B, dt_softplus)
+    lib, b, L, nd, N = _abi.load(), d.batch, d.seqlen, d.channels, d.dstate
+    args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias)
+    row, grp, keep = (b, L, nd), _grouped(b, L, d.ngroups, N), (b, nd, N)
+
+    def io_out(shape, of=u):
+        return None if of is None else torch.empty(shape, dtype=u.dtype, device=u.device)
+
+    def f32_out(shape, of):
+        return None if of is None else torch.empty(shape, dtype=torch.float32, device=u.device)
+
+    r = {"du": io_out(row), "ddt": io_out(row), "dA": f32_out((nd, N), A), "dB": io_out(grp),
+         "dC": io_out(grp), "dD": f32_out((nd,), D), "dz": io_out(row, z),
+         "ddt_bias": f32_out((nd,), dt_bias), "dh0": f32_out(keep, h0)}
+    g = _abi.SsdScanGrads()
+    for k, shape in (("du", row), ("ddt", row), ("dz", row), ("dB", grp), ("dC", grp)):
+        if r[k] is not None:
+            setattr(g, k, _seq(r[k], k, shape, u.dtype, u))
+    for k in ("dA", "dD", "ddt_bias", "dh0"):
+        if r[k] is not None:
+            setattr(g, k, r[k].data_ptr())
+    ws, wp, wn = _workspace(lib.ssd_selective_scan_backward_workspace_size(d, args[1]), workspace,
+                            u, "selective_scan_backward")
+    _abi.check("ssd_selective_scan_backward", lib.ssd_selective_scan_backward(
+        *args, _dense(h0, "h0", keep, torch.float32, u), _seq(gy, "gy", row, u.dtype, u),
+        _dense(gfinal, "gfinal", keep, torch.float32, u), _lengths(lengths, b, u), g, wp, wn,
+        _stream()))
+    return r
+
+
+def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, dt_softplus: bool = False, y=None):
+    """y [b, D] = one token of the scan for every sequence
+    (ssd_selective_scan_step).  u, dt, z [b, D], B, C [b, G, N]; state
+    [b, D, N] float32 is updated in place.  D, z and dt_bias may be None."""
+    if state is None:
+        raise ValueError("state is required")
+    d = _scan_dims(u, A, B, dt_softplus, step=True)
+    args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias, step=True)
+    row = (d.batch, d.channels)
+    y = _out(y, "y", row, u.dtype, u)
+    _abi.check("ssd_selective_scan_step", _abi.load().ssd_selective_scan_step(
+        *args, _dense(state, "state", (d.batch, d.channels, d.dstate), torch.float32, u),
+        _seq(y, "y", row, u.dtype, u), _stream()))
+    return y
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D, z, dt_bias, h0, lengths, dt_softplus):
+        y, final_state = selective_scan_forward(u, dt, A, B, C, D, z, dt_bias, h0, lengths,
+                                                dt_softplus)
+        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, h0, lengths)
+        ctx.dt_softplus = dt_softplus
+        return y, final_state
+
+    @staticmethod
+    def backward(ctx, gy, gfinal):
+        *tensors, lengths = ctx.saved_tensors
+        g = selective_scan_backward(*tensors, gy.contiguous(), gfinal.contiguous(), lengths,
+                                    ctx.dt_softplus)
+        return (*(g[k] for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")),
+                None, None)
+
+
+def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None,
+                   dt_softplus: bool = False):
+    """y, final_state = selective_scan_forward, differentiable with respect to
+    u, dt, A, B, C, D, z, dt_bias and h0."""
+    return _SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias, h0, lengths, dt_softplus)
+
+
+# -------------------------------------------------------- gated group norm
+
+def _norm_dims(x, groups, eps, gate, center):
+    if gate not in _GATES:
+        raise ValueError(f"gate must be 'none', 'input' or 'output', got {gate!r}")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [tokens, D] or [b, L, D]")
+    b, L = (x.shape[0], 1) if x.dim() == 2 else x.shape[:2]
+    return _abi.SsdNormDims(b, L, x.shape[-1], groups, eps, _GATES[gate], 1 if center else 0)
+
+
+def _rows(d):
+    """[tokens, D] runs as one sequence of that many tokens."""
+    if d.seqlen == 1:
+        d.batch, d.seqlen = 1, d.batch
+        return True
+    return False
+
+
+def _norm_view(t, name, x, flat):
+    v = _seq(t, name, x.shape, x.dtype, x)
+    return SsdSeq(v.data, 0, v.batch_stride) if v is not None and flat else v
+
+
+def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float = 1e-5,
+                       gate: str = "input", center: bool = False, y=None):
+    """y = the group norm of every token over each of `groups` groups of
+    channels, with a SiLU gate (ssd_gated_norm): gate "input" normalises
+    x silu(z), "output" multiplies the result by silu(z), "none" takes no z.
+    Root mean square, or centred with `center`.
+
+    x, z [tokens, D] or [b, L, D] in the I/O type, weight and bias [D]
+    float32.  y may be x or z themselves."""
+    d = _norm_dims(x, groups, eps, gate, center)
+    flat, D = _rows(d), x.shape[-1]
+    y = _out(y, "y", x.shape, x.dtype, x)
+    _abi.check("ssd_gated_norm", _abi.load().ssd_gated_norm(
+        d, _io(x, "x"), _norm_view(x, "x", x, flat),
+        _dense(weight, "weight", (D,), torch.float32, x),
+        _dense(bias, "bias", (D,), torch.float32, x), _norm_view(z, "z", x, flat),
+        _norm_view(y, "y", x, flat), _stream()))
+    return y
+
+
+def gated_norm_backward(x, weight, bias=None, z=None, gy=None, groups: int = 1,
+                        eps: float = 1e-5, gate: str = "input", center: bool = False,
+                        workspace=None) -> dict:
+    """Gradients through gated_norm_forward given gy = dL/dy, by
+    ssd_gated_norm_backward: a dict of dx, dz (I/O type; dz None without a
+    gate), dweight and dbias (float32; dbias None without a bias)."""
+    if gy is None:
+        raise ValueError("gy (dL/dy) is required")
+    d = _norm_dims(x, groups, eps, gate, center)
+    flat, D, lib, io = _rows(d), x.shape[-1], _abi.load(), _io(x, "x")
+    ws, wp, wn = _workspace(lib.ssd_gated_norm_backward_workspace_size(d, io), workspace, x,
+                            "gated_norm_backward")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dz = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty((D,), dtype=torch.float32, device=x.device)
+    db = None if bias is None else torch.empty((D,), dtype=torch.float32, device=x.device)
+    _abi.check("ssd_gated_norm_backward", lib.ssd_gated_norm_backward(
+        d, io, _norm_view(x, "x", x, flat), _dense(weight, "weight", (D,), torch.float32, x),
+        _dense(bias, "bias", (D,), torch.float32, x), _norm_view(z, "z", x, flat),
+        _norm_view(gy, "gy", x, flat), _norm_view(dx, "dx", x, flat),
+        _norm_view(dz, "dz", x, flat), dw.data_ptr(), None if db is None else db.data_ptr(), wp,
+        wn, _stream()))
+    return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, z, groups, eps, gate, center):
+        ctx.save_for_backward(x, weight, bias, z)
+        ctx.how = (groups, eps, gate, center)
+        return gated_norm_forward(x, weight, bias, z, *ctx.how)
+
+    @staticmethod
+    def backward(ctx, gy):
+        x, weight, bias, z = ctx.saved_tensors
+        g = gated_norm_backward(x, weight, bias, z, gy.contiguous(), *ctx.how)
+        return g["dx"], g["dweight"], g["dbias"], g["dz"], None, None, None, None
+
+
+def gated_norm(x, weight, bias=None, z=None, groups: int = 1, eps: float = 1e-5,
+               gate: str = "input", center: bool = False):
+    """gated_norm_forward, differentiable with respect to x, weight, bias and
+    z."""
+    return _GatedNorm.apply(x, weight, bias, z, groups, eps, gate, center)
+
+
+# ------------------------------------------- gradient norm and clipping
+
+def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspace=None):
+    """The norm over every element of every tensor of `grads` (a float32
+    scalar on the device), and the tensors scaled by min(1, max_norm / (norm +
+    eps)) (ssd_clip_grad_norm): in place, or into the tensors of `out`.
+
+    Contiguous float32 or bfloat16 tensors of any shapes, mixed; empty ones
+    are skipped.  Nothing waits for the device."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients but {len(out)} outputs")
+    if not grads:
+        raise ValueError("no gradients given")
+    like = grads[0]
+    table = (_abi.SsdGrad * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, out)):
+        io = _io(g, f"grads[{i}]")
+        src = _dense(g, f"grads[{i}]", g.shape, g.dtype, like)
+        dst = src if o is g else _dense(o, f"out[{i}]", g.shape, g.dtype, like)
+        table[i] = (src, dst, g.numel(), io)
+    lib = _abi.load()
+    norm = torch.empty((), dtype=torch.float32, device=like.device)
+    ws, wp, wn = _workspace(lib.ssd_clip_grad_norm_workspace_size(table, len(grads)), workspace,
+                            like, "clip_grad_norm")
+    _abi.check("ssd_clip_grad_norm", lib.ssd_clip_grad_norm(
+        table, len(grads), max_norm, eps, norm.data_ptr(), wp, wn, _stream()))
+    return norm

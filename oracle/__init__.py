@@ -24,6 +24,9 @@ CUDA Tile", section "Mamba-2 architecture":
   kernel would use (reverse pass over chunks, per-chunk masked products,
   the decay gradient as a reverse cumsum of dL/dG), pinned against it.
 
+* ``layer`` -- the operators around the scan (short causal convolution,
+  selective scan, gated group norm, gradient clipping), in numpy.
+
 Parity status: every function here is pinned by the ``-m "not gpu"`` tests
 (hand-worked example, brute-force unrolled sum, linear-attention, B = 0 and
 dt = 0 special cases, chunk invariance, padding, resume, linearity in h0;
@@ -43,3 +46,4 @@ from .ssd_oracle import (  # noqa: F401
     recurrence_np,
     set_threads,
 )
+from . import layer_oracle as layer  # noqa: F401
