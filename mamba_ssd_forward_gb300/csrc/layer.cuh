@@ -86,8 +86,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / (1 + exp(-v)): exact limits at both ends (0 and 1).
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
+// 1 / (1 + exp(-v)): exact limits at both ends (0 and 1); a few ulp between.
+__device__ __forceinline__ float sigmoid(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-kLog2e * v)));
+  return r;
+}
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d silu(v) / dv = sig (1 + v (1 - sig))
 __device__ __forceinline__ float dsilu(float v) {
