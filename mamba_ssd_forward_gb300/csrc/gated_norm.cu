@@ -187,6 +187,390 @@ norm_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
   }
 }
 
+// The kernels below read memory once.  A team of threads (a warp, or a whole
+// block for a group of more than 32 K V channels) takes one group of one token
+// at a time, K vectors of V channels to a thread, and walks the tokens with a
+// fixed stride: the weights are read once a team, dweight and dbias stay in
+// registers.  Vectors of 16 bytes come kStages - 1 tokens ahead through shared
+// memory, each thread copying its own, so no barrier waits for memory.
+
+// V elements as the memory holds them.
+template <typename IO, int V>
+struct Raw {
+  static constexpr int kBytes = V * (int)sizeof(IO);
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const IO *p) {
+    if constexpr (kBytes == 16) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(p);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = *reinterpret_cast<const uint2 *>(p);
+      w[0] = q.x, w[1] = q.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(IO) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+
+// Sums of M values over the team, in every thread; a fixed order.  `turn`
+// alternates the scratch rows, so one barrier a call is enough.
+template <int M>
+__device__ __forceinline__ void team_sum(float (&v)[M], float (*scratch)[M][32], int warps,
+                                         int &turn) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], off);
+  if (warps == 1) return;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0)
+#pragma unroll
+    for (int m = 0; m < M; ++m) scratch[turn][m][threadIdx.x / 32] = v[m];
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = lane < warps ? scratch[turn][m][lane] : 0.f;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], off);
+  turn ^= 1;
+}
+
+// T tensors' vectors of a thread, for kStages tokens.
+constexpr int kStages = 2;
+template <typename IO, int V, int K, int T>
+struct Ahead {
+  static constexpr bool kAsync = V * sizeof(IO) == 16;
+  uint4 *slots;  // this thread's first; the others blockDim apart
+  int stage;
+  __device__ __forceinline__ Ahead(void *smem)
+      : slots(static_cast<uint4 *>(smem) + threadIdx.x), stage(0) {}
+  __device__ __forceinline__ uint4 *slot(int s, int tensor, int k) const {
+    return slots + ((s * T + tensor) * K + k) * (int)blockDim.x;
+  }
+  // Vector k of a tensor of the token `ahead` turns from the present one.
+  __device__ __forceinline__ void copy(int ahead, int tensor, int k, const IO *p) {
+    int s = stage + ahead;
+    if (s >= kStages) s -= kStages;
+    copy16(slot(s, tensor, k), p);
+  }
+  __device__ __forceinline__ void take(int tensor, int k, Raw<IO, V> &r) const {
+    const uint4 q = *slot(stage, tensor, k);
+    if constexpr (kAsync) r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+  }
+  __device__ __forceinline__ void turn() { stage = stage + 1 == kStages ? 0 : stage + 1; }
+};
+
+// A token by sequence and position, walked by a stride without a division
+// while it stays in its sequence.
+struct Place {
+  uint32_t b, t, L;
+  __device__ __forceinline__ Place(int64_t row, int64_t len)
+      : b((uint32_t)row / (uint32_t)len), t((uint32_t)row % (uint32_t)len), L((uint32_t)len) {}
+  __device__ __forceinline__ void step(uint32_t n) {
+    t += n;
+    if (t >= L) {
+      b += t / L;
+      t %= L;
+    }
+  }
+};
+
+struct Teams {
+  int threads;     // of a team: 32, or the block
+  int64_t strides; // teams per group
+};
+
+constexpr int kMaxTeam = 512;
+constexpr int kFwdBlocks = 2, kGradBlocks = 1;  // of that size to an SM
+
+// V fp32 parameters; `vec`: the parameters start on a vector boundary.
+__device__ __forceinline__ bool params_aligned(const float *weight, const float *bias) {
+  return ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
+}
+template <int V>
+__device__ __forceinline__ void load_params(const float *p, bool vec, float (&v)[V]) {
+  if (V % 4 == 0 && vec) {
+#pragma unroll
+    for (int e = 0; e + 3 < V; e += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(p + e);
+      v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = p[e];
+  }
+}
+
+template <typename IO, int V, int K, int gate>
+__global__ void __launch_bounds__(kMaxTeam, kFwdBlocks)
+norm_team_kernel(SeqView<const IO> x, const float *__restrict__ weight,
+                 const float *__restrict__ bias, SeqView<const IO> z, SeqView<IO> y, int64_t L,
+                 int64_t rows, int64_t G, int group, float eps, bool center, Teams tm,
+                 int *err) {
+  __shared__ float scratch[2][1][32];
+  const int per_block = blockDim.x / tm.threads, warps = tm.threads / 32;
+  const int64_t team = (int64_t)blockIdx.x * per_block + threadIdx.x / tm.threads;
+  const int tid = threadIdx.x % tm.threads;
+  if (team >= tm.strides * G) return;  // whole warps, or no thread of the block
+  const int64_t c0 = team % G * group;
+  int turn = 0;
+  const float inv = 1.f / (float)group;
+  const bool vec_params = params_aligned(weight, bias);
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ahead<IO, V, K, 2> ahead(smem);
+  const int64_t first = team / G;
+  Place here(first, L), next(first, L);
+  auto at = [&](const SeqView<const IO> &m, const Place &r, int i) {
+    return m.at(r.b, r.t) + c0 + i;
+  };
+  auto issue = [&](int64_t row, int turns) {  // and on to the next
+    if (row < rows)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = (tid + k * tm.threads) * V;
+        if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 43)) continue;
+        ahead.copy(turns, 0, k, at(x, next, i));
+        if (gate) ahead.copy(turns, 1, k, at(z, next, i));
+      }
+    next.step((uint32_t)tm.strides);
+    copies_issued();
+  };
+  if constexpr (decltype(ahead)::kAsync)
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(first + k * tm.strides, k);
+  for (int64_t row = first; row < rows; row += tm.strides, here.step((uint32_t)tm.strides)) {
+    Raw<IO, V> xr[K], zr[K];
+    if constexpr (decltype(ahead)::kAsync) {
+      issue(row + (kStages - 1) * tm.strides, kStages - 1);
+      copies_landed<kStages - 1>();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = (tid + k * tm.threads) * V;
+      xr[k].clear(), zr[k].clear();
+      if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 43)) continue;
+      if constexpr (decltype(ahead)::kAsync) {
+        ahead.take(0, k, xr[k]);
+        if (gate) ahead.take(1, k, zr[k]);
+      } else {
+        xr[k].load(at(x, here, i));
+        if (gate) zr[k].load(at(z, here, i));
+      }
+    }
+    ahead.turn();
+    float r[K][V], s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        r[k][e] = xr[k].at(e);
+        if (gate == SSD_GATE_INPUT) r[k][e] = __fmul_rn(r[k][e], silu(zr[k].at(e)));
+        if (center) s[0] += r[k][e];
+      }
+    if (center) {
+      team_sum(s, scratch, warps, turn);
+      const float mean = s[0] * inv;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          r[k][e] = (tid + k * tm.threads) * V < group ? r[k][e] - mean : 0.f;
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] = fmaf(r[k][e], r[k][e], s[0]);
+    team_sum(s, scratch, warps, turn);
+    const float rstd = rsqrtf(s[0] * inv + eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = (tid + k * tm.threads) * V;
+      if (i >= group) continue;
+      float o[V], w[V];
+      load_params<V>(weight + c0 + i, vec_params, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = r[k][e] * rstd * w[e];
+      if (bias) {
+        load_params<V>(bias + c0 + i, vec_params, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] += w[e];
+      }
+      if (gate == SSD_GATE_OUTPUT)
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= silu(zr[k].at(e));
+      store_vec<V>(y.at(here.b, here.t) + c0 + i, o);
+    }
+  }
+}
+
+template <typename IO, int V, int K, int gate, bool BIAS>
+__global__ void __launch_bounds__(kMaxTeam, kGradBlocks)
+norm_team_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
+                      const float *__restrict__ bias, SeqView<const IO> z, SeqView<const IO> gy,
+                      SeqView<IO> dx, SeqView<IO> dz, float *__restrict__ part_w,
+                      float *__restrict__ part_b, int64_t L, int64_t rows, int64_t G, int group,
+                      float eps, bool center, Teams tm, int *err) {
+  __shared__ float scratch1[2][1][32], scratch3[2][3][32];
+  const int per_block = blockDim.x / tm.threads, warps = tm.threads / 32;
+  const int64_t team = (int64_t)blockIdx.x * per_block + threadIdx.x / tm.threads;
+  const int tid = threadIdx.x % tm.threads;
+  if (team >= tm.strides * G) return;
+  const int64_t c0 = team % G * group;
+  int turn1 = 0, turn3 = 0;
+  const float inv = 1.f / (float)group;
+  const bool vec_params = params_aligned(weight, bias);
+  float dw[K][V], db[BIAS ? K : 1][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      dw[k][e] = 0.f;
+      if (BIAS) db[k][e] = 0.f;
+    }
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ahead<IO, V, K, 3> ahead(smem);
+  const int64_t first = team / G;
+  Place here(first, L), next(first, L);
+  auto at = [&](const SeqView<const IO> &m, const Place &r, int i) {
+    return m.at(r.b, r.t) + c0 + i;
+  };
+  auto issue = [&](int64_t row, int turns) {  // and on to the next
+    if (row < rows)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = (tid + k * tm.threads) * V;
+        if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 44)) continue;
+        ahead.copy(turns, 0, k, at(x, next, i));
+        ahead.copy(turns, 1, k, at(gy, next, i));
+        if (gate) ahead.copy(turns, 2, k, at(z, next, i));
+      }
+    next.step((uint32_t)tm.strides);
+    copies_issued();
+  };
+  if constexpr (decltype(ahead)::kAsync)
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(first + k * tm.strides, k);
+  for (int64_t row = first; row < rows; row += tm.strides, here.step((uint32_t)tm.strides)) {
+    Raw<IO, V> xc[K], zc[K], gc[K];
+    if constexpr (decltype(ahead)::kAsync) {
+      issue(row + (kStages - 1) * tm.strides, kStages - 1);
+      copies_landed<kStages - 1>();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = (tid + k * tm.threads) * V;
+      xc[k].clear(), zc[k].clear(), gc[k].clear();
+      if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 44)) continue;
+      if constexpr (decltype(ahead)::kAsync) {
+        ahead.take(0, k, xc[k]);
+        ahead.take(1, k, gc[k]);
+        if (gate) ahead.take(2, k, zc[k]);
+      } else {
+        xc[k].load(at(x, here, i));
+        gc[k].load(at(gy, here, i));
+        if (gate) zc[k].load(at(z, here, i));
+      }
+    }
+    ahead.turn();
+    float sig[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sig[k][e] = gate ? sigmoid(zc[k].at(e)) : 0.f;
+    // r and dL/dv of one channel
+    auto r_of = [&](int k, int e) {
+      const float v = xc[k].at(e);
+      return gate == SSD_GATE_INPUT ? __fmul_rn(v, zc[k].at(e) * sig[k][e]) : v;
+    };
+    auto gv_of = [&](int k, int e) {
+      const float v = gc[k].at(e);
+      return gate == SSD_GATE_OUTPUT ? v * (zc[k].at(e) * sig[k][e]) : v;
+    };
+    float mean = 0.f;
+    if (center) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0] += r_of(k, e);
+      team_sum(s, scratch1, warps, turn1);
+      mean = s[0] * inv;
+    }
+    float s[3] = {0.f, 0.f, 0.f};  // sums of d^2, q d, q with d = r - mean
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = (tid + k * tm.threads) * V;
+      if (i >= group) continue;
+      float w[V];
+      load_params<V>(weight + c0 + i, vec_params, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = r_of(k, e) - mean, q = gv_of(k, e) * w[e];
+        s[0] = fmaf(d, d, s[0]);
+        s[1] = fmaf(q, d, s[1]);
+        if (center) s[2] += q;
+      }
+    }
+    team_sum(s, scratch3, warps, turn3);
+    const float rstd = rsqrtf(s[0] * inv + eps);
+    const float qn = s[1] * rstd * inv, qm = center ? s[2] * inv : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = (tid + k * tm.threads) * V;
+      if (i >= group) continue;
+      float ox[V], oz[V], w[V], bi[V];
+      load_params<V>(weight + c0 + i, vec_params, w);
+      if (BIAS && gate == SSD_GATE_OUTPUT) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) bi[e] = 0.f;
+        if (bias) load_params<V>(bias + c0 + i, vec_params, bi);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float zv = zc[k].at(e), xv = xc[k].at(e), sg = sig[k][e], sz = zv * sg;
+        const float gv = gv_of(k, e);
+        const float n = (r_of(k, e) - mean) * rstd;
+        dw[k][e] = fmaf(gv, n, dw[k][e]);
+        if (BIAS) db[k][e] += gv;
+        const float g = rstd * (gv * w[e] - n * qn - qm);
+        const float slope = sg * fmaf(zv, 1.f - sg, 1.f);  // silu'
+        ox[e] = gate == SSD_GATE_INPUT ? g * sz : g;
+        if (gate == SSD_GATE_INPUT) oz[e] = slope * (g * xv);
+        if (gate == SSD_GATE_OUTPUT)
+          oz[e] = slope * (gc[k].at(e) * (BIAS ? fmaf(n, w[e], bi[e]) : n * w[e]));
+      }
+      store_vec<V>(dx.at(here.b, here.t) + c0 + i, ox);
+      if (gate) store_vec<V>(dz.at(here.b, here.t) + c0 + i, oz);
+    }
+  }
+  const int64_t D = G * group, slice = team / G;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int i = (tid + k * tm.threads) * V;
+    if (i >= group) continue;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      part_w[slice * D + c0 + i + e] = dw[k][e];
+      if (BIAS) part_b[slice * D + c0 + i + e] = db[k][e];
+    }
+  }
+}
+
 template <typename T>
 struct tag {
   using type = T;
@@ -198,6 +582,58 @@ cudaError_t dispatch(ssd_dtype io, bool vec, F f) {
                : f(io_c, std::integral_constant<int, 1>{});
   };
   return io == SSD_BF16 ? by_vec(tag<__nv_bfloat16>{}) : by_vec(tag<float>{});
+}
+
+// Elements per vector that the sizes and every address allow: 16 bytes, two
+// elements, or one.
+int vector_of(const NormArgs &a, ssd_dtype io) {
+  const size_t e = io == SSD_BF16 ? 2 : 4;
+  auto fits = [&](size_t n) {
+    return (a.D / a.G) % n == 0 && view_aligned(a.x, e, n * e) && view_aligned(a.z, e, n * e) &&
+           view_aligned(a.y, e, n * e) && view_aligned(a.gy, e, n * e) &&
+           view_aligned(a.dx, e, n * e) && view_aligned(a.dz, e, n * e);
+  };
+  return fits(16 / e) ? (int)(16 / e) : fits(2) ? 2 : 1;
+}
+// Vectors per thread: up to 16 channels (8 of fp32, whose registers are twice
+// as many; 8 single ones in the gradients).
+constexpr int vectors_per_thread(int V, bool back) {
+  return V == 8 || V == 4 ? 2 : V == 2 ? 4 : 8;
+}
+
+// The team for a group, or 0 threads where a block's registers do not hold it.
+int team_threads(const NormArgs &a, ssd_dtype io, bool back) {
+  const int V = vector_of(a, io), per = V * vectors_per_thread(V, back);
+  const int64_t n = (a.D / a.G + per - 1) / per;
+  return n > kMaxTeam ? 0 : (int)((n + 31) / 32 * 32);
+}
+// Teams: about `warps` warps to an SM in all.
+Teams teams_of(const NormArgs &a, int threads, int warps) {
+  Teams t;
+  t.threads = threads;
+  const int64_t want = (int64_t)sm_count() * warps * 32 / threads;
+  t.strides = (want + a.G - 1) / a.G;
+  if (t.strides > a.b * a.L) t.strides = a.b * a.L;
+  return t;
+}
+constexpr int kFwdWarps = 30, kGradWarps = 16;  // what fits at once
+
+template <typename F>
+cudaError_t dispatch_team(ssd_dtype io, int V, int gate, F f) {
+  using std::integral_constant;
+  auto by_gate = [&](auto io_c, auto v_c) {
+    if (gate == SSD_GATE_INPUT) return f(io_c, v_c, integral_constant<int, SSD_GATE_INPUT>{});
+    if (gate == SSD_GATE_OUTPUT) return f(io_c, v_c, integral_constant<int, SSD_GATE_OUTPUT>{});
+    return f(io_c, v_c, integral_constant<int, SSD_GATE_NONE>{});
+  };
+  if (io == SSD_BF16) {
+    if (V == 8) return by_gate(tag<__nv_bfloat16>{}, integral_constant<int, 8>{});
+    if (V == 2) return by_gate(tag<__nv_bfloat16>{}, integral_constant<int, 2>{});
+    return by_gate(tag<__nv_bfloat16>{}, integral_constant<int, 1>{});
+  }
+  if (V == 4) return by_gate(tag<float>{}, integral_constant<int, 4>{});
+  if (V == 2) return by_gate(tag<float>{}, integral_constant<int, 2>{});
+  return by_gate(tag<float>{}, integral_constant<int, 1>{});
 }
 
 bool vectored(const NormArgs &a, ssd_dtype io) {
@@ -218,6 +654,25 @@ int64_t slices(const NormArgs &a) { return (a.b * a.L + slice_rows(a) - 1) / sli
 }  // namespace
 
 cudaError_t launch_gated_norm(const NormArgs &a, ssd_dtype io, int *err, cudaStream_t st) {
+  if (const int threads = team_threads(a, io, false)) {
+    const Teams tm = teams_of(a, threads, kFwdWarps);
+    const int block = threads == 32 ? 256 : threads;
+    const int64_t blocks = (tm.strides * a.G * threads + block - 1) / block;
+    return dispatch_team(io, vector_of(a, io), a.gate, [&](auto io_c, auto v_c, auto gate_c) {
+      using IO = typename decltype(io_c)::type;
+      constexpr int V = decltype(v_c)::value;
+      constexpr int K = vectors_per_thread(V, false), gate = decltype(gate_c)::value;
+      const size_t smem = V * sizeof(IO) == 16 ? (size_t)kStages * 2 * K * 16 * block : 0;
+      const cudaError_t e =
+          cudaFuncSetAttribute(norm_team_kernel<IO, V, K, gate>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      norm_team_kernel<IO, V, K, gate><<<(unsigned)blocks, block, smem, st>>>(
+          view_of<const IO>(a.x), a.weight, a.bias, view_of<const IO>(a.z), view_of<IO>(a.y), a.L,
+          a.b * a.L, a.G, (int)(a.D / a.G), a.eps, a.center, tm, err);
+      return cudaGetLastError();
+    });
+  }
   return dispatch(io, vectored(a, io), [&](auto io_c, auto v_c) {
     using IO = typename decltype(io_c)::type;
     const dim3 grid((unsigned)(a.b * a.L), (unsigned)a.G);
@@ -228,12 +683,48 @@ cudaError_t launch_gated_norm(const NormArgs &a, ssd_dtype io, int *err, cudaStr
   });
 }
 
-size_t gated_norm_backward_workspace(const NormArgs &a, ssd_dtype) {
-  return sizeof(Stat) * (size_t)(a.b * a.L * a.G) + 2 * sizeof(float) * (size_t)(slices(a) * a.D);
+// The team for a group may differ between the size's query and the call (the
+// addresses' alignment is not known to the query): room for either.
+size_t gated_norm_backward_workspace(const NormArgs &a, ssd_dtype io) {
+  const size_t two = sizeof(Stat) * (size_t)(a.b * a.L * a.G) +
+                     2 * sizeof(float) * (size_t)(slices(a) * a.D);
+  const int64_t most = teams_of(a, 32, kGradWarps).strides;  // the smallest team has most
+  const size_t one = 2 * sizeof(float) * (size_t)(most * a.D);
+  return one > two ? one : two;
 }
 
 cudaError_t launch_gated_norm_backward(const NormArgs &a, ssd_dtype io, void *ws, int *err,
                                        cudaStream_t st) {
+  if (const int threads = team_threads(a, io, true)) {
+    const Teams tm = teams_of(a, threads, kGradWarps);
+    float *part_w = static_cast<float *>(ws), *part_b = part_w + tm.strides * a.D;
+    const int block = threads == 32 ? 256 : threads;
+    const int64_t blocks = (tm.strides * a.G * threads + block - 1) / block;
+    const cudaError_t e = dispatch_team(io, vector_of(a, io), a.gate, [&](auto io_c, auto v_c, auto gate_c) {
+      using IO = typename decltype(io_c)::type;
+      constexpr int V = decltype(v_c)::value;
+      constexpr int K = vectors_per_thread(V, true), gate = decltype(gate_c)::value;
+      const size_t smem = V * sizeof(IO) == 16 ? (size_t)kStages * 3 * K * 16 * block : 0;
+      auto go = [&](auto bias_c) {
+        auto kernel = norm_team_grad_kernel<IO, V, K, gate, decltype(bias_c)::value>;
+        const cudaError_t e1 = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e1 != cudaSuccess) return e1;
+        kernel<<<(unsigned)blocks, block, smem, st>>>(
+            view_of<const IO>(a.x), a.weight, a.bias, view_of<const IO>(a.z),
+            view_of<const IO>(a.gy), view_of<IO>(a.dx), view_of<IO>(a.dz), part_w, part_b, a.L,
+            a.b * a.L, a.G, (int)(a.D / a.G), a.eps, a.center, tm, err);
+        return cudaGetLastError();
+      };
+      return a.bias || a.dbias ? go(std::true_type{}) : go(std::false_type{});
+    });
+    if (e != cudaSuccess) return e;
+    ColSum s{};
+    s.nseg = 2;
+    s.seg[0] = {part_w, a.dweight, tm.strides, a.D};
+    s.seg[1] = {part_b, a.dbias, tm.strides, a.D};
+    return launch_colsum(s, err, st);
+  }
   Stat *stat = static_cast<Stat *>(ws);
   float *part_w = reinterpret_cast<float *>(stat + a.b * a.L * a.G);
   float *part_b = part_w + slices(a) * a.D;

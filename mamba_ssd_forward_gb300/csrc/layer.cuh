@@ -35,6 +35,12 @@ template <int V, typename T>
 __device__ __forceinline__ void load_vec(const T *p, float (&v)[V]) {
   if constexpr (V == 1) {
     v[0] = ld_io(p);
+  } else if constexpr (V == 2 && sizeof(T) == 4) {
+    const float2 f = *reinterpret_cast<const float2 *>(p);
+    v[0] = f.x, v[1] = f.y;
+  } else if constexpr (V == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xffff0000u);
   } else if constexpr (sizeof(T) == 4) {
     static_assert(V % 4 == 0, "");
 #pragma unroll
@@ -63,6 +69,10 @@ template <int V, typename T>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
   if constexpr (V == 1) {
     st_io(p, v[0]);
+  } else if constexpr (V == 2 && sizeof(T) == 4) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < V; i += 4)
@@ -79,6 +89,19 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
     else
       *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
   }
+}
+
+// Asynchronous copies of 16 bytes to shared memory.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src));
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;"); }
+// All groups but the newest `left` have landed.
+template <int left>
+__device__ __forceinline__ void copies_landed() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {

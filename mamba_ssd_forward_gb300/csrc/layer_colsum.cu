@@ -1,5 +1,5 @@
 // Column sums of partial arrays (the parameter gradients' last step): one
-// block per 32 columns, eight row slices whose partial sums are added in slice
+// block per 32 columns, 16 row slices whose partial sums are added in slice
 // order.  The order depends on the sizes only, so results repeat bit for bit.
 // Bandwidth-bound on arrays that are small next to what produced them.
 #include "layer.cuh"
@@ -7,7 +7,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kCols = 32, kSlices = 8;
+constexpr int kCols = 32, kSlices = 16;
 
 __global__ void __launch_bounds__(kCols *kSlices) colsum_kernel(ColSum a, int *err) {
   __shared__ float part[kSlices][kCols];
@@ -22,9 +22,11 @@ __global__ void __launch_bounds__(kCols *kSlices) colsum_kernel(ColSum a, int *e
   const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
   const int64_t i = blk * kCols + col;
   float acc = 0.f;
-  if (i < g.n)
-    for (int64_t r = slice; r < g.rows; r += kSlices)
-      if (SSD_IN_BOUNDS(r >= 0 && r < g.rows && i < g.n, err, 60)) acc += g.src[r * g.n + i];
+  if (i < g.n && SSD_IN_BOUNDS(g.rows >= 0, err, 60)) {
+    const float *p = g.src + i;
+#pragma unroll 8
+    for (int64_t r = slice; r < g.rows; r += kSlices) acc += p[r * g.n];
+  }
   part[slice][col] = acc;
   __syncthreads();
   if (slice == 0 && i < g.n) {

@@ -10,6 +10,8 @@
 namespace ssd {
 namespace scan {
 
+constexpr float kLn2 = 0.6931471805599453f;
+
 // The step of a token: v = dt + bias, or log(1 + exp(v)) as
 // max(v, 0) + t q(t) with t = exp(-|v|) in (0, 1], which neither overflows nor
 // loses small values.  q is the degree-8 polynomial of least relative error

@@ -43,18 +43,6 @@ struct Cut {
   int64_t span;         // tokens per segment
 };
 
-__device__ __forceinline__ void copy16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src));
-}
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;"); }
-// All groups but the newest `left` have landed.
-template <int left>
-__device__ __forceinline__ void copies_landed() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
-}
-
 // A warp's copies of kTile tokens' rows of one view into COLS columns of
 // shared memory.  VEC: 16 bytes at a time, asynchronously, the lanes taking
 // turns over the pieces of the rows; else element by element.

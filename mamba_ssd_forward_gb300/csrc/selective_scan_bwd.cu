@@ -1,12 +1,27 @@
 // Gradients of the selective scan.  With e_t = exp(s_t A), o_t = gy_t silu(z_t)
-// and the adjoint state G_t = o_t C_t + e_{t+1} G_{t+1}:
-//   du = s sum_n G B + D o          ds = sum_n G (u B + A e h_{t-1})
-//   dA = sum_t s G e h_{t-1}        dB = sum_d G s u,   dC = sum_d o h
+// and the adjoint state G_t = o_t C_t + q_t, q_{t-1} = e_t G_t:
+//   du = s sum_n G B + D o          ds = sum_n (u G B + A q_{t-1} h_{t-1})
+//   dA = sum_t s q_{t-1} h_{t-1}    dB = sum_d G s u,   dC = sum_d o h
 //   dz = gy (sum_n h C + D u) silu'(z),   ddt = ds softplus'
 //
-// Three steps: the states at every kSpan-th token; then span by span from the
-// end, the states of the span again and the adjoint backwards over it; then
-// the sums over channel tiles (dB, dC) and over sequences (dA, dD, ddt_bias).
+// The states are needed backwards in time, so they are recomputed from the
+// state at the start of each segment of SEG (16) tokens:
+// 1. ends_kernel: each segment's end from a zero state and its steps' sum; per
+//    part of several segments the adjoint that reaches its front, summed
+//    forwards as sum_t exp(A (s_1 + .. + s_t)) o_t C_t.
+// 2. chain_kernel: those joined in order into every segment's start state and
+//    every part's arriving adjoint (and dh0).
+// 3. adjoint_kernel: a warp per part, segment by segment from the last: the
+//    states at every fourth token, kept in shared memory; then four tokens at
+//    a time from the last, their states again (in registers) and the adjoint
+//    back over them.
+// 4. the sums over channel tiles (dB, dC) and over parts (dA, dD, ddt_bias).
+//
+// A lane holds four channels, as two fp32 pairs, of four states: the sums over
+// the channels (dB, dC) and over the states (du, ds, dz) are then both mostly
+// inside the lane, 7 and 6 exchanges a token for 16 states.  Bound by the
+// arithmetic: 3.75 exponentials and some 25 multiply-adds per (token, channel,
+// state) against 46 bytes per (token, channel).
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -14,246 +29,650 @@ namespace {
 
 using namespace scan;
 
-constexpr int kThreads = 128;
-constexpr int kSpan = 16;
+// Warps of the adjoint to an SM: at 8 a lane has 242 registers and spills
+// nothing (4 sequences of 1024 tokens and 2048 channels: 405 us in all; at 10,
+// 168 registers with spills, some 50 us more).
+constexpr int kMin = 8;
+constexpr int kMinEnds = 16;  // 128 registers: 405 us, at 12 warps (162) 429, at 20 (96) 446
 
-template <typename IO, int NL>
-__global__ void __launch_bounds__(kThreads)
-states_kernel(In<IO> in, float *__restrict__ states, int64_t spans, int *err) {
-  const int64_t ch = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL;
-  const int n0 = threadIdx.x % NL * 4, N = in.N;
-  const int64_t b = blockIdx.y;
-  if (ch >= in.D) return;
-  const int64_t d = ch, g = d / in.per_group;
-  if (!SSD_IN_BOUNDS(b < in.nb, err, 71)) return;
-  const int64_t len = tokens_of(in.lengths, b, in.L);
-  float A[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-  load4_tail(in.A + d * N, n0, N, A);
+// How a warp lies over channels and states.
+template <int NL>
+struct Geo {
+  static constexpr int CG = 32 / NL, CW = 4 * CG, NP = 4 * NL;
+  static constexpr int SEG = 512 / CW < 16 ? 512 / CW : 16;  // tokens per segment
+};
+
+// Sums of v[0..V) over LANES lanes, STRIDE apart, spread over them: afterwards
+// lane idx holds the sums of V / LANES values from idx V / LANES on, or, with
+// fewer values than lanes, that of value idx V / LANES.
+template <int STRIDE, int LANES, int V>
+__device__ __forceinline__ void spread(float (&v)[V], int lane) {
+  int half = V / 2;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
-  if (in.h0) load4_tail(in.h0 + (b * in.D + d) * N, n0, N, h);
-  const float bias = in.dt_bias ? in.dt_bias[d] : 0.f;
-  for (int64_t t = 0; t < len; ++t) {
-    if (t % kSpan == 0)
-      store4_tail(states + ((b * spans + t / kSpan) * in.D + d) * N, n0, N, h);
-    float B[4];
-    load4_tail(in.B.at(b, t) + g * N, n0, N, B);
-    const float u = ld_io(in.u.at(b, t) + d);
-    const float s = step_of(ld_io(in.dt.at(b, t) + d) + bias, in.softplus);
+  for (int off = LANES / 2; off > 0; off /= 2) {
+    if (half >= 1) {
+      const bool up = lane / STRIDE & off;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if (i >= half) break;
+        const float send = up ? v[i] : v[half + i], keep = up ? v[half + i] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off * STRIDE);
+      }
+      half /= 2;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off * STRIDE);
+    }
+  }
+}
+
+// The work's division: channel tiles per group, segments per sequence, parts
+// of `per` segments.
+struct Parts {
+  int tiles;
+  int64_t segments, parts;
+  int per;
+};
+
+// Where a warp stands.
+struct Unit {
+  int tile;
+  int64_t g, part, b, tile_id;  // tile_id: over (sequence, group, tile)
+};
+__device__ __forceinline__ Unit unit_of(int64_t i, const Parts &p, int64_t G) {
+  Unit u;
+  u.tile = (int)(i % p.tiles);
+  u.g = i / p.tiles % G;
+  u.part = i / p.tiles / G % p.parts;
+  u.b = i / p.tiles / G / p.parts;
+  u.tile_id = (u.b * G + u.g) * p.tiles + u.tile;
+  return u;
+}
+
+struct Buffers {
+  float2 *ends;        // [tile_id][segment][8][32]: ends, then start states
+  float *sums;         // [tile_id][segment][CW]: the segment's steps
+  float2 *adj;         // [tile_id][part][8][32]: adjoints at the front, then arriving ones
+  float *part_sums;    // [tile_id][part][CW]
+  float *partB, *partC;              // [tile][b, L, G, N]
+  float *partA, *partD, *partBias;   // [b, part, D, N], [b, part, D] twice
+};
+
+// s, s u and o of a segment, and its B and C with every value twice.
+template <int NL>
+struct Stage {
+  using G = Geo<NL>;
+  float s[G::SEG][G::CW], su[G::SEG][G::CW], o[G::SEG][G::CW];
+  float2 B[G::SEG][G::NP], C[G::SEG][G::NP];
+};
+
+// V channels of one token of a view; zero where `ok` is false.
+template <int V, typename IO>
+__device__ __forceinline__ void load_if(bool ok, const SeqView<const IO> &m, int64_t b, int64_t t,
+                                        int64_t c, float (&v)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = 0.f;
+  if (ok) load_vec<V>(m.at(b, t) + c, v);
+}
+
+// Fills a Stage from tokens t0 .. t0 + n of the tile; zero beyond them and
+// beyond the tile's `live` channels, which leaves states and adjoints alone.
+template <typename IO, int NL, int V>
+__device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &gy, Stage<NL> &sm,
+                                     int64_t b, int64_t g, int64_t c0, int live, int64_t t0, int n,
+                                     int lane, int *err) {
+  using Ge = Geo<NL>;
+  constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    const int q = lane + i * 32, r = q / PR, c = q % PR * V;
+    const bool ok = r < n && c < live && SSD_IN_BOUNDS(t0 + r < in.L && c0 + c + V <= in.D, err, 77);
+    float u[V], dt[V], z[V], go[V], s[V], su[V];
+    load_if<V>(ok, in.u, b, t0 + r, c0 + c, u);
+    load_if<V>(ok, in.dt, b, t0 + r, c0 + c, dt);
+    load_if<V>(ok, gy, b, t0 + r, c0 + c, go);
+    load_if<V>(ok && in.z.p, in.z, b, t0 + r, c0 + c, z);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float bias = in.dt_bias && ok ? in.dt_bias[c0 + c + e] : 0.f;
+      s[e] = ok ? step_of(dt[e] + bias, in.softplus) : 0.f;
+      su[e] = s[e] * u[e];
+      if (in.z.p) go[e] *= silu(z[e]);
+    }
+    store_vec<V>(&sm.s[r][c], s);
+    store_vec<V>(&sm.su[r][c], su);
+    store_vec<V>(&sm.o[r][c], go);
+  }
+  for (int q = lane; q < Ge::SEG * Ge::NP; q += 32) {
+    const int r = q / Ge::NP, k = q % Ge::NP;
+    const bool ok = r < n && k < in.N;
+    const float vB = ok ? ld_io(in.B.at(b, t0 + r) + g * in.N + k) : 0.f;
+    const float vC = ok ? ld_io(in.C.at(b, t0 + r) + g * in.N + k) : 0.f;
+    sm.B[r][k] = make_float2(vB, vB);
+    sm.C[r][k] = make_float2(vC, vC);
+  }
+}
+
+// A lane's pairs of a parameter or state row-major over [channels][N].
+__device__ __forceinline__ pair load_pair(const float *p, int64_t d, int c, int live, int n,
+                                          int N, float scale = 1.f) {
+  if (n >= N) return 0;
+  return pack(c < live ? p[(d + c) * N + n] * scale : 0.f,
+              c + 1 < live ? p[(d + c + 1) * N + n] * scale : 0.f);
+}
+
+// Two pairs (four channels) of a row of a Stage array; four values, each
+// twice, of B or C.
+__device__ __forceinline__ void four(const float *p, pair (&v)[2]) {
+  const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p);
+  v[0] = q.x, v[1] = q.y;
+}
+__device__ __forceinline__ void four_twice(const float2 *p, pair (&v)[4]) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+template <typename IO, int NL, int V>
+__global__ void __launch_bounds__(32, kMinEnds)
+ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err) {
+  using Ge = Geo<NL>;
+  __shared__ __align__(16) Stage<NL> sm;
+  const int lane = threadIdx.x, nl = lane % NL, cg = lane / NL;
+  const Unit un = unit_of(blockIdx.x, parts, in.D / in.per_group);
+  const int64_t c0 = un.g * in.per_group + un.tile * Ge::CW;
+  const int live = min(Ge::CW, in.per_group - un.tile * Ge::CW);
+  if (!SSD_IN_BOUNDS(un.b < in.nb && c0 + live <= in.D, err, 71)) return;
+  const int64_t len = tokens_of(in.lengths, un.b, in.L);
+  pair A[4][2], P[4][2], R[4][2], all[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      A[i][p] = load_pair(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, in.N, kLog2e);
+      P[i][p] = both(1.f);
+      R[i][p] = 0;
+    }
+  const int64_t last = min((un.part + 1) * parts.per, parts.segments);
+  for (int64_t seg = un.part * parts.per; seg < last; ++seg) {
+    const int64_t t0 = seg * Ge::SEG;
+    const int n = (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+    pair h[4][2], sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i][0] = h[i][1] = 0;
+    if (n > 0) {
+      __syncwarp();
+      fill<IO, NL, V>(in, gy, sm, un.b, un.g, c0, live, t0, n, lane, err);
+      __syncwarp();
+#pragma unroll 4
+      for (int k = 0; k < Ge::SEG; ++k) {
+        pair s[2], su[2], o[2], B[4], C[4];
+        four(&sm.s[k][cg * 4], s);
+        four(&sm.su[k][cg * 4], su);
+        four(&sm.o[k][cg * 4], o);
+        four_twice(&sm.B[k][nl * 4], B);
+        four_twice(&sm.C[k][nl * 4], C);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          sum[p] = add2(sum[p], s[p]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const pair e = ex2_2(mul2(s[p], A[i][p]));
+            h[i][p] = fma2(e, h[i][p], mul2(su[p], B[i]));
+            P[i][p] = mul2(e, P[i][p]);
+            R[i][p] = fma2(P[i][p], mul2(o[p], C[i]), R[i][p]);
+          }
+        }
+      }
+    }
+    const int64_t at = un.tile_id * parts.segments + seg;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      h[i] = fmaf(ex2(s * A[i]), h[i], n0 + i < N ? s * u * B[i] : 0.f);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        reinterpret_cast<pair *>(buf.ends)[(at * 8 + i * 2 + p) * 32 + lane] = h[i][p];
+    all[0] = add2(all[0], sum[0]), all[1] = add2(all[1], sum[1]);
+    if (nl == 0) {
+      pair *q = reinterpret_cast<pair *>(buf.sums + at * Ge::CW + cg * 4);
+      q[0] = sum[0], q[1] = sum[1];
+    }
+  }
+  const int64_t at = un.tile_id * parts.parts + un.part;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      reinterpret_cast<pair *>(buf.adj)[(at * 8 + i * 2 + p) * 32 + lane] = R[i][p];
+  if (nl == 0) {
+    pair *q = reinterpret_cast<pair *>(buf.part_sums + at * Ge::CW + cg * 4);
+    q[0] = all[0], q[1] = all[1];
+  }
+}
+
+// Two blocks per tile, for the states and for the adjoints: thread (i, p, lane)
+// as the warps above hold the pairs.
+template <int NL>
+__global__ void __launch_bounds__(256)
+chain_kernel(const float *__restrict__ A, const float *__restrict__ h0,
+             const float *__restrict__ gfinal, float *__restrict__ dh0, Parts parts, Buffers buf,
+             int64_t nb, int64_t D, int N, int per_group, int *err) {
+  using Ge = Geo<NL>;
+  constexpr int kBatch = 8;  // entries loaded ahead
+  const int lane = threadIdx.x % 32, ip = threadIdx.x / 32, nl = lane % NL, cg = lane / NL;
+  const int64_t G = D / per_group, id = blockIdx.x;
+  const int tile = (int)(id % parts.tiles);
+  const int64_t g = id / parts.tiles % G, b = id / parts.tiles / G;
+  const int64_t c0 = g * per_group + tile * Ge::CW;
+  const int live = min(Ge::CW, per_group - tile * Ge::CW);
+  if (!SSD_IN_BOUNDS(b < nb && c0 + live <= D, err, 78)) return;
+  const int c = cg * 4 + ip % 2 * 2, n = nl * 4 + ip / 2;
+  const pair a = load_pair(A, c0, c, live, n, N, kLog2e);
+  // x = exp(A sum) x + end over `count` entries, in order or backwards; each
+  // entry is replaced by the x that arrives there
+  auto chain = [&](pair x, pair *v, const float *sum, int64_t count, bool back) {
+    pair end[kBatch], s[kBatch];
+    auto load = [&](int64_t k) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t at = back ? count - 1 - k - j : k + j;
+        end[j] = s[j] = 0;
+        if (k + j < count) {
+          end[j] = v[at * 256];
+          s[j] = *reinterpret_cast<const pair *>(sum + at * Ge::CW);
+        }
+      }
+    };
+    load(0);
+    for (int64_t k = 0; k < count; k += kBatch) {
+      pair e[kBatch], f[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) e[j] = end[j], f[j] = s[j];
+      load(k + kBatch);  // the next entries, before these are replaced
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t at = back ? count - 1 - k - j : k + j;
+        if (k + j < count) v[at * 256] = x;
+        x = fma2(ex2_2(mul2(f[j], a)), x, e[j]);  // past the end: x itself
+      }
+    }
+    return x;
+  };
+  const int64_t row = b * D;
+  if (blockIdx.y == 0) {
+    const pair first = h0 ? load_pair(h0 + row * N, c0, c, live, n, N) : 0;
+    chain(first, reinterpret_cast<pair *>(buf.ends) + id * parts.segments * 256 + ip * 32 + lane,
+          buf.sums + id * parts.segments * Ge::CW + c, parts.segments, false);
+    return;
+  }
+  const pair arriving = gfinal ? load_pair(gfinal + row * N, c0, c, live, n, N) : 0;
+  const pair q =
+      chain(arriving, reinterpret_cast<pair *>(buf.adj) + id * parts.parts * 256 + ip * 32 + lane,
+            buf.part_sums + id * parts.parts * Ge::CW + c, parts.parts, true);
+  if (dh0 && n < N) {
+    float x, y;
+    unpack(q, x, y);
+    if (c < live) dh0[(row + c0 + c) * N + n] = x;
+    if (c + 1 < live) dh0[(row + c0 + c + 1) * N + n] = y;
   }
 }
 
 template <typename IO>
 struct Out {
   SeqView<IO> du, ddt, dz;
-  float *partB, *partC;            // [tile, b, L, G, N]
-  float *partA, *partD, *partBias; // [b, D, N], [b, D], [b, D]
-  float *dh0;
 };
 
-// grid: (tile of channels, group, sequence); a tile's channels share a group.
-template <typename IO, int NL>
-__global__ void __launch_bounds__(kThreads)
-adjoint_kernel(In<IO> in, SeqView<const IO> gy, const float *__restrict__ gfinal,
-               const float *__restrict__ states, int64_t spans, Out<IO> out, int *err) {
-  constexpr int kWarps = kThreads / 32;
-  __shared__ float sumB[kWarps][4 * NL], sumC[kWarps][4 * NL];
-  const int64_t chan = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL;
-  const int lane = threadIdx.x % NL, n0 = lane * 4, N = in.N;
-  const int64_t g = blockIdx.y, G = gridDim.y, b = blockIdx.z;
-  const bool live = chan < in.per_group;
-  const int64_t d = g * in.per_group + (live ? chan : in.per_group - 1);
-  if (!SSD_IN_BOUNDS(b < in.nb && d < in.D, err, 72)) return;
-  const int64_t len = tokens_of(in.lengths, b, in.L);
-  float A[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, ad[4] = {0.f, 0.f, 0.f, 0.f};
-  load4_tail(in.A + d * N, n0, N, A);
-  if (gfinal) load4_tail(gfinal + (b * in.D + d) * N, n0, N, ad);
-  const float bias = in.dt_bias ? in.dt_bias[d] : 0.f, skip = in.Dskip ? in.Dskip[d] : 0.f;
-  float dD = 0.f, dbias = 0.f;
-  for (int64_t sp = (len + kSpan - 1) / kSpan - 1; sp >= 0; --sp) {
-    const int64_t t0 = sp * kSpan;
-    const int n = (int)(len - t0 < kSpan ? len - t0 : kSpan);
-    float h[4], before[kSpan][4];
-    load4_tail(states + ((b * spans + sp) * in.D + d) * N, n0, N, h);
+template <typename IO, int NL, int V>
+__global__ void __launch_bounds__(32, kMin)
+adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO> out, int *err) {
+  using Ge = Geo<NL>;
+  constexpr int SUB = Ge::SEG / 4;
+  struct Smem {
+    Stage<NL> st;
+    float gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
+    pair start[SUB][8][32];  // states in front of every fourth token
+  };
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Smem &sm = *reinterpret_cast<Smem *>(raw_smem);
+  const int lane = threadIdx.x, nl = lane % NL, cg = lane / NL, N = in.N;
+  const int64_t G = in.D / in.per_group;
+  const Unit un = unit_of(blockIdx.x, parts, G);
+  const int64_t c0 = un.g * in.per_group + un.tile * Ge::CW;
+  const int live = min(Ge::CW, in.per_group - un.tile * Ge::CW);
+  if (!SSD_IN_BOUNDS(un.b < in.nb && c0 + live <= in.D, err, 72)) return;
+  const int64_t len = tokens_of(in.lengths, un.b, in.L);
+  pair A[4][2], q[4][2], dA[4][2];
+  const int64_t mine = un.tile_id * parts.parts + un.part;
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) {
-      if (j >= n) break;
-      float B[4];
-      load4_tail(in.B.at(b, t0 + j) + g * N, n0, N, B);
-      const float u = ld_io(in.u.at(b, t0 + j) + d);
-      const float s = step_of(ld_io(in.dt.at(b, t0 + j) + d) + bias, in.softplus);
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        before[j][i] = h[i];
-        h[i] = fmaf(ex2(s * A[i] * kLog2e), h[i], n0 + i < N ? s * u * B[i] : 0.f);
-      }
+    for (int p = 0; p < 2; ++p) {
+      A[i][p] = load_pair(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, N, kLog2e);
+      q[i][p] = reinterpret_cast<const pair *>(buf.adj)[(mine * 8 + i * 2 + p) * 32 + lane];
+      dA[i][p] = 0;
     }
+  constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
+  constexpr int VD = PR >= 32 ? V * (PR / 32) : V;  // this lane's columns
+  float dD[VD], dbias[VD];
 #pragma unroll
-    for (int j = kSpan - 1; j >= 0; --j) {
-      if (j >= n) continue;
-      const int64_t t = t0 + j;
-      float B[4], C[4], pB[4], pC[4];
-      load4_tail(in.B.at(b, t) + g * N, n0, N, B);
-      load4_tail(in.C.at(b, t) + g * N, n0, N, C);
-      const float u = ld_io(in.u.at(b, t) + d);
-      const float raw = ld_io(in.dt.at(b, t) + d) + bias;
-      const float s = step_of(raw, in.softplus);
-      const float gyv = ld_io(gy.at(b, t) + d);
-      const float zv = in.z.p ? ld_io(in.z.at(b, t) + d) : 0.f;
-      const float o = in.z.p ? gyv * silu(zv) : gyv;
-      float yv = 0.f, gB = 0.f, gah = 0.f;
+  for (int e = 0; e < VD; ++e) dD[e] = dbias[e] = 0.f;
+
+  const int64_t last = min((un.part + 1) * parts.per, parts.segments);
+  for (int64_t seg = last - 1; seg >= un.part * parts.per; --seg) {
+    const int64_t t0 = seg * Ge::SEG;
+    const int n = (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+    __syncwarp();
+    if (n > 0) {
+      fill<IO, NL, V>(in, gy, sm.st, un.b, un.g, c0, live, t0, n, lane, err);
+      pair h[4][2];
+      const pair *from = reinterpret_cast<const pair *>(buf.ends) +
+                         (un.tile_id * parts.segments + seg) * 256 + lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = ex2(s * A[i] * kLog2e);
-        const float ht = fmaf(e, before[j][i], n0 + i < N ? s * u * B[i] : 0.f);
-        ad[i] = n0 + i < N ? fmaf(o, C[i], ad[i]) : 0.f;
-        yv = fmaf(ht, C[i], yv);
-        pC[i] = live ? o * ht : 0.f;
-        pB[i] = live && n0 + i < N ? ad[i] * s * u : 0.f;
-        gB = fmaf(ad[i], B[i], gB);
-        ad[i] *= e;
-        const float p = ad[i] * before[j][i];
-        dA[i] = fmaf(s, p, dA[i]);
-        gah = fmaf(A[i], p, gah);
-      }
-      yv = fmaf(skip, u, sum_lanes<NL>(yv));
-      gB = sum_lanes<NL>(gB);
-      gah = sum_lanes<NL>(gah);
-      float ds = fmaf(u, gB, gah);
-      if (in.softplus) ds *= sigmoid(raw);
-      dD = fmaf(o, u, dD);
-      dbias += ds;
-      if (lane == 0 && live) {
-        st_io(out.du.at(b, t) + d, fmaf(s, gB, skip * o));
-        st_io(out.ddt.at(b, t) + d, ds);
-        if (out.dz.p) st_io(out.dz.at(b, t) + d, gyv * yv * dsilu(zv));
-      }
-      // over the tile's channels: lanes with the same states, then warps
+      for (int i = 0; i < 8; ++i) sm.start[0][i][lane] = h[i / 2][i % 2] = from[i * 32];
+      __syncwarp();
+      // the states in front of every fourth token
+#pragma unroll 1
+      for (int sub = 1; sub < SUB; ++sub) {
 #pragma unroll
-      for (int off = NL; off < 32; off <<= 1)
+        for (int k = 0; k < 4; ++k) {
+          const int t = sub * 4 - 4 + k;
+          pair s[2], su[2], B[4];
+          four(&sm.st.s[t][cg * 4], s);
+          four(&sm.st.su[t][cg * 4], su);
+          four_twice(&sm.st.B[t][nl * 4], B);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          pB[i] += __shfl_xor_sync(0xffffffffu, pB[i], off);
-          pC[i] += __shfl_xor_sync(0xffffffffu, pC[i], off);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              h[i][p] = fma2(ex2_2(mul2(s[p], A[i][p])), h[i][p], mul2(su[p], B[i]));
         }
-      if (threadIdx.x % 32 < NL)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sumB[threadIdx.x / 32][n0 + i] = pB[i];
-          sumC[threadIdx.x / 32][n0 + i] = pC[i];
-        }
-      __syncthreads();
-      if ((int)threadIdx.x < N) {
-        float vB = sumB[0][threadIdx.x], vC = sumC[0][threadIdx.x];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) vB += sumB[w][threadIdx.x], vC += sumC[w][threadIdx.x];
-        const int64_t o4 = ((((int64_t)blockIdx.x * in.nb + b) * in.L + t) * G + g) * N + threadIdx.x;
-        out.partB[o4] = vB;
-        out.partC[o4] = vC;
+        for (int i = 0; i < 8; ++i) sm.start[sub][i][lane] = h[i / 2][i % 2];
       }
-      __syncthreads();
+#pragma unroll 1
+      for (int sub = SUB - 1; sub >= 0; --sub) {
+        pair hs[5][4][2];  // before each token, and after the last
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hs[0][i / 2][i % 2] = sm.start[sub][i][lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = sub * 4 + k;
+          pair s[2], su[2], B[4], C[4];
+          four(&sm.st.s[t][cg * 4], s);
+          four(&sm.st.su[t][cg * 4], su);
+          four_twice(&sm.st.B[t][nl * 4], B);
+          four_twice(&sm.st.C[t][nl * 4], C);
+          float y[4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            pair acc = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hs[k + 1][i][p] =
+                  fma2(ex2_2(mul2(s[p], A[i][p])), hs[k][i][p], mul2(su[p], B[i]));
+              acc = fma2(hs[k + 1][i][p], C[i], acc);
+            }
+            unpack(acc, y[2 * p], y[2 * p + 1]);
+          }
+          if (in.z.p) {
+            spread<1, NL, 4>(y, lane);
+            constexpr int KEEP = NL < 4 ? 4 / NL : 1, DUP = NL > 4 ? NL / 4 : 1;
+            if (nl % DUP == 0)
+#pragma unroll
+              for (int j = 0; j < KEEP; ++j) sm.y[t][cg * 4 + nl / DUP * KEEP + j] = y[j];
+          }
+        }
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const int t = sub * 4 + k;
+          pair s[2], su[2], o[2], B[4], C[4];
+          four(&sm.st.s[t][cg * 4], s);
+          four(&sm.st.su[t][cg * 4], su);
+          four(&sm.st.o[t][cg * 4], o);
+          four_twice(&sm.st.B[t][nl * 4], B);
+          four_twice(&sm.st.C[t][nl * 4], C);
+          float over_c[8], over_n[8];  // dB, dC of the states; sums of G B, A q h of the channels
+          pair dB[4], dC[4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            pair gB = 0, gah = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const pair Gt = fma2(o[p], C[i], q[i][p]);
+              dB[i] = p ? fma2(Gt, su[p], dB[i]) : mul2(Gt, su[p]);
+              dC[i] = p ? fma2(hs[k + 1][i][p], o[p], dC[i]) : mul2(hs[k + 1][i][p], o[p]);
+              gB = fma2(Gt, B[i], gB);
+              q[i][p] = mul2(Gt, ex2_2(mul2(s[p], A[i][p])));
+              const pair qh = mul2(q[i][p], hs[k][i][p]);
+              dA[i][p] = fma2(s[p], qh, dA[i][p]);
+              gah = fma2(A[i][p], qh, gah);
+            }
+            unpack(gB, over_n[2 * p], over_n[2 * p + 1]);
+            unpack(gah, over_n[4 + 2 * p], over_n[4 + 2 * p + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) over_c[i] = sum2(dB[i]), over_c[4 + i] = sum2(dC[i]);
+          spread<NL, Ge::CG, 8>(over_c, lane);
+          spread<1, NL, 8>(over_n, lane);
+          {
+            constexpr int KEEP = Ge::CG < 8 ? 8 / Ge::CG : 1, DUP = Ge::CG > 8 ? Ge::CG / 8 : 1;
+            if (cg % DUP == 0 && t < n)
+#pragma unroll
+              for (int j = 0; j < KEEP; ++j) {
+                const int v = cg / DUP * KEEP + j, st = nl * 4 + v % 4;
+                if (st < N)
+                  (v < 4 ? buf.partB : buf.partC)[(((un.tile * in.nb + un.b) * in.L + t0 + t) * G +
+                                                   un.g) * N + st] = over_c[j];
+              }
+          }
+          __syncwarp();  // every lane has read s u of this token
+          {
+            constexpr int KEEP = NL < 8 ? 8 / NL : 1, DUP = NL > 8 ? NL / 8 : 1;
+            if (nl % DUP == 0)
+#pragma unroll
+              for (int j = 0; j < KEEP; ++j) {
+                const int v = nl / DUP * KEEP + j;
+                (v < 4 ? sm.st.su : sm.gah)[t][cg * 4 + v % 4] = over_n[j];
+              }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    // what remains is per token and channel; su now holds the sums of G B
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+      const int idx = lane + i * 32, r = idx / PR, c = idx % PR * V;
+      const int64_t t = t0 + r;
+      if (t >= in.L || c >= live || !SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79)) continue;
+      const bool ok = r < n;
+      float u[V], dt[V], z[V], gyv[V], du[V], ddt[V], dz[V];
+      load_if<V>(ok, in.u, un.b, t, c0 + c, u);
+      load_if<V>(ok, in.dt, un.b, t, c0 + c, dt);
+      load_if<V>(ok && in.z.p, in.z, un.b, t, c0 + c, z);
+      load_if<V>(ok && in.z.p, gy, un.b, t, c0 + c, gyv);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        du[e] = ddt[e] = dz[e] = 0.f;
+        if (!ok) continue;
+        const float skip = in.Dskip ? in.Dskip[c0 + c + e] : 0.f;
+        const float gB = sm.st.su[r][c + e], o = sm.st.o[r][c + e];
+        du[e] = fmaf(sm.st.s[r][c + e], gB, skip * o);
+        ddt[e] = fmaf(u[e], gB, sm.gah[r][c + e] * kLn2);
+        if (in.softplus)
+          ddt[e] *= sigmoid(dt[e] + (in.dt_bias ? in.dt_bias[c0 + c + e] : 0.f));
+        if (in.z.p) dz[e] = gyv[e] * fmaf(skip, u[e], sm.y[r][c + e]) * dsilu(z[e]);
+        const int col = PR >= 32 ? i % (PR >= 32 ? PR / 32 : 1) * V + e : e;
+        dD[col] = fmaf(o, u[e], dD[col]);
+        dbias[col] += ddt[e];
+      }
+      store_vec<V>(out.du.at(un.b, t) + c0 + c, du);
+      store_vec<V>(out.ddt.at(un.b, t) + c0 + c, ddt);
+      if (out.dz.p) store_vec<V>(out.dz.at(un.b, t) + c0 + c, dz);
     }
   }
-  if (!live) return;
-  if (out.dh0) store4_tail(out.dh0 + (b * in.D + d) * N, n0, N, ad);
-  store4_tail(out.partA + (b * in.D + d) * N, n0, N, dA);
-  if (lane == 0) {
-    out.partD[b * in.D + d] = dD;
-    out.partBias[b * in.D + d] = dbias;
-    for (int64_t t = len; t < in.L; ++t) {
-      st_io(out.du.at(b, t) + d, 0.f);
-      st_io(out.ddt.at(b, t) + d, 0.f);
-      if (out.dz.p) st_io(out.dz.at(b, t) + d, 0.f);
+  const int64_t row = un.b * parts.parts + un.part;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float x, y;
+      unpack(dA[i][p], x, y);
+      const int c = cg * 4 + p * 2, st = nl * 4 + i;
+      if (st >= N) continue;
+      if (c < live) buf.partA[(row * in.D + c0 + c) * N + st] = x;
+      if (c + 1 < live) buf.partA[(row * in.D + c0 + c + 1) * N + st] = y;
+    }
+  // lanes with the same columns hold different tokens
+#pragma unroll
+  for (int e = 0; e < VD; ++e) {
+#pragma unroll
+    for (int off = 16; off >= PR; off /= 2) {
+      dD[e] += __shfl_xor_sync(0xffffffffu, dD[e], off);
+      dbias[e] += __shfl_xor_sync(0xffffffffu, dbias[e], off);
+    }
+    const int c = PR >= 32 ? (lane + e / V * 32) * V + e % V : lane % PR * V + e;
+    if (lane < PR && c < live) {
+      buf.partD[row * in.D + c0 + c] = dD[e];
+      buf.partBias[row * in.D + c0 + c] = dbias[e];
     }
   }
 }
 
 // dB and dC: the tiles' parts in order; zero past a sequence's end.
 template <typename IO>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 sum_tiles_kernel(const float *__restrict__ partB, const float *__restrict__ partC, int tiles,
                  SeqView<IO> dB, SeqView<IO> dC, const int32_t *__restrict__ lengths, int64_t nb,
                  int64_t L, int64_t GN, int *err) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = nb * L * GN;
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, n = nb * L * GN;
   if (i >= n) return;
   const int64_t c = i % GN, t = i / GN % L, b = i / GN / L;
   if (!SSD_IN_BOUNDS(b < nb && t < L, err, 73)) return;
-  float vB = 0.f, vC = 0.f;
-  if (t < tokens_of(lengths, b, L))
-    for (int k = 0; k < tiles; ++k) vB += partB[k * n + i], vC += partC[k * n + i];
-  st_io(dB.at(b, t) + c, vB);
-  st_io(dC.at(b, t) + c, vC);
+  float v = 0.f;
+  const float *part = blockIdx.y ? partC : partB;
+  if (t < tokens_of(lengths, b, L)) {
+#pragma unroll 8
+    for (int k = 0; k < tiles; ++k) v += part[k * n + i];
+  }
+  st_io((blockIdx.y ? dC : dB).at(b, t) + c, v);
+}
+
+// Segments to a part: enough parts for about two rounds of resident warps, at
+// most 16 segments (each part writes 2 KB of dA).
+Parts parts_of(const ScanArgs &a, int cw, int seg) {
+  Parts p;
+  p.tiles = (int)((a.D / a.G + cw - 1) / cw);
+  p.segments = (a.L + seg - 1) / seg;
+  const int64_t all = a.b * a.G * p.tiles * p.segments, want = (int64_t)sm_count() * 24;
+  int64_t per = all / want;
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  if (per > p.segments) per = p.segments;
+  p.per = (int)per;
+  p.parts = (p.segments + per - 1) / per;
+  return p;
 }
 
 struct Layout {
-  int64_t spans, tiles;
-  size_t states, partB, partC, partA, partD, partBias, total;  // in floats
+  Parts parts;
+  size_t ends, sums, adj, part_sums, partB, partC, partA, partD, partBias, total;  // in floats
 };
+template <int NL>
 Layout layout_of(const ScanArgs &a) {
+  using Ge = Geo<NL>;
   Layout l;
-  const int64_t per = kThreads / lanes_of(a.N);
-  l.spans = (a.L + kSpan - 1) / kSpan;
-  l.tiles = (a.D / a.G + per - 1) / per;
+  l.parts = parts_of(a, Ge::CW, Ge::SEG);
+  const Parts &p = l.parts;
+  const int64_t ids = a.b * a.G * p.tiles;
   size_t at = 0;
   auto take = [&](int64_t n) {
     const size_t r = at;
     at += (size_t)((n + 63) / 64 * 64);
     return r;
   };
-  l.states = take(a.b * l.spans * a.D * a.N);
-  l.partB = take(l.tiles * a.b * a.L * a.G * a.N);
-  l.partC = take(l.tiles * a.b * a.L * a.G * a.N);
-  l.partA = take(a.b * a.D * a.N);
-  l.partD = take(a.b * a.D);
-  l.partBias = take(a.b * a.D);
+  l.ends = take(ids * p.segments * 512);
+  l.sums = take(ids * p.segments * Ge::CW);
+  l.adj = take(ids * p.parts * 512);
+  l.part_sums = take(ids * p.parts * Ge::CW);
+  l.partB = take(p.tiles * a.b * a.L * a.G * a.N);
+  l.partC = take(p.tiles * a.b * a.L * a.G * a.N);
+  l.partA = take(a.b * p.parts * a.D * a.N);
+  l.partD = take(a.b * p.parts * a.D);
+  l.partBias = take(a.b * p.parts * a.D);
   l.total = at;
   return l;
+}
+
+// Vectors of four along the channels.
+bool vectored(const ScanArgs &a, ssd_dtype io) {
+  const size_t e = io == SSD_BF16 ? 2 : 4;
+  return (a.D / a.G) % 4 == 0 && view_aligned(a.u, e, 4 * e) && view_aligned(a.dt, e, 4 * e) &&
+         view_aligned(a.z, e, 4 * e) && view_aligned(a.gy, e, 4 * e) &&
+         view_aligned(&a.out->du, e, 4 * e) && view_aligned(&a.out->ddt, e, 4 * e) &&
+         view_aligned(&a.out->dz, e, 4 * e);
 }
 
 }  // namespace
 
 size_t selective_scan_backward_workspace(const ScanArgs &a, ssd_dtype) {
-  return sizeof(float) * layout_of(a).total;
+  auto of = [&](auto nl) { return sizeof(float) * layout_of<decltype(nl)::value>(a).total; };
+  switch (lanes_of(a.N)) {
+    case 1: return of(std::integral_constant<int, 1>{});
+    case 2: return of(std::integral_constant<int, 2>{});
+    case 4: return of(std::integral_constant<int, 4>{});
+    case 8: return of(std::integral_constant<int, 8>{});
+    default: return of(std::integral_constant<int, 16>{});
+  }
 }
 
 cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void *ws, int *err,
                                            cudaStream_t st) {
-  const Layout l = layout_of(a);
   float *f = static_cast<float *>(ws);
-  const cudaError_t e = dispatch(io, a.N, [&](auto io_c, auto nl_c) {
+  return dispatch(io, a.N, [&](auto io_c, auto nl_c) {
     using IO = typename decltype(io_c)::type;
     constexpr int NL = decltype(nl_c)::value;
+    using Ge = Geo<NL>;
+    const Layout l = layout_of<NL>(a);
+    Buffers buf;
+    buf.ends = reinterpret_cast<float2 *>(f + l.ends), buf.sums = f + l.sums;
+    buf.adj = reinterpret_cast<float2 *>(f + l.adj), buf.part_sums = f + l.part_sums;
+    buf.partB = f + l.partB, buf.partC = f + l.partC, buf.partA = f + l.partA;
+    buf.partD = f + l.partD, buf.partBias = f + l.partBias;
     const In<IO> in = in_of<IO>(a);
-    const dim3 all((unsigned)((a.D * NL + kThreads - 1) / kThreads), (unsigned)a.b);
-    states_kernel<IO, NL><<<all, kThreads, 0, st>>>(in, f + l.states, l.spans, err);
-    cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return e1;
-    Out<IO> out;
-    out.du = view_of<IO>(&a.out->du), out.ddt = view_of<IO>(&a.out->ddt);
-    out.dz = view_of<IO>(&a.out->dz);
-    out.partB = f + l.partB, out.partC = f + l.partC, out.partA = f + l.partA;
-    out.partD = f + l.partD, out.partBias = f + l.partBias, out.dh0 = a.out->dh0;
-    const dim3 grid((unsigned)l.tiles, (unsigned)a.G, (unsigned)a.b);
-    adjoint_kernel<IO, NL><<<grid, kThreads, 0, st>>>(in, view_of<const IO>(a.gy), a.gfinal,
-                                                      f + l.states, l.spans, out, err);
-    e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return e1;
+    const SeqView<const IO> gy = view_of<const IO>(a.gy);
+    const Out<IO> out{view_of<IO>(&a.out->du), view_of<IO>(&a.out->ddt), view_of<IO>(&a.out->dz)};
+    const int64_t ids = a.b * a.G * l.parts.tiles, units = ids * l.parts.parts;
+    auto run = [&](auto v_c) {
+      constexpr int V = decltype(v_c)::value;
+      ends_kernel<IO, NL, V><<<(unsigned)units, 32, 0, st>>>(in, gy, l.parts, buf, err);
+      cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      chain_kernel<NL><<<dim3((unsigned)ids, 2), 256, 0, st>>>(a.A, a.h0, a.gfinal, a.out->dh0, l.parts,
+                                                      buf, a.b, a.D, (int)a.N, in.per_group, err);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      constexpr size_t smem = sizeof(Stage<NL>) + 2 * 4 * Ge::SEG * Ge::CW + Ge::SEG / 4 * 2048;
+      e = cudaFuncSetAttribute(adjoint_kernel<IO, NL, V>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      adjoint_kernel<IO, NL, V>
+          <<<(unsigned)units, 32, smem, st>>>(in, gy, l.parts, buf, out, err);
+      return cudaGetLastError();
+    };
+    cudaError_t e = vectored(a, io) ? run(std::integral_constant<int, 4>{})
+                                    : run(std::integral_constant<int, 1>{});
+    if (e != cudaSuccess) return e;
     const int64_t n = a.b * a.L * a.G * a.N;
-    sum_tiles_kernel<IO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
-        f + l.partB, f + l.partC, (int)l.tiles, view_of<IO>(&a.out->dB),
-        view_of<IO>(&a.out->dC), a.lengths, a.b, a.L, a.G * a.N, err);
-    return cudaGetLastError();
+    sum_tiles_kernel<IO><<<dim3((unsigned)((n + 127) / 128), 2), 128, 0, st>>>(
+        buf.partB, buf.partC, l.parts.tiles, view_of<IO>(&a.out->dB), view_of<IO>(&a.out->dC),
+        a.lengths, a.b, a.L, a.G * a.N, err);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ColSum s{};
+    s.nseg = 3;
+    s.seg[0] = {buf.partA, a.out->dA, a.b * l.parts.parts, a.D * a.N};
+    s.seg[1] = {buf.partD, a.out->dD, a.b * l.parts.parts, a.D};
+    s.seg[2] = {buf.partBias, a.out->ddt_bias, a.b * l.parts.parts, a.D};
+    return launch_colsum(s, err, st);
   });
-  if (e != cudaSuccess) return e;
-  ColSum s{};
-  s.nseg = 3;
-  s.seg[0] = {f + l.partA, a.out->dA, a.b, a.D * a.N};
-  s.seg[1] = {f + l.partD, a.out->dD, a.b, a.D};
-  s.seg[2] = {f + l.partBias, a.out->ddt_bias, a.b, a.D};
-  return launch_colsum(s, err, st);
 }
 
 }  // namespace ssd
