@@ -91,13 +91,20 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
   }
 }
 
-// Asynchronous copies of 16 bytes to shared memory.
+// Asynchronous copies of 16 or 8 bytes to shared memory.
+__device__ __forceinline__ void copy8(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                    (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src));
+               "l"(src)
+               : "memory");
 }
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;"); }
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All groups but the newest `left` have landed.
 template <int left>
 __device__ __forceinline__ void copies_landed() {

@@ -10,7 +10,8 @@ using namespace scan;
 
 constexpr int kThreads = 128;
 
-template <typename IO, int NL>
+// VEC: four states at a time (N a multiple of four, rows on such boundaries).
+template <typename IO, int NL, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 step_kernel(In<IO> in, SeqView<IO> y, float *__restrict__ state, int *err) {
   const int64_t ch = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / NL;
@@ -22,10 +23,15 @@ step_kernel(In<IO> in, SeqView<IO> y, float *__restrict__ state, int *err) {
   if (!SSD_IN_BOUNDS(b < in.nb && g * in.per_group <= d && d < in.D, err, 76)) return;
   float *hs = state + (b * in.D + d) * N;
   float A[4], h[4], B[4], C[4], acc = 0.f;
-  load4_tail(hs, n0, N, h);
-  load4_tail(in.A + d * N, n0, N, A);
-  load4_tail(in.B.at(b, 0) + g * N, n0, N, B);
-  load4_tail(in.C.at(b, 0) + g * N, n0, N, C);
+  auto four = [&](const auto *row, float (&v)[4]) {
+    if (!VEC) return load4_tail(row, n0, N, v);
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+    if (n0 < N) load_vec<4>(row + n0, v);
+  };
+  four(hs, h);
+  four(in.A + d * N, A);
+  four(in.B.at(b, 0) + g * N, B);
+  four(in.C.at(b, 0) + g * N, C);
   const float u = ld_io(in.u.at(b, 0) + d);
   const float s = step_of(ld_io(in.dt.at(b, 0) + d) + (in.dt_bias ? in.dt_bias[d] : 0.f),
                           in.softplus);
@@ -38,7 +44,10 @@ step_kernel(In<IO> in, SeqView<IO> y, float *__restrict__ state, int *err) {
   if (in.z.p) acc *= silu(ld_io(in.z.at(b, 0) + d));
   if (!live) return;
   if (lane == 0) st_io(y.at(b, 0) + d, acc);
-  store4_tail(hs, n0, N, h);
+  if (!VEC)
+    store4_tail(hs, n0, N, h);
+  else if (n0 < N)
+    store_vec<4>(hs + n0, h);
 }
 
 }  // namespace
@@ -49,8 +58,15 @@ cudaError_t launch_selective_scan_step(const ScanArgs &a, ssd_dtype io, int *err
     using IO = typename decltype(io_c)::type;
     constexpr int NL = decltype(nl_c)::value;
     const dim3 grid((unsigned)((a.D * NL + kThreads - 1) / kThreads), (unsigned)a.b);
-    step_kernel<IO, NL>
-        <<<grid, kThreads, 0, st>>>(in_of<IO>(a), view_of<IO>(a.y), a.final_state, err);
+    const size_t e = sizeof(IO);
+    const bool vec = a.N % 4 == 0 && ptr_aligned(a.final_state, 16) && ptr_aligned(a.A, 16) &&
+                     view_aligned(a.B, e, 4 * e) && view_aligned(a.C, e, 4 * e);
+    if (vec)
+      step_kernel<IO, NL, true>
+          <<<grid, kThreads, 0, st>>>(in_of<IO>(a), view_of<IO>(a.y), a.final_state, err);
+    else
+      step_kernel<IO, NL, false>
+          <<<grid, kThreads, 0, st>>>(in_of<IO>(a), view_of<IO>(a.y), a.final_state, err);
     return cudaGetLastError();
   });
 }

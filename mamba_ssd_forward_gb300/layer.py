@@ -33,61 +33,66 @@ def _io(t, name):
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}") from None
 
 
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
+def _stream(like):
+    """The current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(like.device.index)
 
 
-def _check(t, name, shape, dtype, like):
-    """A tensor of exactly this shape and type on the device of `like`."""
+def _refuse(t, name, shape, dtype, like):
+    """Says what is wrong with a tensor that is not as it has to be."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda or t.device != like.device:
         raise ValueError(f"{name} must be a CUDA tensor on the same device as the input")
+    raise ValueError(f"{name} must be contiguous" if t.stride()[-1:] == (1,) else
+                     f"{name} must be dense along its last axes")
 
 
 def _dense(t, name, shape, dtype, like):
     """Address of a dense tensor (None stays None)."""
     if t is None:
         return None
-    _check(t, name, shape, dtype, like)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda
+            or not t.is_contiguous()):
+        _refuse(t, name, shape, dtype, like)
     return t.data_ptr()
 
 
 def _seq(t, name, shape, dtype, like):
-    """View of an activation [b, L, D], [b, D] (one token each) or, with the
-    last two axes groups and states, one axis more; None stays None."""
+    """View of an activation [b, L, D]; None stays None."""
     if t is None:
         return None
-    _check(t, name, shape, dtype, like)
-    st, sh = t.stride(), t.shape
-    lead = len(sh)
-    step = 1
-    while lead > len(shape) - _inner(shape):
-        lead -= 1
-        if sh[lead] != 1 and st[lead] != step:
-            raise ValueError(f"{name} must be dense along its last axes")
-        step *= sh[lead]
-    return SsdSeq(t.data_ptr(), st[0] if sh[0] > 1 else 0,
-                  st[1] if lead == 2 and sh[1] > 1 else 0)
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+        _refuse(t, name, shape, dtype, like)
+    sb, st, sc = t.stride()
+    if sc != 1 and shape[2] != 1:
+        _refuse(t, name, shape, dtype, like)
+    return SsdSeq(t.data_ptr(), sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0)
 
 
-class _Shape(tuple):
-    """A shape whose last `inner` axes are dense."""
-    inner = 1
+def _token(t, name, shape, dtype, like):
+    """The same of one token each, [b, D]."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+        _refuse(t, name, shape, dtype, like)
+    sb, sc = t.stride()
+    if sc != 1 and shape[1] != 1:
+        _refuse(t, name, shape, dtype, like)
+    return SsdSeq(t.data_ptr(), sb if shape[0] > 1 else 0, 0)
 
 
-def _inner(shape):
-    return getattr(shape, "inner", 1)
-
-
-def _grouped(*dims):
-    s = _Shape(dims)
-    s.inner = 2
-    return s
+def _grouped(t, name, shape, dtype, like):
+    """A view [b, L, G, N] or [b, G, N] whose last two axes are dense together."""
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+        _refuse(t, name, shape, dtype, like)
+    *lead, sg, sn = t.stride()
+    if (sn != 1 and shape[-1] != 1) or (sg != shape[-1] and shape[-2] != 1):
+        raise ValueError(f"{name} must be dense along its last axes")
+    return SsdSeq(t.data_ptr(), lead[0] if shape[0] > 1 else 0,
+                  lead[1] if len(lead) == 2 and shape[1] > 1 else 0)
 
 
 def _sized(nbytes, device):
@@ -148,7 +153,7 @@ def causal_conv_forward(x, weight, bias=None, state=None, lengths=None, activati
         _dense(weight, "weight", (D, W), torch.float32, x),
         _dense(bias, "bias", (D,), torch.float32, x), _dense(state, "state", keep, x.dtype, x),
         _lengths(lengths, b, x), _seq(y, "y", (b, L, D), x.dtype, x),
-        _dense(final_state, "final_state", keep, x.dtype, x), _stream()))
+        _dense(final_state, "final_state", keep, x.dtype, x), _stream(x)))
     return y, final_state
 
 
@@ -176,7 +181,7 @@ def causal_conv_backward(x, weight, bias=None, state=None, gy=None, gfinal=None,
         _seq(gy, "gy", (b, L, D), x.dtype, x), _dense(gfinal, "gfinal", keep, x.dtype, x),
         _lengths(lengths, b, x), _seq(dx, "dx", (b, L, D), x.dtype, x), dw.data_ptr(),
         None if db is None else db.data_ptr(), None if ds is None else ds.data_ptr(), wp, wn,
-        _stream()))
+        _stream(x)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
 
 
@@ -189,11 +194,11 @@ def causal_conv_step(x, weight, bias, state, activation="silu", y=None):
     if state is None:
         raise ValueError("state is required")
     _abi.check("ssd_causal_conv_step", _abi.load().ssd_causal_conv_step(
-        d, _io(x, "x"), _seq(x, "x", (b, D), x.dtype, x),
+        d, _io(x, "x"), _token(x, "x", (b, D), x.dtype, x),
         _dense(weight, "weight", (D, W), torch.float32, x),
         _dense(bias, "bias", (D,), torch.float32, x),
-        _dense(state, "state", (b, W - 1, D), x.dtype, x), _seq(y, "y", (b, D), x.dtype, x),
-        _stream()))
+        _dense(state, "state", (b, W - 1, D), x.dtype, x), _token(y, "y", (b, D), x.dtype, x),
+        _stream(x)))
     return y
 
 
@@ -233,13 +238,12 @@ def _scan_dims(u, A, B, dt_softplus, step=False):
 def _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias, step=False):
     """The leading arguments of the scan's calls, checked."""
     lead = (d.batch,) if step else (d.batch, d.seqlen)
-    row, grp = lead + (d.channels,), _grouped(*lead, d.ngroups, d.dstate)
-    io = u.dtype
-    return [d, _io(u, "u"), _seq(u, "u", row, io, u), _seq(dt, "dt", row, io, u),
-            _dense(A, "A", (d.channels, d.dstate), torch.float32, u),
-            _seq(B, "B", grp, io, u), _seq(C, "C", grp, io, u),
-            _dense(D, "D", (d.channels,), torch.float32, u), _seq(z, "z", row, io, u),
-            _dense(dt_bias, "dt_bias", (d.channels,), torch.float32, u)]
+    nd, view = d.channels, _token if step else _seq
+    row, grp, io = (*lead, nd), (*lead, d.ngroups, d.dstate), u.dtype
+    return [d, _io(u, "u"), view(u, "u", row, io, u), view(dt, "dt", row, io, u),
+            _dense(A, "A", (nd, d.dstate), torch.float32, u), _grouped(B, "B", grp, io, u),
+            _grouped(C, "C", grp, io, u), _dense(D, "D", (nd,), torch.float32, u),
+            view(z, "z", row, io, u), _dense(dt_bias, "dt_bias", (nd,), torch.float32, u)]
 
 
 def selective_scan_workspace_size(u, A, B) -> int:
@@ -269,7 +273,7 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     _abi.check("ssd_selective_scan", lib.ssd_selective_scan(
         *args, _dense(h0, "h0", keep, torch.float32, u), _lengths(lengths, b, u),
         _seq(y, "y", (b, L, nd), u.dtype, u),
-        _dense(final_state, "final_state", keep, torch.float32, u), wp, wn, _stream()))
+        _dense(final_state, "final_state", keep, torch.float32, u), wp, wn, _stream(u)))
     return y, final_state
 
 
@@ -285,7 +289,7 @@ def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=Non
     d = _scan_dims(u, A, B, dt_softplus)
     lib, b, L, nd, N = _abi.load(), d.batch, d.seqlen, d.channels, d.dstate
     args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias)
-    row, grp, keep = (b, L, nd), _grouped(b, L, d.ngroups, N), (b, nd, N)
+    row, grp, keep = (b, L, nd), (b, L, d.ngroups, N), (b, nd, N)
 
     def io_out(shape, of=u):
         return None if of is None else torch.empty(shape, dtype=u.dtype, device=u.device)
@@ -297,9 +301,11 @@ def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=Non
          "dC": io_out(grp), "dD": f32_out((nd,), D), "dz": io_out(row, z),
          "ddt_bias": f32_out((nd,), dt_bias), "dh0": f32_out(keep, h0)}
     g = _abi.SsdScanGrads()
-    for k, shape in (("du", row), ("ddt", row), ("dz", row), ("dB", grp), ("dC", grp)):
+    for k in ("du", "ddt", "dz"):
         if r[k] is not None:
-            setattr(g, k, _seq(r[k], k, shape, u.dtype, u))
+            setattr(g, k, _seq(r[k], k, row, u.dtype, u))
+    for k in ("dB", "dC"):
+        setattr(g, k, _grouped(r[k], k, grp, u.dtype, u))
     for k in ("dA", "dD", "ddt_bias", "dh0"):
         if r[k] is not None:
             setattr(g, k, r[k].data_ptr())
@@ -308,7 +314,7 @@ def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=Non
     _abi.check("ssd_selective_scan_backward", lib.ssd_selective_scan_backward(
         *args, _dense(h0, "h0", keep, torch.float32, u), _seq(gy, "gy", row, u.dtype, u),
         _dense(gfinal, "gfinal", keep, torch.float32, u), _lengths(lengths, b, u), g, wp, wn,
-        _stream()))
+        _stream(u)))
     return r
 
 
@@ -324,7 +330,7 @@ def selective_scan_step(u, dt, A, B, C, D, z, dt_bias, state, dt_softplus: bool 
     y = _out(y, "y", row, u.dtype, u)
     _abi.check("ssd_selective_scan_step", _abi.load().ssd_selective_scan_step(
         *args, _dense(state, "state", (d.batch, d.channels, d.dstate), torch.float32, u),
-        _seq(y, "y", row, u.dtype, u), _stream()))
+        _token(y, "y", row, u.dtype, u), _stream(u)))
     return y
 
 
@@ -373,8 +379,13 @@ def _rows(d):
 
 
 def _norm_view(t, name, x, flat):
-    v = _seq(t, name, x.shape, x.dtype, x)
-    return SsdSeq(v.data, 0, v.batch_stride) if v is not None and flat else v
+    if x.dim() == 3:
+        v = _seq(t, name, x.shape, x.dtype, x)
+    else:
+        v = _token(t, name, x.shape, x.dtype, x)
+    if flat and v is not None:
+        v.batch_stride, v.token_stride = 0, v.batch_stride
+    return v
 
 
 def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float = 1e-5,
@@ -393,7 +404,7 @@ def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float
         d, _io(x, "x"), _norm_view(x, "x", x, flat),
         _dense(weight, "weight", (D,), torch.float32, x),
         _dense(bias, "bias", (D,), torch.float32, x), _norm_view(z, "z", x, flat),
-        _norm_view(y, "y", x, flat), _stream()))
+        _norm_view(y, "y", x, flat), _stream(x)))
     return y
 
 
@@ -418,7 +429,7 @@ def gated_norm_backward(x, weight, bias=None, z=None, gy=None, groups: int = 1,
         _dense(bias, "bias", (D,), torch.float32, x), _norm_view(z, "z", x, flat),
         _norm_view(gy, "gy", x, flat), _norm_view(dx, "dx", x, flat),
         _norm_view(dz, "dz", x, flat), dw.data_ptr(), None if db is None else db.data_ptr(), wp,
-        wn, _stream()))
+        wn, _stream(x)))
     return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
 
 
@@ -459,16 +470,20 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspac
     if not grads:
         raise ValueError("no gradients given")
     like = grads[0]
-    table = (_abi.SsdGrad * len(grads))()
+    dev, rows = like.device, []
     for i, (g, o) in enumerate(zip(grads, out)):
-        io = _io(g, f"grads[{i}]")
-        src = _dense(g, f"grads[{i}]", g.shape, g.dtype, like)
+        io = _IO.get(g.dtype)
+        if io is None or g.device != dev or not g.is_cuda or not g.is_contiguous():
+            _io(g, f"grads[{i}]")
+            _refuse(g, f"grads[{i}]", g.shape, g.dtype, like)
+        src = g.data_ptr()
         dst = src if o is g else _dense(o, f"out[{i}]", g.shape, g.dtype, like)
-        table[i] = (src, dst, g.numel(), io)
+        rows.append((src, dst, g.numel(), io))
+    table = (_abi.SsdGrad * len(rows))(*rows)
     lib = _abi.load()
     norm = torch.empty((), dtype=torch.float32, device=like.device)
     ws, wp, wn = _workspace(lib.ssd_clip_grad_norm_workspace_size(table, len(grads)), workspace,
                             like, "clip_grad_norm")
     _abi.check("ssd_clip_grad_norm", lib.ssd_clip_grad_norm(
-        table, len(grads), max_norm, eps, norm.data_ptr(), wp, wn, _stream()))
+        table, len(grads), max_norm, eps, norm.data_ptr(), wp, wn, _stream(like)))
     return norm
