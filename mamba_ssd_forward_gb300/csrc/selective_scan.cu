@@ -15,8 +15,8 @@
 // it needs no barrier but its own.
 //
 // Measured (bf16, 16 states, GB300): 16 sequences of 512 tokens and 5120
-// channels, uncut: 255 us, 2.6e12 (token, channel, state) a second; two of
-// 2048 tokens, in five segments: 207 us; 16384 tokens of 1536 channels: 222 us.
+// channels, uncut: 247 us, 2.7e12 (token, channel, state) a second; two of
+// 2048 tokens, in five segments: 202 us; 16384 tokens of 1536 channels: 216 us.
 // A pair multiply-add with three register operands takes three cycles of a
 // scheduler, so the body is 107 cycles a token and warp where nothing stalls.
 //
@@ -86,7 +86,7 @@ struct __align__(16) Warp {
   struct __align__(16) {  // a tile as it is in memory, and the next one
     IO u[T][CW], dt[T][CW], z[TO][CW], B[T][NP], C[TO][NP];
   } raw[2];
-  Step step[T][32];  // s, s u and, for the outputs, D u and silu(z)
+  Step step[T][CW];  // s, s u and, for the outputs, D u and silu(z)
   float B[T][NP], C[TO][NP];
 };
 
@@ -138,16 +138,17 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
   if (OUT)
     for (int64_t k = 0; k < seg; ++k) {
       const float *e = ends + slot(k) * NPT * 32 + lane;
-      const pair total = both(sums[slot(k) * 32 + lane]);
+      const pair total = both(sums[slot(k) * CW + lane / NL]);
 #pragma unroll
       for (int i = 0; i < NPT / 2; ++i)
         h[i] = fma2(ex2_2(mul2(total, A[i])), h[i], pack(e[2 * i * 32], e[(2 * i + 1) * 32]));
     }
-  const float bias = in.dt_bias ? in.dt_bias[d] : 0.f;
-  const float skip = OUT && in.Dskip ? in.Dskip[d] : 0.f;
-
   const int cols = min(CW, in.per_group - tile * CW);
   const int64_t c0 = g * in.per_group + tile * CW;
+  // the channel whose tokens this lane prepares
+  const int mine = lane % CW;
+  const float bias = in.dt_bias && mine < cols ? in.dt_bias[c0 + mine] : 0.f;
+  const float skip = OUT && in.Dskip && mine < cols ? in.Dskip[c0 + mine] : 0.f;
   RowCopy<IO, CW, VEC> cu(in.u, b, first, c0, cols, lane), cd(in.dt, b, first, c0, cols, lane),
       cz(in.z, b, first, c0, cols, lane);
   RowCopy<IO, NP, VEC> cB(in.B, b, first, g * N, N, lane), cC(in.C, b, first, g * N, N, lane);
@@ -182,28 +183,36 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
     const auto &raw = sm.raw[turn];
     // what the tokens need besides the states
     constexpr int EB = TT * NP / 32;
+    constexpr int EV = EB % 4 == 0 ? 4 : 1;
 #pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      (&sm.B[0][0])[lane * EB + i] = ld_io(&raw.B[0][0] + lane * EB + i);
-      if (OUT) (&sm.C[0][0])[lane * EB + i] = ld_io(&raw.C[0][0] + lane * EB + i);
+    for (int i = 0; i < EB; i += EV) {
+      float v[EV];
+      load_vec<EV>(&raw.B[0][0] + lane * EB + i, v);
+      store_vec<EV>(&sm.B[0][0] + lane * EB + i, v);
+      if (OUT) {
+        load_vec<EV>(&raw.C[0][0] + lane * EB + i, v);
+        store_vec<EV>(&sm.C[0][0] + lane * EB + i, v);
+      }
     }
-    const int my = lane / NL;
+    constexpr int EACH = TT * CW / 32;  // tokens of its channel that a lane prepares
 #pragma unroll
-    for (int k = 0; k < TT; ++k) {
-      const float uk = ld_io(&raw.u[k][my]);
-      const float s = step_of(ld_io(&raw.dt[k][my]) + bias, in.softplus);
+    for (int i = 0; i < (EACH > 0 ? EACH : 1); ++i) {
+      const int k = lane / CW + i * (32 / CW);
+      if (EACH == 0 && k >= TT) break;
+      const float uk = ld_io(&raw.u[k][mine]);
+      const float s = step_of(ld_io(&raw.dt[k][mine]) + bias, in.softplus);
       if constexpr (OUT) {
-        sm.step[k][lane] =
-            make_float4(s, s * uk, skip * uk, gated ? silu(ld_io(&raw.z[k][my])) : 1.f);
+        sm.step[k][mine] =
+            make_float4(s, s * uk, skip * uk, gated ? silu(ld_io(&raw.z[k][mine])) : 1.f);
       } else {
-        sm.step[k][lane] = make_float2(s, s * uk);
+        sm.step[k][mine] = make_float2(s, s * uk);
         if (k < n) total += s;
       }
     }
     __syncwarp();
 #pragma unroll kUnroll
     for (int k = 0; k < n; ++k) {
-      const Step st = sm.step[k][lane];
+      const Step st = sm.step[k][lane / NL];
       const pair ss = both(st.x), su = both(st.y);
       pair acc = 0;
       const ulonglong2 *pB = reinterpret_cast<const ulonglong2 *>(&sm.B[k][n0]);
@@ -249,7 +258,9 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
       e[2 * i * 32] = h0;
       e[(2 * i + 1) * 32] = h1;
     }
-    sums[slot(seg) * 32 + lane] = total;
+#pragma unroll
+    for (int off = 16; off >= CW; off /= 2) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (lane < CW) sums[slot(seg) * CW + lane] = total;
   }
 }
 
@@ -261,9 +272,16 @@ bool vectored(const ScanArgs &a, ssd_dtype io) {
          view_aligned(a.C, e, 16);
 }
 
-// States per lane and lanes per channel.
-int npt_of(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : 16; }
-int nl_of(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
+// States per lane and lanes per channel.  (Four or eight states to a lane give
+// more warps, which would not have to be cut: 16 states on four lanes took 312
+// us where five segments take 202.)
+struct Split {
+  int npt, nl;
+};
+Split split_of(const ScanArgs &a) {
+  if (a.N <= 16) return {a.N <= 4 ? 4 : a.N <= 8 ? 8 : 16, 1};
+  return {16, a.N <= 32 ? 2 : 4};
+}
 
 // Segments: as many as the warps resident at once (three blocks to an SM; at
 // 24 warps to an SM in all 16384 tokens of 1536 channels took 247 us, at 12
@@ -273,7 +291,7 @@ int nl_of(int64_t N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }
 constexpr int kPerSm = 12;
 Cut cut_of(const ScanArgs &a) {
   Cut c;
-  const int cw = 32 / nl_of(a.N);
+  const int cw = 32 / split_of(a).nl;
   c.tiles = (int)((a.D / a.G + cw - 1) / cw);
   const int64_t warps = a.b * a.G * c.tiles, room = (int64_t)sm_count() * kPerSm;
   int64_t s = room / warps;
@@ -291,7 +309,7 @@ int64_t slots_of(const ScanArgs &a, const Cut &c) {
 
 size_t selective_scan_workspace(const ScanArgs &a, ssd_dtype) {
   const Cut c = cut_of(a);
-  return c.segments == 1 ? 0 : sizeof(float) * 32 * (npt_of(a.N) + 1) * slots_of(a, c);
+  return c.segments == 1 ? 0 : sizeof(float) * 32 * (split_of(a).npt + 1) * slots_of(a, c);
 }
 
 cudaError_t launch_selective_scan(const ScanArgs &a, ssd_dtype io, void *ws, int *err,
@@ -299,7 +317,7 @@ cudaError_t launch_selective_scan(const ScanArgs &a, ssd_dtype io, void *ws, int
   const Cut c = cut_of(a);
   const int64_t per_seg = a.b * a.G * c.tiles;
   float *ends = static_cast<float *>(ws);
-  float *sums = ends + (c.segments == 1 ? 0 : slots_of(a, c) * 32 * npt_of(a.N));
+  float *sums = ends + (c.segments == 1 ? 0 : slots_of(a, c) * 32 * split_of(a).npt);
   auto go = [&](auto io_c, auto npt_c, auto nl_c, auto vec_c) {
     using IO = typename decltype(io_c)::type;
     constexpr int NPT = decltype(npt_c)::value, NL = decltype(nl_c)::value;
@@ -329,13 +347,18 @@ cudaError_t launch_selective_scan(const ScanArgs &a, ssd_dtype io, void *ws, int
                            : go(io_c, npt_c, nl_c, std::false_type{});
   };
   auto by_n = [&](auto io_c) {
-    using one = std::integral_constant<int, 1>;
-    using sixteen = std::integral_constant<int, 16>;
-    if (a.N <= 4) return by_vec(io_c, std::integral_constant<int, 4>{}, one{});
-    if (a.N <= 8) return by_vec(io_c, std::integral_constant<int, 8>{}, one{});
-    if (a.N <= 16) return by_vec(io_c, sixteen{}, one{});
-    if (a.N <= 32) return by_vec(io_c, sixteen{}, std::integral_constant<int, 2>{});
-    return by_vec(io_c, sixteen{}, std::integral_constant<int, 4>{});
+    using std::integral_constant;
+    const Split p = split_of(a);
+    using four = integral_constant<int, 4>;
+    using eight = integral_constant<int, 8>;
+    using sixteen = integral_constant<int, 16>;
+    using one = integral_constant<int, 1>;
+    using two = integral_constant<int, 2>;
+    if (p.npt == 4) return by_vec(io_c, four{}, one{});
+    if (p.npt == 8) return by_vec(io_c, eight{}, one{});
+    if (p.nl == 1) return by_vec(io_c, sixteen{}, one{});
+    if (p.nl == 2) return by_vec(io_c, sixteen{}, two{});
+    return by_vec(io_c, sixteen{}, four{});
   };
   return io == SSD_BF16 ? by_n(tag<__nv_bfloat16>{}) : by_n(tag<float>{});
 }
