@@ -105,6 +105,42 @@ struct Stage {
   float2 B[G::SEG][G::NP], C[G::SEG][G::NP];
 };
 
+// A segment's inputs as they are in memory, copied one segment ahead.
+template <typename IO, int NL>
+struct __align__(16) Raw {
+  using G = Geo<NL>;
+  IO u[G::SEG][G::CW], dt[G::SEG][G::CW], gy[G::SEG][G::CW], z[G::SEG][G::CW];
+  IO B[G::SEG][G::NP], C[G::SEG][G::NP];
+};
+
+// The first n rows from token t0 on of a view's columns, 16 bytes at a time.
+template <int COLS, int ROWS, typename IO>
+__device__ __forceinline__ void copy_rows(IO *dst, const SeqView<const IO> &m, int64_t b,
+                                          int64_t t0, int n, int64_t first, int cols, int lane) {
+  constexpr int kPer = 16 / (int)sizeof(IO), kPieces = COLS >= kPer ? COLS / kPer : 1;
+  const int row = lane / kPieces, col = lane % kPieces * kPer;
+  const IO *p = m.at(b, t0 + row) + first + col;
+#pragma unroll
+  for (int r = 0; r < ROWS; r += 32 / kPieces)
+    if (col < cols && row + r < n && row + r < ROWS)
+      copy16(dst + (row + r) * COLS + col, p + r * m.ts);
+}
+template <typename IO, int NL>
+__device__ __forceinline__ void copy_segment(const In<IO> &in, const SeqView<const IO> &gy,
+                                             Raw<IO, NL> &raw, int64_t b, int64_t g, int64_t c0,
+                                             int live, int64_t t0, int n, int lane, int *err) {
+  using Ge = Geo<NL>;
+  if (n > 0 && SSD_IN_BOUNDS(t0 >= 0 && t0 + n <= in.L, err, 80)) {
+    copy_rows<Ge::CW, Ge::SEG>(raw.u[0], in.u, b, t0, n, c0, live, lane);
+    copy_rows<Ge::CW, Ge::SEG>(raw.dt[0], in.dt, b, t0, n, c0, live, lane);
+    copy_rows<Ge::CW, Ge::SEG>(raw.gy[0], gy, b, t0, n, c0, live, lane);
+    if (in.z.p) copy_rows<Ge::CW, Ge::SEG>(raw.z[0], in.z, b, t0, n, c0, live, lane);
+    copy_rows<Ge::NP, Ge::SEG>(raw.B[0], in.B, b, t0, n, g * in.N, in.N, lane);
+    copy_rows<Ge::NP, Ge::SEG>(raw.C[0], in.C, b, t0, n, g * in.N, in.N, lane);
+  }
+  copies_issued();
+}
+
 // V channels of one token of a view; zero where `ok` is false.
 template <int V, typename IO>
 __device__ __forceinline__ void load_if(bool ok, const SeqView<const IO> &m, int64_t b, int64_t t,
@@ -114,12 +150,13 @@ __device__ __forceinline__ void load_if(bool ok, const SeqView<const IO> &m, int
   if (ok) load_vec<V>(m.at(b, t) + c, v);
 }
 
-// Fills a Stage from tokens t0 .. t0 + n of the tile; zero beyond them and
-// beyond the tile's `live` channels, which leaves states and adjoints alone.
-template <typename IO, int NL, int V>
-__device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &gy, Stage<NL> &sm,
-                                     int64_t b, int64_t g, int64_t c0, int live, int64_t t0, int n,
-                                     int lane, int *err) {
+// Fills a Stage from tokens t0 .. t0 + n of the tile, out of `raw` where they
+// were copied (AHEAD); zero beyond them and beyond the tile's `live` channels,
+// which leaves states and adjoints alone.
+template <typename IO, int NL, int V, bool AHEAD>
+__device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &gy,
+                                     const Raw<IO, NL> &raw, Stage<NL> &sm, int64_t b, int64_t g,
+                                     int64_t c0, int live, int64_t t0, int n, int lane, int *err) {
   using Ge = Geo<NL>;
   constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
 #pragma unroll
@@ -127,26 +164,37 @@ __device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &
     const int q = lane + i * 32, r = q / PR, c = q % PR * V;
     const bool ok = r < n && c < live && SSD_IN_BOUNDS(t0 + r < in.L && c0 + c + V <= in.D, err, 77);
     float u[V], dt[V], z[V], go[V], s[V], su[V];
-    load_if<V>(ok, in.u, b, t0 + r, c0 + c, u);
-    load_if<V>(ok, in.dt, b, t0 + r, c0 + c, dt);
-    load_if<V>(ok, gy, b, t0 + r, c0 + c, go);
-    load_if<V>(ok && in.z.p, in.z, b, t0 + r, c0 + c, z);
+    if constexpr (AHEAD) {
+      load_vec<V>(&raw.u[r][c], u);
+      load_vec<V>(&raw.dt[r][c], dt);
+      load_vec<V>(&raw.gy[r][c], go);
+      load_vec<V>(&raw.z[r][c], z);
+    } else {
+      load_if<V>(ok, in.u, b, t0 + r, c0 + c, u);
+      load_if<V>(ok, in.dt, b, t0 + r, c0 + c, dt);
+      load_if<V>(ok, gy, b, t0 + r, c0 + c, go);
+      load_if<V>(ok && in.z.p, in.z, b, t0 + r, c0 + c, z);
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float bias = in.dt_bias && ok ? in.dt_bias[c0 + c + e] : 0.f;
       s[e] = ok ? step_of(dt[e] + bias, in.softplus) : 0.f;
-      su[e] = s[e] * u[e];
-      if (in.z.p) go[e] *= silu(z[e]);
+      su[e] = ok ? s[e] * u[e] : 0.f;
+      go[e] = !ok ? 0.f : in.z.p ? go[e] * silu(z[e]) : go[e];
     }
     store_vec<V>(&sm.s[r][c], s);
     store_vec<V>(&sm.su[r][c], su);
     store_vec<V>(&sm.o[r][c], go);
   }
+#pragma unroll
   for (int q = lane; q < Ge::SEG * Ge::NP; q += 32) {
     const int r = q / Ge::NP, k = q % Ge::NP;
     const bool ok = r < n && k < in.N;
-    const float vB = ok ? ld_io(in.B.at(b, t0 + r) + g * in.N + k) : 0.f;
-    const float vC = ok ? ld_io(in.C.at(b, t0 + r) + g * in.N + k) : 0.f;
+    float vB = 0.f, vC = 0.f;
+    if (ok) {
+      vB = AHEAD ? ld_io(&raw.B[r][k]) : ld_io(in.B.at(b, t0 + r) + g * in.N + k);
+      vC = AHEAD ? ld_io(&raw.C[r][k]) : ld_io(in.C.at(b, t0 + r) + g * in.N + k);
+    }
     sm.B[r][k] = make_float2(vB, vB);
     sm.C[r][k] = make_float2(vC, vC);
   }
@@ -172,11 +220,13 @@ __device__ __forceinline__ void four_twice(const float2 *p, pair (&v)[4]) {
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
-template <typename IO, int NL, int V>
+template <typename IO, int NL, int V, bool AHEAD>
 __global__ void __launch_bounds__(32, kMinEnds)
 ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err) {
   using Ge = Geo<NL>;
-  __shared__ __align__(16) Stage<NL> sm;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Stage<NL> &sm = *reinterpret_cast<Stage<NL> *>(raw_smem);
+  Raw<IO, NL> &raw = *reinterpret_cast<Raw<IO, NL> *>(raw_smem + sizeof(Stage<NL>));
   const int lane = threadIdx.x, nl = lane % NL, cg = lane / NL;
   const Unit un = unit_of(blockIdx.x, parts, in.D / in.per_group);
   const int64_t c0 = un.g * in.per_group + un.tile * Ge::CW;
@@ -193,16 +243,28 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err)
       R[i][p] = 0;
     }
   const int64_t last = min((un.part + 1) * parts.per, parts.segments);
+  auto tokens = [&](int64_t seg) {  // of a segment
+    const int64_t t0 = seg * Ge::SEG;
+    return (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+  };
+  auto ahead = [&](int64_t seg) {
+    if (AHEAD)
+      copy_segment<IO, NL>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
+                           seg < last ? tokens(seg) : 0, lane, err);
+  };
+  ahead(un.part * parts.per);
   for (int64_t seg = un.part * parts.per; seg < last; ++seg) {
     const int64_t t0 = seg * Ge::SEG;
-    const int n = (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+    const int n = tokens(seg);
     pair h[4][2], sum[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i][0] = h[i][1] = 0;
     if (n > 0) {
+      if (AHEAD) copies_landed<0>();
       __syncwarp();
-      fill<IO, NL, V>(in, gy, sm, un.b, un.g, c0, live, t0, n, lane, err);
+      fill<IO, NL, V, AHEAD>(in, gy, raw, sm, un.b, un.g, c0, live, t0, n, lane, err);
       __syncwarp();
+      ahead(seg + 1);
 #pragma unroll 4
       for (int k = 0; k < Ge::SEG; ++k) {
         pair s[2], su[2], o[2], B[4], C[4];
@@ -320,18 +382,24 @@ struct Out {
   SeqView<IO> du, ddt, dz;
 };
 
-template <typename IO, int NL, int V>
+template <typename IO, int NL, bool AHEAD>
+struct AdjointSmem {
+  using Ge = Geo<NL>;
+  static constexpr int SUB = Ge::SEG / 4;
+  Stage<NL> st;
+  float gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
+  pair start[SUB > 1 ? SUB - 1 : 1][8][32];  // states in front of tokens 4, 8, ..
+  unsigned char raw[AHEAD ? sizeof(Raw<IO, NL>) : 16];
+};
+
+template <typename IO, int NL, int V, bool AHEAD>
 __global__ void __launch_bounds__(32, kMin)
 adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO> out, int *err) {
   using Ge = Geo<NL>;
   constexpr int SUB = Ge::SEG / 4;
-  struct Smem {
-    Stage<NL> st;
-    float gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
-    pair start[SUB][8][32];  // states in front of every fourth token
-  };
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  Smem &sm = *reinterpret_cast<Smem *>(raw_smem);
+  auto &sm = *reinterpret_cast<AdjointSmem<IO, NL, AHEAD> *>(raw_smem);
+  Raw<IO, NL> &raw = *reinterpret_cast<Raw<IO, NL> *>(sm.raw);
   const int lane = threadIdx.x, nl = lane % NL, cg = lane / NL, N = in.N;
   const int64_t G = in.D / in.per_group;
   const Unit un = unit_of(blockIdx.x, parts, G);
@@ -356,18 +424,30 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   for (int e = 0; e < VD; ++e) dD[e] = dbias[e] = 0.f;
 
   const int64_t last = min((un.part + 1) * parts.per, parts.segments);
+  auto tokens = [&](int64_t seg) {  // of a segment
+    const int64_t t0 = seg * Ge::SEG;
+    return (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+  };
+  auto ahead = [&](int64_t seg) {
+    if (AHEAD)
+      copy_segment<IO, NL>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
+                           seg >= un.part * parts.per ? tokens(seg) : 0, lane, err);
+  };
+  ahead(last - 1);
   for (int64_t seg = last - 1; seg >= un.part * parts.per; --seg) {
     const int64_t t0 = seg * Ge::SEG;
-    const int n = (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
+    const int n = tokens(seg);
+    if (AHEAD) copies_landed<0>();
     __syncwarp();
     if (n > 0) {
-      fill<IO, NL, V>(in, gy, sm.st, un.b, un.g, c0, live, t0, n, lane, err);
+      fill<IO, NL, V, AHEAD>(in, gy, raw, sm.st, un.b, un.g, c0, live, t0, n, lane, err);
+      __syncwarp();
+      ahead(seg - 1);
       pair h[4][2];
       const pair *from = reinterpret_cast<const pair *>(buf.ends) +
                          (un.tile_id * parts.segments + seg) * 256 + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sm.start[0][i][lane] = h[i / 2][i % 2] = from[i * 32];
-      __syncwarp();
+      for (int i = 0; i < 8; ++i) h[i / 2][i % 2] = from[i * 32];
       // the states in front of every fourth token
 #pragma unroll 1
       for (int sub = 1; sub < SUB; ++sub) {
@@ -385,13 +465,14 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
               h[i][p] = fma2(ex2_2(mul2(s[p], A[i][p])), h[i][p], mul2(su[p], B[i]));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sm.start[sub][i][lane] = h[i / 2][i % 2];
+        for (int i = 0; i < 8; ++i) sm.start[sub - 1][i][lane] = h[i / 2][i % 2];
       }
 #pragma unroll 1
       for (int sub = SUB - 1; sub >= 0; --sub) {
         pair hs[5][4][2];  // before each token, and after the last
 #pragma unroll
-        for (int i = 0; i < 8; ++i) hs[0][i / 2][i % 2] = sm.start[sub][i][lane];
+        for (int i = 0; i < 8; ++i)
+          hs[0][i / 2][i % 2] = sub > 0 ? sm.start[sub > 0 ? sub - 1 : 0][i][lane] : from[i * 32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int t = sub * 4 + k;
@@ -477,6 +558,7 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
       }
       __syncwarp();
     }
+    if (n == 0) ahead(seg - 1);
     // what remains is per token and channel; su now holds the sums of G B
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
@@ -601,11 +683,13 @@ Layout layout_of(const ScanArgs &a) {
   return l;
 }
 
-// Vectors of four along the channels.
+// Whether every row is whole pieces of 16 bytes, and the outputs' rows vectors
+// of four.
 bool vectored(const ScanArgs &a, ssd_dtype io) {
   const size_t e = io == SSD_BF16 ? 2 : 4;
-  return (a.D / a.G) % 4 == 0 && view_aligned(a.u, e, 4 * e) && view_aligned(a.dt, e, 4 * e) &&
-         view_aligned(a.z, e, 4 * e) && view_aligned(a.gy, e, 4 * e) &&
+  return a.N * e % 16 == 0 && (a.D / a.G) * e % 16 == 0 && view_aligned(a.u, e, 16) &&
+         view_aligned(a.dt, e, 16) && view_aligned(a.z, e, 16) && view_aligned(a.gy, e, 16) &&
+         view_aligned(a.B, e, 16) && view_aligned(a.C, e, 16) &&
          view_aligned(&a.out->du, e, 4 * e) && view_aligned(&a.out->ddt, e, 4 * e) &&
          view_aligned(&a.out->dz, e, 4 * e);
 }
@@ -642,19 +726,24 @@ cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void
     const int64_t ids = a.b * a.G * l.parts.tiles, units = ids * l.parts.parts;
     auto run = [&](auto v_c) {
       constexpr int V = decltype(v_c)::value;
-      ends_kernel<IO, NL, V><<<(unsigned)units, 32, 0, st>>>(in, gy, l.parts, buf, err);
-      cudaError_t e = cudaGetLastError();
+      constexpr bool AHEAD = V > 1;
+      constexpr size_t m0 = sizeof(Stage<NL>) + (AHEAD ? sizeof(Raw<IO, NL>) : 0);
+      constexpr size_t m1 = sizeof(AdjointSmem<IO, NL, AHEAD>);
+      cudaError_t e = cudaFuncSetAttribute(ends_kernel<IO, NL, V, AHEAD>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)m0);
+      if (e != cudaSuccess) return e;
+      ends_kernel<IO, NL, V, AHEAD><<<(unsigned)units, 32, m0, st>>>(in, gy, l.parts, buf, err);
+      e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       chain_kernel<NL><<<dim3((unsigned)ids, 2), 256, 0, st>>>(a.A, a.h0, a.gfinal, a.out->dh0, l.parts,
                                                       buf, a.b, a.D, (int)a.N, in.per_group, err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      constexpr size_t smem = sizeof(Stage<NL>) + 2 * 4 * Ge::SEG * Ge::CW + Ge::SEG / 4 * 2048;
-      e = cudaFuncSetAttribute(adjoint_kernel<IO, NL, V>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(adjoint_kernel<IO, NL, V, AHEAD>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)m1);
       if (e != cudaSuccess) return e;
-      adjoint_kernel<IO, NL, V>
-          <<<(unsigned)units, 32, smem, st>>>(in, gy, l.parts, buf, out, err);
+      adjoint_kernel<IO, NL, V, AHEAD>
+          <<<(unsigned)units, 32, m1, st>>>(in, gy, l.parts, buf, out, err);
       return cudaGetLastError();
     };
     cudaError_t e = vectored(a, io) ? run(std::integral_constant<int, 4>{})
