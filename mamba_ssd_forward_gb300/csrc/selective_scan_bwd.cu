@@ -437,17 +437,17 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   for (int64_t seg = last - 1; seg >= un.part * parts.per; --seg) {
     const int64_t t0 = seg * Ge::SEG;
     const int n = tokens(seg);
+    const pair *from = reinterpret_cast<const pair *>(buf.ends) +
+                       (un.tile_id * parts.segments + seg) * 256 + lane;
+    pair h[4][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i / 2][i % 2] = from[i * 32];
     if (AHEAD) copies_landed<0>();
     __syncwarp();
     if (n > 0) {
       fill<IO, NL, V, AHEAD>(in, gy, raw, sm.st, un.b, un.g, c0, live, t0, n, lane, err);
       __syncwarp();
       ahead(seg - 1);
-      pair h[4][2];
-      const pair *from = reinterpret_cast<const pair *>(buf.ends) +
-                         (un.tile_id * parts.segments + seg) * 256 + lane;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i / 2][i % 2] = from[i * 32];
       // the states in front of every fourth token
 #pragma unroll 1
       for (int sub = 1; sub < SUB; ++sub) {
@@ -560,35 +560,45 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     }
     if (n == 0) ahead(seg - 1);
     // what remains is per token and channel; su now holds the sums of G B
+    constexpr int BATCH = TURNS < 4 ? TURNS : 4;  // turns whose loads go out together
 #pragma unroll
-    for (int i = 0; i < TURNS; ++i) {
-      const int idx = lane + i * 32, r = idx / PR, c = idx % PR * V;
-      const int64_t t = t0 + r;
-      if (t >= in.L || c >= live || !SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79)) continue;
-      const bool ok = r < n;
-      float u[V], dt[V], z[V], gyv[V], du[V], ddt[V], dz[V];
-      load_if<V>(ok, in.u, un.b, t, c0 + c, u);
-      load_if<V>(ok, in.dt, un.b, t, c0 + c, dt);
-      load_if<V>(ok && in.z.p, in.z, un.b, t, c0 + c, z);
-      load_if<V>(ok && in.z.p, gy, un.b, t, c0 + c, gyv);
+    for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
+      float u[BATCH][V], dt[BATCH][V], z[BATCH][V], gyv[BATCH][V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        du[e] = ddt[e] = dz[e] = 0.f;
-        if (!ok) continue;
-        const float skip = in.Dskip ? in.Dskip[c0 + c + e] : 0.f;
-        const float gB = sm.st.su[r][c + e], o = sm.st.o[r][c + e];
-        du[e] = fmaf(sm.st.s[r][c + e], gB, skip * o);
-        ddt[e] = fmaf(u[e], gB, sm.gah[r][c + e] * kLn2);
-        if (in.softplus)
-          ddt[e] *= sigmoid(dt[e] + (in.dt_bias ? in.dt_bias[c0 + c + e] : 0.f));
-        if (in.z.p) dz[e] = gyv[e] * fmaf(skip, u[e], sm.y[r][c + e]) * dsilu(z[e]);
-        const int col = PR >= 32 ? i % (PR >= 32 ? PR / 32 : 1) * V + e : e;
-        dD[col] = fmaf(o, u[e], dD[col]);
-        dbias[col] += ddt[e];
+      for (int j = 0; j < BATCH; ++j) {
+        const int idx = lane + (i0 + j) * 32, r = idx / PR, c = idx % PR * V;
+        const bool ok = r < n && c < live && SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79);
+        load_if<V>(ok, in.u, un.b, t0 + r, c0 + c, u[j]);
+        load_if<V>(ok, in.dt, un.b, t0 + r, c0 + c, dt[j]);
+        load_if<V>(ok && in.z.p, in.z, un.b, t0 + r, c0 + c, z[j]);
+        load_if<V>(ok && in.z.p, gy, un.b, t0 + r, c0 + c, gyv[j]);
       }
-      store_vec<V>(out.du.at(un.b, t) + c0 + c, du);
-      store_vec<V>(out.ddt.at(un.b, t) + c0 + c, ddt);
-      if (out.dz.p) store_vec<V>(out.dz.at(un.b, t) + c0 + c, dz);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int idx = lane + (i0 + j) * 32, r = idx / PR, c = idx % PR * V;
+        const int64_t t = t0 + r;
+        if (t >= in.L || c >= live || !SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79)) continue;
+        const bool ok = r < n;
+        float du[V], ddt[V], dz[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          du[e] = ddt[e] = dz[e] = 0.f;
+          if (!ok) continue;
+          const float skip = in.Dskip ? in.Dskip[c0 + c + e] : 0.f;
+          const float gB = sm.st.su[r][c + e], o = sm.st.o[r][c + e];
+          du[e] = fmaf(sm.st.s[r][c + e], gB, skip * o);
+          ddt[e] = fmaf(u[j][e], gB, sm.gah[r][c + e] * kLn2);
+          if (in.softplus)
+            ddt[e] *= sigmoid(dt[j][e] + (in.dt_bias ? in.dt_bias[c0 + c + e] : 0.f));
+          if (in.z.p) dz[e] = gyv[j][e] * fmaf(skip, u[j][e], sm.y[r][c + e]) * dsilu(z[j][e]);
+          const int col = PR >= 32 ? (i0 + j) % (PR >= 32 ? PR / 32 : 1) * V + e : e;
+          dD[col] = fmaf(o, u[j][e], dD[col]);
+          dbias[col] += ddt[e];
+        }
+        store_vec<V>(out.du.at(un.b, t) + c0 + c, du);
+        store_vec<V>(out.ddt.at(un.b, t) + c0 + c, ddt);
+        if (out.dz.p) store_vec<V>(out.dz.at(un.b, t) + c0 + c, dz);
+      }
     }
   }
   const int64_t row = un.b * parts.parts + un.part;
@@ -619,23 +629,33 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   }
 }
 
-// dB and dC: the tiles' parts in order; zero past a sequence's end.
-template <typename IO>
+// dB and dC: the tiles' parts in order; zero past a sequence's end.  V states
+// of a token to a thread.
+template <typename IO, int V>
 __global__ void __launch_bounds__(128)
 sum_tiles_kernel(const float *__restrict__ partB, const float *__restrict__ partC, int tiles,
                  SeqView<IO> dB, SeqView<IO> dC, const int32_t *__restrict__ lengths, int64_t nb,
                  int64_t L, int64_t GN, int *err) {
-  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, n = nb * L * GN;
+  const int64_t i = ((int64_t)blockIdx.x * 128 + threadIdx.x) * V, n = nb * L * GN;
   if (i >= n) return;
   const int64_t c = i % GN, t = i / GN % L, b = i / GN / L;
-  if (!SSD_IN_BOUNDS(b < nb && t < L, err, 73)) return;
-  float v = 0.f;
-  const float *part = blockIdx.y ? partC : partB;
+  if (!SSD_IN_BOUNDS(b < nb && t < L && c + V <= GN, err, 73)) return;
+  float s[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) s[e] = 0.f;
+  const float *part = (blockIdx.y ? partC : partB) + i;
   if (t < tokens_of(lengths, b, L)) {
 #pragma unroll 8
-    for (int k = 0; k < tiles; ++k) v += part[k * n + i];
+    for (int k = 0; k < tiles; ++k) {
+      float v[V];
+      load_vec<V>(part + k * n, v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] += v[e];
+    }
   }
-  st_io((blockIdx.y ? dC : dB).at(b, t) + c, v);
+  IO *o = (blockIdx.y ? dC : dB).at(b, t) + c;
+#pragma unroll
+  for (int e = 0; e < V; ++e) st_io(o + e, s[e]);
 }
 
 // Segments to a part: enough parts for about two rounds of resident warps, at
@@ -750,9 +770,16 @@ cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void
                                     : run(std::integral_constant<int, 1>{});
     if (e != cudaSuccess) return e;
     const int64_t n = a.b * a.L * a.G * a.N;
-    sum_tiles_kernel<IO><<<dim3((unsigned)((n + 127) / 128), 2), 128, 0, st>>>(
-        buf.partB, buf.partC, l.parts.tiles, view_of<IO>(&a.out->dB), view_of<IO>(&a.out->dC),
-        a.lengths, a.b, a.L, a.G * a.N, err);
+    auto tiles = [&](auto v_c) {
+      constexpr int V = decltype(v_c)::value;
+      sum_tiles_kernel<IO, V><<<dim3((unsigned)((n / V + 127) / 128), 2), 128, 0, st>>>(
+          buf.partB, buf.partC, l.parts.tiles, view_of<IO>(&a.out->dB), view_of<IO>(&a.out->dC),
+          a.lengths, a.b, a.L, a.G * a.N, err);
+    };
+    if (a.G * a.N % 4 == 0)
+      tiles(std::integral_constant<int, 4>{});
+    else
+      tiles(std::integral_constant<int, 1>{});
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ColSum s{};
