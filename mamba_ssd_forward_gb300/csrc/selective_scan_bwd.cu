@@ -387,7 +387,7 @@ struct AdjointSmem {
   using Ge = Geo<NL>;
   static constexpr int SUB = Ge::SEG / 4;
   Stage<NL> st;
-  float gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
+  float gB[Ge::SEG][Ge::CW], gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
   pair start[SUB > 1 ? SUB - 1 : 1][8][32];  // states in front of tokens 4, 8, ..
   unsigned char raw[AHEAD ? sizeof(Raw<IO, NL>) : 16];
 };
@@ -417,6 +417,24 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
       q[i][p] = reinterpret_cast<const pair *>(buf.adj)[(mine * 8 + i * 2 + p) * 32 + lane];
       dA[i][p] = 0;
     }
+  // which sums this lane is left with, and where they go: dB and dC of states
+  // (KC of the eight over the channels), the sums of G B and A q h of channels
+  // (KN of the eight over the states)
+  constexpr int KC = Ge::CG < 8 ? 8 / Ge::CG : 1, DC = Ge::CG > 8 ? Ge::CG / 8 : 1;
+  constexpr int KN = NL < 8 ? 8 / NL : 1, DN = NL > 8 ? NL / 8 : 1;
+  constexpr int kRow = Ge::SEG * Ge::CW;  // from gB to gah
+  const bool keeps_c = cg % DC == 0, keeps_n = nl % DN == 0;
+  const int64_t per_token = G * N;
+  float *to_part[KC];
+#pragma unroll
+  for (int j = 0; j < KC; ++j) {
+    const int v = cg / DC * KC + j, st = nl * 4 + v % 4;
+    to_part[j] = st >= N ? nullptr
+                         : (v < 4 ? buf.partB : buf.partC) +
+                               ((un.tile * in.nb + un.b) * in.L * G + un.g) * N + st;
+  }
+  const int vn = nl / DN * KN;
+  float *to_sums = &sm.gB[0][0] + vn / 4 * kRow + cg * 4 + vn % 4;
   constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
   constexpr int VD = PR >= 32 ? V * (PR / 32) : V;  // this lane's columns
   float dD[VD], dbias[VD];
@@ -493,13 +511,11 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
             }
             unpack(acc, y[2 * p], y[2 * p + 1]);
           }
-          if (in.z.p) {
-            spread<1, NL, 4>(y, lane);
-            constexpr int KEEP = NL < 4 ? 4 / NL : 1, DUP = NL > 4 ? NL / 4 : 1;
-            if (nl % DUP == 0)
+          spread<1, NL, 4>(y, lane);
+          constexpr int KEEP = NL < 4 ? 4 / NL : 1, DUP = NL > 4 ? NL / 4 : 1;
+          if (nl % DUP == 0)
 #pragma unroll
-              for (int j = 0; j < KEEP; ++j) sm.y[t][cg * 4 + nl / DUP * KEEP + j] = y[j];
-          }
+            for (int j = 0; j < KEEP; ++j) sm.y[t][cg * 4 + nl / DUP * KEEP + j] = y[j];
         }
 #pragma unroll
         for (int k = 3; k >= 0; --k) {
@@ -533,33 +549,19 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
           for (int i = 0; i < 4; ++i) over_c[i] = sum2(dB[i]), over_c[4 + i] = sum2(dC[i]);
           spread<NL, Ge::CG, 8>(over_c, lane);
           spread<1, NL, 8>(over_n, lane);
-          {
-            constexpr int KEEP = Ge::CG < 8 ? 8 / Ge::CG : 1, DUP = Ge::CG > 8 ? Ge::CG / 8 : 1;
-            if (cg % DUP == 0 && t < n)
+          if (keeps_c && t < n)
 #pragma unroll
-              for (int j = 0; j < KEEP; ++j) {
-                const int v = cg / DUP * KEEP + j, st = nl * 4 + v % 4;
-                if (st < N)
-                  (v < 4 ? buf.partB : buf.partC)[(((un.tile * in.nb + un.b) * in.L + t0 + t) * G +
-                                                   un.g) * N + st] = over_c[j];
-              }
-          }
-          __syncwarp();  // every lane has read s u of this token
-          {
-            constexpr int KEEP = NL < 8 ? 8 / NL : 1, DUP = NL > 8 ? NL / 8 : 1;
-            if (nl % DUP == 0)
+            for (int j = 0; j < KC; ++j)
+              if (to_part[j]) to_part[j][(t0 + t) * per_token] = over_c[j];
+          if (keeps_n)
 #pragma unroll
-              for (int j = 0; j < KEEP; ++j) {
-                const int v = nl / DUP * KEEP + j;
-                (v < 4 ? sm.st.su : sm.gah)[t][cg * 4 + v % 4] = over_n[j];
-              }
-          }
+            for (int j = 0; j < KN; ++j) to_sums[t * Ge::CW + j % 4 + j / 4 * kRow] = over_n[j];
         }
       }
       __syncwarp();
     }
     if (n == 0) ahead(seg - 1);
-    // what remains is per token and channel; su now holds the sums of G B
+    // what remains is per token and channel
     constexpr int BATCH = TURNS < 4 ? TURNS : 4;  // turns whose loads go out together
 #pragma unroll
     for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
@@ -585,7 +587,7 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
           du[e] = ddt[e] = dz[e] = 0.f;
           if (!ok) continue;
           const float skip = in.Dskip ? in.Dskip[c0 + c + e] : 0.f;
-          const float gB = sm.st.su[r][c + e], o = sm.st.o[r][c + e];
+          const float gB = sm.gB[r][c + e], o = sm.st.o[r][c + e];
           du[e] = fmaf(sm.st.s[r][c + e], gB, skip * o);
           ddt[e] = fmaf(u[j][e], gB, sm.gah[r][c + e] * kLn2);
           if (in.softplus)
