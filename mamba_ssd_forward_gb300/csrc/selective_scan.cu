@@ -10,13 +10,13 @@
 // A lane holds a channel and up to 16 of its states as fp32 pairs, so the sum
 // over the states stays in the lane, each u, dt and z is read by one lane, and
 // B and C, equal for the warp's 32 channels, are broadcast from shared memory.
-// A warp runs alone, kTile tokens at a time: it stages their B and C and what
-// each channel needs of them (s, s u, D u, silu(z)), then runs the states;
-// it needs no barrier but its own.
+// A warp runs alone, kTile tokens at a time: it stages their B and C and
+// prepares what each channel needs of them (s, s u, D u, silu(z)), then runs
+// the states; it needs no barrier but its own.
 //
 // Measured (bf16, 16 states, GB300): 16 sequences of 512 tokens and 5120
 // channels, uncut: 247 us, 2.7e12 (token, channel, state) a second; two of
-// 2048 tokens, in five segments: 202 us; 16384 tokens of 1536 channels: 216 us.
+// 2048 tokens, in five segments: 194 us; 16384 tokens of 1536 channels: 208 us.
 // A pair multiply-add with three register operands takes three cycles of a
 // scheduler, so the body is 107 cycles a token and warp where nothing stalls.
 //
@@ -33,9 +33,8 @@ namespace {
 using namespace scan;
 
 constexpr int kWarps = 4;  // independent warps per block
-constexpr int kBlocks = 3;  // per SM; four blocks of 128 registers ran slower (292 us against 255)
+constexpr int kBlocks = 3;  // per SM; four blocks of 128 registers ran slower (218 us against 194)
 constexpr int kTile = 8;    // tokens staged at a time
-constexpr int kUnroll = 8;
 
 // A warp's part of the work: sequence, group, channel tile, segment.
 struct Cut {
@@ -86,7 +85,7 @@ struct __align__(16) Warp {
   struct __align__(16) {  // a tile as it is in memory, and the next one
     IO u[T][CW], dt[T][CW], z[TO][CW], B[T][NP], C[TO][NP];
   } raw[2];
-  Step step[T][CW];  // s, s u and, for the outputs, D u and silu(z)
+  Step step[NL > 1 ? T : 1][CW];  // s, s u and, for the outputs, D u and silu(z)
   float B[T][NP], C[TO][NP];
 };
 
@@ -186,33 +185,45 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
     constexpr int EV = EB % 4 == 0 ? 4 : 1;
 #pragma unroll
     for (int i = 0; i < EB; i += EV) {
-      float v[EV];
-      load_vec<EV>(&raw.B[0][0] + lane * EB + i, v);
-      store_vec<EV>(&sm.B[0][0] + lane * EB + i, v);
-      if (OUT) {
-        load_vec<EV>(&raw.C[0][0] + lane * EB + i, v);
-        store_vec<EV>(&sm.C[0][0] + lane * EB + i, v);
-      }
+      const bool here = (lane * EB + i) / NP < n;  // nothing was copied for the tokens after
+      auto stage = [&](const IO *from, float *to) {
+        float v[EV];
+        load_vec<EV>(from + lane * EB + i, v);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) v[e] = here ? v[e] : 0.f;
+        store_vec<EV>(to + lane * EB + i, v);
+      };
+      stage(&raw.B[0][0], &sm.B[0][0]);
+      if (OUT) stage(&raw.C[0][0], &sm.C[0][0]);
     }
     constexpr int EACH = TT * CW / 32;  // tokens of its channel that a lane prepares
+    Step own[NL > 1 ? 1 : TT];
 #pragma unroll
     for (int i = 0; i < (EACH > 0 ? EACH : 1); ++i) {
       const int k = lane / CW + i * (32 / CW);
       if (EACH == 0 && k >= TT) break;
       const float uk = ld_io(&raw.u[k][mine]);
       const float s = step_of(ld_io(&raw.dt[k][mine]) + bias, in.softplus);
-      if constexpr (OUT) {
-        sm.step[k][mine] =
-            make_float4(s, s * uk, skip * uk, gated ? silu(ld_io(&raw.z[k][mine])) : 1.f);
-      } else {
-        sm.step[k][mine] = make_float2(s, s * uk);
-        if (k < n) total += s;
-      }
+      Step st;
+      if constexpr (OUT)
+        st = make_float4(s, s * uk, skip * uk, gated ? silu(ld_io(&raw.z[k][mine])) : 1.f);
+      else
+        st = make_float2(s, s * uk);
+      if (k >= n) st.x = st.y = 0.f;  // leaves the state as it is
+      if (!OUT) total += st.x;
+      if constexpr (NL > 1)
+        sm.step[k][mine] = st;
+      else
+        own[i] = st;  // the lane's own channel: it stays in registers
     }
     __syncwarp();
-#pragma unroll kUnroll
-    for (int k = 0; k < n; ++k) {
-      const Step st = sm.step[k][lane / NL];
+#pragma unroll
+    for (int k = 0; k < TT; ++k) {
+      Step st;
+      if constexpr (NL > 1)
+        st = sm.step[k][lane / NL];
+      else
+        st = own[k];
       const pair ss = both(st.x), su = both(st.y);
       pair acc = 0;
       const ulonglong2 *pB = reinterpret_cast<const ulonglong2 *>(&sm.B[k][n0]);
@@ -230,7 +241,7 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
       }
       if constexpr (OUT) {
         const float o = (sum_lanes<NL>(sum2(acc)) + st.z) * st.w;
-        if (stores) st_io(py, o);
+        if (k < n && stores) st_io(py, o);
         py += y.ts;
       }
     }
@@ -274,7 +285,7 @@ bool vectored(const ScanArgs &a, ssd_dtype io) {
 
 // States per lane and lanes per channel.  (Four or eight states to a lane give
 // more warps, which would not have to be cut: 16 states on four lanes took 312
-// us where five segments take 202.)
+// us where five segments take 194.)
 struct Split {
   int npt, nl;
 };
@@ -283,10 +294,9 @@ Split split_of(const ScanArgs &a) {
   return {16, a.N <= 32 ? 2 : 4};
 }
 
-// Segments: as many as the warps resident at once (three blocks to an SM; at
-// 24 warps to an SM in all 16384 tokens of 1536 channels took 247 us, at 12
-// 222 us), of 32 tokens at least (512 tokens of 1536 channels: 28 us, at 64
-// tokens 34 us).  Fewer than three are not worth the first launch: 1280 warps
+// Segments: as many as the warps resident at once (three blocks to an SM;
+// twice as many took a tenth longer on 16384 tokens of 1536 channels), of 32
+// tokens at least (512 tokens of 1536 channels: 28 us, at 64 tokens 34 us).  Fewer than three are not worth the first launch: 1280 warps
 // of their own run uncut.
 constexpr int kPerSm = 12;
 Cut cut_of(const ScanArgs &a) {
