@@ -13,7 +13,7 @@ device, or None) gives the real tokens of each padded sequence.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
@@ -35,7 +35,7 @@ def _io(t, name):
 
 def _stream(like):
     """The current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(like.device.index)
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
 
 
 def _refuse(t, name, shape, dtype, like):
@@ -54,8 +54,8 @@ def _dense(t, name, shape, dtype, like):
     """Address of a dense tensor (None stays None)."""
     if t is None:
         return None
-    if (t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda
-            or not t.is_contiguous()):
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or (dev := t.get_device()) < 0 or dev != like.get_device()):
         _refuse(t, name, shape, dtype, like)
     return t.data_ptr()
 
@@ -64,7 +64,8 @@ def _seq(t, name, shape, dtype, like):
     """View of an activation [b, L, D]; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+    if (t.dtype is not dtype or t.shape != shape or (dev := t.get_device()) < 0
+            or dev != like.get_device()):
         _refuse(t, name, shape, dtype, like)
     sb, st, sc = t.stride()
     if sc != 1 and shape[2] != 1:
@@ -76,7 +77,8 @@ def _token(t, name, shape, dtype, like):
     """The same of one token each, [b, D]."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+    if (t.dtype is not dtype or t.shape != shape or (dev := t.get_device()) < 0
+            or dev != like.get_device()):
         _refuse(t, name, shape, dtype, like)
     sb, sc = t.stride()
     if sc != 1 and shape[1] != 1:
@@ -86,7 +88,8 @@ def _token(t, name, shape, dtype, like):
 
 def _grouped(t, name, shape, dtype, like):
     """A view [b, L, G, N] or [b, G, N] whose last two axes are dense together."""
-    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_cuda:
+    if (t.dtype is not dtype or t.shape != shape or (dev := t.get_device()) < 0
+            or dev != like.get_device()):
         _refuse(t, name, shape, dtype, like)
     *lead, sg, sn = t.stride()
     if (sn != 1 and shape[-1] != 1) or (sg != shape[-1] and shape[-2] != 1):
@@ -470,20 +473,27 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspac
     if not grads:
         raise ValueError("no gradients given")
     like = grads[0]
-    dev, rows = like.device, []
+    dev, flat = like.get_device(), []
     for i, (g, o) in enumerate(zip(grads, out)):
         io = _IO.get(g.dtype)
-        if io is None or g.device != dev or not g.is_cuda or not g.is_contiguous():
+        if io is None or dev < 0 or g.get_device() != dev or not g.is_contiguous():
             _io(g, f"grads[{i}]")
             _refuse(g, f"grads[{i}]", g.shape, g.dtype, like)
         src = g.data_ptr()
-        dst = src if o is g else _dense(o, f"out[{i}]", g.shape, g.dtype, like)
-        rows.append((src, dst, g.numel(), io))
-    table = (_abi.SsdGrad * len(rows))(*rows)
+        if o is g:
+            dst = src
+        else:
+            if (o.dtype is not g.dtype or o.get_device() != dev or not o.is_contiguous()
+                    or o.shape != g.shape):
+                _refuse(o, f"out[{i}]", g.shape, g.dtype, like)
+            dst = o.data_ptr()
+        flat += (src, dst, g.numel(), io)
+    n = len(grads)
+    table = (_abi.SsdGrad * n).from_buffer_copy(struct.pack("@" + "PPqi4x" * n, *flat))
     lib = _abi.load()
     norm = torch.empty((), dtype=torch.float32, device=like.device)
-    ws, wp, wn = _workspace(lib.ssd_clip_grad_norm_workspace_size(table, len(grads)), workspace,
+    ws, wp, wn = _workspace(lib.ssd_clip_grad_norm_workspace_size(table, n), workspace,
                             like, "clip_grad_norm")
     _abi.check("ssd_clip_grad_norm", lib.ssd_clip_grad_norm(
-        table, len(grads), max_norm, eps, norm.data_ptr(), wp, wn, _stream(like)))
+        table, n, max_norm, eps, norm.data_ptr(), wp, wn, _stream(like)))
     return norm
