@@ -22,6 +22,10 @@
 // inside the lane, 7 and 6 exchanges a token for 16 states.  Bound by the
 // arithmetic: 3.75 exponentials and some 25 multiply-adds per (token, channel,
 // state) against 46 bytes per (token, channel).
+//
+// Measured, bf16, 4 sequences of 1024 tokens, 2048 channels of 16 states: 304
+// us in all; ends 59, chain 15, adjoint 214, the sums 21.  A segment's inputs
+// are copied to shared memory while the one before is worked on (405 -> 366).
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -29,11 +33,10 @@ namespace {
 
 using namespace scan;
 
-// Warps of the adjoint to an SM: at 8 a lane has 242 registers and spills
-// nothing (4 sequences of 1024 tokens and 2048 channels: 405 us in all; at 10,
-// 168 registers with spills, some 50 us more).
+// Warps of the adjoint to an SM: at 8 a lane has some 240 registers and spills
+// nothing; at 10, 168 registers with spills, a tenth more time.
 constexpr int kMin = 8;
-constexpr int kMinEnds = 16;  // 128 registers: 405 us, at 12 warps (162) 429, at 20 (96) 446
+constexpr int kMinEnds = 16;  // 128 registers; 12 warps (162) and 20 (96) were slower
 
 // How a warp lies over channels and states.
 template <int NL>
@@ -150,15 +153,38 @@ __device__ __forceinline__ void load_if(bool ok, const SeqView<const IO> &m, int
   if (ok) load_vec<V>(m.at(b, t) + c, v);
 }
 
+// The columns of a segment that a lane prepares and finishes, V at a time:
+// `kCols` of them, turn i's being kCols' (i mod kCols / V)-th vector.
+template <int NL, int V>
+struct Lanes {
+  using Ge = Geo<NL>;
+  static constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
+  static constexpr int kCols = PR >= 32 ? V * (PR / 32) : V;
+  __device__ static __forceinline__ constexpr int at(int turn, int e) {
+    return turn * V % kCols + e;
+  }
+  // a parameter of those columns
+  __device__ static __forceinline__ void load(const float *p, int64_t c0, int live, int lane,
+                                              float (&v)[kCols]) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int c = (lane + j / V * 32) % PR * V + j % V;
+      v[j] = p && c < live ? p[c0 + c] : 0.f;
+    }
+  }
+};
+
 // Fills a Stage from tokens t0 .. t0 + n of the tile, out of `raw` where they
 // were copied (AHEAD); zero beyond them and beyond the tile's `live` channels,
 // which leaves states and adjoints alone.
 template <typename IO, int NL, int V, bool AHEAD>
 __device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &gy,
                                      const Raw<IO, NL> &raw, Stage<NL> &sm, int64_t b, int64_t g,
-                                     int64_t c0, int live, int64_t t0, int n, int lane, int *err) {
+                                     int64_t c0, int live, int64_t t0, int n, int lane,
+                                     const float (&bias)[Lanes<NL, V>::kCols], int *err) {
   using Ge = Geo<NL>;
-  constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
+  using La = Lanes<NL, V>;
+  constexpr int PR = La::PR, TURNS = La::TURNS;
 #pragma unroll
   for (int i = 0; i < TURNS; ++i) {
     const int q = lane + i * 32, r = q / PR, c = q % PR * V;
@@ -177,8 +203,7 @@ __device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float bias = in.dt_bias && ok ? in.dt_bias[c0 + c + e] : 0.f;
-      s[e] = ok ? step_of(dt[e] + bias, in.softplus) : 0.f;
+      s[e] = ok ? step_of(dt[e] + bias[La::at(i, e)], in.softplus) : 0.f;
       su[e] = ok ? s[e] * u[e] : 0.f;
       go[e] = !ok ? 0.f : in.z.p ? go[e] * silu(z[e]) : go[e];
     }
@@ -233,6 +258,8 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err)
   const int live = min(Ge::CW, in.per_group - un.tile * Ge::CW);
   if (!SSD_IN_BOUNDS(un.b < in.nb && c0 + live <= in.D, err, 71)) return;
   const int64_t len = tokens_of(in.lengths, un.b, in.L);
+  float bias[Lanes<NL, V>::kCols];
+  Lanes<NL, V>::load(in.dt_bias, c0, live, lane, bias);
   pair A[4][2], P[4][2], R[4][2], all[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -262,7 +289,7 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err)
     if (n > 0) {
       if (AHEAD) copies_landed<0>();
       __syncwarp();
-      fill<IO, NL, V, AHEAD>(in, gy, raw, sm, un.b, un.g, c0, live, t0, n, lane, err);
+      fill<IO, NL, V, AHEAD>(in, gy, raw, sm, un.b, un.g, c0, live, t0, n, lane, bias, err);
       __syncwarp();
       ahead(seg + 1);
 #pragma unroll 4
@@ -435,8 +462,11 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   }
   const int vn = nl / DN * KN;
   float *to_sums = &sm.gB[0][0] + vn / 4 * kRow + cg * 4 + vn % 4;
-  constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
-  constexpr int VD = PR >= 32 ? V * (PR / 32) : V;  // this lane's columns
+  using La = Lanes<NL, V>;
+  constexpr int PR = La::PR, TURNS = La::TURNS, VD = La::kCols;
+  float bias[VD], skip[VD];
+  La::load(in.dt_bias, c0, live, lane, bias);
+  La::load(in.Dskip, c0, live, lane, skip);
   float dD[VD], dbias[VD];
 #pragma unroll
   for (int e = 0; e < VD; ++e) dD[e] = dbias[e] = 0.f;
@@ -463,7 +493,7 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     if (AHEAD) copies_landed<0>();
     __syncwarp();
     if (n > 0) {
-      fill<IO, NL, V, AHEAD>(in, gy, raw, sm.st, un.b, un.g, c0, live, t0, n, lane, err);
+      fill<IO, NL, V, AHEAD>(in, gy, raw, sm.st, un.b, un.g, c0, live, t0, n, lane, bias, err);
       __syncwarp();
       ahead(seg - 1);
       // the states in front of every fourth token
@@ -586,14 +616,13 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
         for (int e = 0; e < V; ++e) {
           du[e] = ddt[e] = dz[e] = 0.f;
           if (!ok) continue;
-          const float skip = in.Dskip ? in.Dskip[c0 + c + e] : 0.f;
+          const int col = La::at(i0 + j, e);
           const float gB = sm.gB[r][c + e], o = sm.st.o[r][c + e];
-          du[e] = fmaf(sm.st.s[r][c + e], gB, skip * o);
+          du[e] = fmaf(sm.st.s[r][c + e], gB, skip[col] * o);
           ddt[e] = fmaf(u[j][e], gB, sm.gah[r][c + e] * kLn2);
-          if (in.softplus)
-            ddt[e] *= sigmoid(dt[j][e] + (in.dt_bias ? in.dt_bias[c0 + c + e] : 0.f));
-          if (in.z.p) dz[e] = gyv[j][e] * fmaf(skip, u[j][e], sm.y[r][c + e]) * dsilu(z[j][e]);
-          const int col = PR >= 32 ? (i0 + j) % (PR >= 32 ? PR / 32 : 1) * V + e : e;
+          if (in.softplus) ddt[e] *= sigmoid(dt[j][e] + bias[col]);
+          if (in.z.p)
+            dz[e] = gyv[j][e] * fmaf(skip[col], u[j][e], sm.y[r][c + e]) * dsilu(z[j][e]);
           dD[col] = fmaf(o, u[j][e], dD[col]);
           dbias[col] += ddt[e];
         }
