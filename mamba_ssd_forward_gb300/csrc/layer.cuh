@@ -91,7 +91,13 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[V]) {
   }
 }
 
-// Asynchronous copies of 16 or 8 bytes to shared memory.
+// Asynchronous copies of 16, 8 or 4 bytes to shared memory.
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void copy8(void *dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
                    (uint32_t)__cvta_generic_to_shared(dst)),

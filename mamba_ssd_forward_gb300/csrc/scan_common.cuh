@@ -133,6 +133,57 @@ cudaError_t dispatch(ssd_dtype io, int64_t N, F f) {
   return io == SSD_BF16 ? by_lanes(tag<__nv_bfloat16>{}) : by_lanes(tag<float>{});
 }
 
+// Bytes of the pieces in which rows of the inputs can be copied: 16 where
+// every row is whole such pieces, else 4 (always for fp32), else single
+// elements of 2.
+inline int piece_of(const ScanArgs &a, ssd_dtype io) {
+  const size_t e = io == SSD_BF16 ? 2 : 4;
+  auto fits = [&](size_t n) {
+    return a.N * e % n == 0 && (a.D / a.G) * e % n == 0 && view_aligned(a.u, e, n) &&
+           view_aligned(a.dt, e, n) && view_aligned(a.z, e, n) && view_aligned(a.gy, e, n) &&
+           view_aligned(a.B, e, n) && view_aligned(a.C, e, n);
+  };
+  return fits(16) ? 16 : fits(4) ? 4 : 2;
+}
+
+// The first n of ROWS rows from p on, `cols` of COLS columns, to shared memory
+// in pieces of E elements: 4 bytes asynchronously, or single elements at once,
+// which leaves zeros elsewhere.  A lane keeps its column.
+template <int COLS, int ROWS, int E, typename IO>
+__device__ __forceinline__ void copy_pieces(IO *dst, const IO *p, int64_t ts, int n, int cols,
+                                            int lane) {
+  constexpr bool WORDS = E * sizeof(IO) == 4;
+  constexpr int W = COLS / E, LANES = W < 32 ? W : 32, STEP = 32 / LANES;
+  constexpr int TURNS = ROWS / STEP > 1 ? ROWS / STEP : 1;
+  const int r = lane / LANES;
+#pragma unroll
+  for (int c = lane % LANES * E; c < COLS; c += 32 * E) {
+    const IO *q = p + r * ts + c;
+    IO v[TURNS];
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) {
+      const bool ok = c < cols && r + k * STEP < n;
+      if (WORDS) {
+        if (ok) copy4(dst + (r + k * STEP) * COLS + c, q + k * STEP * ts);
+      } else {
+        v[k] = ok ? q[k * STEP * ts] : IO(0.f);
+      }
+    }
+    if (!WORDS)
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k)
+        if (r + k * STEP < ROWS) dst[(r + k * STEP) * COLS + c] = v[k];
+  }
+}
+template <int COLS, int ROWS, typename IO>
+__device__ __forceinline__ void copy_small(IO *dst, const IO *p, int64_t ts, int n, int cols,
+                                           int lane, bool words) {
+  if (words || sizeof(IO) == 4)
+    copy_pieces<COLS, ROWS, 4 / (int)sizeof(IO)>(dst, p, ts, n, cols, lane);
+  else
+    copy_pieces<COLS, ROWS, 1>(dst, p, ts, n, cols, lane);
+}
+
 // The inputs of the forward recurrence, as the kernels take them.
 template <typename IO>
 struct In {

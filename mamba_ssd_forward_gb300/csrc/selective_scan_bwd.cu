@@ -128,12 +128,26 @@ __device__ __forceinline__ void copy_rows(IO *dst, const SeqView<const IO> &m, i
     if (col < cols && row + r < n && row + r < ROWS)
       copy16(dst + (row + r) * COLS + col, p + r * m.ts);
 }
-template <typename IO, int NL>
+template <bool VEC, typename IO, int NL>
 __device__ __forceinline__ void copy_segment(const In<IO> &in, const SeqView<const IO> &gy,
                                              Raw<IO, NL> &raw, int64_t b, int64_t g, int64_t c0,
-                                             int live, int64_t t0, int n, int lane, int *err) {
+                                             int live, int64_t t0, int n, int lane, bool words,
+                                             int *err) {
   using Ge = Geo<NL>;
-  if (n > 0 && SSD_IN_BOUNDS(t0 >= 0 && t0 + n <= in.L, err, 80)) {
+  if constexpr (!VEC) {
+    if (n > 0 && SSD_IN_BOUNDS(t0 >= 0 && t0 + n <= in.L, err, 80)) {
+      auto rows = [&](IO *dst, const SeqView<const IO> &m) {
+        copy_small<Ge::CW, Ge::SEG>(dst, m.at(b, t0) + c0, m.ts, n, live, lane, words);
+      };
+      rows(raw.u[0], in.u);
+      rows(raw.dt[0], in.dt);
+      rows(raw.gy[0], gy);
+      if (in.z.p) rows(raw.z[0], in.z);
+      const int64_t col = g * in.N;
+      copy_small<Ge::NP, Ge::SEG>(raw.B[0], in.B.at(b, t0) + col, in.B.ts, n, in.N, lane, words);
+      copy_small<Ge::NP, Ge::SEG>(raw.C[0], in.C.at(b, t0) + col, in.C.ts, n, in.N, lane, words);
+    }
+  } else if (n > 0 && SSD_IN_BOUNDS(t0 >= 0 && t0 + n <= in.L, err, 80)) {
     copy_rows<Ge::CW, Ge::SEG>(raw.u[0], in.u, b, t0, n, c0, live, lane);
     copy_rows<Ge::CW, Ge::SEG>(raw.dt[0], in.dt, b, t0, n, c0, live, lane);
     copy_rows<Ge::CW, Ge::SEG>(raw.gy[0], gy, b, t0, n, c0, live, lane);
@@ -144,82 +158,86 @@ __device__ __forceinline__ void copy_segment(const In<IO> &in, const SeqView<con
   copies_issued();
 }
 
-// V channels of one token of a view; zero where `ok` is false.
-template <int V, typename IO>
-__device__ __forceinline__ void load_if(bool ok, const SeqView<const IO> &m, int64_t b, int64_t t,
-                                        int64_t c, float (&v)[V]) {
+// Four channels of one token of a view, the first `count` of them (maybe none);
+// zero beyond.  VEC: all four or none, on their boundary.
+template <bool VEC, typename IO>
+__device__ __forceinline__ void load_four(const SeqView<const IO> &m, int64_t b, int64_t t,
+                                          int64_t c, int count, float (&v)[4]) {
+  v[0] = v[1] = v[2] = v[3] = 0.f;
+  if (count <= 0) return;
+  const IO *p = m.at(b, t) + c;
+  if constexpr (VEC) {
+    load_vec<4>(p, v);
+  } else {
 #pragma unroll
-  for (int e = 0; e < V; ++e) v[e] = 0.f;
-  if (ok) load_vec<V>(m.at(b, t) + c, v);
+    for (int e = 0; e < 4; ++e)
+      if (e < count) v[e] = ld_io(p + e);
+  }
+}
+template <bool VEC, typename IO>
+__device__ __forceinline__ void store_four(const SeqView<IO> &m, int64_t b, int64_t t, int64_t c,
+                                           int count, const float (&v)[4]) {
+  IO *p = m.at(b, t) + c;
+  if constexpr (VEC) {
+    store_vec<4>(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) st_io(p + e, v[e]);
+  }
 }
 
-// The columns of a segment that a lane prepares and finishes, V at a time:
-// `kCols` of them, turn i's being kCols' (i mod kCols / V)-th vector.
-template <int NL, int V>
+// The columns of a segment that a lane prepares and finishes, four at a time:
+// always the same four, over TURNS tokens.
+template <int NL>
 struct Lanes {
   using Ge = Geo<NL>;
-  static constexpr int PR = Ge::CW / V, TURNS = Ge::SEG * PR / 32;
-  static constexpr int kCols = PR >= 32 ? V * (PR / 32) : V;
-  __device__ static __forceinline__ constexpr int at(int turn, int e) {
-    return turn * V % kCols + e;
-  }
+  static constexpr int PR = Ge::CW / 4, TURNS = Ge::SEG * PR / 32;
+  static_assert(PR <= 32 && TURNS >= 1, "");
   // a parameter of those columns
   __device__ static __forceinline__ void load(const float *p, int64_t c0, int live, int lane,
-                                              float (&v)[kCols]) {
+                                              float (&v)[4]) {
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int c = (lane + j / V * 32) % PR * V + j % V;
-      v[j] = p && c < live ? p[c0 + c] : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const int c = lane % PR * 4 + e;
+      v[e] = p && c < live ? p[c0 + c] : 0.f;
     }
   }
 };
 
-// Fills a Stage from tokens t0 .. t0 + n of the tile, out of `raw` where they
-// were copied (AHEAD); zero beyond them and beyond the tile's `live` channels,
-// which leaves states and adjoints alone.
-template <typename IO, int NL, int V, bool AHEAD>
-__device__ __forceinline__ void fill(const In<IO> &in, const SeqView<const IO> &gy,
-                                     const Raw<IO, NL> &raw, Stage<NL> &sm, int64_t b, int64_t g,
-                                     int64_t c0, int live, int64_t t0, int n, int lane,
-                                     const float (&bias)[Lanes<NL, V>::kCols], int *err) {
+// Fills a Stage from `raw`, where n tokens of the segment were copied; zero
+// beyond them and beyond the tile's `live` channels, which leaves states and
+// adjoints alone.
+template <typename IO, int NL>
+__device__ __forceinline__ void fill(const In<IO> &in, const Raw<IO, NL> &raw, Stage<NL> &sm,
+                                     int live, int n, int lane, const float (&bias)[4]) {
   using Ge = Geo<NL>;
-  using La = Lanes<NL, V>;
-  constexpr int PR = La::PR, TURNS = La::TURNS;
+  using La = Lanes<NL>;
+  const int c = lane % La::PR * 4;
 #pragma unroll
-  for (int i = 0; i < TURNS; ++i) {
-    const int q = lane + i * 32, r = q / PR, c = q % PR * V;
-    const bool ok = r < n && c < live && SSD_IN_BOUNDS(t0 + r < in.L && c0 + c + V <= in.D, err, 77);
-    float u[V], dt[V], z[V], go[V], s[V], su[V];
-    if constexpr (AHEAD) {
-      load_vec<V>(&raw.u[r][c], u);
-      load_vec<V>(&raw.dt[r][c], dt);
-      load_vec<V>(&raw.gy[r][c], go);
-      load_vec<V>(&raw.z[r][c], z);
-    } else {
-      load_if<V>(ok, in.u, b, t0 + r, c0 + c, u);
-      load_if<V>(ok, in.dt, b, t0 + r, c0 + c, dt);
-      load_if<V>(ok, gy, b, t0 + r, c0 + c, go);
-      load_if<V>(ok && in.z.p, in.z, b, t0 + r, c0 + c, z);
-    }
+  for (int i = 0; i < La::TURNS; ++i) {
+    const int r = (lane + i * 32) / La::PR;
+    float u[4], dt[4], z[4], go[4], s[4], su[4];
+    load_vec<4>(&raw.u[r][c], u);
+    load_vec<4>(&raw.dt[r][c], dt);
+    load_vec<4>(&raw.gy[r][c], go);
+    load_vec<4>(&raw.z[r][c], z);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      s[e] = ok ? step_of(dt[e] + bias[La::at(i, e)], in.softplus) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const bool ok = r < n && c + e < live;
+      s[e] = ok ? step_of(dt[e] + bias[e], in.softplus) : 0.f;
       su[e] = ok ? s[e] * u[e] : 0.f;
       go[e] = !ok ? 0.f : in.z.p ? go[e] * silu(z[e]) : go[e];
     }
-    store_vec<V>(&sm.s[r][c], s);
-    store_vec<V>(&sm.su[r][c], su);
-    store_vec<V>(&sm.o[r][c], go);
+    store_vec<4>(&sm.s[r][c], s);
+    store_vec<4>(&sm.su[r][c], su);
+    store_vec<4>(&sm.o[r][c], go);
   }
 #pragma unroll
   for (int q = lane; q < Ge::SEG * Ge::NP; q += 32) {
     const int r = q / Ge::NP, k = q % Ge::NP;
     const bool ok = r < n && k < in.N;
-    float vB = 0.f, vC = 0.f;
-    if (ok) {
-      vB = AHEAD ? ld_io(&raw.B[r][k]) : ld_io(in.B.at(b, t0 + r) + g * in.N + k);
-      vC = AHEAD ? ld_io(&raw.C[r][k]) : ld_io(in.C.at(b, t0 + r) + g * in.N + k);
-    }
+    const float vB = ok ? ld_io(&raw.B[r][k]) : 0.f, vC = ok ? ld_io(&raw.C[r][k]) : 0.f;
     sm.B[r][k] = make_float2(vB, vB);
     sm.C[r][k] = make_float2(vC, vC);
   }
@@ -245,9 +263,9 @@ __device__ __forceinline__ void four_twice(const float2 *p, pair (&v)[4]) {
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
-template <typename IO, int NL, int V, bool AHEAD>
+template <typename IO, int NL, bool VEC>
 __global__ void __launch_bounds__(32, kMinEnds)
-ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err) {
+ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, bool words, int *err) {
   using Ge = Geo<NL>;
   extern __shared__ __align__(16) unsigned char raw_smem[];
   Stage<NL> &sm = *reinterpret_cast<Stage<NL> *>(raw_smem);
@@ -258,8 +276,8 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err)
   const int live = min(Ge::CW, in.per_group - un.tile * Ge::CW);
   if (!SSD_IN_BOUNDS(un.b < in.nb && c0 + live <= in.D, err, 71)) return;
   const int64_t len = tokens_of(in.lengths, un.b, in.L);
-  float bias[Lanes<NL, V>::kCols];
-  Lanes<NL, V>::load(in.dt_bias, c0, live, lane, bias);
+  float bias[4];
+  Lanes<NL>::load(in.dt_bias, c0, live, lane, bias);
   pair A[4][2], P[4][2], R[4][2], all[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -275,21 +293,19 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, int *err)
     return (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
   };
   auto ahead = [&](int64_t seg) {
-    if (AHEAD)
-      copy_segment<IO, NL>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
-                           seg < last ? tokens(seg) : 0, lane, err);
+    copy_segment<VEC>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
+                         seg < last ? tokens(seg) : 0, lane, words, err);
   };
   ahead(un.part * parts.per);
   for (int64_t seg = un.part * parts.per; seg < last; ++seg) {
-    const int64_t t0 = seg * Ge::SEG;
     const int n = tokens(seg);
     pair h[4][2], sum[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i][0] = h[i][1] = 0;
     if (n > 0) {
-      if (AHEAD) copies_landed<0>();
+      copies_landed<0>();
       __syncwarp();
-      fill<IO, NL, V, AHEAD>(in, gy, raw, sm, un.b, un.g, c0, live, t0, n, lane, bias, err);
+      fill<IO, NL>(in, raw, sm, live, n, lane, bias);
       __syncwarp();
       ahead(seg + 1);
 #pragma unroll 4
@@ -409,24 +425,25 @@ struct Out {
   SeqView<IO> du, ddt, dz;
 };
 
-template <typename IO, int NL, bool AHEAD>
+template <typename IO, int NL>
 struct AdjointSmem {
   using Ge = Geo<NL>;
   static constexpr int SUB = Ge::SEG / 4;
   Stage<NL> st;
   float gB[Ge::SEG][Ge::CW], gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
   pair start[SUB > 1 ? SUB - 1 : 1][8][32];  // states in front of tokens 4, 8, ..
-  unsigned char raw[AHEAD ? sizeof(Raw<IO, NL>) : 16];
+  Raw<IO, NL> raw;
 };
 
-template <typename IO, int NL, int V, bool AHEAD>
+template <typename IO, int NL, bool VEC>
 __global__ void __launch_bounds__(32, kMin)
-adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO> out, int *err) {
+adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO> out, bool words,
+               int *err) {
   using Ge = Geo<NL>;
   constexpr int SUB = Ge::SEG / 4;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  auto &sm = *reinterpret_cast<AdjointSmem<IO, NL, AHEAD> *>(raw_smem);
-  Raw<IO, NL> &raw = *reinterpret_cast<Raw<IO, NL> *>(sm.raw);
+  auto &sm = *reinterpret_cast<AdjointSmem<IO, NL> *>(raw_smem);
+  Raw<IO, NL> &raw = sm.raw;
   const int lane = threadIdx.x, nl = lane % NL, cg = lane / NL, N = in.N;
   const int64_t G = in.D / in.per_group;
   const Unit un = unit_of(blockIdx.x, parts, G);
@@ -462,14 +479,14 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   }
   const int vn = nl / DN * KN;
   float *to_sums = &sm.gB[0][0] + vn / 4 * kRow + cg * 4 + vn % 4;
-  using La = Lanes<NL, V>;
-  constexpr int PR = La::PR, TURNS = La::TURNS, VD = La::kCols;
-  float bias[VD], skip[VD];
+  using La = Lanes<NL>;
+  constexpr int PR = La::PR, TURNS = La::TURNS;
+  float bias[4], skip[4];
   La::load(in.dt_bias, c0, live, lane, bias);
   La::load(in.Dskip, c0, live, lane, skip);
-  float dD[VD], dbias[VD];
+  float dD[4], dbias[4];
 #pragma unroll
-  for (int e = 0; e < VD; ++e) dD[e] = dbias[e] = 0.f;
+  for (int e = 0; e < 4; ++e) dD[e] = dbias[e] = 0.f;
 
   const int64_t last = min((un.part + 1) * parts.per, parts.segments);
   auto tokens = [&](int64_t seg) {  // of a segment
@@ -477,9 +494,8 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     return (int)(len - t0 < 0 ? 0 : len - t0 < Ge::SEG ? len - t0 : Ge::SEG);
   };
   auto ahead = [&](int64_t seg) {
-    if (AHEAD)
-      copy_segment<IO, NL>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
-                           seg >= un.part * parts.per ? tokens(seg) : 0, lane, err);
+    copy_segment<VEC>(in, gy, raw, un.b, un.g, c0, live, seg * Ge::SEG,
+                         seg >= un.part * parts.per ? tokens(seg) : 0, lane, words, err);
   };
   ahead(last - 1);
   for (int64_t seg = last - 1; seg >= un.part * parts.per; --seg) {
@@ -490,10 +506,10 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     pair h[4][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i / 2][i % 2] = from[i * 32];
-    if (AHEAD) copies_landed<0>();
+    copies_landed<0>();
     __syncwarp();
     if (n > 0) {
-      fill<IO, NL, V, AHEAD>(in, gy, raw, sm.st, un.b, un.g, c0, live, t0, n, lane, bias, err);
+      fill<IO, NL>(in, raw, sm.st, live, n, lane, bias);
       __syncwarp();
       ahead(seg - 1);
       // the states in front of every fourth token
@@ -592,44 +608,39 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     }
     if (n == 0) ahead(seg - 1);
     // what remains is per token and channel
-    constexpr int BATCH = TURNS < 4 ? TURNS : 4;  // turns whose loads go out together
+    const int c = lane % PR * 4, cols = live - c;  // this lane's, if any
+    float u[TURNS][4], dt[TURNS][4], z[TURNS][4], gyv[TURNS][4];
 #pragma unroll
-    for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
-      float u[BATCH][V], dt[BATCH][V], z[BATCH][V], gyv[BATCH][V];
+    for (int i = 0; i < TURNS; ++i) {  // every load before the first use
+      const int r = (lane + i * 32) / PR;
+      const int count = r < n && SSD_IN_BOUNDS(t0 + r < in.L, err, 79) ? cols : 0;
+      load_four<VEC>(in.u, un.b, t0 + r, c0 + c, count, u[i]);
+      load_four<VEC>(in.dt, un.b, t0 + r, c0 + c, count, dt[i]);
+      load_four<VEC>(in.z, un.b, t0 + r, c0 + c, in.z.p ? count : 0, z[i]);
+      load_four<VEC>(gy, un.b, t0 + r, c0 + c, in.z.p ? count : 0, gyv[i]);
+    }
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int idx = lane + (i0 + j) * 32, r = idx / PR, c = idx % PR * V;
-        const bool ok = r < n && c < live && SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79);
-        load_if<V>(ok, in.u, un.b, t0 + r, c0 + c, u[j]);
-        load_if<V>(ok, in.dt, un.b, t0 + r, c0 + c, dt[j]);
-        load_if<V>(ok && in.z.p, in.z, un.b, t0 + r, c0 + c, z[j]);
-        load_if<V>(ok && in.z.p, gy, un.b, t0 + r, c0 + c, gyv[j]);
+    for (int i = 0; i < TURNS; ++i) {
+      const int r = (lane + i * 32) / PR;
+      const int64_t t = t0 + r;
+      if (t >= in.L || cols <= 0) continue;
+      float du[4], ddt[4], dz[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        du[e] = ddt[e] = dz[e] = 0.f;
+        if (r >= n) continue;
+        const float gB = sm.gB[r][c + e], o = sm.st.o[r][c + e];
+        du[e] = fmaf(sm.st.s[r][c + e], gB, skip[e] * o);
+        ddt[e] = fmaf(u[i][e], gB, sm.gah[r][c + e] * kLn2);
+        if (in.softplus) ddt[e] *= sigmoid(dt[i][e] + bias[e]);
+        if (in.z.p)
+          dz[e] = gyv[i][e] * fmaf(skip[e], u[i][e], sm.y[r][c + e]) * dsilu(z[i][e]);
+        dD[e] = fmaf(o, u[i][e], dD[e]);
+        dbias[e] += ddt[e];
       }
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int idx = lane + (i0 + j) * 32, r = idx / PR, c = idx % PR * V;
-        const int64_t t = t0 + r;
-        if (t >= in.L || c >= live || !SSD_IN_BOUNDS(c0 + c + V <= in.D, err, 79)) continue;
-        const bool ok = r < n;
-        float du[V], ddt[V], dz[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          du[e] = ddt[e] = dz[e] = 0.f;
-          if (!ok) continue;
-          const int col = La::at(i0 + j, e);
-          const float gB = sm.gB[r][c + e], o = sm.st.o[r][c + e];
-          du[e] = fmaf(sm.st.s[r][c + e], gB, skip[col] * o);
-          ddt[e] = fmaf(u[j][e], gB, sm.gah[r][c + e] * kLn2);
-          if (in.softplus) ddt[e] *= sigmoid(dt[j][e] + bias[col]);
-          if (in.z.p)
-            dz[e] = gyv[j][e] * fmaf(skip[col], u[j][e], sm.y[r][c + e]) * dsilu(z[j][e]);
-          dD[col] = fmaf(o, u[j][e], dD[col]);
-          dbias[col] += ddt[e];
-        }
-        store_vec<V>(out.du.at(un.b, t) + c0 + c, du);
-        store_vec<V>(out.ddt.at(un.b, t) + c0 + c, ddt);
-        if (out.dz.p) store_vec<V>(out.dz.at(un.b, t) + c0 + c, dz);
-      }
+      store_four<VEC>(out.du, un.b, t, c0 + c, cols, du);
+      store_four<VEC>(out.ddt, un.b, t, c0 + c, cols, ddt);
+      if (out.dz.p) store_four<VEC>(out.dz, un.b, t, c0 + c, cols, dz);
     }
   }
   const int64_t row = un.b * parts.parts + un.part;
@@ -646,13 +657,13 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     }
   // lanes with the same columns hold different tokens
 #pragma unroll
-  for (int e = 0; e < VD; ++e) {
+  for (int e = 0; e < 4; ++e) {
 #pragma unroll
     for (int off = 16; off >= PR; off /= 2) {
       dD[e] += __shfl_xor_sync(0xffffffffu, dD[e], off);
       dbias[e] += __shfl_xor_sync(0xffffffffu, dbias[e], off);
     }
-    const int c = PR >= 32 ? (lane + e / V * 32) * V + e % V : lane % PR * V + e;
+    const int c = lane % PR * 4 + e;
     if (lane < PR && c < live) {
       buf.partD[row * in.D + c0 + c] = dD[e];
       buf.partBias[row * in.D + c0 + c] = dbias[e];
@@ -734,14 +745,10 @@ Layout layout_of(const ScanArgs &a) {
   return l;
 }
 
-// Whether every row is whole pieces of 16 bytes, and the outputs' rows vectors
-// of four.
-bool vectored(const ScanArgs &a, ssd_dtype io) {
+// Whether the outputs' rows are vectors of four.
+bool whole_fours(const ScanArgs &a, ssd_dtype io) {
   const size_t e = io == SSD_BF16 ? 2 : 4;
-  return a.N * e % 16 == 0 && (a.D / a.G) * e % 16 == 0 && view_aligned(a.u, e, 16) &&
-         view_aligned(a.dt, e, 16) && view_aligned(a.z, e, 16) && view_aligned(a.gy, e, 16) &&
-         view_aligned(a.B, e, 16) && view_aligned(a.C, e, 16) &&
-         view_aligned(&a.out->du, e, 4 * e) && view_aligned(&a.out->ddt, e, 4 * e) &&
+  return view_aligned(&a.out->du, e, 4 * e) && view_aligned(&a.out->ddt, e, 4 * e) &&
          view_aligned(&a.out->dz, e, 4 * e);
 }
 
@@ -775,30 +782,33 @@ cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void
     const SeqView<const IO> gy = view_of<const IO>(a.gy);
     const Out<IO> out{view_of<IO>(&a.out->du), view_of<IO>(&a.out->ddt), view_of<IO>(&a.out->dz)};
     const int64_t ids = a.b * a.G * l.parts.tiles, units = ids * l.parts.parts;
-    auto run = [&](auto v_c) {
-      constexpr int V = decltype(v_c)::value;
-      constexpr bool AHEAD = V > 1;
-      constexpr size_t m0 = sizeof(Stage<NL>) + (AHEAD ? sizeof(Raw<IO, NL>) : 0);
-      constexpr size_t m1 = sizeof(AdjointSmem<IO, NL, AHEAD>);
-      cudaError_t e = cudaFuncSetAttribute(ends_kernel<IO, NL, V, AHEAD>,
+    const int piece = piece_of(a, io);
+    auto run = [&](auto vec_c) {
+      constexpr bool VEC = decltype(vec_c)::value;
+      constexpr size_t m0 = sizeof(Stage<NL>) + sizeof(Raw<IO, NL>);
+      constexpr size_t m1 = sizeof(AdjointSmem<IO, NL>);
+      cudaError_t e = cudaFuncSetAttribute(ends_kernel<IO, NL, VEC>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)m0);
       if (e != cudaSuccess) return e;
-      ends_kernel<IO, NL, V, AHEAD><<<(unsigned)units, 32, m0, st>>>(in, gy, l.parts, buf, err);
+      ends_kernel<IO, NL, VEC><<<(unsigned)units, 32, m0, st>>>(in, gy, l.parts, buf, piece == 4,
+                                                                err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      chain_kernel<NL><<<dim3((unsigned)ids, 2), 256, 0, st>>>(a.A, a.h0, a.gfinal, a.out->dh0, l.parts,
-                                                      buf, a.b, a.D, (int)a.N, in.per_group, err);
+      chain_kernel<NL><<<dim3((unsigned)ids, 2), 256, 0, st>>>(
+          a.A, a.h0, a.gfinal, a.out->dh0, l.parts, buf, a.b, a.D, (int)a.N, in.per_group, err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(adjoint_kernel<IO, NL, V, AHEAD>,
+      e = cudaFuncSetAttribute(adjoint_kernel<IO, NL, VEC>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)m1);
       if (e != cudaSuccess) return e;
-      adjoint_kernel<IO, NL, V, AHEAD>
-          <<<(unsigned)units, 32, m1, st>>>(in, gy, l.parts, buf, out, err);
+      adjoint_kernel<IO, NL, VEC><<<(unsigned)units, 32, m1, st>>>(in, gy, l.parts, buf, out,
+                                                                   piece == 4, err);
       return cudaGetLastError();
     };
-    cudaError_t e = vectored(a, io) ? run(std::integral_constant<int, 4>{})
-                                    : run(std::integral_constant<int, 1>{});
+    // 16-byte pieces of rows in and vectors of four out, or any rows (N = 16,
+    // 2 x 1024 x 1536: 146 us, at odd offsets 200 in bf16 and 222 in fp32)
+    cudaError_t e =
+        piece == 16 && whole_fours(a, io) ? run(std::true_type{}) : run(std::false_type{});
     if (e != cudaSuccess) return e;
     const int64_t n = a.b * a.L * a.G * a.N;
     auto tiles = [&](auto v_c) {
