@@ -361,16 +361,21 @@ norm_team_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = (tid + k * tm.threads) * V;
-      xr[k].clear(), zr[k].clear();
-      if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 43)) continue;
       if constexpr (decltype(ahead)::kAsync) {
+        xr[k].clear(), zr[k].clear();
+        if (i >= group) continue;
         ahead.take(0, k, xr[k]);
         if (gate) ahead.take(1, k, zr[k]);
-      } else {
-        xr[k].load(at(x, here, i));
-        if (gate) zr[k].load(at(z, here, i));
+      } else {  // without a branch, so that all the loads go out together
+        if (!SSD_IN_BOUNDS(c0 + group <= G * group, err, 43)) return;
+        xr[k].load(at(x, here, i < group ? i : 0));
+        if (gate) zr[k].load(at(z, here, i < group ? i : 0));
       }
     }
+    if constexpr (!decltype(ahead)::kAsync)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if ((tid + k * tm.threads) * V >= group) xr[k].clear(), zr[k].clear();
     ahead.turn();
     float r[K][V], s[1] = {0.f};
 #pragma unroll
@@ -400,20 +405,20 @@ norm_team_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = (tid + k * tm.threads) * V;
-      if (i >= group) continue;
+      const int64_t p = c0 + (i < group ? i : 0);
       float o[V], w[V];
-      load_params<V>(weight + c0 + i, vec_params, w);
+      load_params<V>(weight + p, vec_params, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = r[k][e] * rstd * w[e];
       if (bias) {
-        load_params<V>(bias + c0 + i, vec_params, w);
+        load_params<V>(bias + p, vec_params, w);
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] += w[e];
       }
       if (gate == SSD_GATE_OUTPUT)
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] *= silu(zr[k].at(e));
-      store_vec<V>(y.at(here.b, here.t) + c0 + i, o);
+      if (i < group) store_vec<V>(y.at(here.b, here.t) + c0 + i, o);
     }
   }
 }
@@ -474,18 +479,24 @@ norm_team_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = (tid + k * tm.threads) * V;
-      xc[k].clear(), zc[k].clear(), gc[k].clear();
-      if (i >= group || !SSD_IN_BOUNDS(c0 + group <= G * group, err, 44)) continue;
       if constexpr (decltype(ahead)::kAsync) {
+        xc[k].clear(), zc[k].clear(), gc[k].clear();
+        if (i >= group) continue;
         ahead.take(0, k, xc[k]);
         ahead.take(1, k, gc[k]);
         if (gate) ahead.take(2, k, zc[k]);
-      } else {
-        xc[k].load(at(x, here, i));
-        gc[k].load(at(gy, here, i));
-        if (gate) zc[k].load(at(z, here, i));
+      } else {  // without a branch, so that all the loads go out together
+        if (!SSD_IN_BOUNDS(c0 + group <= G * group, err, 44)) return;
+        const int j = i < group ? i : 0;
+        xc[k].load(at(x, here, j));
+        gc[k].load(at(gy, here, j));
+        if (gate) zc[k].load(at(z, here, j));
       }
     }
+    if constexpr (!decltype(ahead)::kAsync)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if ((tid + k * tm.threads) * V >= group) xc[k].clear(), zc[k].clear(), gc[k].clear();
     ahead.turn();
     float sig[K][V];
 #pragma unroll
@@ -515,12 +526,12 @@ norm_team_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = (tid + k * tm.threads) * V;
-      if (i >= group) continue;
+      const bool ok = i < group;
       float w[V];
-      load_params<V>(weight + c0 + i, vec_params, w);
+      load_params<V>(weight + c0 + (ok ? i : 0), vec_params, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = r_of(k, e) - mean, q = gv_of(k, e) * w[e];
+        const float d = ok ? r_of(k, e) - mean : 0.f, q = ok ? gv_of(k, e) * w[e] : 0.f;
         s[0] = fmaf(d, d, s[0]);
         s[1] = fmaf(q, d, s[1]);
         if (center) s[2] += q;
@@ -532,13 +543,13 @@ norm_team_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = (tid + k * tm.threads) * V;
-      if (i >= group) continue;
+      const int64_t p = c0 + (i < group ? i : 0);
       float ox[V], oz[V], w[V], bi[V];
-      load_params<V>(weight + c0 + i, vec_params, w);
+      load_params<V>(weight + p, vec_params, w);
       if (BIAS && gate == SSD_GATE_OUTPUT) {
 #pragma unroll
         for (int e = 0; e < V; ++e) bi[e] = 0.f;
-        if (bias) load_params<V>(bias + c0 + i, vec_params, bi);
+        if (bias) load_params<V>(bias + p, vec_params, bi);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -554,6 +565,7 @@ norm_team_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
         if (gate == SSD_GATE_OUTPUT)
           oz[e] = slope * (gc[k].at(e) * (BIAS ? fmaf(n, w[e], bi[e]) : n * w[e]));
       }
+      if (i >= group) continue;
       store_vec<V>(dx.at(here.b, here.t) + c0 + i, ox);
       if (gate) store_vec<V>(dz.at(here.b, here.t) + c0 + i, oz);
     }
