@@ -16,7 +16,7 @@
 //
 // Measured (bf16, 16 states, GB300): 16 sequences of 512 tokens and 5120
 // channels, uncut: 247 us, 2.7e12 (token, channel, state) a second; two of
-// 2048 tokens, in five segments: 194 us; 16384 tokens of 1536 channels: 208 us.
+// 2048 tokens, in five segments: 177 us; 16384 tokens of 1536 channels: 208 us.
 // A pair multiply-add with three register operands takes three cycles of a
 // scheduler, so the body is 107 cycles a token and warp where nothing stalls.
 //
@@ -36,10 +36,11 @@ constexpr int kWarps = 4;  // independent warps per block
 constexpr int kBlocks = 3;  // per SM; four blocks of 128 registers ran slower (218 us against 194)
 constexpr int kTile = 8;    // tokens staged at a time
 
-// A warp's part of the work: sequence, group, channel tile, segment.
+// A warp's part of the work: sequence, group, channel tile, segment.  The
+// first launch cuts each segment but the last into parts.
 struct Cut {
-  int tiles, segments;  // tiles per group
-  int64_t span;         // tokens per segment
+  int tiles, segments, parts;  // tiles per group, parts per segment
+  int64_t span;                // tokens per part
 };
 
 // A warp's copies of kTile tokens' rows of one view into COLS columns of
@@ -98,15 +99,16 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
   auto &sm = reinterpret_cast<Warp<IO, NPT, NL, OUT> *>(smem)[warp];
   int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
   if (unit >= units) return;
-  // units run over tiles, groups, segments, sequences; the first launch
-  // leaves out the last segment
+  // units run over tiles, groups, segments (parts of them but the last in the
+  // first launch), sequences
   const int tile = (int)(unit % cut.tiles);
   const int64_t G = in.D / in.per_group;
   const int64_t g = unit / cut.tiles % G;
-  const int segs = OUT ? cut.segments : cut.segments - 1;
+  const int ends_of = (cut.segments - 1) * cut.parts, segs = OUT ? cut.segments : ends_of;
+  const int64_t span = OUT ? cut.span * cut.parts : cut.span;
   const int64_t seg = unit / cut.tiles / G % segs, b = unit / cut.tiles / G / segs;
-  auto slot = [&](int64_t j) {  // of segment j's end
-    return ((b * cut.segments + j) * G + g) * cut.tiles + tile;
+  auto slot = [&](int64_t j) {  // of part j's end
+    return ((b * ends_of + j) * G + g) * cut.tiles + tile;
   };
   const int c = tile * CW + lane / NL;
   const bool live = c < in.per_group, stores = live && nl == 0;
@@ -114,7 +116,7 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
   const int N = in.N, n0 = nl * NPT;
   if (!SSD_IN_BOUNDS(b < in.nb && d < in.D, err, 70)) return;
   const int64_t len = tokens_of(in.lengths, b, in.L);
-  const int64_t first = seg * cut.span, last = min(first + cut.span, in.L);
+  const int64_t first = seg * span, last = min(first + span, in.L);
   const int64_t t1 = min(last, len);
 
   pair A[NPT / 2], h[NPT / 2];
@@ -130,7 +132,8 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
     }
   }
   if (OUT)
-    for (int64_t k = 0; k < seg; ++k) {
+#pragma unroll 2
+    for (int64_t k = 0; k < seg * cut.parts; ++k) {
       const float *e = ends + slot(k) * NPT * 32 + lane;
       const pair total = both(sums[slot(k) * CW + lane / NL]);
 #pragma unroll
@@ -272,7 +275,7 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
 
 // States per lane and lanes per channel.  (Four or eight states to a lane give
 // more warps, which would not have to be cut: 16 states on four lanes took 312
-// us where five segments take 194.)
+// us where segments take 177.)
 struct Split {
   int npt, nl;
 };
@@ -283,8 +286,16 @@ Split split_of(const ScanArgs &a) {
 
 // Segments: as many as the warps resident at once (three blocks to an SM;
 // twice as many took a tenth longer on 16384 tokens of 1536 channels), of 32
-// tokens at least (512 tokens of 1536 channels: 28 us, at 64 tokens 34 us).  Fewer than three are not worth the first launch: 1280 warps
-// of their own run uncut.
+// tokens at least (512 tokens of 1536 channels: 28 us, at 64 tokens 34 us), and
+// no more than they hold tokens each, since a segment joins all the ends before
+// it (32 channels of 100000 tokens: 317 segments 150 us, 1786 400 us).
+// Fewer than three are not worth the first launch: 1280 warps of their own run
+// uncut.  The first launch has a segment less, and its warps fill their rounds
+// badly: it cuts segments further where rounds of shorter parts take less time
+// in all (2 x 2048 x 5120: 1280 warps of 1824, 194 us; four parts each, 2.8
+// rounds, 177; three or five parts 185, 187).  Every part is one more end to
+// join, so there are kEnds at most.
+constexpr int kEnds = 16;
 constexpr int kPerSm = 12;
 Cut cut_of(const ScanArgs &a) {
   Cut c;
@@ -293,13 +304,18 @@ Cut cut_of(const ScanArgs &a) {
   const int64_t warps = a.b * a.G * c.tiles, room = (int64_t)sm_count() * kPerSm;
   int64_t s = room / warps;
   s = min(s, (a.L + 31) / 32);
+  while (s * s > a.L) --s;
   if (s < 3) s = 1;
-  c.span = ((a.L + s - 1) / s + 15) / 16 * 16;
-  c.segments = (int)((a.L + c.span - 1) / c.span);
+  c.parts = 1;
+  auto rounds = [&](int64_t p) { return (warps * (s - 1) * p + room - 1) / room; };
+  for (int p = 2; p * (s - 1) <= kEnds && 32 * p * s <= a.L; ++p)
+    if (rounds(p) * c.parts < rounds(c.parts) * p) c.parts = p;
+  c.span = ((a.L + s * c.parts - 1) / (s * c.parts) + 7) / 8 * 8;
+  c.segments = (int)((a.L + c.span * c.parts - 1) / (c.span * c.parts));
   return c;
 }
 int64_t slots_of(const ScanArgs &a, const Cut &c) {
-  return a.b * c.segments * a.G * c.tiles;
+  return a.b * (c.segments - 1) * c.parts * a.G * c.tiles;
 }
 
 }  // namespace
@@ -329,7 +345,7 @@ cudaError_t launch_selective_scan(const ScanArgs &a, ssd_dtype io, void *ws, int
     const SeqView<IO> y = view_of<IO>(a.y);
     auto blocks = [](int64_t units) { return (unsigned)((units + kWarps - 1) / kWarps); };
     if (c.segments > 1) {
-      const int64_t n = per_seg * (c.segments - 1);
+      const int64_t n = per_seg * (c.segments - 1) * c.parts;
       scan_kernel<IO, NPT, NL, VEC, false>
           <<<blocks(n), 32 * kWarps, m0, st>>>(in, c, y, nullptr, ends, sums, n, err);
       const cudaError_t e = cudaGetLastError();
