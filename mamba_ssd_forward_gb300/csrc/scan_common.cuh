@@ -32,6 +32,20 @@ __device__ __forceinline__ float step_of(float v, bool softplus) {
   return fmaf(t, q, fmaxf(v, 0.f));
 }
 
+// The slope of softplus where its value is s: 1 - exp(-s), by its series where
+// the difference would cancel (the term left out is below 1e-8 of it).
+__device__ __forceinline__ float slope_of_step(float s) {
+  float q = -1.f / 40320.f;
+  q = fmaf(q, s, 1.f / 5040.f);
+  q = fmaf(q, s, -1.f / 720.f);
+  q = fmaf(q, s, 1.f / 120.f);
+  q = fmaf(q, s, -1.f / 24.f);
+  q = fmaf(q, s, 1.f / 6.f);
+  q = fmaf(q, s, -0.5f);
+  q = fmaf(q, s, 1.f);
+  return s < 0.5f ? q * s : 1.f - ex2(-kLog2e * s);
+}
+
 // Pairs of fp32 in 64-bit registers: one instruction for two products.
 typedef unsigned long long pair;
 __device__ __forceinline__ pair pack(float a, float b) {

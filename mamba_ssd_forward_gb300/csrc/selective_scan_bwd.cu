@@ -23,8 +23,8 @@
 // arithmetic: 3.75 exponentials and some 25 multiply-adds per (token, channel,
 // state) against 46 bytes per (token, channel).
 //
-// Measured, bf16, 4 sequences of 1024 tokens, 2048 channels of 16 states: 304
-// us in all; ends 59, chain 15, adjoint 214, the sums 21.  A segment's inputs
+// Measured, bf16, 4 sequences of 1024 tokens, 2048 channels of 16 states: 294
+// us in all; ends 59, chain 15, adjoint 202, the sums 21.  A segment's inputs
 // are copied to shared memory while the one before is worked on (405 -> 366).
 #include "scan_common.cuh"
 
@@ -100,11 +100,11 @@ struct Buffers {
   float *partA, *partD, *partBias;   // [b, part, D, N], [b, part, D] twice
 };
 
-// s, s u and o of a segment, and its B and C with every value twice.
+// s, u and o of a segment, and its B and C with every value twice.
 template <int NL>
 struct Stage {
   using G = Geo<NL>;
-  float s[G::SEG][G::CW], su[G::SEG][G::CW], o[G::SEG][G::CW];
+  float s[G::SEG][G::CW], u[G::SEG][G::CW], o[G::SEG][G::CW];
   float2 B[G::SEG][G::NP], C[G::SEG][G::NP];
 };
 
@@ -158,22 +158,8 @@ __device__ __forceinline__ void copy_segment(const In<IO> &in, const SeqView<con
   copies_issued();
 }
 
-// Four channels of one token of a view, the first `count` of them (maybe none);
-// zero beyond.  VEC: all four or none, on their boundary.
-template <bool VEC, typename IO>
-__device__ __forceinline__ void load_four(const SeqView<const IO> &m, int64_t b, int64_t t,
-                                          int64_t c, int count, float (&v)[4]) {
-  v[0] = v[1] = v[2] = v[3] = 0.f;
-  if (count <= 0) return;
-  const IO *p = m.at(b, t) + c;
-  if constexpr (VEC) {
-    load_vec<4>(p, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < count) v[e] = ld_io(p + e);
-  }
-}
+// Four channels of one token of a view, the first `count` of them.  VEC: all
+// four, on their boundary.
 template <bool VEC, typename IO>
 __device__ __forceinline__ void store_four(const SeqView<IO> &m, int64_t b, int64_t t, int64_t c,
                                            int count, const float (&v)[4]) {
@@ -205,19 +191,20 @@ struct Lanes {
   }
 };
 
-// Fills a Stage from `raw`, where n tokens of the segment were copied; zero
-// beyond them and beyond the tile's `live` channels, which leaves states and
-// adjoints alone.
+// Fills a Stage from `raw`, where n tokens of the segment were copied, and gz =
+// gy silu'(z) if asked; zero beyond them and beyond the tile's `live` channels,
+// which leaves states and adjoints alone.
 template <typename IO, int NL>
 __device__ __forceinline__ void fill(const In<IO> &in, const Raw<IO, NL> &raw, Stage<NL> &sm,
-                                     int live, int n, int lane, const float (&bias)[4]) {
+                                     float (*gz)[Geo<NL>::CW], int live, int n, int lane,
+                                     const float (&bias)[4]) {
   using Ge = Geo<NL>;
   using La = Lanes<NL>;
   const int c = lane % La::PR * 4;
 #pragma unroll
   for (int i = 0; i < La::TURNS; ++i) {
     const int r = (lane + i * 32) / La::PR;
-    float u[4], dt[4], z[4], go[4], s[4], su[4];
+    float u[4], dt[4], z[4], go[4], s[4], gd[4];
     load_vec<4>(&raw.u[r][c], u);
     load_vec<4>(&raw.dt[r][c], dt);
     load_vec<4>(&raw.gy[r][c], go);
@@ -226,12 +213,19 @@ __device__ __forceinline__ void fill(const In<IO> &in, const Raw<IO, NL> &raw, S
     for (int e = 0; e < 4; ++e) {
       const bool ok = r < n && c + e < live;
       s[e] = ok ? step_of(dt[e] + bias[e], in.softplus) : 0.f;
-      su[e] = ok ? s[e] * u[e] : 0.f;
-      go[e] = !ok ? 0.f : in.z.p ? go[e] * silu(z[e]) : go[e];
+      u[e] = ok ? u[e] : 0.f;
+      gd[e] = 0.f;
+      if (!ok) go[e] = 0.f;
+      if (ok && in.z.p) {
+        const float sig = sigmoid(z[e]);
+        gd[e] = go[e] * (sig * fmaf(z[e], 1.f - sig, 1.f));
+        go[e] *= z[e] * sig;
+      }
     }
     store_vec<4>(&sm.s[r][c], s);
-    store_vec<4>(&sm.su[r][c], su);
+    store_vec<4>(&sm.u[r][c], u);
     store_vec<4>(&sm.o[r][c], go);
+    if (gz) store_vec<4>(&gz[r][c], gd);
   }
 #pragma unroll
   for (int q = lane; q < Ge::SEG * Ge::NP; q += 32) {
@@ -305,14 +299,15 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, bool word
     if (n > 0) {
       copies_landed<0>();
       __syncwarp();
-      fill<IO, NL>(in, raw, sm, live, n, lane, bias);
+      fill<IO, NL>(in, raw, sm, nullptr, live, n, lane, bias);
       __syncwarp();
       ahead(seg + 1);
 #pragma unroll 4
       for (int k = 0; k < Ge::SEG; ++k) {
         pair s[2], su[2], o[2], B[4], C[4];
         four(&sm.s[k][cg * 4], s);
-        four(&sm.su[k][cg * 4], su);
+        four(&sm.u[k][cg * 4], su);
+        su[0] = mul2(su[0], s[0]), su[1] = mul2(su[1], s[1]);
         four(&sm.o[k][cg * 4], o);
         four_twice(&sm.B[k][nl * 4], B);
         four_twice(&sm.C[k][nl * 4], C);
@@ -430,7 +425,8 @@ struct AdjointSmem {
   using Ge = Geo<NL>;
   static constexpr int SUB = Ge::SEG / 4;
   Stage<NL> st;
-  float gB[Ge::SEG][Ge::CW], gah[Ge::SEG][Ge::CW], y[Ge::SEG][Ge::CW];
+  float gB[Ge::SEG][Ge::CW], gah[Ge::SEG][Ge::CW];
+  float dz[Ge::SEG][Ge::CW];  // gy silu'(z), then times the ungated output
   pair start[SUB > 1 ? SUB - 1 : 1][8][32];  // states in front of tokens 4, 8, ..
   Raw<IO, NL> raw;
 };
@@ -487,6 +483,13 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   float dD[4], dbias[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) dD[e] = dbias[e] = 0.f;
+  // the channels whose output this lane is left with
+  constexpr int KEEP = NL < 4 ? 4 / NL : 1, DUP = NL > 4 ? NL / 4 : 1;
+  const int out_c = cg * 4 + nl / DUP * KEEP;
+  float out_skip[KEEP];
+#pragma unroll
+  for (int j = 0; j < KEEP; ++j)
+    out_skip[j] = in.Dskip && out_c + j < live ? in.Dskip[c0 + out_c + j] : 0.f;
 
   const int64_t last = min((un.part + 1) * parts.per, parts.segments);
   auto tokens = [&](int64_t seg) {  // of a segment
@@ -509,7 +512,7 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     copies_landed<0>();
     __syncwarp();
     if (n > 0) {
-      fill<IO, NL>(in, raw, sm.st, live, n, lane, bias);
+      fill<IO, NL>(in, raw, sm.st, in.z.p ? sm.dz : nullptr, live, n, lane, bias);
       __syncwarp();
       ahead(seg - 1);
       // the states in front of every fourth token
@@ -520,7 +523,8 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
           const int t = sub * 4 - 4 + k;
           pair s[2], su[2], B[4];
           four(&sm.st.s[t][cg * 4], s);
-          four(&sm.st.su[t][cg * 4], su);
+          four(&sm.st.u[t][cg * 4], su);
+          su[0] = mul2(su[0], s[0]), su[1] = mul2(su[1], s[1]);
           four_twice(&sm.st.B[t][nl * 4], B);
 #pragma unroll
           for (int p = 0; p < 2; ++p)
@@ -542,7 +546,8 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
           const int t = sub * 4 + k;
           pair s[2], su[2], B[4], C[4];
           four(&sm.st.s[t][cg * 4], s);
-          four(&sm.st.su[t][cg * 4], su);
+          four(&sm.st.u[t][cg * 4], su);
+          su[0] = mul2(su[0], s[0]), su[1] = mul2(su[1], s[1]);
           four_twice(&sm.st.B[t][nl * 4], B);
           four_twice(&sm.st.C[t][nl * 4], C);
           float y[4];
@@ -558,17 +563,19 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
             unpack(acc, y[2 * p], y[2 * p + 1]);
           }
           spread<1, NL, 4>(y, lane);
-          constexpr int KEEP = NL < 4 ? 4 / NL : 1, DUP = NL > 4 ? NL / 4 : 1;
-          if (nl % DUP == 0)
+          if (in.z.p && nl % DUP == 0)
 #pragma unroll
-            for (int j = 0; j < KEEP; ++j) sm.y[t][cg * 4 + nl / DUP * KEEP + j] = y[j];
+            for (int j = 0; j < KEEP; ++j)
+              sm.dz[t][out_c + j] *=
+                  fmaf(NL == 1 ? skip[j] : out_skip[j], sm.st.u[t][out_c + j], y[j]);
         }
 #pragma unroll
         for (int k = 3; k >= 0; --k) {
           const int t = sub * 4 + k;
           pair s[2], su[2], o[2], B[4], C[4];
           four(&sm.st.s[t][cg * 4], s);
-          four(&sm.st.su[t][cg * 4], su);
+          four(&sm.st.u[t][cg * 4], su);
+          su[0] = mul2(su[0], s[0]), su[1] = mul2(su[1], s[1]);
           four(&sm.st.o[t][cg * 4], o);
           four_twice(&sm.st.B[t][nl * 4], B);
           four_twice(&sm.st.C[t][nl * 4], C);
@@ -609,33 +616,26 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
     if (n == 0) ahead(seg - 1);
     // what remains is per token and channel
     const int c = lane % PR * 4, cols = live - c;  // this lane's, if any
-    float u[TURNS][4], dt[TURNS][4], z[TURNS][4], gyv[TURNS][4];
-#pragma unroll
-    for (int i = 0; i < TURNS; ++i) {  // every load before the first use
-      const int r = (lane + i * 32) / PR;
-      const int count = r < n && SSD_IN_BOUNDS(t0 + r < in.L, err, 79) ? cols : 0;
-      load_four<VEC>(in.u, un.b, t0 + r, c0 + c, count, u[i]);
-      load_four<VEC>(in.dt, un.b, t0 + r, c0 + c, count, dt[i]);
-      load_four<VEC>(in.z, un.b, t0 + r, c0 + c, in.z.p ? count : 0, z[i]);
-      load_four<VEC>(gy, un.b, t0 + r, c0 + c, in.z.p ? count : 0, gyv[i]);
-    }
-#pragma unroll
+#pragma unroll NL == 1 ? 1 : TURNS
     for (int i = 0; i < TURNS; ++i) {
       const int r = (lane + i * 32) / PR;
       const int64_t t = t0 + r;
       if (t >= in.L || cols <= 0) continue;
-      float du[4], ddt[4], dz[4];
+      float s[4], u[4], o[4], gB[4], gah[4], dz[4], du[4], ddt[4];
+      load_vec<4>(&sm.st.s[r][c], s);
+      load_vec<4>(&sm.st.u[r][c], u);
+      load_vec<4>(&sm.st.o[r][c], o);
+      load_vec<4>(&sm.gB[r][c], gB);
+      load_vec<4>(&sm.gah[r][c], gah);
+      load_vec<4>(&sm.dz[r][c], dz);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        du[e] = ddt[e] = dz[e] = 0.f;
-        if (r >= n) continue;
-        const float gB = sm.gB[r][c + e], o = sm.st.o[r][c + e];
-        du[e] = fmaf(sm.st.s[r][c + e], gB, skip[e] * o);
-        ddt[e] = fmaf(u[i][e], gB, sm.gah[r][c + e] * kLn2);
-        if (in.softplus) ddt[e] *= sigmoid(dt[i][e] + bias[e]);
-        if (in.z.p)
-          dz[e] = gyv[i][e] * fmaf(skip[e], u[i][e], sm.y[r][c + e]) * dsilu(z[i][e]);
-        dD[e] = fmaf(o, u[i][e], dD[e]);
+        const bool ok = r < n;
+        du[e] = ok ? fmaf(s[e], gB[e], skip[e] * o[e]) : 0.f;
+        const float g = fmaf(u[e], gB[e], gah[e] * kLn2);
+        ddt[e] = !ok ? 0.f : in.softplus ? g * slope_of_step(s[e]) : g;
+        dz[e] = ok ? dz[e] : 0.f;
+        if (ok) dD[e] = fmaf(o[e], u[e], dD[e]);
         dbias[e] += ddt[e];
       }
       store_four<VEC>(out.du, un.b, t, c0 + c, cols, du);
@@ -806,7 +806,7 @@ cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void
       return cudaGetLastError();
     };
     // 16-byte pieces of rows in and vectors of four out, or any rows (N = 16,
-    // 2 x 1024 x 1536: 146 us, at odd offsets 200 in bf16 and 222 in fp32)
+    // 2 x 1024 x 1536: 142 us, at odd offsets 185 in bf16 and 222 in fp32)
     cudaError_t e =
         piece == 16 && whole_fours(a, io) ? run(std::true_type{}) : run(std::false_type{});
     if (e != cudaSuccess) return e;
