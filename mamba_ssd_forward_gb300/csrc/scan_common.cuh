@@ -83,22 +83,6 @@ __device__ __forceinline__ pair add2(pair a, pair b) {
   return r;
 }
 __device__ __forceinline__ pair both(float v) { return pack(v, v); }
-// step_of of two channels at once.
-__device__ __forceinline__ pair step_of2(pair v, bool softplus) {
-  if (!softplus) return v;
-  float a, b;
-  unpack(v, a, b);
-  const pair t = pack(ex2(-kLog2e * fabsf(a)), ex2(-kLog2e * fabsf(b)));
-  pair q = fma2(both(0.0052326940931379795f), t, both(-0.02950523979961872f));
-  q = fma2(q, t, both(0.07822595536708832f));
-  q = fma2(q, t, both(-0.13663245737552643f));
-  q = fma2(q, t, both(0.19106006622314453f));
-  q = fma2(q, t, both(-0.2484298199415207f));
-  q = fma2(q, t, both(0.3331909775733948f));
-  q = fma2(q, t, both(-0.4999949336051941f));
-  q = fma2(q, t, both(0.9999999403953552f));
-  return fma2(t, q, pack(fmaxf(a, 0.f), fmaxf(b, 0.f)));
-}
 
 // The four states of a lane: loads of a row of N floats or I/O elements from
 // index n0 on, zero past N.

@@ -34,7 +34,7 @@ namespace {
 using namespace scan;
 
 // Warps of the adjoint to an SM: at 8 a lane has some 240 registers and spills
-// nothing; at 10, 168 registers with spills, a tenth more time.
+// next to nothing; at 10, 168 registers with spills, a tenth more time.
 constexpr int kMin = 8;
 constexpr int kMinEnds = 16;  // 128 registers; 12 warps (162) and 20 (96) were slower
 
