@@ -138,6 +138,44 @@ def test_scan(ssd, O, b, L, D, N, G, wide, lengths, more, dtype):
     ssd.device_error()
 
 
+# rows on 4 bytes but not on 16
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("b,L,D,N,G,wide,lengths,more", [
+    (2, 100, 264, 16, 1, 2, [100, 37], {}), (2, 50, 36, 14, 2, 6, None, {"h0": False}),
+    (1, 21, 132, 3, 1, 1, None, {}), (2, 35, 140, 40, 1, 10, [35, 2], {"z": False}),
+    (3, 18, 300, 4, 1, 0, [18, 0, 5], {"bias": False}),
+])
+def test_scan_rows_on_small_boundaries(ssd, O, b, L, D, N, G, wide, lengths, more, dtype):
+    test_scan(ssd, O, b, L, D, N, G, wide, lengths, more, dtype)
+
+
+def test_step_and_its_slope_everywhere(ssd):
+    # one token and state, everything else 1: y = softplus(v), ddt = sigmoid(v)
+    v = torch.linspace(-40, 40, 2001, device="cuda")
+    one = torch.ones(1, 1, v.numel(), device="cuda")
+    a = dict(u=one, dt=v[None, None], A=-torch.ones(v.numel(), 1, device="cuda"),
+             B=one[..., :1, None], C=one[..., :1, None])
+    y, _ = ssd.selective_scan_forward(**a, dt_softplus=True)
+    ddt = ssd.selective_scan_backward(**a, gy=one, dt_softplus=True)["ddt"]
+    w = to64(v)
+    for got, ref in ((y, np.log1p(np.exp(-abs(w))) + np.maximum(w, 0)), (ddt, 1 / (1 + np.exp(-w)))):
+        assert (abs(to64(got)[0, 0] - ref) <= tol(torch.float32) * ref).all()
+
+
+# enough warps to cut each segment into parts; long sequences of few channels
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("b,L,D,N,lengths", [
+    (16, 700, 640, 16, [700, 0, 1, 140, 141, 699, 560, 561, 35, 36, 420, 700, 700, 8, 9, 333]),
+    (1, 3000, 8, 4, None), (2, 1500, 33, 2, [1500, 777]),
+])
+def test_scan_cuts(ssd, O, b, L, D, N, lengths, dtype):
+    a, _, _ = scan_inputs(b, L, D, N, 1, dtype, seed=L)
+    yr, fr = O.selective_scan(**host(a), lengths=lengths, dt_softplus=True)
+    y, fin = ssd.selective_scan_forward(**a, lengths=lengths_of(lengths), dt_softplus=True)
+    close(y, yr, tol(y.dtype, tokens=L, terms=N), "y")
+    close(fin, fr, tol(torch.float32, tokens=L), "final_state")
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("b,D,N,G,wide", [(1, 8, 16, 1, 0), (5, 130, 16, 2, 2), (3, 31, 7, 1, 5),
                                           (2, 16, 64, 1, 0)])
