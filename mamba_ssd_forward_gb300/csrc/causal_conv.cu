@@ -513,6 +513,22 @@ bool vectored(const ConvArgs &a, ssd_dtype io, int bf16) {
          ptr_aligned(a.final_state, bytes) && ptr_aligned(a.dstate, bytes);
 }
 
+// Tokens per run of the forward: the run whose rounds of resident blocks are
+// shortest in all, a run's start costing about ten tokens.  2 x 4096 x 5376: 39
+// us at 32 tokens (2.2 rounds), 35 at 72 (one); longer runs spread the memory's
+// accesses too far (four times as many tokens: 117 us at 72, 133 at 288).
+int fwd_run(const ConvArgs &a, int64_t nv, int threads, int per_sm) {
+  const int64_t room = (int64_t)sm_count() * per_sm;
+  int best = 4;
+  int64_t least = 0;
+  for (int run = 4; run <= 72; run += 4) {
+    const int64_t blocks = (nv * ((a.L + run - 1) / run) + threads - 1) / threads * a.b;
+    const int64_t cost = (blocks + room - 1) / room * (run + 10);
+    if (run == 4 || cost < least) best = run, least = cost;
+  }
+  return best;
+}
+
 // Tokens per run of the backward: short runs when long ones would leave SMs
 // idle, longer ones where the grid's second dimension would overflow.
 int bwd_run(const ConvArgs &a) {
@@ -532,10 +548,8 @@ cudaError_t launch_causal_conv(const ConvArgs &a, ssd_dtype io, int *err, cudaSt
   return dispatch<8, 4>(io, a.W, vec, [&](auto io_c, auto w_c, auto v_c) {
     using IO = typename decltype(io_c)::type;
     constexpr int W = decltype(w_c)::value, V = decltype(v_c)::value;
-    // the longest run that leaves every SM its threads twice over
-    const int64_t nv = a.D / V, want = (int64_t)sm_count() * kRingThreads * kRingBlocks * 2;
-    int run = 32;
-    while (run > 4 && a.b * nv * ((a.L + run - 1) / run) < want) run /= 2;
+    const int64_t nv = a.D / V;
+    const int run = fwd_run(a, nv, V > 1 ? kRingThreads : kThreads, V > 1 ? kRingBlocks : 8);
     const int64_t items = nv * ((a.L + run - 1) / run);
     auto blocks = [&](int threads) {
       return dim3((unsigned)((items + threads - 1) / threads), (unsigned)a.b);
