@@ -8,8 +8,8 @@
 // tokens in front of each run (which the neighbouring run brought into L2).
 // Tokens come by asynchronous copies through a ring of the thread's own in
 // shared memory, which keeps eight rows in flight without their registers.
-// Measured at W = 4: 2 x 4096 x 5376 in bf16 in 39 us (4.5 TB/s; 26 us at the
-// copy bandwidth), the gradients of 4 x 2048 x 1792 in fp32 in 42 (the same
+// Measured at W = 4: 2 x 4096 x 5376 in bf16 in 35 us (5.1 TB/s; 26 us at the
+// copy bandwidth), the gradients of 4 x 2048 x 1792 in fp32 in 39 (the same
 // bytes).  Half of the issue slots are taken, and warps wait for rows the rest.
 #include <type_traits>
 
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRingThreads = 128, kRingBlocks = 4;
-constexpr int kRing = 8, kRingBack = 4, kBackBlocks = 2;
+constexpr int kRing = 8, kRingBack = 4, kBackBlocks = 2, kBackBlocks1 = 3;
 
 template <int V>
 __device__ __forceinline__ void zero(float (&v)[V]) {
@@ -322,7 +322,7 @@ conv_ring_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 constexpr int kRuns = 8;
 
 template <typename IO, int W, int V, bool ASYNC, bool ACT>
-__global__ void __launch_bounds__(32 * kRuns, V > 1 ? kBackBlocks : 3)
+__global__ void __launch_bounds__(32 * kRuns, V > 1 ? kBackBlocks : kBackBlocks1)
 conv_bwd_kernel(SeqView<const IO> x, const float *__restrict__ weight,
                 const float *__restrict__ bias, const IO *__restrict__ state,
                 SeqView<const IO> gy, const IO *__restrict__ gfinal,
@@ -529,12 +529,25 @@ int fwd_run(const ConvArgs &a, int64_t nv, int threads, int per_sm) {
   return best;
 }
 
-// Tokens per run of the backward: short runs when long ones would leave SMs
-// idle, longer ones where the grid's second dimension would overflow.
+// The same of the backward, kRuns runs and 32 vectors of four channels (or 32
+// channels that are not whole fours) to a block: long enough for the grid's
+// second dimension, and the same whatever the alignment, which the workspace's
+// size does not know.  A run's start, its last tokens' neighbours and a block's
+// sums cost about 16 tokens.  2 x 4096 x 2688 in bf16: 46 us at 80 tokens (one
+// round), 58 at 64 (1.1).
 int bwd_run(const ConvArgs &a) {
-  const int64_t run = a.b * a.L * a.D >= (int64_t)1 << 22 ? 64 : 8;
-  const int64_t least = (a.L + 65535 * kRuns - 1) / (65535 * kRuns);
-  return (int)(run > least ? run : least);
+  const int wide = a.D % 4 == 0 ? 128 : 32;
+  const int64_t room = (int64_t)sm_count() * (wide == 128 ? kBackBlocks : kBackBlocks1);
+  const int64_t tiles = (a.D + wide - 1) / wide * a.b;
+  int best = 8;
+  int64_t least = 0;
+  for (int run = 8; run <= 128; run += 8) {
+    const int64_t blocks = tiles * ((a.L + run * kRuns - 1) / (run * kRuns));
+    const int64_t cost = (blocks + room - 1) / room * (run + 16);
+    if (run == 8 || cost < least) best = run, least = cost;
+  }
+  const int64_t longest = (a.L + 65535 * kRuns - 1) / (65535 * kRuns);
+  return (int)(best > longest ? best : longest);
 }
 int64_t bwd_rows(const ConvArgs &a) {
   const int64_t per = (int64_t)bwd_run(a) * kRuns;
