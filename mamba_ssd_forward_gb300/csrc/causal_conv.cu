@@ -106,9 +106,9 @@ __device__ __forceinline__ void input_row(const SeqView<const IO> &x, const IO *
     load_vec<V>(state + (b * (W - 1) + (p + W - 1)) * D + c, v);
 }
 
-// Rows on any boundary, a channel to a thread, loads in batches of A rows: 55 us
-// for 8192 bf16 tokens of 5376 channels at odd offsets, against 43 of the ring
-// kernel on aligned ones.  A = 4 took 67, A = 16 56.
+// Rows on any boundary, a channel to a thread, loads in batches of A rows: 53 us
+// for 8192 bf16 tokens of 5376 channels at odd offsets, against 40 of the ring
+// kernel on aligned ones (in runs of 32 tokens 55; A = 4 67, A = 16 56).
 template <typename IO, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_kernel(SeqView<const IO> x, const float *__restrict__ weight, const float *__restrict__ bias,
