@@ -616,6 +616,18 @@ constexpr int vectors_per_thread(int V, bool back) {
   return V == 8 || V == 4 ? 2 : V == 2 ? 4 : 8;
 }
 
+// Shared memory of a block of `block` threads for T tensors' vectors ahead.
+constexpr int ahead_bytes(int V, size_t elem, int K, int T, int block) {
+  return V * elem == 16 ? kStages * T * K * 16 * block : 0;
+}
+// Lets `kernel` have the shared memory of its largest block.  Always the same
+// amount: the attribute belongs to the kernel, not to the call, so an amount
+// of this call's own could fall between another thread's and its launch.
+template <typename F>
+cudaError_t allow_smem(F kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // The team for a group, or 0 threads where a block's registers do not hold it.
 int team_threads(const NormArgs &a, ssd_dtype io, bool back) {
   const int V = vector_of(a, io), per = V * vectors_per_thread(V, back);
@@ -677,12 +689,10 @@ cudaError_t launch_gated_norm(const NormArgs &a, ssd_dtype io, int *err, cudaStr
       using IO = typename decltype(io_c)::type;
       constexpr int V = decltype(v_c)::value;
       constexpr int K = vectors_per_thread(V, false), gate = decltype(gate_c)::value;
-      const size_t smem = V * sizeof(IO) == 16 ? (size_t)kStages * 2 * K * 16 * block : 0;
-      const cudaError_t e =
-          cudaFuncSetAttribute(norm_team_kernel<IO, V, K, gate>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      const auto kernel = norm_team_kernel<IO, V, K, gate>;
+      const cudaError_t e = allow_smem(kernel, ahead_bytes(V, sizeof(IO), K, 2, kMaxTeam));
       if (e != cudaSuccess) return e;
-      norm_team_kernel<IO, V, K, gate><<<(unsigned)blocks, block, smem, st>>>(
+      kernel<<<(unsigned)blocks, block, ahead_bytes(V, sizeof(IO), K, 2, block), st>>>(
           view_of<const IO>(a.x), a.weight, a.bias, view_of<const IO>(a.z), view_of<IO>(a.y), a.L,
           a.b * a.L, a.G, (int)(a.D / a.G), a.eps, a.center, tm, err);
       return cudaGetLastError();
@@ -719,13 +729,11 @@ cudaError_t launch_gated_norm_backward(const NormArgs &a, ssd_dtype io, void *ws
       using IO = typename decltype(io_c)::type;
       constexpr int V = decltype(v_c)::value;
       constexpr int K = vectors_per_thread(V, true), gate = decltype(gate_c)::value;
-      const size_t smem = V * sizeof(IO) == 16 ? (size_t)kStages * 3 * K * 16 * block : 0;
       auto go = [&](auto bias_c) {
-        auto kernel = norm_team_grad_kernel<IO, V, K, gate, decltype(bias_c)::value>;
-        const cudaError_t e1 = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const auto kernel = norm_team_grad_kernel<IO, V, K, gate, decltype(bias_c)::value>;
+        const cudaError_t e1 = allow_smem(kernel, ahead_bytes(V, sizeof(IO), K, 3, kMaxTeam));
         if (e1 != cudaSuccess) return e1;
-        kernel<<<(unsigned)blocks, block, smem, st>>>(
+        kernel<<<(unsigned)blocks, block, ahead_bytes(V, sizeof(IO), K, 3, block), st>>>(
             view_of<const IO>(a.x), a.weight, a.bias, view_of<const IO>(a.z),
             view_of<const IO>(a.gy), view_of<IO>(a.dx), view_of<IO>(a.dz), part_w, part_b, a.L,
             a.b * a.L, a.G, (int)(a.D / a.G), a.eps, a.center, tm, err);

@@ -1,0 +1,80 @@
+"""How the operators around the scan are called: from several host threads, in
+graphs, with some gradients only, with given outputs and workspaces, and with
+values at the ends of the number range."""
+import threading
+
+import pytest
+import torch
+
+from layer_cases import norm_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mamba_ssd_forward_gb300 import build
+    build.build()
+    import mamba_ssd_forward_gb300 as m
+    return m
+
+
+def test_norms_of_two_widths_from_two_threads(ssd):
+    """Groups of 8192 and of 512 channels run the same kernel with different
+    amounts of shared memory; neither call may undo the other's."""
+    from mamba_ssd_forward_gb300 import _abi
+    lib, calls, kept = _abi.load(), [], []
+    for D in (8192, 512):
+        a, gy = norm_inputs(2, D, "bf16", bias=False)
+        d = _abi.SsdNormDims(1, 2, D, 1, 1e-5, _abi.SSD_GATE_INPUT, 0)
+        ws = torch.empty(lib.ssd_gated_norm_backward_workspace_size(d, _abi.SSD_BF16),
+                         dtype=torch.uint8, device="cuda")
+        outs = [torch.empty_like(a["x"]) for _ in range(3)]
+        dw = torch.empty_like(a["weight"])
+        x, z, g, y, dx, dz = (_abi.SsdSeq(t.data_ptr(), 0, D) for t in (a["x"], a["z"], gy, *outs))
+        w, st = a["weight"].data_ptr(), torch.cuda.Stream()
+        kept += [a, gy, ws, outs, dw, st]
+        calls.append((
+            (d, _abi.SSD_BF16, x, w, None, z, y, st.cuda_stream),
+            (d, _abi.SSD_BF16, x, w, None, z, g, dx, dz, dw.data_ptr(), None, ws.data_ptr(),
+             ws.numel(), st.cuda_stream)))
+    torch.cuda.synchronize()
+    start, codes = threading.Barrier(2), [set(), set()]
+
+    def work(k):
+        forward, backward = calls[k]
+        start.wait()
+        for _ in range(10000):  # the library runs without the interpreter's lock
+            codes[k].add(lib.ssd_gated_norm(*forward))
+            codes[k].add(lib.ssd_gated_norm_backward(*backward))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}, {0}]
+
+
+def test_norms_of_two_widths_in_one_graph(ssd):
+    cases = [norm_inputs(3, D, "bf16", seed=D, bias=False) for D in (8192, 512)]
+
+    def everything():
+        out = []
+        for a, gy in cases:
+            out += [ssd.gated_norm_forward(**a), ssd.gated_norm_backward(**a, gy=gy)["dx"]]
+        return out
+
+    ref = [t.clone() for t in everything()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = everything()
+    for t in got:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(ref, got))
