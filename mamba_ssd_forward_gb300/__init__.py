@@ -5,7 +5,7 @@ dimensions from tensor shapes, allocates outputs and workspace with torch on
 the current CUDA stream, and passes raw device pointers.  All arithmetic runs
 in the library's CUDA kernels; there is no CPU or PyTorch fallback.
 
-Tensor layouts (all contiguous, on one CUDA device):
+Tensor layouts (all contiguous, on the current CUDA device):
     x [b, L, nh, P], dt [b, L, nh], B/C [b, L, ng, S] -- float32 or bfloat16
     A [nh], D [nh], h0 [b, nh, P, S]                   -- float32
 
@@ -20,6 +20,7 @@ import torch
 
 from . import _abi
 from ._abi import SSD_BF16, SSD_F32, SsdError  # noqa: F401
+from .layer import _stream
 from .layer import (  # noqa: F401
     causal_conv,
     causal_conv_backward,
@@ -66,10 +67,6 @@ def _f32(t, name):
     if t is not None and t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32")
     return t
-
-
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def dims_of(x: torch.Tensor, B: torch.Tensor, chunk: int) -> _abi.SsdDims:
@@ -131,7 +128,7 @@ def forward(x, dt, A, B, C, D=None, h0=None, chunk: int = 256, workspace=None,
         ctypes.byref(d), io, _ptr(x), _ptr(dt), _ptr(_f32(A, "A")), _ptr(B), _ptr(C),
         _ptr(_f32(D, "D")), _ptr(_f32(h0, "h0")), _ptr(y), _ptr(final_state),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _plan_ref(plan),
-        _stream()))
+        _stream(x)))
     return y, final_state
 
 
@@ -173,7 +170,7 @@ def backward(x, dt, A, B, C, D=None, h0=None, gy=None, gfinal=None, chunk: int =
             _ptr(_f32(D, "D")), _ptr(_f32(h0, "h0")), _ptr(gy), _ptr(_f32(gfinal, "gfinal")),
             _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
             _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dh0"]), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream()]
+            workspace.numel() * workspace.element_size(), _stream(x)]
     if events is None:
         _abi.check("ssd_backward", lib.ssd_backward(*args))
         return out
@@ -198,7 +195,7 @@ def chunk_cumsum(dt, A, chunk: int, headdim: int = 16, dstate: int = 16, out=Non
     G = out if out is not None else torch.empty(
         (b, nh, _nchunks(d) * d.chunk), dtype=torch.float32, device=dt.device)
     _abi.check("ssd_chunk_cumsum", lib.ssd_chunk_cumsum(
-        ctypes.byref(d), _io_code(dt), _ptr(dt), _ptr(_f32(A, "A")), _ptr(G), _stream()))
+        ctypes.byref(d), _io_code(dt), _ptr(dt), _ptr(_f32(A, "A")), _ptr(G), _stream(dt)))
     return G
 
 
@@ -212,7 +209,7 @@ def chunk_state(x, B, dt, G, chunk: int, out=None):
                           dtype=torch.float32, device=x.device)
     _abi.check("ssd_chunk_state", lib.ssd_chunk_state(
         ctypes.byref(d), _io_code(x), _ptr(x), _ptr(B), _ptr(dt), _ptr(_f32(G, "G")),
-        _ptr(out), _stream()))
+        _ptr(out), _stream(x)))
     return out
 
 
@@ -232,7 +229,7 @@ def state_passing(dstates, G, h0=None, chunk: int = 256, seqlen: int | None = No
         final = torch.empty((b, nh, P, S), dtype=torch.float32, device=dstates.device)
     _abi.check("ssd_state_passing", lib.ssd_state_passing(
         ctypes.byref(d), _ptr(_f32(dstates, "dstates")), _ptr(_f32(G, "G")),
-        _ptr(_f32(h0, "h0")), _ptr(states), _ptr(final), _stream()))
+        _ptr(_f32(h0, "h0")), _ptr(states), _ptr(final), _stream(dstates)))
     return states, final
 
 
@@ -245,7 +242,7 @@ def chunk_scan(x, B, C, dt, G, states, D=None, chunk: int = 256, y=None):
     _abi.check("ssd_chunk_scan", lib.ssd_chunk_scan(
         ctypes.byref(d), _io_code(x), _ptr(x), _ptr(B), _ptr(C), _ptr(dt),
         _ptr(_f32(G, "G")), _ptr(_f32(states, "states")), _ptr(_f32(D, "D")), _ptr(y),
-        _stream()))
+        _stream(x)))
     return y
 
 
@@ -261,7 +258,7 @@ def decode_step(x, dt, A, B, C, D, state, y=None):
         y = torch.empty_like(x)
     _abi.check("ssd_decode_step", lib.ssd_decode_step(
         ctypes.byref(d), _io_code(x), _ptr(x), _ptr(dt), _ptr(_f32(A, "A")), _ptr(B), _ptr(C),
-        _ptr(_f32(D, "D")), _ptr(_f32(state, "state")), _ptr(y), _stream()))
+        _ptr(_f32(D, "D")), _ptr(_f32(state, "state")), _ptr(y), _stream(x)))
     return y
 
 
@@ -279,7 +276,7 @@ def forward_profiled(x, dt, A, B, C, D, h0, chunk, workspace, y, final_state, ev
     _abi.check("ssd_forward_profiled", lib.ssd_forward_profiled(
         ctypes.byref(d), _io_code(x), _ptr(x), _ptr(dt), _ptr(_f32(A, "A")), _ptr(B), _ptr(C),
         _ptr(_f32(D, "D")), _ptr(_f32(h0, "h0")), _ptr(y), _ptr(final_state), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _plan_ref(plan), _stream(), handles,
+        workspace.numel() * workspace.element_size(), _plan_ref(plan), _stream(x), handles,
         len(events), ctypes.byref(n)))
     return n.value
 
@@ -309,7 +306,8 @@ def forward_host(x, dt, A, B, C, D, h0, chunk, workspace, y, final_state=None, p
     _abi.check("ssd_forward_host", lib.ssd_forward_host(
         ctypes.byref(d), _io_code(x), _host_ptr(x), _host_ptr(dt), _host_ptr(A), _host_ptr(B),
         _host_ptr(C), _host_ptr(D), _host_ptr(h0), _host_ptr(y), _host_ptr(final_state),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _plan_ref(plan), _stream()))
+        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _plan_ref(plan),
+        _stream(workspace)))
 
 
 def host_overlapped_workspace_size(x, B, chunk, n_slices, has_D=True, has_h0=False,
@@ -334,7 +332,7 @@ def forward_host_overlapped(x, dt, A, B, C, D, h0, chunk, workspace, y, final_st
         ctypes.byref(d), _io_code(x), _host_ptr(x), _host_ptr(dt), _host_ptr(A), _host_ptr(B),
         _host_ptr(C), _host_ptr(D), _host_ptr(h0), _host_ptr(y), _host_ptr(final_state),
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), int(n_slices),
-        _plan_ref(plan), _stream(), sh(h2d_stream), sh(d2h_stream)))
+        _plan_ref(plan), _stream(workspace), sh(h2d_stream), sh(d2h_stream)))
 
 
 def plan_candidates(d: _abi.SsdDims, io: int = 1) -> list[dict]:
@@ -376,7 +374,7 @@ def tune(x, dt, A, B, C, D=None, h0=None, chunk: int = 256, reps: int = 5, works
         ctypes.byref(d), io, _ptr(x), _ptr(dt), _ptr(_f32(A, "A")), _ptr(B), _ptr(C),
         _ptr(_f32(D, "D")), _ptr(_f32(h0, "h0")), _ptr(y), _ptr(final_state),
         _ptr(workspace), workspace.numel() * workspace.element_size(), int(reps),
-        _ptr(flush), 0 if flush is None else flush.numel() * flush.element_size(), _stream(),
+        _ptr(flush), 0 if flush is None else flush.numel() * flush.element_size(), _stream(x),
         ctypes.byref(p)))
     return p.as_dict(), y, final_state
 
@@ -385,14 +383,16 @@ def workspace_error(workspace) -> None:
     """Synchronise the current stream and raise SsdError if a kernel of a
     call that used `workspace` gave up a bounded wait since the last check
     (ssd_workspace_error); clears the workspace's error word."""
-    _abi.check("ssd_workspace_error", _abi.load().ssd_workspace_error(_ptr(workspace), _stream()))
+    _abi.check("ssd_workspace_error",
+               _abi.load().ssd_workspace_error(_ptr(workspace), _stream(workspace)))
 
 
 def device_error() -> None:
     """Synchronise the current stream and raise SsdError if a call without a
     workspace (the step-wise entry points, ssd_forward_noalloc) gave up a
     bounded wait since the last check (ssd_device_error)."""
-    _abi.check("ssd_device_error", _abi.load().ssd_device_error(_stream()))
+    _abi.check("ssd_device_error",
+               _abi.load().ssd_device_error(torch.cuda.current_stream().cuda_stream))
 
 
 class _SsdFunction(torch.autograd.Function):

@@ -9,7 +9,8 @@ all arithmetic runs in the library's kernels.
 Activations ([b, L, D] and the like) may be views with any strides between
 sequences and tokens as long as the last axis is dense, such as slices of a
 wider projection; other views are refused.  `lengths` (int32 [b] on the
-device, or None) gives the real tokens of each padded sequence.
+device, or None) gives the real tokens of each padded sequence.  The tensors'
+device has to be the current one.
 """
 from __future__ import annotations
 
@@ -34,8 +35,13 @@ def _io(t, name):
 
 
 def _stream(like):
-    """The current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(like.get_device())
+    """The current stream.  The library launches on the current device, which
+    therefore has to be the tensor's."""
+    dev = like.get_device()
+    if dev != (current := torch._C._cuda_getDevice()):
+        raise ValueError(f"the tensors are on cuda:{dev} but the current device is "
+                         f"cuda:{current}: call within torch.cuda.device({dev})")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _refuse(t, name, shape, dtype, like):
