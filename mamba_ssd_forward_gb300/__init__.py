@@ -20,7 +20,7 @@ import torch
 
 from . import _abi
 from ._abi import SSD_BF16, SSD_F32, SsdError  # noqa: F401
-from .layer import _stream
+from .layer import _first_order, _stream
 from .layer import (  # noqa: F401
     causal_conv,
     causal_conv_backward,
@@ -409,6 +409,7 @@ class _SsdFunction(torch.autograd.Function):
         return y, final_state
 
     @staticmethod
+    @_first_order
     def backward(ctx, gy, gfinal):
         x, dt, A, B, C, D, h0 = ctx.saved_tensors
         need = ctx.needs_input_grad

@@ -14,6 +14,7 @@ device has to be the current one.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 import torch
@@ -130,6 +131,36 @@ def _out(t, name, shape, dtype, like):
     return t
 
 
+class _Last(torch.autograd.Function):
+    """A gradient that stands for a function of `sources` without a gradient
+    of its own: differentiating it raises."""
+
+    @staticmethod
+    def forward(ctx, grad, *sources):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("second derivatives of this library's operators are not available")
+
+
+def _first_order(backward):
+    """Wraps the backward pass of an autograd function whose gradients come
+    from kernels, which autograd cannot follow.  Under create_graph they would
+    come back as constants and a term that depends on them lose its part
+    silently."""
+    @functools.wraps(backward)
+    def wrapped(ctx, *cotangents):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *cotangents)
+        with torch.no_grad():
+            grads = backward(ctx, *cotangents)
+        sources = [t for t in (*ctx.saved_tensors, *cotangents)
+                   if t is not None and t.requires_grad]
+        return tuple(None if g is None else _Last.apply(g, *sources) for g in grads)
+    return wrapped
+
+
 # ------------------------------------------------------ causal convolution
 
 def _conv_dims(x, weight, activation, step=False):
@@ -220,6 +251,7 @@ class _CausalConv(torch.autograd.Function):
         return y, final_state
 
     @staticmethod
+    @_first_order
     def backward(ctx, gy, gfinal):
         x, weight, bias, state, lengths = ctx.saved_tensors
         g = causal_conv_backward(x, weight, bias, state, gy.contiguous(), gfinal.contiguous(),
@@ -353,6 +385,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, final_state
 
     @staticmethod
+    @_first_order
     def backward(ctx, gy, gfinal):
         *tensors, lengths = ctx.saved_tensors
         g = selective_scan_backward(*tensors, gy.contiguous(), gfinal.contiguous(), lengths,
@@ -450,6 +483,7 @@ class _GatedNorm(torch.autograd.Function):
         return gated_norm_forward(x, weight, bias, z, *ctx.how)
 
     @staticmethod
+    @_first_order
     def backward(ctx, gy):
         x, weight, bias, z = ctx.saved_tensors
         g = gated_norm_backward(x, weight, bias, z, gy.contiguous(), *ctx.how)

@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from layer_cases import norm_inputs
+from layer_cases import conv_inputs, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,15 @@ def test_norms_of_two_widths_in_one_graph(ssd):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(ref, got))
+
+
+def test_first_derivatives_within_a_graph_and_no_second(ssd):
+    a, gy, _ = conv_inputs(2, 20, 24, 4, "fp32", seed=3)
+    leaf = {k: v.clone().requires_grad_() for k, v in a.items()}
+    y = ssd.causal_conv(**leaf)[0]
+    g = torch.autograd.grad(y, list(leaf.values()), gy, create_graph=True)
+    ref = ssd.causal_conv_backward(**a, gy=gy)
+    for k, got in zip(leaf, g):
+        assert torch.equal(got, ref["d" + k]), k
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        torch.autograd.grad((g[0] ** 2).sum(), leaf["x"])

@@ -46,3 +46,61 @@ def test_tensors_of_another_device_are_refused(name, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="cuda:1.*current.*cuda:0"):
         _calls()[name]()
+
+
+def _differentiated(monkeypatch):
+    """(outputs, inputs) of each differentiable call, its kernels replaced by
+    host arithmetic of the same shapes."""
+    from mamba_ssd_forward_gb300 import layer
+    like = torch.zeros_like
+
+    def pair(x, *a, **k):
+        return 2.0 * x, like(x)
+
+    monkeypatch.setattr(layer, "causal_conv_forward", pair)
+    monkeypatch.setattr(layer, "causal_conv_backward", lambda x, w, *a, **k: {
+        "dx": 2.0 * x, "dweight": like(w), "dbias": None, "dstate": None})
+    monkeypatch.setattr(layer, "selective_scan_forward", pair)
+    monkeypatch.setattr(layer, "selective_scan_backward", lambda u, dt, A, B, C, *a, **k: {
+        "du": 2.0 * u, "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C),
+        **dict.fromkeys(("dD", "dz", "ddt_bias", "dh0"))})
+    monkeypatch.setattr(layer, "gated_norm_forward", lambda x, *a, **k: 2.0 * x)
+    monkeypatch.setattr(layer, "gated_norm_backward", lambda x, w, *a, **k: {
+        "dx": 2.0 * x, "dweight": like(w), "dbias": None, "dz": None})
+    monkeypatch.setattr(ssd, "forward", pair)
+    monkeypatch.setattr(ssd, "backward", lambda x, dt, A, B, C, *a, **k: {
+        "dx": 2.0 * x, "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C),
+        "dD": None, "dh0": None})
+
+    def leaf(*shape):
+        return torch.randn(*shape, requires_grad=True)
+
+    x, w, A, B = leaf(2, 5, 8), leaf(8, 4), leaf(8, 4), leaf(2, 5, 1, 4)
+    yield "conv", ssd.causal_conv(x, w)[0], x
+    yield "scan", ssd.selective_scan(x, x, A, B, B)[0], x
+    yield "norm", ssd.gated_norm(x, leaf(8), gate="none"), x
+    x4 = leaf(1, 64, 2, 64)
+    yield "ssd", ssd.ssd(x4, leaf(1, 64, 2), leaf(2), leaf(1, 64, 1, 64), leaf(1, 64, 1, 64))[0], x4
+
+
+@pytest.mark.parametrize("which", ["conv", "scan", "norm", "ssd"])
+def test_second_derivatives_are_refused(which, monkeypatch):
+    """The gradients come from kernels without gradients of their own: asking
+    for them raises, also where other terms have some."""
+    y, x = next((y, x) for name, y, x in _differentiated(monkeypatch) if name == which)
+    g, = torch.autograd.grad(y.sum(), x, create_graph=True)
+    penalty = (g * g).sum() + (x ** 3).sum()
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        torch.autograd.grad(penalty, x)
+
+
+@pytest.mark.parametrize("which", ["conv", "scan", "norm", "ssd"])
+def test_first_derivatives_within_a_graph(which, monkeypatch):
+    """create_graph alone changes nothing: other terms are differentiated twice."""
+    y, x = next((y, x) for name, y, x in _differentiated(monkeypatch) if name == which)
+    plain, = torch.autograd.grad(y.sum(), x, retain_graph=True)
+    g, = torch.autograd.grad((x ** 3).sum() + y.sum(), x, create_graph=True)
+    assert torch.equal(g.detach(), 3 * x.detach() ** 2 + plain)
+    h, = torch.autograd.grad((x ** 3).sum(), x, create_graph=True)
+    hh, = torch.autograd.grad(h.sum(), x)
+    assert torch.allclose(hh, 6 * x.detach())
