@@ -144,6 +144,21 @@ class _Last(torch.autograd.Function):
         raise RuntimeError("second derivatives of this library's operators are not available")
 
 
+def _wanted(want, names, fn):
+    """The gradients asked for: a function of the name and of whether the
+    input is there."""
+    if want is None:
+        return lambda name, there=True: there
+    if unknown := set(want) - set(names):
+        raise ValueError(f"{fn}: no gradient {sorted(unknown)[0]!r} (there are {', '.join(names)})")
+    return lambda name, there=True: there and name in want
+
+
+def _needed(ctx, names):
+    """The gradients that autograd asks for, by the leading inputs' names."""
+    return tuple(n for n, need in zip(names, ctx.needs_input_grad) if need)
+
+
 def _first_order(backward):
     """Wraps the backward pass of an autograd function whose gradients come
     from kernels, which autograd cannot follow.  Under create_graph they would
@@ -197,31 +212,39 @@ def causal_conv_forward(x, weight, bias=None, state=None, lengths=None, activati
     return y, final_state
 
 
+_CONV_GRADS = ("dx", "dweight", "dbias", "dstate")
+
+
 def causal_conv_backward(x, weight, bias=None, state=None, gy=None, gfinal=None, lengths=None,
-                         activation="silu", workspace=None) -> dict:
+                         activation="silu", workspace=None, want=None) -> dict:
     """Gradients through causal_conv_forward given gy = dL/dy and gfinal =
     dL/dfinal_state (None = 0), by ssd_causal_conv_backward: a dict of dx (I/O
     type), dweight, dbias (float32; dbias None without a bias) and dstate (None
-    without a state)."""
+    without a state).  `want` names those to compute (None = all); the others
+    are None."""
     if gy is None:
         raise ValueError("gy (dL/dy) is required")
+    has = _wanted(want, _CONV_GRADS, "causal_conv_backward")
     d = _conv_dims(x, weight, activation)
     io, b, L, D, W = _io(x, "x"), d.batch, d.seqlen, d.channels, d.width
     lib, keep = _abi.load(), (b, W - 1, D)
     ws, wp, wn = _workspace(lib.ssd_causal_conv_backward_workspace_size(d, io), workspace, x,
                             "causal_conv_backward")
-    dx = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
-    dw = torch.empty((D, W), dtype=torch.float32, device=x.device)
-    db = None if bias is None else torch.empty((D,), dtype=torch.float32, device=x.device)
-    ds = None if state is None else torch.empty(keep, dtype=x.dtype, device=x.device)
+
+    def out(name, there, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=x.device) if has(name, there) else None
+
+    dx = out("dx", True, (b, L, D), x.dtype)
+    dw = out("dweight", True, (D, W), torch.float32)
+    db = out("dbias", bias is not None, (D,), torch.float32)
+    ds = out("dstate", state is not None, keep, x.dtype)
     _abi.check("ssd_causal_conv_backward", lib.ssd_causal_conv_backward(
         d, io, _seq(x, "x", (b, L, D), x.dtype, x),
         _dense(weight, "weight", (D, W), torch.float32, x),
         _dense(bias, "bias", (D,), torch.float32, x), _dense(state, "state", keep, x.dtype, x),
         _seq(gy, "gy", (b, L, D), x.dtype, x), _dense(gfinal, "gfinal", keep, x.dtype, x),
-        _lengths(lengths, b, x), _seq(dx, "dx", (b, L, D), x.dtype, x), dw.data_ptr(),
-        None if db is None else db.data_ptr(), None if ds is None else ds.data_ptr(), wp, wn,
-        _stream(x)))
+        _lengths(lengths, b, x), _seq(dx, "dx", (b, L, D), x.dtype, x),
+        *(None if t is None else t.data_ptr() for t in (dw, db, ds)), wp, wn, _stream(x)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
 
 
@@ -255,8 +278,8 @@ class _CausalConv(torch.autograd.Function):
     def backward(ctx, gy, gfinal):
         x, weight, bias, state, lengths = ctx.saved_tensors
         g = causal_conv_backward(x, weight, bias, state, gy.contiguous(), gfinal.contiguous(),
-                                 lengths, ctx.activation)
-        return g["dx"], g["dweight"], g["dbias"], g["dstate"], None, None
+                                 lengths, ctx.activation, want=_needed(ctx, _CONV_GRADS))
+        return (*(g[k] for k in _CONV_GRADS), None, None)
 
 
 def causal_conv(x, weight, bias=None, state=None, lengths=None, activation="silu"):
@@ -318,29 +341,36 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     return y, final_state
 
 
+_SCAN_GRADS = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+
+
 def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, gy=None,
                             gfinal=None, lengths=None, dt_softplus: bool = False,
-                            workspace=None) -> dict:
+                            workspace=None, want=None) -> dict:
     """Gradients through selective_scan_forward given gy = dL/dy and gfinal =
     dL/dfinal_state (None = 0), by ssd_selective_scan_backward: a dict of du,
     ddt, dB, dC, dz (I/O type), dA, dD, ddt_bias, dh0 (float32); those of
-    absent inputs are None."""
+    absent inputs are None.  `want` names those to compute (None = all) and the
+    others are None, but du, ddt, dB and dC are always computed."""
     if gy is None:
         raise ValueError("gy (dL/dy) is required")
+    has = _wanted(want, _SCAN_GRADS, "selective_scan_backward")
     d = _scan_dims(u, A, B, dt_softplus)
     lib, b, L, nd, N = _abi.load(), d.batch, d.seqlen, d.channels, d.dstate
     args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias)
     row, grp, keep = (b, L, nd), (b, L, d.ngroups, N), (b, nd, N)
 
-    def io_out(shape, of=u):
-        return None if of is None else torch.empty(shape, dtype=u.dtype, device=u.device)
+    def io_out(shape, there=True):
+        return torch.empty(shape, dtype=u.dtype, device=u.device) if there else None
 
-    def f32_out(shape, of):
-        return None if of is None else torch.empty(shape, dtype=torch.float32, device=u.device)
+    def f32_out(name, shape, of):
+        return torch.empty(shape, dtype=torch.float32, device=u.device) \
+            if has(name, of is not None) else None
 
-    r = {"du": io_out(row), "ddt": io_out(row), "dA": f32_out((nd, N), A), "dB": io_out(grp),
-         "dC": io_out(grp), "dD": f32_out((nd,), D), "dz": io_out(row, z),
-         "ddt_bias": f32_out((nd,), dt_bias), "dh0": f32_out(keep, h0)}
+    r = {"du": io_out(row), "ddt": io_out(row), "dA": f32_out("dA", (nd, N), A),
+         "dB": io_out(grp), "dC": io_out(grp), "dD": f32_out("dD", (nd,), D),
+         "dz": io_out(row, has("dz", z is not None)),
+         "ddt_bias": f32_out("ddt_bias", (nd,), dt_bias), "dh0": f32_out("dh0", keep, h0)}
     g = _abi.SsdScanGrads()
     for k in ("du", "ddt", "dz"):
         if r[k] is not None:
@@ -388,10 +418,10 @@ class _SelectiveScan(torch.autograd.Function):
     @_first_order
     def backward(ctx, gy, gfinal):
         *tensors, lengths = ctx.saved_tensors
+        want = _needed(ctx, _SCAN_GRADS)
         g = selective_scan_backward(*tensors, gy.contiguous(), gfinal.contiguous(), lengths,
-                                    ctx.dt_softplus)
-        return (*(g[k] for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")),
-                None, None)
+                                    ctx.dt_softplus, want=want)
+        return (*(g[k] if k in want else None for k in _SCAN_GRADS), None, None)
 
 
 def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None,
@@ -450,28 +480,34 @@ def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float
     return y
 
 
+_NORM_GRADS = ("dx", "dweight", "dbias", "dz")
+
+
 def gated_norm_backward(x, weight, bias=None, z=None, gy=None, groups: int = 1,
                         eps: float = 1e-5, gate: str = "input", center: bool = False,
-                        workspace=None) -> dict:
+                        workspace=None, want=None) -> dict:
     """Gradients through gated_norm_forward given gy = dL/dy, by
     ssd_gated_norm_backward: a dict of dx, dz (I/O type; dz None without a
-    gate), dweight and dbias (float32; dbias None without a bias)."""
+    gate), dweight and dbias (float32; dbias None without a bias).  `want` names
+    those to compute (None = all) and the others are None, but dx and dz are
+    always computed."""
     if gy is None:
         raise ValueError("gy (dL/dy) is required")
+    has = _wanted(want, _NORM_GRADS, "gated_norm_backward")
     d = _norm_dims(x, groups, eps, gate, center)
     flat, D, lib, io = _rows(d), x.shape[-1], _abi.load(), _io(x, "x")
     ws, wp, wn = _workspace(lib.ssd_gated_norm_backward_workspace_size(d, io), workspace, x,
                             "gated_norm_backward")
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     dz = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = torch.empty((D,), dtype=torch.float32, device=x.device)
-    db = None if bias is None else torch.empty((D,), dtype=torch.float32, device=x.device)
+    dw, db = (torch.empty((D,), dtype=torch.float32, device=x.device) if has(name, there) else None
+              for name, there in (("dweight", True), ("dbias", bias is not None)))
     _abi.check("ssd_gated_norm_backward", lib.ssd_gated_norm_backward(
         d, io, _norm_view(x, "x", x, flat), _dense(weight, "weight", (D,), torch.float32, x),
         _dense(bias, "bias", (D,), torch.float32, x), _norm_view(z, "z", x, flat),
         _norm_view(gy, "gy", x, flat), _norm_view(dx, "dx", x, flat),
-        _norm_view(dz, "dz", x, flat), dw.data_ptr(), None if db is None else db.data_ptr(), wp,
-        wn, _stream(x)))
+        _norm_view(dz, "dz", x, flat), *(None if t is None else t.data_ptr() for t in (dw, db)),
+        wp, wn, _stream(x)))
     return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
 
 
@@ -486,8 +522,9 @@ class _GatedNorm(torch.autograd.Function):
     @_first_order
     def backward(ctx, gy):
         x, weight, bias, z = ctx.saved_tensors
-        g = gated_norm_backward(x, weight, bias, z, gy.contiguous(), *ctx.how)
-        return g["dx"], g["dweight"], g["dbias"], g["dz"], None, None, None, None
+        want = _needed(ctx, _NORM_GRADS)
+        g = gated_norm_backward(x, weight, bias, z, gy.contiguous(), *ctx.how, want=want)
+        return (*(g[k] if k in want else None for k in _NORM_GRADS), None, None, None, None)
 
 
 def gated_norm(x, weight, bias=None, z=None, groups: int = 1, eps: float = 1e-5,

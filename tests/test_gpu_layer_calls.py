@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from layer_cases import conv_inputs, norm_inputs
+from layer_cases import conv_inputs, norm_inputs, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,24 @@ def test_first_derivatives_within_a_graph_and_no_second(ssd):
         assert torch.equal(got, ref["d" + k]), k
     with pytest.raises(RuntimeError, match="second derivatives"):
         torch.autograd.grad((g[0] ** 2).sum(), leaf["x"])
+
+
+def test_some_gradients_only(ssd):
+    """Those asked for have the same bits; the others are None."""
+    a, gy, gf = conv_inputs(2, 40, 24, 4, "bf16", seed=3)
+    s, sgy, sgf = scan_inputs(2, 40, 24, 16, 1, "bf16", seed=3)
+    n, ngy = norm_inputs(30, 24, "bf16", seed=3)
+    for fn, args, more, always in (
+            (ssd.causal_conv_backward, a, dict(gy=gy, gfinal=gf), ()),
+            (ssd.selective_scan_backward, s, dict(gy=sgy, gfinal=sgf, dt_softplus=True),
+             ("du", "ddt", "dB", "dC")),
+            (ssd.gated_norm_backward, n, dict(gy=ngy), ("dx", "dz"))):
+        full = fn(**args, **more)
+        assert all(v is not None for v in full.values())
+        for want in [()] + [(k,) for k in full] + [tuple(full)]:
+            got = fn(**args, **more, want=want)
+            assert got.keys() == full.keys()
+            for k, v in got.items():
+                assert (v is not None) == (k in want or k in always), (want, k)
+                assert v is None or torch.equal(v, full[k]), (want, k)
+    ssd.device_error()

@@ -104,3 +104,39 @@ def test_first_derivatives_within_a_graph(which, monkeypatch):
     h, = torch.autograd.grad((x ** 3).sum(), x, create_graph=True)
     hh, = torch.autograd.grad(h.sum(), x)
     assert torch.allclose(hh, 6 * x.detach())
+
+
+@pytest.mark.parametrize("fn,args,names", [
+    ("causal_conv", dict(x=(2, 5, 8), weight=(8, 4), bias=(8,), state=(2, 3, 8)),
+     ("dx", "dweight", "dbias", "dstate")),
+    ("selective_scan", dict(u=(2, 5, 8), dt=(2, 5, 8), A=(8, 4), B=(2, 5, 1, 4), C=(2, 5, 1, 4),
+                            D=(8,), z=(2, 5, 8), dt_bias=(8,), h0=(2, 8, 4)),
+     ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")),
+    ("gated_norm", dict(x=(2, 5, 8), weight=(8,), bias=(8,), z=(2, 5, 8)),
+     ("dx", "dweight", "dbias", "dz"))])
+def test_only_needed_gradients_are_asked_for(fn, args, names, monkeypatch):
+    from mamba_ssd_forward_gb300 import layer
+    pair = fn != "gated_norm"
+    monkeypatch.setattr(layer, fn + "_forward", lambda x, *a, **k:
+                        (2.0 * x, torch.zeros(3)) if pair else 2.0 * x)
+    asked = []
+
+    def backward(*a, want=None, **k):
+        asked.append(want)
+        return {n: torch.ones(s) for n, s in zip(names, args.values())}
+
+    monkeypatch.setattr(layer, fn + "_backward", backward)
+    for frozen in ((names[1],), names[1:], (names[0], names[-1])):
+        leaf = {k: torch.randn(s, requires_grad=n not in frozen)
+                for (k, s), n in zip(args.items(), names)}
+        y = getattr(ssd, fn)(**leaf)
+        (y[0] if pair else y).sum().backward()
+        assert asked[-1] == tuple(n for n in names if n not in frozen)
+        for t, n in zip(leaf.values(), names):
+            assert (t.grad is None) == (n in frozen)
+
+
+def test_gradients_that_do_not_exist_are_refused():
+    x = torch.zeros(2, 5, 8)
+    with pytest.raises(ValueError, match="no gradient 'dy'"):
+        ssd.causal_conv_backward(x, torch.zeros(8, 4), gy=x, want=("dx", "dy"))
