@@ -308,8 +308,9 @@ Cut cut_of(const ScanArgs &a) {
   if (s < 3) s = 1;
   c.parts = 1;
   auto rounds = [&](int64_t p) { return (warps * (s - 1) * p + room - 1) / room; };
-  for (int p = 2; p * (s - 1) <= kEnds && 32 * p * s <= a.L; ++p)
-    if (rounds(p) * c.parts < rounds(c.parts) * p) c.parts = p;
+  if (s > 1)
+    for (int64_t p = 2; p * (s - 1) <= kEnds && 32 * p * s <= a.L; ++p)
+      if (rounds(p) * c.parts < rounds(c.parts) * p) c.parts = (int)p;
   c.span = ((a.L + s * c.parts - 1) / (s * c.parts) + 7) / 8 * 8;
   c.segments = (int)((a.L + c.span * c.parts - 1) / (c.span * c.parts));
   return c;

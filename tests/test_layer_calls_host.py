@@ -140,3 +140,20 @@ def test_gradients_that_do_not_exist_are_refused():
     x = torch.zeros(2, 5, 8)
     with pytest.raises(ValueError, match="no gradient 'dy'"):
         ssd.causal_conv_backward(x, torch.zeros(8, 4), gy=x, want=("dx", "dy"))
+
+
+def test_workspace_queries_do_not_grow_with_the_length():
+    """How a sequence is cut is decided in every call: a decision that walks
+    along the tokens would delay the launch (0.3 ms at a million of them)."""
+    import time
+    from mamba_ssd_forward_gb300 import _abi, build
+    build.build()
+    lib = _abi.load()
+    for L in (1 << 24, 1 << 28, (1 << 31) - 1):
+        for b, D in ((8, 5120), (1, 64)):
+            d = _abi.SsdScanDims(b, L, D, 16, 1, 1)
+            start = time.perf_counter()
+            for _ in range(10):
+                need = lib.ssd_selective_scan_workspace_size(d, _abi.SSD_BF16)
+            assert time.perf_counter() - start < 0.05, (b, L, D)
+            assert (need > 0) == (b == 1)
