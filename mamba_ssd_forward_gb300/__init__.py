@@ -24,14 +24,18 @@ from .layer import _first_order, _stream
 from .layer import (  # noqa: F401
     causal_conv,
     causal_conv_backward,
+    causal_conv_backward_workspace_size,
     causal_conv_forward,
     causal_conv_step,
     clip_grad_norm,
+    clip_grad_norm_workspace_size,
     gated_norm,
     gated_norm_backward,
+    gated_norm_backward_workspace_size,
     gated_norm_forward,
     selective_scan,
     selective_scan_backward,
+    selective_scan_backward_workspace_size,
     selective_scan_forward,
     selective_scan_step,
     selective_scan_workspace_size,
@@ -44,6 +48,8 @@ __all__ = ["forward", "chunk_cumsum", "chunk_state", "state_passing", "chunk_sca
            "selective_scan", "selective_scan_forward", "selective_scan_backward",
            "selective_scan_step", "selective_scan_workspace_size",
            "gated_norm", "gated_norm_forward", "gated_norm_backward", "clip_grad_norm",
+           "causal_conv_backward_workspace_size", "selective_scan_backward_workspace_size",
+           "gated_norm_backward_workspace_size", "clip_grad_norm_workspace_size",
            "SsdError"]
 
 

@@ -115,9 +115,16 @@ def _workspace(need, workspace, like, fn):
         if need == 0:
             return None, None, 0
         workspace = _sized(need, like.device)
-    elif workspace.dtype != torch.uint8 or workspace.device != like.device:
-        raise ValueError(f"{fn}: workspace must be a uint8 tensor on the inputs' device")
-    return workspace, workspace.data_ptr(), workspace.numel()
+        return workspace, workspace.data_ptr(), need
+    if (workspace.dtype != torch.uint8 or workspace.device != like.device
+            or not workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous uint8 tensor on the inputs' device")
+    at, have = workspace.data_ptr(), workspace.numel()
+    if have < need:
+        raise ValueError(f"{fn}: workspace has {have} bytes, {need} are needed")
+    if at % 256:
+        raise ValueError(f"{fn}: workspace must start on 256 bytes")
+    return workspace, at, have
 
 
 def _lengths(lengths, b, like):
@@ -213,6 +220,12 @@ def causal_conv_forward(x, weight, bias=None, state=None, lengths=None, activati
 
 
 _CONV_GRADS = ("dx", "dweight", "dbias", "dstate")
+
+
+def causal_conv_backward_workspace_size(x, weight) -> int:
+    """Bytes of workspace that causal_conv_backward needs."""
+    d = _conv_dims(x, weight, None)
+    return int(_abi.load().ssd_causal_conv_backward_workspace_size(d, _io(x, "x")))
 
 
 def causal_conv_backward(x, weight, bias=None, state=None, gy=None, gfinal=None, lengths=None,
@@ -311,6 +324,7 @@ def _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias, step=False):
 
 
 def selective_scan_workspace_size(u, A, B) -> int:
+    """Bytes of workspace that selective_scan_forward needs (may be 0)."""
     d = _scan_dims(u, A, B, False)
     return int(_abi.load().ssd_selective_scan_workspace_size(d, _io(u, "u")))
 
@@ -342,6 +356,12 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
 
 
 _SCAN_GRADS = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+
+
+def selective_scan_backward_workspace_size(u, A, B) -> int:
+    """Bytes of workspace that selective_scan_backward needs."""
+    d = _scan_dims(u, A, B, False)
+    return int(_abi.load().ssd_selective_scan_backward_workspace_size(d, _io(u, "u")))
 
 
 def selective_scan_backward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, gy=None,
@@ -483,6 +503,13 @@ def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float
 _NORM_GRADS = ("dx", "dweight", "dbias", "dz")
 
 
+def gated_norm_backward_workspace_size(x, groups: int = 1) -> int:
+    """Bytes of workspace that gated_norm_backward needs."""
+    d = _norm_dims(x, groups, 1e-5, "none", False)
+    _rows(d)
+    return int(_abi.load().ssd_gated_norm_backward_workspace_size(d, _io(x, "x")))
+
+
 def gated_norm_backward(x, weight, bias=None, z=None, gy=None, groups: int = 1,
                         eps: float = 1e-5, gate: str = "input", center: bool = False,
                         workspace=None, want=None) -> dict:
@@ -535,6 +562,14 @@ def gated_norm(x, weight, bias=None, z=None, groups: int = 1, eps: float = 1e-5,
 
 
 # ------------------------------------------- gradient norm and clipping
+
+def clip_grad_norm_workspace_size(grads) -> int:
+    """Bytes of workspace that clip_grad_norm needs for tensors of these sizes
+    and types."""
+    table = (_abi.SsdGrad * len(grads))(*((256, 256, g.numel(), _io(g, "grads"))
+                                          for g in grads))  # any aligned address will do
+    return int(_abi.load().ssd_clip_grad_norm_workspace_size(table, len(grads)))
+
 
 def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspace=None):
     """The norm over every element of every tensor of `grads` (a float32

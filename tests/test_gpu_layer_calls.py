@@ -111,3 +111,44 @@ def test_some_gradients_only(ssd):
                 assert (v is not None) == (k in want or k in always), (want, k)
                 assert v is None or torch.equal(v, full[k]), (want, k)
     ssd.device_error()
+
+
+# aligned and not: the schedules, and what they keep in the workspace, differ
+@pytest.mark.parametrize("wide", [0, 1])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_given_workspaces(ssd, dtype, wide):
+    """Workspaces of the queried sizes, not initialised and nothing behind
+    them: the same bits, and the bytes behind them stay."""
+    a, gy, gf = conv_inputs(3, 700, 132, 4, dtype, seed=5, wide=wide)
+    s, sgy, sgf = scan_inputs(3, 700, 132, 16, 2, dtype, seed=5, wide=wide)
+    n, ngy = norm_inputs(900, 264, dtype, seed=5, wide=wide)
+    big, gbig = norm_inputs(5, 20480, dtype, seed=6, wide=wide)
+    grads = [torch.randn(300000, device="cuda"), torch.randn(77, device="cuda").bfloat16()]
+    scaled = [torch.empty_like(t) for t in grads]
+    calls = [
+        (ssd.causal_conv_backward, dict(a, gy=gy, gfinal=gf),
+         ssd.causal_conv_backward_workspace_size(a["x"], a["weight"])),
+        (ssd.selective_scan_forward, dict(s, dt_softplus=True),
+         ssd.selective_scan_workspace_size(s["u"], s["A"], s["B"])),
+        (ssd.selective_scan_backward, dict(s, gy=sgy, gfinal=sgf, dt_softplus=True),
+         ssd.selective_scan_backward_workspace_size(s["u"], s["A"], s["B"])),
+        (ssd.gated_norm_backward, dict(n, gy=ngy, groups=2),
+         ssd.gated_norm_backward_workspace_size(n["x"], groups=2)),
+        (ssd.gated_norm_backward, dict(big, gy=gbig),
+         ssd.gated_norm_backward_workspace_size(big["x"])),
+        (ssd.clip_grad_norm, dict(grads=grads, max_norm=0.5, out=scaled),
+         ssd.clip_grad_norm_workspace_size(grads)),
+    ]
+    for fn, args, need in calls:
+        assert need > 0, fn
+
+        def outputs(r):
+            r = list(r.values()) if isinstance(r, dict) else [r] if torch.is_tensor(r) else list(r)
+            return [t.clone() for t in r + (scaled if fn is ssd.clip_grad_norm else [])]
+
+        ref = outputs(fn(**args))
+        room = torch.full((need + 65536,), 255, dtype=torch.uint8, device="cuda")  # NaN
+        got = outputs(fn(**args, workspace=room[:need]))
+        assert all(torch.equal(p, q) for p, q in zip(ref, got)), fn
+        assert bool((room[need:] == 255).all()), fn
+    ssd.device_error()

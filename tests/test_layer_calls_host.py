@@ -157,3 +157,46 @@ def test_workspace_queries_do_not_grow_with_the_length():
                 need = lib.ssd_selective_scan_workspace_size(d, _abi.SSD_BF16)
             assert time.perf_counter() - start < 0.05, (b, L, D)
             assert (need > 0) == (b == 1)
+
+
+def test_workspaces_are_checked_by_name(monkeypatch):
+    """A given workspace that is too small, off its boundary, of another type
+    or not dense is refused before the library sees it."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    x, A, B = far(2, 4096, 64), far(64, 16), far(2, 4096, 1, 16)
+    need = ssd.selective_scan_workspace_size(x, A, B)
+    assert need > 0
+    room = far(need + 512, dtype=torch.uint8)
+    room = room[-room.data_ptr() % 256:]  # from a boundary on
+
+    def call(workspace):
+        ssd.selective_scan_forward(x, x, A, B, B, y=far(2, 4096, 64), workspace=workspace,
+                                   return_final_state=False)
+
+    for bad, what in ((room[:need - 1], f"{need - 1} bytes, {need} are needed"),
+                      (room[16:], "256 bytes"), (room[::2], "contiguous uint8"),
+                      (far(need), "contiguous uint8")):
+        with pytest.raises(ValueError, match=f"selective_scan_forward: .*{what}"):
+            call(bad)
+
+
+def test_workspace_sizes_match_the_library():
+    from mamba_ssd_forward_gb300 import _abi, build
+    build.build()
+    lib = _abi.load()
+    x, w = torch.zeros(2, 300, 48), torch.zeros(48, 3)
+    d = _abi.SsdConvDims(2, 300, 48, 3, _abi.SSD_ACT_SILU)
+    need = lib.ssd_causal_conv_backward_workspace_size(d, _abi.SSD_F32)
+    assert ssd.causal_conv_backward_workspace_size(x, w) == need > 0
+    A, B = torch.zeros(48, 8), torch.zeros(2, 300, 2, 8)
+    d = _abi.SsdScanDims(2, 300, 48, 8, 2, 1)
+    need = lib.ssd_selective_scan_backward_workspace_size(d, _abi.SSD_F32)
+    assert ssd.selective_scan_backward_workspace_size(x, A, B) == need > 0
+    for t, (b, L) in ((x, (2, 300)), (x[0], (1, 300)), (x[:, :1], (1, 2))):
+        d = _abi.SsdNormDims(b, L, 48, 3, 1e-5, _abi.SSD_GATE_INPUT, 1)
+        need = lib.ssd_gated_norm_backward_workspace_size(d, _abi.SSD_F32)
+        assert ssd.gated_norm_backward_workspace_size(t, groups=3) == need > 0
+    grads = [torch.zeros(1000), torch.zeros(7, dtype=torch.bfloat16), torch.zeros(0)]
+    table = (_abi.SsdGrad * 3)((256, 256, 1000, 0), (512, 512, 7, 1), (0, 0, 0, 0))
+    need = lib.ssd_clip_grad_norm_workspace_size(table, 3)
+    assert ssd.clip_grad_norm_workspace_size(grads) == need > 0
