@@ -470,6 +470,13 @@ def _rows(d):
     return False
 
 
+def _check_gate(z, gate):
+    if z is None and gate != "none":
+        raise ValueError(f"gate {gate!r} needs z (without a gate: gate='none')")
+    if z is not None and gate == "none":
+        raise ValueError("z is given but gate is 'none'")
+
+
 def _norm_view(t, name, x, flat):
     if x.dim() == 3:
         v = _seq(t, name, x.shape, x.dtype, x)
@@ -490,6 +497,7 @@ def gated_norm_forward(x, weight, bias=None, z=None, groups: int = 1, eps: float
     x, z [tokens, D] or [b, L, D] in the I/O type, weight and bias [D]
     float32.  y may be x or z themselves."""
     d = _norm_dims(x, groups, eps, gate, center)
+    _check_gate(z, gate)
     flat, D = _rows(d), x.shape[-1]
     y = _out(y, "y", x.shape, x.dtype, x)
     _abi.check("ssd_gated_norm", _abi.load().ssd_gated_norm(
@@ -522,6 +530,7 @@ def gated_norm_backward(x, weight, bias=None, z=None, gy=None, groups: int = 1,
         raise ValueError("gy (dL/dy) is required")
     has = _wanted(want, _NORM_GRADS, "gated_norm_backward")
     d = _norm_dims(x, groups, eps, gate, center)
+    _check_gate(z, gate)
     flat, D, lib, io = _rows(d), x.shape[-1], _abi.load(), _io(x, "x")
     ws, wp, wn = _workspace(lib.ssd_gated_norm_backward_workspace_size(d, io), workspace, x,
                             "gated_norm_backward")

@@ -200,3 +200,16 @@ def test_workspace_sizes_match_the_library():
     table = (_abi.SsdGrad * 3)((256, 256, 1000, 0), (512, 512, 7, 1), (0, 0, 0, 0))
     need = lib.ssd_clip_grad_norm_workspace_size(table, 3)
     assert ssd.clip_grad_norm_workspace_size(grads) == need > 0
+
+
+def test_gate_and_its_values_go_together():
+    x, w = torch.zeros(5, 8), torch.zeros(8)
+    for gate in ("input", "output"):
+        with pytest.raises(ValueError, match=f"gate '{gate}' needs z"):
+            ssd.gated_norm_forward(x, w, gate=gate)
+        with pytest.raises(ValueError, match=f"gate '{gate}' needs z"):
+            ssd.gated_norm_backward(x, w, gy=x, gate=gate)
+    with pytest.raises(ValueError, match="gate '.*' needs z"):
+        ssd.gated_norm(x, w)  # the default gate
+    with pytest.raises(ValueError, match="gate is 'none'"):
+        ssd.gated_norm_forward(x, w, z=x, gate="none")
