@@ -111,9 +111,9 @@ def _sized(nbytes, device):
 
 def _workspace(need, workspace, like, fn):
     """(tensor kept alive, address, bytes) of a workspace of `need` bytes."""
+    if need == 0:
+        return None, None, 0
     if workspace is None:
-        if need == 0:
-            return None, None, 0
         workspace = _sized(need, like.device)
         return workspace, workspace.data_ptr(), need
     if (workspace.dtype != torch.uint8 or workspace.device != like.device

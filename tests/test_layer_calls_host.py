@@ -213,3 +213,14 @@ def test_gate_and_its_values_go_together():
         ssd.gated_norm(x, w)  # the default gate
     with pytest.raises(ValueError, match="gate is 'none'"):
         ssd.gated_norm_forward(x, w, z=x, gate="none")
+
+
+def test_a_workspace_that_is_not_needed_is_not_looked_at(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    x, A, B = far(2, 5, 8), far(8, 4), far(2, 5, 1, 4)
+    assert ssd.selective_scan_workspace_size(x, A, B) == 0
+    room = far(512, dtype=torch.uint8)
+    off = room[-room.data_ptr() % 256 + 16:][:8]
+    with pytest.raises(ValueError, match="current device"):  # what is wrong next
+        ssd.selective_scan_forward(x, x, A, B, B, y=far(2, 5, 8), workspace=off,
+                                   return_final_state=False)
