@@ -12,8 +12,8 @@
  *   between tokens, channels dense.  A slice of a wider projection is passed
  *   as it is.  A view or parameter needs the alignment of its element only;
  *   base addresses and strides that are multiples of 16 bytes run the
- *   vectorised kernels.  Strides are >= 0; an output view must not make two
- *   of its elements share an address.
+ *   vectorised kernels.  Strides are >= 0; an output view whose elements
+ *   share an address is refused.
  * - State tensors (convolution state, h0, final states, their gradients) are
  *   dense.  Parameters and their gradients are dense fp32.
  * - `lengths` (device int32 [batch], NULL = every sequence has seqlen tokens)

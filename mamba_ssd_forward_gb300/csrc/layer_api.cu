@@ -29,6 +29,28 @@ bool req_view(const ssd_seq *s, ssd_dtype t, int64_t b, int64_t L) {
 bool opt_view(const ssd_seq *s, ssd_dtype t, int64_t b, int64_t L) {
   return !has(s) || good(s, t, b, L);
 }
+// Whether no two elements of a view share an address: its b x L rows of `width`
+// elements lie apart.
+bool apart(const ssd_seq *s, int64_t b, int64_t L, int64_t width) {
+  const int64_t bs = s->batch_stride, ts = s->token_stride;
+  if ((b > 1 && bs < width) || (L > 1 && ts < width)) return false;
+  if (b == 1 || L == 1 || bs >= (L - 1) * ts + width || ts >= (b - 1) * bs + width) return true;
+  for (int64_t k = 1; k < b; ++k) {  // sequences k apart against tokens j, j + 1 apart
+    const int64_t j = k * bs / ts, rest = k * bs % ts;
+    if (j >= L) break;
+    if (rest < width || (j + 1 < L && ts - rest < width)) return false;
+  }
+  return true;
+}
+bool req_out(const ssd_seq *s, ssd_dtype t, int64_t b, int64_t L, int64_t width) {
+  return req_view(s, t, b, L) && apart(s, b, L, width);
+}
+bool opt_out(const ssd_seq *s, ssd_dtype t, int64_t b, int64_t L, int64_t width) {
+  return !has(s) || req_out(s, t, b, L, width);
+}
+bool req_token(const ssd_seq *s, ssd_dtype t, int64_t b, int64_t width) {  // one row each
+  return req_view(s, t, b, 0) && apart(s, b, 1, width);
+}
 bool good_ws(const void *ws, size_t have, size_t need) {
   return need == 0 || (ws && natural(ws, 256) && have >= need);
 }
@@ -110,7 +132,7 @@ ssd_status ssd_causal_conv(const ssd_conv_dims *dims, ssd_dtype dtype, const ssd
   ssd::ConvArgs a;
   const ssd_status s = conv_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
-  if (!req_view(x, dtype, a.b, a.L) || !req_view(y, dtype, a.b, a.L) || !req(weight) ||
+  if (!req_view(x, dtype, a.b, a.L) || !req_out(y, dtype, a.b, a.L, a.D) || !req(weight) ||
       !opt(bias) || !opt(state, elem(dtype)) || !opt(lengths) || !opt(final_state, elem(dtype)))
     return SSD_ERR_INVALID_ARG;
   a.x = x, a.y = y, a.weight = weight, a.bias = bias, a.state = state, a.lengths = lengths;
@@ -126,7 +148,7 @@ ssd_status ssd_causal_conv_step(const ssd_conv_dims *dims, ssd_dtype dtype, cons
   ssd::ConvArgs a;
   const ssd_status s = conv_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
-  if (a.L != 1 || !req_view(x, dtype, a.b, 0) || !req_view(y, dtype, a.b, 0) || !req(weight) ||
+  if (a.L != 1 || !req_view(x, dtype, a.b, 0) || !req_token(y, dtype, a.b, a.D) || !req(weight) ||
       !opt(bias) || !req(state, elem(dtype)))
     return SSD_ERR_INVALID_ARG;
   a.x = x, a.y = y, a.weight = weight, a.bias = bias, a.final_state = state;
@@ -150,7 +172,7 @@ ssd_status ssd_causal_conv_backward(const ssd_conv_dims *dims, ssd_dtype dtype, 
   if (s != SSD_OK) return s;
   const size_t e = elem(dtype);
   if (!req_view(x, dtype, a.b, a.L) || !req_view(gy, dtype, a.b, a.L) ||
-      !opt_view(dx, dtype, a.b, a.L) || !req(weight) || !opt(bias) || !opt(state, e) ||
+      !opt_out(dx, dtype, a.b, a.L, a.D) || !req(weight) || !opt(bias) || !opt(state, e) ||
       !opt(gfinal, e) || !opt(lengths) || !opt(dweight) || !opt(dbias) || !opt(dstate, e) ||
       !good_ws(workspace, ws_bytes, ssd::causal_conv_backward_workspace(a, dtype)))
     return SSD_ERR_INVALID_ARG;
@@ -178,7 +200,7 @@ ssd_status ssd_selective_scan(const ssd_scan_dims *dims, ssd_dtype dtype, const 
   const ssd_status s = scan_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
   if (!scan_inputs(&a, dtype, u, dt, A, B, C, D, z, dt_bias) || !opt(h0) || !opt(lengths) ||
-      !req_view(y, dtype, a.b, a.L) || !opt(final_state) ||
+      !req_out(y, dtype, a.b, a.L, a.D) || !opt(final_state) ||
       !good_ws(workspace, ws_bytes, ssd::selective_scan_workspace(a, dtype)))
     return SSD_ERR_INVALID_ARG;
   a.h0 = h0, a.lengths = lengths, a.y = y, a.final_state = final_state;
@@ -196,7 +218,7 @@ ssd_status ssd_selective_scan_step(const ssd_scan_dims *dims, ssd_dtype dtype, c
   const ssd_status s = scan_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
   if (a.L != 1 || !scan_inputs(&a, dtype, u, dt, A, B, C, D, z, dt_bias) || !req(state) ||
-      !req_view(y, dtype, a.b, 0))
+      !req_token(y, dtype, a.b, a.D))
     return SSD_ERR_INVALID_ARG;
   a.y = y, a.final_state = state;
   int *err = ssd::device_error_word();
@@ -223,9 +245,10 @@ ssd_status ssd_selective_scan_backward(
       !req_view(gy, dtype, a.b, a.L) || !opt(gfinal) || !out ||
       !good_ws(workspace, ws_bytes, ssd::selective_scan_backward_workspace(a, dtype)))
     return SSD_ERR_INVALID_ARG;
-  if (!req_view(&out->du, dtype, a.b, a.L) || !req_view(&out->ddt, dtype, a.b, a.L) ||
-      !req_view(&out->dB, dtype, a.b, a.L) || !req_view(&out->dC, dtype, a.b, a.L) ||
-      !opt_view(&out->dz, dtype, a.b, a.L) || (has(&out->dz) && !a.z) || !opt(out->dA) ||
+  if (!req_out(&out->du, dtype, a.b, a.L, a.D) || !req_out(&out->ddt, dtype, a.b, a.L, a.D) ||
+      !req_out(&out->dB, dtype, a.b, a.L, a.G * a.N) ||
+      !req_out(&out->dC, dtype, a.b, a.L, a.G * a.N) ||
+      !opt_out(&out->dz, dtype, a.b, a.L, a.D) || (has(&out->dz) && !a.z) || !opt(out->dA) ||
       !opt(out->dD) || !opt(out->ddt_bias) || !opt(out->dh0))
     return SSD_ERR_INVALID_ARG;
   a.h0 = h0, a.lengths = lengths, a.gy = gy, a.gfinal = gfinal, a.out = out;
@@ -241,7 +264,7 @@ ssd_status ssd_gated_norm(const ssd_norm_dims *dims, ssd_dtype dtype, const ssd_
   ssd::NormArgs a;
   const ssd_status s = norm_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
-  if (!req_view(x, dtype, a.b, a.L) || !req_view(y, dtype, a.b, a.L) || !req(weight) ||
+  if (!req_view(x, dtype, a.b, a.L) || !req_out(y, dtype, a.b, a.L, a.D) || !req(weight) ||
       !opt(bias) || has(z) != (a.gate != SSD_GATE_NONE) || !opt_view(z, dtype, a.b, a.L))
     return SSD_ERR_INVALID_ARG;
   a.x = x, a.y = y, a.z = or_null(z), a.weight = weight, a.bias = bias;
@@ -265,8 +288,8 @@ ssd_status ssd_gated_norm_backward(const ssd_norm_dims *dims, ssd_dtype dtype, c
   if (s != SSD_OK) return s;
   const bool gated = a.gate != SSD_GATE_NONE;
   if (!req_view(x, dtype, a.b, a.L) || !req_view(gy, dtype, a.b, a.L) ||
-      !req_view(dx, dtype, a.b, a.L) || !req(weight) || !opt(bias) || has(z) != gated ||
-      !opt_view(z, dtype, a.b, a.L) || has(dz) != gated || !opt_view(dz, dtype, a.b, a.L) ||
+      !req_out(dx, dtype, a.b, a.L, a.D) || !req(weight) || !opt(bias) || has(z) != gated ||
+      !opt_view(z, dtype, a.b, a.L) || has(dz) != gated || !opt_out(dz, dtype, a.b, a.L, a.D) ||
       !opt(dweight) || !opt(dbias) ||
       !good_ws(workspace, ws_bytes, ssd::gated_norm_backward_workspace(a, dtype)))
     return SSD_ERR_INVALID_ARG;

@@ -132,10 +132,29 @@ def _lengths(lengths, b, like):
 
 
 def _out(t, name, shape, dtype, like):
-    """A given output, checked, or a new dense one."""
+    """A given output, whose rows have to lie apart, or a new dense one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.shape == shape and not t.is_contiguous() and not _apart(t):
+        raise ValueError(f"{name}: rows of an output must not share addresses "
+                         f"(strides {t.stride()} for {tuple(shape)})")
     return t
+
+
+def _apart(t):
+    """Whether the rows [.., D] of a view of two or three axes lie apart."""
+    *sizes, D = t.shape
+    steps = [(s, n) for s, n in zip(t.stride(), sizes) if n > 1]
+    if any(s < D for s, _ in steps):
+        return False
+    if len(steps) < 2:
+        return True
+    (s, n), (large, m) = sorted(steps)
+    # rows k large steps apart against those j, j + 1 small ones apart
+    return large >= (n - 1) * s + D or all(
+        k * large // s >= n or (k * large % s >= D and
+                                (k * large // s + 1 >= n or s - k * large % s >= D))
+        for k in range(1, m))
 
 
 class _Last(torch.autograd.Function):

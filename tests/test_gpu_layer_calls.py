@@ -152,3 +152,23 @@ def test_given_workspaces(ssd, dtype, wide):
         assert all(torch.equal(p, q) for p, q in zip(ref, got)), fn
         assert bool((room[need:] == 255).all()), fn
     ssd.device_error()
+
+
+def test_outputs_of_any_order_of_rows(ssd):
+    """Tokens before sequences, and rows of two sequences between each other."""
+    b, L, D = 2, 9, 24
+    a, _, _ = conv_inputs(b, L, D, 4, "bf16", seed=8)
+    s, _, _ = scan_inputs(b, L, D, 16, 1, "bf16", seed=8)
+    n, _ = norm_inputs((b, L), D, "bf16", seed=8)
+    for strides in ((D, b * D), (D, 2 * D), (3 * D, 2 * D), (2 * L * D, 2 * D + 1)):
+        buf = torch.zeros(4 * L * D + 64, dtype=torch.bfloat16, device="cuda")
+        y = buf.as_strided((b, L, D), (*strides, 1))
+        for fn, args in ((ssd.causal_conv_forward, a),
+                         (ssd.selective_scan_forward, dict(s, dt_softplus=True)),
+                         (ssd.gated_norm_forward, n)):
+            ref = fn(**args)
+            got = fn(**args, y=y)
+            if isinstance(ref, tuple):
+                ref, got = ref[0], got[0]
+            assert got is y and torch.equal(got, ref), (fn, strides)
+    ssd.device_error()

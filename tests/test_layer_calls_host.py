@@ -224,3 +224,73 @@ def test_a_workspace_that_is_not_needed_is_not_looked_at(monkeypatch):
     with pytest.raises(ValueError, match="current device"):  # what is wrong next
         ssd.selective_scan_forward(x, x, A, B, B, y=far(2, 5, 8), workspace=off,
                                    return_final_state=False)
+
+
+def test_rows_that_share_addresses():
+    """The rule for two axes of rows against a count of the addresses."""
+    from mamba_ssd_forward_gb300.layer import _apart
+    seen = set()
+    for b in (1, 2, 3, 5):
+        for L in (1, 2, 4):
+            for D in (1, 3):
+                for bs in range(0, 18):
+                    for ts in range(0, 18):
+                        t = torch.empty(200).as_strided((b, L, D), (bs, ts, 1))
+                        all_of = torch.arange(200).as_strided((b, L, D), (bs, ts, 1)).flatten()
+                        want = all_of.unique().numel() == all_of.numel()
+                        assert _apart(t) == want, (b, L, D, bs, ts)
+                        seen.add((want, bs < ts))
+    assert len(seen) == 4
+
+
+def test_outputs_whose_rows_share_addresses_are_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    x, w, tok = far(2, 5, 8), far(8, 4), far(2, 8)
+    A, B = far(8, 4), far(2, 5, 1, 4)
+    for y in (far(5, 8).expand(2, 5, 8), far(2, 1, 8).expand(2, 5, 8), far(1, 8).expand(2, 5, 8),
+              far(100).as_strided((2, 5, 8), (40, 4, 1))):
+        for call in (lambda: ssd.causal_conv_forward(x, w, y=y),
+                     lambda: ssd.selective_scan_forward(x, x, A, B, B, y=y),
+                     lambda: ssd.gated_norm_forward(x, far(8), gate="none", y=y)):
+            with pytest.raises(ValueError, match="y: rows of an output must not share"):
+                call()
+    y = far(8).expand(2, 8)
+    for call in (lambda: ssd.causal_conv_step(tok, w, None, far(2, 3, 8), y=y),
+                 lambda: ssd.selective_scan_step(tok, tok, A, B[:, 0], B[:, 0], None, None, None,
+                                                 far(2, 8, 4), y=y),
+                 lambda: ssd.gated_norm_forward(tok, far(8), gate="none", y=y)):
+        with pytest.raises(ValueError, match="y: rows of an output must not share"):
+            call()
+
+
+def test_the_library_refuses_outputs_whose_rows_share_addresses():
+    """Nothing is launched: every call here has a view that is refused."""
+    from mamba_ssd_forward_gb300 import _abi, build
+    build.build()
+    lib, ok = _abi.load(), 1 << 20
+    b, L, D = 3, 8, 64
+    x = _abi.SsdSeq(ok, L * D, D)
+    conv, one = (_abi.SsdConvDims(b, n, D, 4, 1) for n in (L, 1))
+    scan, scan1 = (_abi.SsdScanDims(b, n, D, 16, 2, 1) for n in (L, 1))
+    norm = _abi.SsdNormDims(b, L, D, 2, 1e-5, 1, 0)
+    ins, big = [x, x, ok, x, x, None, None, None], 1 << 40
+    # (batch, token) strides: repeated sequences or tokens, rows half apart, a
+    # sequence on another's last rows, one token of one sequence on another's
+    for bs, ts in ((0, D), (L * D, 0), (L * D, D - 1), (L * D - 1, D), (D, 2 * D), (3 * D, 2 * D)):
+        y = _abi.SsdSeq(ok, bs, ts)
+        assert lib.ssd_causal_conv(conv, 1, x, ok, None, None, None, y, None, None) == 1
+        assert lib.ssd_causal_conv_backward(conv, 1, x, ok, None, None, x, None, None, y, ok,
+                                            None, None, ok, big, None) == 1
+        assert lib.ssd_selective_scan(scan, 1, *ins, None, None, y, None, ok, big, None) == 1
+        for k in ("du", "ddt", "dB", "dC"):
+            v = y if k in ("du", "ddt") else _abi.SsdSeq(ok, bs // 2, ts // 2)  # rows of 32
+            g = _abi.SsdScanGrads(**{**dict(du=x, ddt=x, dB=x, dC=x), k: v})
+            assert lib.ssd_selective_scan_backward(scan, 1, *ins, None, x, None, None, g, ok,
+                                                   big, None) == 1, k
+        assert lib.ssd_gated_norm(norm, 1, x, ok, None, x, y, None) == 1
+        for dx, dz in ((x, y), (y, x)):
+            assert lib.ssd_gated_norm_backward(norm, 1, x, ok, None, x, x, dx, dz, ok, None, ok,
+                                               big, None) == 1
+    y = _abi.SsdSeq(ok, D - 1, 0)
+    assert lib.ssd_causal_conv_step(one, 1, x, ok, None, ok, y, None) == 1
+    assert lib.ssd_selective_scan_step(scan1, 1, *ins, ok, y, None) == 1
