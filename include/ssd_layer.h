@@ -14,6 +14,8 @@
  *   base addresses and strides that are multiples of 16 bytes run the
  *   vectorised kernels.  Strides are >= 0; an output view whose elements
  *   share an address is refused.
+ * - At most 65535 sequences (the norm: 2^31 - 1 tokens in all), 2^31 - 1
+ *   tokens a sequence and 2^24 channels, else SSD_ERR_UNSUPPORTED.
  * - State tensors (convolution state, h0, final states, their gradients) are
  *   dense.  Parameters and their gradients are dense fp32.
  * - `lengths` (device int32 [batch], NULL = every sequence has seqlen tokens)

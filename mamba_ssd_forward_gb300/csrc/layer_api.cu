@@ -7,6 +7,7 @@
 namespace {
 
 constexpr int64_t kMaxTokens = 0x7fffffffLL;  // tokens index grids in 31 bits
+constexpr int64_t kMaxBatch = 65535;          // sequences index a grid's second dimension
 constexpr double kBig = 4.0e18;               // element counts stay within 62 bits
 
 bool valid_dtype(ssd_dtype t) { return t == SSD_F32 || t == SSD_BF16; }
@@ -56,9 +57,9 @@ bool good_ws(const void *ws, size_t have, size_t need) {
 }
 const ssd_seq *or_null(const ssd_seq *s) { return has(s) ? s : nullptr; }
 
-ssd_status common_dims(int64_t b, int64_t L, int64_t D) {
+ssd_status common_dims(int64_t b, int64_t L, int64_t D, int64_t most = kMaxBatch) {
   if (b < 1 || L < 1 || D < 1) return SSD_ERR_INVALID_ARG;
-  if (b > 65535 || L > kMaxTokens || D > (1 << 24)) return SSD_ERR_UNSUPPORTED;
+  if (b > most || L > kMaxTokens || D > (1 << 24)) return SSD_ERR_UNSUPPORTED;
   if ((double)b * L * D > kBig / 8) return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
@@ -96,7 +97,7 @@ ssd_status norm_args(const ssd_norm_dims *d, ssd_dtype t, ssd::NormArgs *a) {
   if (!d || !valid_dtype(t) || d->ngroups < 1 || !(d->eps > 0.f) || !std::isfinite(d->eps) ||
       d->gate < SSD_GATE_NONE || d->gate > SSD_GATE_OUTPUT || (d->center != 0 && d->center != 1))
     return SSD_ERR_INVALID_ARG;
-  const ssd_status s = common_dims(d->batch, d->seqlen, d->channels);
+  const ssd_status s = common_dims(d->batch, d->seqlen, d->channels, kMaxTokens);
   if (s != SSD_OK) return s;
   if (d->channels % d->ngroups) return SSD_ERR_INVALID_ARG;
   if (d->channels / d->ngroups > 65536 || d->ngroups > 65535 ||

@@ -172,3 +172,25 @@ def test_outputs_of_any_order_of_rows(ssd):
                 ref, got = ref[0], got[0]
             assert got is y and torch.equal(got, ref), (fn, strides)
     ssd.device_error()
+
+
+# channels of a group that a block's registers hold, and that they do not
+@pytest.mark.parametrize("D", [8, 4104])
+def test_norm_of_many_sequences(ssd, D):
+    """More sequences than a grid's second dimension: as one sequence of all
+    their tokens."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    b, L = 65537, 2
+    x, z, gy = (torch.randn(b, L, D, generator=g, device="cuda") for _ in range(3))
+    w = 1.0 + 0.2 * torch.randn(D, generator=g, device="cuda")
+    flat = [t.view(1, b * L, D) for t in (x, z, gy)]
+    y = ssd.gated_norm_forward(x, w, z=z)
+    assert torch.equal(y.view(1, b * L, D), ssd.gated_norm_forward(flat[0], w, z=flat[1]))
+    last = ssd.gated_norm_forward(x[-1], w, z=z[-1])
+    assert torch.equal(y[-1], last)
+    got = ssd.gated_norm_backward(x, w, z=z, gy=gy)
+    ref = ssd.gated_norm_backward(flat[0], w, z=flat[1], gy=flat[2])
+    for k in ("dx", "dz", "dweight"):
+        assert torch.equal(got[k].flatten(), ref[k].flatten()), k
+    ssd.device_error()

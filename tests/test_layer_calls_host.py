@@ -294,3 +294,17 @@ def test_the_library_refuses_outputs_whose_rows_share_addresses():
     y = _abi.SsdSeq(ok, D - 1, 0)
     assert lib.ssd_causal_conv_step(one, 1, x, ok, None, ok, y, None) == 1
     assert lib.ssd_selective_scan_step(scan1, 1, *ins, ok, y, None) == 1
+
+
+def test_norm_takes_as_many_sequences_as_tokens():
+    from mamba_ssd_forward_gb300 import _abi, build
+    build.build()
+    lib = _abi.load()
+
+    def need(b, L):
+        d = _abi.SsdNormDims(b, L, 64, 2, 1e-5, 1, 0)
+        return lib.ssd_gated_norm_backward_workspace_size(d, 1)
+
+    assert need(1 << 17, 3) == need(1, 3 << 17) > 0
+    assert need(65536, 1) > 0 and need((1 << 31) - 1, 1) > 0
+    assert need(1 << 16, 1 << 15) == 0  # 2^31 tokens
