@@ -28,7 +28,9 @@
  *   output is rounded once.  Sums over tokens, channels or sequences are
  *   taken in an order that depends on the sizes only: repeated calls give
  *   the same bits.
- * - Outputs must not overlap inputs unless said otherwise.
+ * - Outputs must not overlap inputs, nor one another, unless said otherwise.
+ *   (Refused where it is cheap to see: y at x's address in ssd_causal_conv,
+ *   final_state at h0's in ssd_selective_scan.)
  * - A workspace (>= the matching *_workspace_size bytes, 256-byte aligned)
  *   needs no initialisation: each call writes what it reads there.  Every
  *   call reports to the library-wide error word (ssd_device_error).

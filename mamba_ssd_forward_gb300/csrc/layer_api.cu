@@ -134,7 +134,8 @@ ssd_status ssd_causal_conv(const ssd_conv_dims *dims, ssd_dtype dtype, const ssd
   const ssd_status s = conv_args(dims, dtype, &a);
   if (s != SSD_OK) return s;
   if (!req_view(x, dtype, a.b, a.L) || !req_out(y, dtype, a.b, a.L, a.D) || !req(weight) ||
-      !opt(bias) || !opt(state, elem(dtype)) || !opt(lengths) || !opt(final_state, elem(dtype)))
+      !opt(bias) || !opt(state, elem(dtype)) || !opt(lengths) || !opt(final_state, elem(dtype)) ||
+      x->data == y->data)  // a run reads the tokens in front of it, which are another's
     return SSD_ERR_INVALID_ARG;
   a.x = x, a.y = y, a.weight = weight, a.bias = bias, a.state = state, a.lengths = lengths;
   a.final_state = final_state;
@@ -202,6 +203,7 @@ ssd_status ssd_selective_scan(const ssd_scan_dims *dims, ssd_dtype dtype, const 
   if (s != SSD_OK) return s;
   if (!scan_inputs(&a, dtype, u, dt, A, B, C, D, z, dt_bias) || !opt(h0) || !opt(lengths) ||
       !req_out(y, dtype, a.b, a.L, a.D) || !opt(final_state) ||
+      (h0 && final_state == h0) ||  // every segment of a sequence starts from h0
       !good_ws(workspace, ws_bytes, ssd::selective_scan_workspace(a, dtype)))
     return SSD_ERR_INVALID_ARG;
   a.h0 = h0, a.lengths = lengths, a.y = y, a.final_state = final_state;

@@ -141,6 +141,13 @@ def _out(t, name, shape, dtype, like):
     return t
 
 
+def _separate(out, name, source, source_name):
+    """Refuses an output given in the memory of an input that other threads
+    still read."""
+    if out is not None and source is not None and out.data_ptr() == source.data_ptr():
+        raise ValueError(f"{name} must not be the memory of {source_name}")
+
+
 def _apart(t):
     """Whether the rows [.., D] of a view of two or three axes lie apart."""
     *sizes, D = t.shape
@@ -222,8 +229,9 @@ def causal_conv_forward(x, weight, bias=None, state=None, lengths=None, activati
     x [b, L, D] and state [b, W - 1, D] (the inputs before the first token,
     oldest first; None = zeros) in the I/O type, weight [D, W] and bias [D]
     float32.  final_state holds the last W - 1 inputs, for a later call or
-    causal_conv_step."""
+    causal_conv_step.  y must not be x."""
     d = _conv_dims(x, weight, activation)
+    _separate(y, "y", x, "x")
     io, b, L, D, W = _io(x, "x"), d.batch, d.seqlen, d.channels, d.width
     y = _out(y, "y", (b, L, D), x.dtype, x)
     keep = (b, W - 1, D)
@@ -357,8 +365,10 @@ def selective_scan_forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
 
     u, dt, z [b, L, D] and B, C [b, L, G, N] in the I/O type (G groups of
     channels share B and C, N <= 64); A [D, N], D [D], dt_bias [D] and h0
-    [b, D, N] float32.  With z, y is multiplied by silu(z)."""
+    [b, D, N] float32.  With z, y is multiplied by silu(z).  final_state must
+    not be h0."""
     d = _scan_dims(u, A, B, dt_softplus)
+    _separate(final_state, "final_state", h0, "h0")
     lib, b, L, nd = _abi.load(), d.batch, d.seqlen, d.channels
     args = _scan_inputs(d, u, dt, A, B, C, D, z, dt_bias)
     keep = (b, nd, d.dstate)

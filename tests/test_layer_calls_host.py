@@ -308,3 +308,24 @@ def test_norm_takes_as_many_sequences_as_tokens():
     assert need(1 << 17, 3) == need(1, 3 << 17) > 0
     assert need(65536, 1) > 0 and need((1 << 31) - 1, 1) > 0
     assert need(1 << 16, 1 << 15) == 0  # 2^31 tokens
+
+
+def test_outputs_in_memory_that_is_still_read_are_refused(monkeypatch):
+    """Threads of the same launch read the convolution's tokens in front of
+    theirs, and h0 at the start of every segment."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    x, w, h = far(2, 5, 8), far(8, 4), far(2, 8, 4)
+    A, B = far(8, 4), far(2, 5, 1, 4)
+    with pytest.raises(ValueError, match="y must not be the memory of x"):
+        ssd.causal_conv_forward(x, w, y=x)
+    with pytest.raises(ValueError, match="final_state must not be the memory of h0"):
+        ssd.selective_scan_forward(x, x, A, B, B, h0=h, final_state=h, y=far(2, 5, 8))
+    from mamba_ssd_forward_gb300 import _abi, build
+    build.build()
+    lib, ok = _abi.load(), 1 << 20
+    v, y = _abi.SsdSeq(ok, 512, 64), _abi.SsdSeq(2 * ok, 512, 64)
+    conv = _abi.SsdConvDims(2, 8, 64, 4, 1)
+    assert lib.ssd_causal_conv(conv, 1, v, ok, None, None, None, v, None, None) == 1
+    scan = _abi.SsdScanDims(2, 8, 64, 16, 2, 1)
+    assert lib.ssd_selective_scan(scan, 1, v, v, ok, v, v, None, None, None, ok, None, y, ok, ok,
+                                  1 << 40, None) == 1
