@@ -615,7 +615,8 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspac
     eps)) (ssd_clip_grad_norm): in place, or into the tensors of `out`.
 
     Contiguous float32 or bfloat16 tensors of any shapes, mixed; empty ones
-    are skipped.  Nothing waits for the device."""
+    are skipped.  A tensor may be given once only.  Nothing waits for the
+    device."""
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):
@@ -639,6 +640,10 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspac
             dst = o.data_ptr()
         flat += (src, dst, g.numel(), io)
     n = len(grads)
+    if len(set(flat[1::4])) < n:  # empty tensors may share an address
+        written = [at for at, k in zip(flat[1::4], flat[2::4]) if k]
+        if len(set(written)) < len(written):
+            raise ValueError("a tensor is given more than once: it would be scaled twice at once")
     table = (_abi.SsdGrad * n).from_buffer_copy(struct.pack("@" + "PPqi4x" * n, *flat))
     lib = _abi.load()
     norm = torch.empty((), dtype=torch.float32, device=like.device)

@@ -329,3 +329,14 @@ def test_outputs_in_memory_that_is_still_read_are_refused(monkeypatch):
     scan = _abi.SsdScanDims(2, 8, 64, 16, 2, 1)
     assert lib.ssd_selective_scan(scan, 1, v, v, ok, v, v, None, None, None, ok, None, y, ok, ok,
                                   1 << 40, None) == 1
+
+
+def test_a_gradient_given_twice_is_refused():
+    t, e = far(10), far(0)
+    with pytest.raises(ValueError, match="more than once"):
+        ssd.clip_grad_norm([t, far(3), t], 1.0)
+    with pytest.raises(ValueError, match="more than once"):
+        ssd.clip_grad_norm([far(10), far(10)], 1.0, out=[t, t])
+    with pytest.raises(Exception) as other:  # empty ones may be: there is no such device
+        ssd.clip_grad_norm([e, t, e], 1.0)
+    assert "more than once" not in str(other.value)
