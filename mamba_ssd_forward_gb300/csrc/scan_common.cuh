@@ -3,6 +3,7 @@
 // last lanes are kept at zero.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "layer.cuh"
@@ -30,6 +31,13 @@ __device__ __forceinline__ float step_of(float v, bool softplus) {
   q = fmaf(q, t, -0.4999949336051941f);
   q = fmaf(q, t, 0.9999999403953552f);
   return fmaf(t, q, fmaxf(v, 0.f));
+}
+
+// A in units of log2, finite: A = -inf is a decay of zero, but the places that
+// hold no token take steps of zero, and there the decay has to be one.
+__device__ __forceinline__ float log2_decay(float a) {
+  a *= kLog2e;
+  return a < -FLT_MAX ? -FLT_MAX : a;
 }
 
 // The slope of softplus where its value is s: 1 - exp(-s), by its series where

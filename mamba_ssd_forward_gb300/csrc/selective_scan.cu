@@ -124,7 +124,7 @@ scan_kernel(In<IO> in, Cut cut, SeqView<IO> y, float *__restrict__ final_state,
   for (int i = 0; i < NPT / 2; ++i) {
     const int n = n0 + 2 * i;
     const float *row = in.A + d * N;
-    A[i] = pack(n < N ? row[n] * kLog2e : 0.f, n + 1 < N ? row[n + 1] * kLog2e : 0.f);
+    A[i] = pack(n < N ? log2_decay(row[n]) : 0.f, n + 1 < N ? log2_decay(row[n + 1]) : 0.f);
     h[i] = 0;
     if (OUT && in.h0) {
       row = in.h0 + (b * in.D + d) * N;

@@ -237,12 +237,18 @@ __device__ __forceinline__ void fill(const In<IO> &in, const Raw<IO, NL> &raw, S
   }
 }
 
-// A lane's pairs of a parameter or state row-major over [channels][N].
+// A lane's pairs of a state row-major over [channels][N], and of A.
 __device__ __forceinline__ pair load_pair(const float *p, int64_t d, int c, int live, int n,
-                                          int N, float scale = 1.f) {
+                                          int N) {
   if (n >= N) return 0;
-  return pack(c < live ? p[(d + c) * N + n] * scale : 0.f,
-              c + 1 < live ? p[(d + c + 1) * N + n] * scale : 0.f);
+  return pack(c < live ? p[(d + c) * N + n] : 0.f,
+              c + 1 < live ? p[(d + c + 1) * N + n] : 0.f);
+}
+__device__ __forceinline__ pair load_decays(const float *A, int64_t d, int c, int live, int n,
+                                            int N) {
+  float a, b;
+  unpack(load_pair(A, d, c, live, n, N), a, b);
+  return pack(log2_decay(a), log2_decay(b));
 }
 
 // Two pairs (four channels) of a row of a Stage array; four values, each
@@ -277,7 +283,7 @@ ends_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, bool word
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      A[i][p] = load_pair(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, in.N, kLog2e);
+      A[i][p] = load_decays(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, in.N);
       P[i][p] = both(1.f);
       R[i][p] = 0;
     }
@@ -365,7 +371,7 @@ chain_kernel(const float *__restrict__ A, const float *__restrict__ h0,
   const int live = min(Ge::CW, per_group - tile * Ge::CW);
   if (!SSD_IN_BOUNDS(b < nb && c0 + live <= D, err, 78)) return;
   const int c = cg * 4 + ip % 2 * 2, n = nl * 4 + ip / 2;
-  const pair a = load_pair(A, c0, c, live, n, N, kLog2e);
+  const pair a = load_decays(A, c0, c, live, n, N);
   // x = exp(A sum) x + end over `count` entries, in order or backwards; each
   // entry is replaced by the x that arrives there
   auto chain = [&](pair x, pair *v, const float *sum, int64_t count, bool back) {
@@ -453,7 +459,7 @@ adjoint_kernel(In<IO> in, SeqView<const IO> gy, Parts parts, Buffers buf, Out<IO
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      A[i][p] = load_pair(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, N, kLog2e);
+      A[i][p] = load_decays(in.A, c0, cg * 4 + p * 2, live, nl * 4 + i, N);
       q[i][p] = reinterpret_cast<const pair *>(buf.adj)[(mine * 8 + i * 2 + p) * 32 + lane];
       dA[i][p] = 0;
     }

@@ -46,7 +46,7 @@ step_kernel(In<IO> in, SeqView<IO> y, float *__restrict__ state, int *err) {
   four(in.A + d * N, A);
   const float bias = in.dt_bias ? in.dt_bias[d] : 0.f, skip = in.Dskip ? in.Dskip[d] : 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+  for (int i = 0; i < 4; ++i) A[i] = log2_decay(A[i]);
 #pragma unroll
   for (int q = 0; q < SEQS; ++q) {
     const int64_t b = b0 + q;

@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from layer_cases import conv_inputs, norm_inputs, scan_inputs
+from layer_cases import conv_inputs, lengths_of, norm_inputs, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -193,4 +193,34 @@ def test_norm_of_many_sequences(ssd, D):
     ref = ssd.gated_norm_backward(flat[0], w, z=flat[1], gy=flat[2])
     for k in ("dx", "dz", "dweight"):
         assert torch.equal(got[k].flatten(), ref[k].flatten()), k
+    ssd.device_error()
+
+
+# within a tile, over several, cut into segments, with sequences that end early
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("b,L,D,N,lengths", [(1, 5, 40, 16, None), (2, 70, 33, 5, [70, 41]),
+                                             (2, 700, 64, 16, [700, 333]),
+                                             (3, 40, 8, 40, [40, 0, 1])])
+def test_states_that_are_forgotten_at_once(ssd, b, L, D, N, lengths, dtype):
+    """A = -inf is a decay of zero: as a finite A that is as steep, also where
+    the places after a sequence's end hold steps of zero."""
+    s, gy, gfinal = scan_inputs(b, L, D, N, 1, dtype, seed=L)
+    steep, none = (s["A"].clone() for _ in range(2))
+    some = torch.rand(D, N, device="cuda") < 0.3
+    some[0, 0], some[-1, -1] = True, True
+    steep[some], none[some] = -1e30, -float("inf")
+    n = lengths_of(lengths)
+
+    def everything(A):
+        a = {**s, "A": A}
+        out = list(ssd.selective_scan_forward(**a, lengths=n, dt_softplus=True))
+        out += ssd.selective_scan_backward(**a, gy=gy, gfinal=gfinal, lengths=n,
+                                           dt_softplus=True).values()
+        state = s["h0"].clone()
+        at = {k: v[:, 0] if k in ("u", "dt", "B", "C", "z") else v for k, v in a.items()}
+        del at["h0"]
+        return out + [ssd.selective_scan_step(**at, state=state, dt_softplus=True), state]
+
+    for i, (p, q) in enumerate(zip(everything(steep), everything(none))):
+        assert torch.isfinite(p).all() and torch.equal(p, q), i
     ssd.device_error()
