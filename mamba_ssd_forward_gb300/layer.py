@@ -625,17 +625,20 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspac
         raise ValueError("no gradients given")
     like = grads[0]
     dev, flat = like.get_device(), []
-    for i, (g, o) in enumerate(zip(grads, out)):
+    if dev < 0:
+        _io(like, "grads[0]")
+        _refuse(like, "grads[0]", like.shape, like.dtype, like)
+    for g, o in zip(grads, out):
         io = _IO.get(g.dtype)
-        if io is None or dev < 0 or g.get_device() != dev or not g.is_contiguous():
+        if io is None or g.get_device() != dev or not g.is_contiguous():
+            i = next(i for i, t in enumerate(grads) if t is g)
             _io(g, f"grads[{i}]")
             _refuse(g, f"grads[{i}]", g.shape, g.dtype, like)
-        src = g.data_ptr()
-        if o is g:
-            dst = src
-        else:
+        src = dst = g.data_ptr()
+        if o is not g:
             if (o.dtype is not g.dtype or o.get_device() != dev or not o.is_contiguous()
                     or o.shape != g.shape):
+                i = next(i for i, t in enumerate(out) if t is o)
                 _refuse(o, f"out[{i}]", g.shape, g.dtype, like)
             dst = o.data_ptr()
         flat += (src, dst, g.numel(), io)
