@@ -4,8 +4,10 @@
 //   v = n weight + bias;  y = v silu(z) or v
 //
 // A bandwidth kernel: x and z read once, y written once.  The product x silu(z)
-// is rounded by itself (no fused multiply-add with the mean), so r - mean(r)
-// is exactly zero where all of a group's r are equal.
+// is rounded by itself (no fused multiply-add with the mean), so that the r in
+// r - mean(r) is the r that the mean was taken of: of a group of one channel
+// the difference is exactly zero, where 1 / sqrt(eps) would enlarge a rounding.
+// Of a group of equal r it is the rounding of their mean, a few ulp of r.
 #include <type_traits>
 
 #include "layer.cuh"
@@ -190,12 +192,15 @@ norm_grad_kernel(SeqView<const IO> x, const float *__restrict__ weight,
 // The kernels below read memory once.  A team of threads (a warp, or a whole
 // block for a group of more than 32 K V channels) takes one group of one token
 // at a time, K vectors of V channels to a thread, and walks the tokens with a
-// fixed stride: the weights are read once a team, dweight and dbias stay in
-// registers.  Vectors of 16 bytes come kStages - 1 tokens ahead through shared
+// fixed stride: dweight and dbias stay in registers, the weights come from L1
+// at every token (held, they would cost as many registers).  Vectors of 16 bytes come kStages - 1 tokens ahead through shared
 // memory, each thread copying its own, so no barrier waits for memory.
 // Measured, bf16 and gated: 8192 x 5120 in 47 us (252 MB, 5.4 TB/s), the
-// gradients of 8192 x 4096 in 8 groups in 66 (336 MB, 5.1 TB/s).  At odd offsets
-// 8192 x 2003 takes 42 us and its gradients 77 (51 at 2000 channels).
+// gradients of 8192 x 4096 in 8 groups in 68 (336 MB, 4.9 TB/s).  At odd offsets
+// 8192 x 2003 takes 42 us and its gradients 74 (50 at 2000 channels).  Wider
+// groups (above 8192 channels; above 4096 in fp32, or where vectors of 16 bytes
+// do not fit) take the kernels above, which read memory twice: the gradients of
+// 4096 x 5120 in fp32 132 us, of 4096 x 4096 66.
 
 // V elements as the memory holds them.
 template <typename IO, int V>
@@ -610,11 +615,9 @@ int vector_of(const NormArgs &a, ssd_dtype io) {
   };
   return fits(16 / e) ? (int)(16 / e) : fits(2) ? 2 : 1;
 }
-// Vectors per thread: up to 16 channels (8 of fp32, whose registers are twice
-// as many; 8 single ones in the gradients).
-constexpr int vectors_per_thread(int V, bool back) {
-  return V == 8 || V == 4 ? 2 : V == 2 ? 4 : 8;
-}
+// Vectors per thread: 16 channels where they come eight at a time (bf16), 8 of
+// any other (fp32's registers are twice as many).
+constexpr int vectors_per_thread(int V) { return V == 8 || V == 4 ? 2 : V == 2 ? 4 : 8; }
 
 // Shared memory of a block of `block` threads for T tensors' vectors ahead.
 constexpr int ahead_bytes(int V, size_t elem, int K, int T, int block) {
@@ -629,8 +632,8 @@ cudaError_t allow_smem(F kernel, int bytes) {
 }
 
 // The team for a group, or 0 threads where a block's registers do not hold it.
-int team_threads(const NormArgs &a, ssd_dtype io, bool back) {
-  const int V = vector_of(a, io), per = V * vectors_per_thread(V, back);
+int team_threads(const NormArgs &a, ssd_dtype io) {
+  const int V = vector_of(a, io), per = V * vectors_per_thread(V);
   const int64_t n = (a.D / a.G + per - 1) / per;
   return n > kMaxTeam ? 0 : (int)((n + 31) / 32 * 32);
 }
@@ -681,14 +684,14 @@ int64_t slices(const NormArgs &a) { return (a.b * a.L + slice_rows(a) - 1) / sli
 }  // namespace
 
 cudaError_t launch_gated_norm(const NormArgs &a, ssd_dtype io, int *err, cudaStream_t st) {
-  if (const int threads = team_threads(a, io, false)) {
+  if (const int threads = team_threads(a, io)) {
     const Teams tm = teams_of(a, threads, kFwdWarps);
     const int block = threads == 32 ? 256 : threads;
     const int64_t blocks = (tm.strides * a.G * threads + block - 1) / block;
     return dispatch_team(io, vector_of(a, io), a.gate, [&](auto io_c, auto v_c, auto gate_c) {
       using IO = typename decltype(io_c)::type;
       constexpr int V = decltype(v_c)::value;
-      constexpr int K = vectors_per_thread(V, false), gate = decltype(gate_c)::value;
+      constexpr int K = vectors_per_thread(V), gate = decltype(gate_c)::value;
       const auto kernel = norm_team_kernel<IO, V, K, gate>;
       const cudaError_t e = allow_smem(kernel, ahead_bytes(V, sizeof(IO), K, 2, kMaxTeam));
       if (e != cudaSuccess) return e;
@@ -720,7 +723,7 @@ size_t gated_norm_backward_workspace(const NormArgs &a, ssd_dtype io) {
 
 cudaError_t launch_gated_norm_backward(const NormArgs &a, ssd_dtype io, void *ws, int *err,
                                        cudaStream_t st) {
-  if (const int threads = team_threads(a, io, true)) {
+  if (const int threads = team_threads(a, io)) {
     const Teams tm = teams_of(a, threads, kGradWarps);
     float *part_w = static_cast<float *>(ws), *part_b = part_w + tm.strides * a.D;
     const int block = threads == 32 ? 256 : threads;
@@ -728,7 +731,7 @@ cudaError_t launch_gated_norm_backward(const NormArgs &a, ssd_dtype io, void *ws
     const cudaError_t e = dispatch_team(io, vector_of(a, io), a.gate, [&](auto io_c, auto v_c, auto gate_c) {
       using IO = typename decltype(io_c)::type;
       constexpr int V = decltype(v_c)::value;
-      constexpr int K = vectors_per_thread(V, true), gate = decltype(gate_c)::value;
+      constexpr int K = vectors_per_thread(V), gate = decltype(gate_c)::value;
       auto go = [&](auto bias_c) {
         const auto kernel = norm_team_grad_kernel<IO, V, K, gate, decltype(bias_c)::value>;
         const cudaError_t e1 = allow_smem(kernel, ahead_bytes(V, sizeof(IO), K, 3, kMaxTeam));
