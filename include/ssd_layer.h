@@ -26,8 +26,9 @@
  *   a sequence without one).
  * - Arithmetic, states and sums are fp32 with either I/O type; an SSD_BF16
  *   output is rounded once.  Sums over tokens, channels or sequences are
- *   taken in an order that depends on the sizes only: repeated calls give
- *   the same bits.
+ *   taken in a fixed order: calls of equal sizes, types, strides and
+ *   alignments of the addresses on the same kind of device give the same
+ *   bits.  (Aligned and unaligned views may differ in theirs.)
  * - Outputs must not overlap inputs, nor one another, unless said otherwise.
  *   (Refused where it is cheap to see: y at x's address in ssd_causal_conv,
  *   final_state at h0's in ssd_selective_scan.)
@@ -216,7 +217,8 @@ SSD_API size_t ssd_clip_grad_norm_workspace_size(const ssd_grad *grads, int n_gr
 /* norm = sqrt(sum over every tensor and element of g^2), written to *norm
  * (device f32); dst = src * min(1, max_norm / (norm + eps)).  A norm that is
  * not a number makes every output not a number; an infinite one makes finite
- * elements zero.  `grads` is a host array, read before the call returns.
+ * elements zero (not numbers, where max_norm is infinite too).  `grads` is a
+ * host array, read before the call returns; no two dst may overlap.
  * max_norm >= 0, eps >= 0 with max_norm finite or +infinity.  Squares are
  * summed in fp32: an element beyond 1.8e19 makes the norm infinite. */
 SSD_API ssd_status ssd_clip_grad_norm(const ssd_grad *grads, int n_grads, float max_norm,

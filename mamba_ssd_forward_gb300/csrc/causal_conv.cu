@@ -8,8 +8,8 @@
 // tokens in front of each run (which the neighbouring run brought into L2).
 // Tokens come by asynchronous copies through a ring of the thread's own in
 // shared memory, which keeps eight rows in flight without their registers.
-// Measured at W = 4: 2 x 4096 x 5376 in bf16 in 35 us (5.1 TB/s; 26 us at the
-// copy bandwidth), the gradients of 4 x 2048 x 1792 in fp32 in 39 (the same
+// Measured at W = 4: 2 x 4096 x 5376 in bf16 in 35 us (5.0 TB/s; 26 us at the
+// copy bandwidth), the gradients of 4 x 2048 x 1792 in fp32 in 41 (the same
 // bytes).  Half of the issue slots are taken, and warps wait for rows the rest.
 #include <type_traits>
 
@@ -106,9 +106,9 @@ __device__ __forceinline__ void input_row(const SeqView<const IO> &x, const IO *
     load_vec<V>(state + (b * (W - 1) + (p + W - 1)) * D + c, v);
 }
 
-// Rows on any boundary, a channel to a thread, loads in batches of A rows: 53 us
-// for 8192 bf16 tokens of 5376 channels at odd offsets, against 40 of the ring
-// kernel on aligned ones (in runs of 32 tokens 55; A = 4 67, A = 16 56).
+// Rows on any boundary, a channel to a thread, loads in batches of A rows: 48 us
+// for 8192 bf16 tokens of 5376 channels at odd offsets, against 33 of the ring
+// kernel on aligned ones (A was chosen at 53 us: A = 4 67, A = 16 56).
 template <typename IO, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_kernel(SeqView<const IO> x, const float *__restrict__ weight, const float *__restrict__ bias,

@@ -15,8 +15,8 @@
 // the states; it needs no barrier but its own.
 //
 // Measured (bf16, 16 states, GB300): 16 sequences of 512 tokens and 5120
-// channels, uncut: 247 us, 2.7e12 (token, channel, state) a second; two of
-// 2048 tokens, in five segments: 177 us; 16384 tokens of 1536 channels: 208 us.
+// channels, uncut: 248 us, 2.7e12 (token, channel, state) a second; two of
+// 2048 tokens, in five segments: 176 us; 16384 tokens of 1536 channels: 205 us.
 // A pair multiply-add with three register operands takes three cycles of a
 // scheduler, so the body is 107 cycles a token and warp where nothing stalls.
 //
@@ -33,7 +33,9 @@ namespace {
 using namespace scan;
 
 constexpr int kWarps = 4;  // independent warps per block
-constexpr int kBlocks = 3;  // per SM; four blocks of 128 registers ran slower (218 us against 194)
+// Per SM.  Four blocks of 128 registers ran slower when that was measured (218 us
+// where three took 194; with what followed three take 176).
+constexpr int kBlocks = 3;
 constexpr int kTile = 8;    // tokens staged at a time
 
 // A warp's part of the work: sequence, group, channel tile, segment.  The
@@ -45,8 +47,8 @@ struct Cut {
 
 // A warp's copies of kTile tokens' rows of one view into COLS columns of
 // shared memory.  VEC: 16 bytes at a time, the lanes taking turns over the
-// pieces of the rows; else element by element (2 x 2048 x 1536, N = 16: 64.6 us
-// against 77 in fp32 and 89 in bf16, whose elements cannot be copied asynchronously).
+// pieces of the rows; else element by element (2 x 2048 x 1536, N = 16: 64 to 66 us
+// against 78 in fp32 and 87 in bf16, whose elements cannot be copied asynchronously).
 template <typename IO, int COLS, bool VEC>
 struct RowCopy {
   static constexpr int kPer = 16 / (int)sizeof(IO), kPieces = COLS >= kPer ? COLS / kPer : 1;

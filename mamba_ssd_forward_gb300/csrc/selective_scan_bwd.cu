@@ -23,8 +23,8 @@
 // arithmetic: 3.75 exponentials and some 25 multiply-adds per (token, channel,
 // state) against 46 bytes per (token, channel).
 //
-// Measured, bf16, 4 sequences of 1024 tokens, 2048 channels of 16 states: 294
-// us in all; ends 59, chain 15, adjoint 202, the sums 21.  A segment's inputs
+// Measured, bf16, 4 sequences of 1024 tokens, 2048 channels of 16 states: 297
+// us in all; ends 59, chain 14, adjoint 202, the sums 21.  A segment's inputs
 // are copied to shared memory while the one before is worked on (405 -> 366).
 #include "scan_common.cuh"
 
@@ -812,7 +812,7 @@ cudaError_t launch_selective_scan_backward(const ScanArgs &a, ssd_dtype io, void
       return cudaGetLastError();
     };
     // 16-byte pieces of rows in and vectors of four out, or any rows (N = 16,
-    // 2 x 1024 x 1536: 142 us, at odd offsets 185 in bf16 and 222 in fp32)
+    // 2 x 1024 x 1536: 138 us in bf16 and 166 in fp32, at odd offsets 181 and 209)
     cudaError_t e =
         piece == 16 && whole_fours(a, io) ? run(std::true_type{}) : run(std::false_type{});
     if (e != cudaSuccess) return e;
