@@ -10,7 +10,9 @@ Tensor layouts (all contiguous, on the current CUDA device):
     A [nh], D [nh], h0 [b, nh, P, S]                   -- float32
 
 The operators around the scan in a layer (causal_conv*, selective_scan*,
-gated_norm*, clip_grad_norm) are in layer.py and exported here.
+gated_norm*, clip_grad_norm) are in layer.py and exported here, those around
+the blocks of a language model (add_norm*, linear_cross_entropy*,
+orthogonalize) are in model.py.
 """
 from __future__ import annotations
 
@@ -40,6 +42,21 @@ from .layer import (  # noqa: F401
     selective_scan_step,
     selective_scan_workspace_size,
 )
+from .model import (  # noqa: F401
+    ORTH_COEFFICIENTS,
+    add_norm,
+    add_norm_backward,
+    add_norm_backward_workspace_size,
+    add_norm_forward,
+    add_norm_quantized,
+    linear_cross_entropy,
+    linear_cross_entropy_backward,
+    linear_cross_entropy_backward_workspace_size,
+    linear_cross_entropy_forward,
+    linear_cross_entropy_workspace_size,
+    orthogonalize,
+    orthogonalize_workspace_size,
+)
 
 __all__ = ["forward", "chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
            "decode_step", "workspace_size", "new_workspace", "workspace_error", "dims_of",
@@ -50,6 +67,12 @@ __all__ = ["forward", "chunk_cumsum", "chunk_state", "state_passing", "chunk_sca
            "gated_norm", "gated_norm_forward", "gated_norm_backward", "clip_grad_norm",
            "causal_conv_backward_workspace_size", "selective_scan_backward_workspace_size",
            "gated_norm_backward_workspace_size", "clip_grad_norm_workspace_size",
+           "add_norm", "add_norm_forward", "add_norm_quantized", "add_norm_backward",
+           "add_norm_backward_workspace_size",
+           "linear_cross_entropy", "linear_cross_entropy_forward",
+           "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
+           "linear_cross_entropy_backward_workspace_size",
+           "orthogonalize", "orthogonalize_workspace_size", "ORTH_COEFFICIENTS",
            "SsdError"]
 
 

@@ -61,10 +61,21 @@ EXPORTS = (
     "ssd_gated_norm_backward",
     "ssd_clip_grad_norm_workspace_size",
     "ssd_clip_grad_norm",
+    "ssd_add_norm",
+    "ssd_add_norm_quantized",
+    "ssd_add_norm_backward_workspace_size",
+    "ssd_add_norm_backward",
+    "ssd_linear_cross_entropy_workspace_size",
+    "ssd_linear_cross_entropy",
+    "ssd_linear_cross_entropy_backward_workspace_size",
+    "ssd_linear_cross_entropy_backward",
+    "ssd_orthogonalize_workspace_size",
+    "ssd_orthogonalize",
 )
 
 SSD_ACT_NONE, SSD_ACT_SILU = 0, 1
 SSD_GATE_NONE, SSD_GATE_INPUT, SSD_GATE_OUTPUT = 0, 1, 2
+SSD_REDUCE_NONE, SSD_REDUCE_SUM, SSD_REDUCE_MEAN = 0, 1, 2
 
 
 class SsdDims(ctypes.Structure):
@@ -109,6 +120,22 @@ class SsdNormDims(ctypes.Structure):
 class SsdGrad(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
+
+
+class SsdAddNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels")] + \
+        [("eps", ctypes.c_float)]
+
+
+class SsdLossDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "channels", "vocab", "ignore_index")] + \
+        [("reduction", ctypes.c_int32)]
+
+
+class SsdOrthDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("count", "rows", "cols")] + \
+        [("steps", ctypes.c_int32)] + [(n, ctypes.c_float) for n in ("a", "b", "c", "eps")]
 
 
 class SsdError(RuntimeError):
@@ -186,7 +213,8 @@ def load(path: str | None = None):
                                           [sz, vp, vp, i32, ctypes.POINTER(ctypes.c_int)])
     P = ctypes.POINTER
     seq, conv, scan, norm = P(SsdSeq), P(SsdConvDims), P(SsdScanDims), P(SsdNormDims)
-    f32 = ctypes.c_float
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    add, loss, orth = P(SsdAddNormDims), P(SsdLossDims), P(SsdOrthDims)
     for name, res, args in (
             ("ssd_causal_conv", i32, [conv, i32, seq, vp, vp, vp, vp, seq, vp, vp]),
             ("ssd_causal_conv_backward_workspace_size", sz, [conv, i32]),
@@ -207,7 +235,21 @@ def load(path: str | None = None):
             ("ssd_gated_norm_backward", i32,
              [norm, i32, seq, vp, vp, seq, seq, seq, seq, vp, vp, vp, sz, vp]),
             ("ssd_clip_grad_norm_workspace_size", sz, [P(SsdGrad), i32]),
-            ("ssd_clip_grad_norm", i32, [P(SsdGrad), i32, f32, f32, vp, vp, sz, vp])):
+            ("ssd_clip_grad_norm", i32, [P(SsdGrad), i32, f32, f32, vp, vp, sz, vp]),
+            ("ssd_add_norm", i32, [add, i32, i32, seq, seq, vp, seq, seq, vp]),
+            ("ssd_add_norm_quantized", i32,
+             [add, i32, i32, i64, seq, seq, vp, seq, vp, seq, vp]),
+            ("ssd_add_norm_backward_workspace_size", sz, [add, i32, i32]),
+            ("ssd_add_norm_backward", i32,
+             [add, i32, i32, seq, vp, seq, seq, seq, seq, vp, vp, sz, vp]),
+            ("ssd_linear_cross_entropy_workspace_size", sz, [loss, i32, seq]),
+            ("ssd_linear_cross_entropy", i32,
+             [loss, i32, seq, seq, vp, vp, vp, vp, vp, sz, vp]),
+            ("ssd_linear_cross_entropy_backward_workspace_size", sz, [loss, i32, seq]),
+            ("ssd_linear_cross_entropy_backward", i32,
+             [loss, i32, seq, seq, vp, vp, vp, seq, vp, vp, sz, vp]),
+            ("ssd_orthogonalize_workspace_size", sz, [orth, i32, i32]),
+            ("ssd_orthogonalize", i32, [orth, i32, i32, seq, seq, vp, sz, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     if path is None:

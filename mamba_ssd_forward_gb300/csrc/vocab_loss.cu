@@ -1,0 +1,686 @@
+// Softmax cross entropy of hidden states against a large vocabulary, without
+// its logits in memory:
+//   z = x W^T,  lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_i,target
+//   dz = (exp(z - lse) - onehot) g,  dx = dz W,  dW = dz^T x
+//
+// Forward: one product (gemm.cuh) whose epilogue keeps, for each row and run of
+// columns, the largest logit and the sum of exponentials about it; a second
+// launch joins the runs.  Backward: in pieces of the vocabulary the logits are
+// computed again, their epilogue writes the piece of dz, and one launch adds its
+// shares of dx and computes its rows of dW.  Bound by the tensor cores: 2 n V d
+// operations forward, 6 n V d backward.
+//
+// Tokens without a target are left out before the products: the others' rows of
+// x are packed together (so whatever the left out rows hold reaches nothing),
+// their number stays on the device.
+//
+// bf16: the logits are exact products with fp32 sums.  dz is rounded once to
+// bf16, as the operand of both gradient products (2^-9 of each term, as far off
+// as the gradients' own rounding); a factor common to all tokens is applied to
+// the fp32 sums instead.  fp32: x, W and dz are split into two fp16 planes after
+// scaling by powers of two that take the largest value to 2^14..2^15 (values
+// below 2^-28 of the largest keep 2^-39 of it), three products each.
+#include <cmath>
+
+#include "gemm.cuh"
+#include "model.cuh"
+
+namespace ssd {
+namespace {
+
+using gemm::Product;
+using gemm::Tile;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBN = 256;
+constexpr int kRun = kBN / 2;  // columns of one epilogue warp: a run of the statistics
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// ------------------------------------------------- largest values, and scales
+
+// The power of two that takes values of the size of `top` (a float's bits) to
+// 2^14 .. 2^15; 1 for zero, infinity and NaN.  Held within 2^62 both ways.
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  if (top == 0 || top >= 0x7f800000u) return 1.f;
+  int e = (int)(top >> 23) - 127;
+  e = e < -48 ? -48 : e > 76 ? 76 : e;
+  return __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+}
+__device__ __forceinline__ float inverse_of(float pow2) {
+  return __uint_as_float((254u << 23) - __float_as_uint(pow2));
+}
+
+enum Top { kTopX, kTopW, kTopG, kTops };
+
+__device__ __forceinline__ bool counted(int64_t target, int64_t ignore) { return target != ignore; }
+
+// Bits of the largest |value| (of a NaN: above infinity's) of x's rows with a
+// target, of W, and of the tokens' factors.  The order of the maxima has no say.
+__global__ void __launch_bounds__(256)
+top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t ignore, int64_t L,
+           int64_t n, const float *__restrict__ w, int64_t ws, int64_t V, int64_t d,
+           const float *__restrict__ g, uint32_t *__restrict__ top, int *err) {
+  uint32_t most[kTops] = {0, 0, 0};
+  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
+  const int64_t warps = (int64_t)gridDim.x * blockDim.x / 32;
+  for (int64_t r = warp; r < n + V; r += warps) {
+    if (r < n && !counted(targets[r], ignore)) continue;
+    const float *p = r < n ? x.at(r / L, r % L) : w + (r - n) * ws;
+    uint32_t m = 0;
+    if (!SSD_IN_BOUNDS(r < n + V, err, 70)) continue;
+#pragma unroll 4
+    for (int64_t c = lane; c < d; c += 32) m = max(m, __float_as_uint(p[c]) & 0x7fffffffu);
+    if (r < n) {
+      most[kTopX] = max(most[kTopX], m);
+      if (g) most[kTopG] = max(most[kTopG], __float_as_uint(g[r]) & 0x7fffffffu);
+    } else {
+      most[kTopW] = max(most[kTopW], m);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kTops; ++k) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, most[k]);
+    if (lane == 0 && m) atomicMax(top + k, m);
+  }
+}
+
+// --------------------------------------------------------------- packed rows
+
+// One value in the operand type: bf16 as it is, or the planes of an fp32.
+__device__ __forceinline__ void split(float v, float scale, __half &hi, __half &lo) {
+  const float s = v * scale;
+  hi = __float2half_rn(s);
+  lo = __float2half_rn(s - __half2float(hi));
+}
+// A row of `d` values into its place (and, fp32, into the second plane `ps`
+// elements on).
+__device__ __forceinline__ void pack_row(const __nv_bfloat16 *src, uint16_t *dst, int64_t,
+                                         int64_t d, float, int tid, int threads) {
+  const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
+  const int64_t wide = ((reinterpret_cast<uintptr_t>(src) & 15) == 0) ? d / 8 : 0;
+#pragma unroll 4
+  for (int64_t i = tid; i < wide; i += threads)
+    reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(s)[i];
+  for (int64_t i = 8 * wide + tid; i < d; i += threads) dst[i] = s[i];
+}
+__device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_t ps, int64_t d,
+                                         float scale, int tid, int threads) {
+#pragma unroll 4
+  for (int64_t i = tid; i < d; i += threads) {
+    __half hi, lo;
+    split(src[i], scale, hi, lo);
+    dst[i] = __half_as_ushort(hi);
+    dst[ps + i] = __half_as_ushort(lo);
+  }
+}
+
+// What the later launches know of the rows with a target.
+struct Rows {
+  int *live;       // their number
+  int *token;      // [n] which token each is
+  int *target;     // [n] its target, -1 if that is no word
+  float *zt;       // [n] its target's logit (forward)
+  float *lse, *g;  // [n] (backward)
+};
+
+constexpr int kPackTokens = 32, kPackThreads = 256;
+
+// A block takes kPackTokens tokens.  It counts the targets in front of them
+// itself (they come from L2), so no launch of its own makes the list.
+template <typename IO>
+__global__ void __launch_bounds__(kPackThreads)
+pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
+            int64_t L, int64_t n, int64_t d, const float *__restrict__ lse,
+            const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
+            float *__restrict__ lse_out, Rows rows, uint16_t *__restrict__ xp, int64_t ld,
+            int64_t ps, int planes, const uint32_t *__restrict__ top, int *err) {
+  __shared__ int sums[kPackThreads / 32], place[kPackTokens];
+  const int64_t first = (int64_t)blockIdx.x * kPackTokens;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  int before = 0;
+#pragma unroll 4
+  for (int64_t i = tid; i < first; i += kPackThreads) before += counted(targets[i], ignore);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) sums[warp] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < kPackThreads / 32; ++w) before += sums[w];
+  const int here = (int)(n - first < kPackTokens ? n - first : kPackTokens);
+  if (warp == 0) {
+    const bool mine = lane < here && counted(targets[first + (lane < here ? lane : 0)], ignore);
+    const unsigned all = __ballot_sync(0xffffffffu, mine);
+    place[lane] = mine ? before + __popc(all & ((1u << lane) - 1)) : -1;
+    if (lane == 0) sums[0] = __popc(all);
+    if (lane < here) {
+      const int64_t t = first + lane;
+      if (mine && SSD_IN_BOUNDS(place[lane] < n, err, 71)) {
+        const int64_t word = targets[t];
+        const bool real = word >= 0 && word < V;
+        rows.token[place[lane]] = (int)t;
+        rows.target[place[lane]] = real ? (int)word : -1;
+        if (rows.zt) rows.zt[place[lane]] = __int_as_float(0x7fc00000);  // until a tile writes it
+        if (rows.lse) {
+          rows.lse[place[lane]] = lse[t];
+          rows.g[place[lane]] = !real ? __int_as_float(0x7fc00000) : gloss ? gloss[t] : 1.f;
+        }
+      } else if (!mine) {
+        if (loss) loss[t] = 0.f;
+        if (lse_out) lse_out[t] = 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  const float scale = top ? scale_of(top[kTopX]) : 1.f;
+  for (int i = warp; i < here; i += kPackThreads / 32) {
+    const int64_t t = first + i, b = t / L, at = t % L;
+    if (place[i] >= 0)
+      pack_row(x.at(b, at), xp + (int64_t)place[i] * ld, ps, d, scale, lane, 32);
+    else if (dx.p)
+      for (int64_t c = lane; c < d; c += 32) st_io(dx.at(b, at) + c, 0.f);
+  }
+  if (first + kPackTokens >= n) {
+    const int64_t live = before + sums[0], end = (live + gemm::kTileM - 1) / gemm::kTileM * gemm::kTileM;
+    if (tid == 0) *rows.live = (int)live;
+    // the last tile's other rows are operands too: zero
+    for (int p = 0; p < planes; ++p)
+      for (int64_t i = live * ld + tid; i < end * ld; i += kPackThreads) xp[p * ps + i] = 0;
+  }
+}
+
+// Rows of W for the products, where TMA cannot take them as they are.
+template <typename IO>
+__global__ void __launch_bounds__(256)
+pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d,
+                   uint16_t *__restrict__ wp, int64_t ld, int64_t ps,
+                   const uint32_t *__restrict__ top, int *err) {
+  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (r >= rows || !SSD_IN_BOUNDS(ld >= d && ws >= 0, err, 72)) return;
+  pack_row(w + r * ws, wp + r * ld, ps, d, top ? scale_of(top[kTopW]) : 1.f, threadIdx.x % 32, 32);
+}
+
+// ------------------------------------------------------------------ epilogues
+
+// The logits' statistics.  In units of log2 (the largest logit m and the sum of
+// 2^(z - m)), so that the exponential is one multiply-add and one ex2: its
+// error, 2^-22 relative, is the sum's.
+struct StatsEpi {
+  struct Args {
+    float2 *part;  // [runs][ld]
+    int64_t ld;
+    Rows rows;
+    const uint32_t *top;
+    int V, word0, run0;  // words of this piece; its first word and run
+  };
+  const Args &a;
+  int *err;
+  float unit, scale, m, s;  // of the sums: a logit, and its log2e
+  int row, run, target;
+  bool live;
+  __device__ __forceinline__ StatsEpi(const Args &args, int *e) : a(args), err(e) {
+    unit = a.top ? inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW])) : 1.f;
+    scale = unit * kLog2e;
+  }
+  __device__ __forceinline__ void begin(const Tile &, int r, int col, int M) {
+    row = r, live = r < M, run = a.run0 + col / kRun;
+    m = -INFINITY, s = 0.f;
+    target = live ? a.rows.target[r] - a.word0 : -1;
+  }
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
+    if (col >= a.V) return;
+    const int words = a.V - col;
+    const int at = target - col;
+    if (at >= 0 && at < gemm::kChunk && at < words) {
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk; ++i) z = i == at ? v[i] : z;
+      if (SSD_IN_BOUNDS(row < a.ld, err, 73)) a.rows.zt[row] = z * unit;
+    }
+    if (words < gemm::kChunk) {
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk; ++i) v[i] = i < words ? v[i] : -INFINITY;
+    }
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < gemm::kChunk; ++i) top = fmaxf(top, v[i]);
+    const float next = fmaxf(m, top * scale);
+    const float about = next == -INFINITY ? 0.f : next;  // of nothing but -inf the sum is zero
+    float q[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < gemm::kChunk; ++i) q[i % 4] += ex2(fmaf(v[i], scale, -about));
+    s = s * ex2(m - about) + ((q[0] + q[1]) + (q[2] + q[3]));
+    m = next;
+  }
+  __device__ __forceinline__ void end() {
+    if (live && SSD_IN_BOUNDS(row < a.ld, err, 74))
+      a.part[(int64_t)run * a.ld + row] = make_float2(m, s);
+  }
+};
+
+// dz of a piece of the vocabulary.
+template <typename IO>
+struct DlogitEpi {
+  struct Args {
+    uint16_t *dz;  // [planes][.., ld]
+    int64_t ld, ps;
+    Rows rows;
+    const uint32_t *top;
+    int V, word0, uniform;
+  };
+  static constexpr bool kSplit = sizeof(IO) == 4;
+  const Args &a;
+  int *err;
+  float scale, up, lse, g;
+  int row, target;
+  bool live;
+  __device__ __forceinline__ DlogitEpi(const Args &args, int *e) : a(args), err(e) {
+    scale = up = 1.f;
+    if constexpr (kSplit) {
+      scale = inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW]));
+      up = a.uniform ? 16384.f : scale_of(a.top[kTopG]);
+    }
+  }
+  __device__ __forceinline__ void begin(const Tile &, int r, int, int M) {
+    row = r, live = r < M;
+    lse = live ? a.rows.lse[r] : 0.f;
+    g = live ? a.rows.g[r] * up : 0.f;
+    target = live ? a.rows.target[r] - a.word0 : -1;
+  }
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
+    const int words = a.V - col, at = target - col;
+#pragma unroll
+    for (int i = 0; i < gemm::kChunk; ++i) {
+      float p = ex2(fmaf(v[i], scale, -lse) * kLog2e);
+      if (i == at) p -= 1.f;
+      v[i] = live && i < words ? p * g : 0.f;
+    }
+    if (!SSD_IN_BOUNDS(col + gemm::kChunk <= a.ld, err, 75)) return;
+    uint16_t *o = a.dz + (int64_t)row * a.ld + col;
+    if constexpr (kSplit) {
+      uint32_t hi[gemm::kChunk / 2], lo[gemm::kChunk / 2];
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk / 2; ++i) {
+        __half h0, l0, h1, l1;
+        split(v[2 * i], 1.f, h0, l0);
+        split(v[2 * i + 1], 1.f, h1, l1);
+        hi[i] = __half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
+        lo[i] = __half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
+      }
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk / 8; ++i) {
+        reinterpret_cast<uint4 *>(o)[i] = *reinterpret_cast<const uint4 *>(hi + 4 * i);
+        reinterpret_cast<uint4 *>(o + a.ps)[i] = *reinterpret_cast<const uint4 *>(lo + 4 * i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk / 8; ++i) {
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = v[8 * i + k];
+        store_vec<8>(reinterpret_cast<__nv_bfloat16 *>(o) + 8 * i, w);
+      }
+    }
+  }
+  __device__ __forceinline__ void end() {}
+};
+
+// The gradients: product 0 adds up dx over the pieces, product 1 is a piece of dW.
+template <typename IO>
+struct GradEpi {
+  struct Args {
+    float *sum;  // [.., ld] dx of the pieces so far; unused with a single one
+    int64_t ld;
+    SeqView<IO> dx;
+    IO *dw;
+    Rows rows;
+    const uint32_t *top;
+    const float *gloss;  // one value for all tokens (uniform), or NULL
+    int64_t L;
+    int d, uniform, mean, first, last, wide_x, wide_w;
+  };
+  static constexpr int kVec = 16 / (int)sizeof(IO);
+  const Args &a;
+  int *err;
+  float factor, fx, fw;
+  int which, row;
+  bool live;
+  IO *out;
+  __device__ __forceinline__ GradEpi(const Args &args, int *e) : a(args), err(e) {
+    factor = a.uniform && a.gloss ? *a.gloss : 1.f;
+    if (a.mean) {
+      const int n = *a.rows.live;
+      factor /= (float)(n > 1 ? n : 1);
+    }
+    fx = fw = 1.f;
+    if (a.top) {
+      const float down = a.uniform ? 1.f / 16384.f : inverse_of(scale_of(a.top[kTopG]));
+      fx = down * inverse_of(scale_of(a.top[kTopW]));
+      fw = down * inverse_of(scale_of(a.top[kTopX]));
+    }
+  }
+  __device__ __forceinline__ void begin(const Tile &o, int r, int, int M) {
+    which = o.which, row = r, live = r < M;
+    out = nullptr;
+    if (!live) return;
+    if (which) {
+      out = a.dw + (int64_t)r * a.d;
+    } else if (a.last) {
+      const int64_t t = a.rows.token[r];
+      out = a.dx.at(t / a.L, t % a.L);
+    }
+  }
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
+    if (!live || col >= a.d) return;
+    const float f = which ? fw : fx;
+#pragma unroll
+    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= f;
+    if (!which && !(a.first && a.last)) {
+      float4 *p = reinterpret_cast<float4 *>(a.sum + (int64_t)row * a.ld + col);
+      if (!SSD_IN_BOUNDS(col + gemm::kChunk <= a.ld, err, 76)) return;
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk / 4; ++i) {
+        float4 s = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : p[i];
+        s.x += v[4 * i], s.y += v[4 * i + 1], s.z += v[4 * i + 2], s.w += v[4 * i + 3];
+        if (!a.last) p[i] = s;
+        v[4 * i] = s.x, v[4 * i + 1] = s.y, v[4 * i + 2] = s.z, v[4 * i + 3] = s.w;
+      }
+      if (!a.last) return;
+    }
+    const bool wide = which ? a.wide_w : a.wide_x;
+#pragma unroll
+    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= factor;
+    if (wide && col + gemm::kChunk <= a.d) {
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk / kVec; ++i) {
+        float w[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) w[k] = v[kVec * i + k];
+        store_vec<kVec>(out + col + kVec * i, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < gemm::kChunk; ++i)
+        if (col + i < a.d) st_io(out + col + i, v[i]);
+    }
+  }
+  __device__ __forceinline__ void end() {}
+};
+
+// ------------------------------------------------------------ joining the runs
+
+// 32 rows (lanes) to a block; its warps take the runs in turn and their results
+// are joined in the warps' order.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
+            float *__restrict__ loss, float *__restrict__ lse, int *err) {
+  __shared__ float2 each[kJoinWarps][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const bool live = row < *rows.live;
+  float m = -INFINITY, s = 0.f;
+  auto join = [&](float2 q) {
+    const float next = fmaxf(m, q.x), about = next == -INFINITY ? 0.f : next;
+    s = s * ex2(m - about) + q.y * ex2(q.x - about);
+    m = next;
+  };
+  if (live && SSD_IN_BOUNDS(row < ld, err, 77)) {
+#pragma unroll 4
+    for (int r = warp; r < runs; r += kJoinWarps) join(part[(int64_t)r * ld + row]);
+  }
+  each[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp || !live) return;
+  for (int w = 1; w < kJoinWarps; ++w) join(each[w][lane]);
+  const float l = fmaf(m, kLn2, logf(s));
+  const int t = rows.token[row];
+  lse[t] = l;
+  loss[t] = l - rows.zt[row];
+}
+
+// The sum of every token's loss (or the mean over those with a target, 0 without one), in a fixed order.
+__global__ void __launch_bounds__(1024)
+total_kernel(const float *__restrict__ loss, int64_t n, const int *__restrict__ live, int mean,
+             float *__restrict__ total, int *err) {
+  __shared__ float sums[32];
+  float s = 0.f;
+  if (SSD_IN_BOUNDS(n > 0, err, 78))
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += 1024) s += loss[i];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  s = sums[threadIdx.x];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (threadIdx.x == 0) *total = mean ? s / (float)(*live > 1 ? *live : 1) : s;
+}
+
+// -------------------------------------------------------------------- the host
+
+// What a call keeps where.  Pieces: words to a piece (forward: all where W can be
+// taken as it is, else as many as keep the packed rows near 256 MB; backward: as
+// many as keep dz near that, where a piece of 2048 already fills the tiles).
+struct Plan {
+  int planes;
+  int64_t rows, ld, piece, dz_ld;  // padded rows; elements to a packed row; words; dz's row
+  bool direct;                     // W as it is
+  uint32_t *top;
+  Rows r;
+  uint16_t *xp, *wp, *dz;
+  float2 *part;
+  float *loss, *sum;
+  int64_t runs;
+  size_t bytes;
+};
+
+constexpr int64_t kPieceBytes = 256ll << 20;
+
+Plan plan_of(const LossArgs &a, ssd_dtype io, bool back, void *ws) {
+  Plan p{};
+  p.planes = io == SSD_F32 ? 2 : 1;
+  p.rows = round_up(a.n, gemm::kTileM);
+  p.ld = gemm::padded(a.d);
+  p.direct = io == SSD_BF16 && ptr_aligned(a.weight->data, 16) &&
+             a.weight->token_stride % 8 == 0 && a.weight->token_stride >= a.d;
+  const int64_t all = round_up(a.V, kBN);
+  const int64_t per = 2 * p.planes * (back ? p.rows : p.ld);  // bytes to a word
+  int64_t piece = kPieceBytes / per / kBN * kBN;
+  if (piece < 2048) piece = 2048;
+  if (!back && p.direct) piece = all;
+  const int64_t pieces = (all + piece - 1) / piece;
+  p.piece = round_up((all + pieces - 1) / pieces, kBN);
+  p.dz_ld = p.piece;
+  p.runs = all / kRun;
+  Carver c(ws);
+  p.top = c.take<uint32_t>(kTops);
+  p.r.live = c.take<int>(1);
+  p.r.token = c.take<int>(a.n);
+  p.r.target = c.take<int>(a.n);
+  p.xp = c.take<uint16_t>(p.planes * p.rows * p.ld);
+  p.wp = c.take<uint16_t>(p.direct ? 0 : p.planes * p.piece * p.ld);
+  if (back) {
+    p.r.lse = c.take<float>(a.n);
+    p.r.g = c.take<float>(a.n);
+    p.dz = c.take<uint16_t>(p.planes * p.rows * p.dz_ld);
+    p.sum = c.take<float>(p.piece < a.V ? p.rows * round_up(a.d, gemm::kChunk) : 0);
+  } else {
+    p.r.zt = c.take<float>(a.n);
+    p.loss = c.take<float>(a.n);
+    p.part = c.take<float2>(p.runs * p.rows);
+  }
+  p.bytes = c.used;
+  return p;
+}
+
+template <typename IO>
+struct Calls {
+  static constexpr int kPlanes = sizeof(IO) == 4 ? 2 : 1;
+  static constexpr bool kBf16 = sizeof(IO) == 2;
+  static constexpr int kSegment = kBf16 ? 0 : gemm::kExact;
+
+  static cudaError_t pack(const LossArgs &a, const Plan &p, bool back, float *loss, float *lse,
+                          int *err, cudaStream_t st) {
+    const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
+    const float *g = back && a.reduction == SSD_REDUCE_NONE ? a.gloss : nullptr;
+    if (top) {
+      cudaError_t e = cudaMemsetAsync(p.top, 0, kTops * sizeof(uint32_t), st);
+      if (e != cudaSuccess) return e;
+      if constexpr (kPlanes == 2)
+        top_kernel<<<4 * sm_count(), 256, 0, st>>>(
+            view_of<const float>(a.x), a.targets, a.ignore, a.L, a.n,
+            static_cast<const float *>(a.weight->data), a.weight->token_stride, a.V, a.d, g, p.top,
+            err);
+    }
+    pack_kernel<IO><<<(unsigned)((a.n + kPackTokens - 1) / kPackTokens), kPackThreads, 0, st>>>(
+        view_of<const IO>(a.x), a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
+        view_of<IO>(a.dx), loss, lse, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, top, err);
+    return cudaGetLastError();
+  }
+
+  // The words word0 .. of W as an operand array: its address and strides.
+  struct Words {
+    const void *at;
+    int64_t n, ld, zs;
+  };
+  static cudaError_t words(const LossArgs &a, const Plan &p, int64_t word0, Words *w, int *err,
+                           cudaStream_t st) {
+    w->n = a.V - word0 < p.piece ? a.V - word0 : p.piece;
+    const IO *src = static_cast<const IO *>(a.weight->data) + word0 * a.weight->token_stride;
+    if (p.direct) {
+      w->at = src, w->ld = a.weight->token_stride, w->zs = w->n * w->ld;
+      return cudaSuccess;
+    }
+    w->at = p.wp, w->ld = p.ld, w->zs = p.piece * p.ld;
+    pack_weight_kernel<IO><<<(unsigned)((w->n + 7) / 8), 256, 0, st>>>(
+        src, a.weight->token_stride, w->n, a.d, p.wp, p.ld, w->zs,
+        kPlanes == 2 ? p.top : nullptr, err);
+    return cudaGetLastError();
+  }
+
+  static Product product(int64_t M, int64_t N, int64_t K) {
+    Product q{};
+    q.M = (int)M, q.N = (int)N, q.K = (int)K, q.batch = 1;
+    q.pairs = kPlanes == 2 ? 3 : 1;
+    q.a_planes = q.b_planes = kPlanes;
+    return q;
+  }
+
+  // maps and product of the logits of a piece
+  static bool logits(const LossArgs &a, const Plan &p, const Words &w, CUtensorMap *maps,
+                     Product *q) {
+    *q = product(a.n, w.n, a.d);
+    q->live_m = p.r.live;
+    return gemm::make_map(&maps[0], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, false,
+                          gemm::kRows) &&
+           gemm::make_map(&maps[1], w.at, a.d, w.n, kPlanes, w.ld, w.zs, false, kBN / 2);
+  }
+
+  static cudaError_t forward(const LossArgs &a, void *ws, int *err, cudaStream_t st) {
+    const Plan p = plan_of(a, kBf16 ? SSD_BF16 : SSD_F32, false, ws);
+    float *loss = a.loss ? a.loss : p.loss;
+    cudaError_t e = pack(a, p, false, loss, a.lse, err, st);
+    for (int64_t word0 = 0; word0 < a.V && e == cudaSuccess; word0 += p.piece) {
+      Words w;
+      e = words(a, p, word0, &w, err, st);
+      if (e != cudaSuccess) break;
+      CUtensorMap maps[2];
+      Product q;
+      if (!logits(a, p, w, maps, &q)) return cudaErrorInvalidValue;
+      const StatsEpi::Args s{p.part, p.rows, p.r, kPlanes == 2 ? p.top : nullptr, (int)w.n,
+                             (int)word0, (int)(word0 / kRun)};
+      e = gemm::launch<StatsEpi, kBN, kSegment>(maps, &q, 1, kBf16, s, err, st);
+    }
+    if (e != cudaSuccess) return e;
+    join_kernel<<<(unsigned)((a.n + 31) / 32), 32 * kJoinWarps, 0, st>>>(
+        p.part, p.rows, (int)p.runs, p.r, loss, a.lse, err);
+    if (a.total)
+      total_kernel<<<1, 1024, 0, st>>>(loss, a.n, p.r.live, a.reduction == SSD_REDUCE_MEAN,
+                                       a.total, err);
+    return cudaGetLastError();
+  }
+
+  static cudaError_t backward(const LossArgs &a, void *ws, int *err, cudaStream_t st) {
+    const Plan p = plan_of(a, kBf16 ? SSD_BF16 : SSD_F32, true, ws);
+    const bool uniform = a.reduction != SSD_REDUCE_NONE || !a.gloss;
+    const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
+    const int64_t ps = p.rows * p.dz_ld;
+    cudaError_t e = pack(a, p, true, nullptr, nullptr, err, st);
+    for (int64_t word0 = 0; word0 < a.V && e == cudaSuccess; word0 += p.piece) {
+      Words w;
+      e = words(a, p, word0, &w, err, st);
+      if (e != cudaSuccess) break;
+      CUtensorMap maps[4];
+      Product q[2];
+      if (!logits(a, p, w, maps, q)) return cudaErrorInvalidValue;
+      const typename DlogitEpi<IO>::Args z{p.dz, p.dz_ld, ps, p.r, top, (int)w.n, (int)word0,
+                                           uniform};
+      e = gemm::launch<DlogitEpi<IO>, kBN, kSegment>(maps, q, 1, kBf16, z, err, st);
+      if (e != cudaSuccess) break;
+      // dx [n, d] += dz [n, words] W [words, d];  dW [words, d] = dz^T x
+      int count = 0;
+      if (a.dx) {
+        q[0] = product(a.n, a.d, w.n);
+        q[0].live_m = p.r.live, q[0].b_mn = 1;
+        if (!gemm::make_map(&maps[0], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, false,
+                            gemm::kRows) ||
+            !gemm::make_map(&maps[1], w.at, a.d, w.n, kPlanes, w.ld, w.zs, true, kBN / 2))
+          return cudaErrorInvalidValue;
+        count = 1;
+      }
+      if (a.dweight) {
+        q[1] = product(w.n, a.d, a.n);
+        q[1].live_k = p.r.live, q[1].a_mn = q[1].b_mn = 1;
+        if (!gemm::make_map(&maps[2], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, true,
+                            gemm::kRows) ||
+            !gemm::make_map(&maps[3], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, true,
+                            kBN / 2))
+          return cudaErrorInvalidValue;
+        ++count;
+      }
+      if (count == 0) continue;
+      typename GradEpi<IO>::Args g{};
+      g.sum = p.sum, g.ld = round_up(a.d, gemm::kChunk), g.dx = view_of<IO>(a.dx);
+      g.dw = static_cast<IO *>(a.dweight) + word0 * a.d;
+      g.rows = p.r, g.top = top, g.gloss = uniform ? a.gloss : nullptr, g.L = a.L;
+      g.d = (int)a.d, g.uniform = uniform;
+      g.mean = a.reduction == SSD_REDUCE_MEAN;
+      g.first = word0 == 0, g.last = word0 + p.piece >= a.V;
+      g.wide_x = view_aligned(a.dx, sizeof(IO), 16);
+      g.wide_w = ptr_aligned(a.dweight, 16) && a.d * sizeof(IO) % 16 == 0;
+      // with dW alone it is still product 1 to the epilogue: product 0 has no rows
+      if (!a.dx) {
+        q[0] = q[1];
+        q[0].M = 0, q[0].live_m = nullptr;
+        maps[0] = maps[2], maps[1] = maps[3];
+        count = 2;
+      }
+      e = gemm::launch<GradEpi<IO>, kBN, kSegment>(maps, q, count, kBf16, g, err, st);
+    }
+    return e;
+  }
+};
+
+}  // namespace
+
+size_t vocab_loss_workspace(const LossArgs &a, ssd_dtype io) {
+  return plan_of(a, io, false, nullptr).bytes;
+}
+size_t vocab_loss_backward_workspace(const LossArgs &a, ssd_dtype io) {
+  return plan_of(a, io, true, nullptr).bytes;
+}
+cudaError_t launch_vocab_loss(const LossArgs &a, ssd_dtype io, void *ws, int *err,
+                              cudaStream_t st) {
+  return io == SSD_BF16 ? Calls<__nv_bfloat16>::forward(a, ws, err, st)
+                        : Calls<float>::forward(a, ws, err, st);
+}
+cudaError_t launch_vocab_loss_backward(const LossArgs &a, ssd_dtype io, void *ws, int *err,
+                                       cudaStream_t st) {
+  return io == SSD_BF16 ? Calls<__nv_bfloat16>::backward(a, ws, err, st)
+                        : Calls<float>::backward(a, ws, err, st);
+}
+
+}  // namespace ssd
