@@ -49,12 +49,16 @@ constexpr int kChunk = 32;  // columns an epilogue thread holds at a time
 constexpr int kExact = 4;   // stages to a segment where fp32's precision is asked for
 constexpr int kBytesA = kRows * 128;
 
-template <int kBN>
+constexpr int kPane = 32 * 128;  // bytes of a pane: 32 rows of 128 bytes, swizzled
+
+// kStaged: the epilogue's warps have two panes each.
+template <int kBN, bool kStaged>
 struct Shape {
   static constexpr int kBytesB = kBN / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kPanes = kStaged ? 2 * kEpiWarps * kPane : 0;
+  static constexpr int kStages = (229376 - kPanes) / kStage;
+  static constexpr int kSmem = kStages * kStage + kPanes + 1024;
   static constexpr uint32_t kTmemCols = 2 * kBN;
 };
 
@@ -66,11 +70,13 @@ struct Product {
   int pairs;               // 1, or 3 with operands of two planes
   int a_planes, b_planes;  // planes that each operand's array holds
   int symmetric;           // D is: only tiles on and above the diagonal
+  int part;                // > 0: batch i sums k from i part kTileK on, part stages of them
 };
 
 // What a block does of a tile: rows m .. m + 127, columns n .. n + kBN - 1.
 struct Tile {
-  int which, batch, m, n, steps;  // product; batch; k steps of one pair of planes
+  int which, batch, m, n;
+  int k0, steps;  // first stage of k, and stages, of one pair of planes
   int mirror;                     // D is symmetric and this tile lies above the diagonal
 };
 
@@ -118,7 +124,9 @@ struct Walk {  // the tiles of up to two products, in order; in shared memory
     }
     o.m = mi * kTileM + rank * kRows;
     o.n = ni * kBN;
-    o.steps = (K[i] + kTileK - 1) / kTileK;
+    o.k0 = o.batch * p[i].part;
+    o.steps = (K[i] + kTileK - 1) / kTileK - o.k0;
+    if (p[i].part) o.steps = max(0, min(o.steps, p[i].part));
     o.mirror = p[i].symmetric && o.n >= (mi + 1) * kTileM;
     return o;
   }
@@ -135,7 +143,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 // The address of a barrier in the pair's first block.
-__device__ __forceinline__ uint32_t in_first(uint64_t *bar) {
+__device__ __forceinline__ uint32_t in_first(const uint64_t *bar) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(bar)));
   return a;
@@ -187,28 +195,87 @@ __device__ __forceinline__ uint32_t idesc(int n, int bf16, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) |
          ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
 }
-// Descriptor of step kk (16 k) of a landed operand.  K-major: rows of 128
-// bytes, 8-row groups 1024 bytes apart, a step is 32 bytes along the row.
-// MN-major: blocks of 64 (m or n) x 64 k, 8192 bytes apart, a step is 16 rows.
-__device__ __forceinline__ uint64_t desc(uint32_t at, int mn, int kk) {
-  return mn ? ptx::smem_desc(at + 2048 * kk, 8192, 1024, ptx::kSw128)
-            : ptx::smem_desc(at + 32 * kk, 16, 1024, ptx::kSw128);
+// Descriptor of a landed operand at address 0 (the address is added in units of
+// 16 bytes; shared memory has 2^14 of them at most).  K-major: rows of 128
+// bytes, 8-row groups 1024 bytes apart, 16 k are 32 bytes along the row.
+// MN-major: blocks of 64 (m or n) x 64 k, 8192 bytes apart, 16 k are 16 rows.
+__device__ __forceinline__ uint64_t desc(int mn) {
+  return ptx::smem_desc(0, mn ? 8192 : 16, 1024, ptx::kSw128);
 }
 
-// Loads `rows` rows (m or n, from r0) x 64 k (from k0) of an operand.
-__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, int mn,
-                                             int rows, int r0, int k0, int z, uint32_t bar) {
+// Loads kCount rows (m or n, from r0) x 64 k (from k0) of an operand.
+template <int kCount>
+__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *map, int mn, int r0,
+                                             int k0, int z, uint32_t bar) {
   if (!mn) {
     load(dst, map, k0, r0, z, bar);
   } else {
-    for (int j = 0; j < rows / 64; ++j) load(dst + 8192 * j, map, r0 + 64 * j, k0, z, bar);
+#pragma unroll
+    for (int j = 0; j < kCount / 64; ++j) load(dst + 8192 * j, map, r0 + 64 * j, k0, z, bar);
   }
 }
 
+// A warp's two panes in shared memory.  A thread holds a row of the tile; through a
+// pane, 32 rows of 128 bytes go to memory and come from it by TMA, which clips
+// what lies outside the array.  (Row by row from registers every access would
+// touch 32 lines: measured 16000 clocks a tile against 6000 of products.)
+struct Panes {
+  uint8_t *at;
+  uint64_t *bar;
+  int *err;
+  int lane;
+  uint32_t parity;
+  __device__ __forceinline__ Panes(uint8_t *p, uint64_t *b, int *e)
+      : at(p), bar(b), err(e), lane(threadIdx.x & 31), parity(0) {}
+  // 16 bytes of this thread's row: piece 0 .. 7 of pane i
+  __device__ __forceinline__ uint4 &cell(int i, int piece) const {
+    return *reinterpret_cast<uint4 *>(at + i * kPane + lane * 128 + ((piece ^ (lane & 7)) << 4));
+  }
+  // 4 bytes of row r: word `lane` of pane i
+  __device__ __forceinline__ uint32_t word(int i, int r) const {
+    return *reinterpret_cast<const uint32_t *>(at + i * kPane + r * 128 +
+                                               (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+  }
+  // All but the newest kLeft groups of stores have read their panes.
+  template <int kLeft>
+  __device__ __forceinline__ void reuse() const {
+    if (lane == 0) ptx::bulk_wait_read<kLeft>();
+    __syncwarp();
+  }
+  // The warp has written its panes: lane 0 may store them.
+  __device__ __forceinline__ void written() const {
+    ptx::fence_async_smem();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void store(int i, const CUtensorMap *map, int col, int row,
+                                        int z) const {  // lane 0, then commit
+    ptx::tma_store_3d(map, at + i * kPane, col, row, z);
+  }
+  __device__ __forceinline__ void add(int i, const CUtensorMap *map, int col, int row,
+                                      int z) const {  // fp32
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+        " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(ptx::smem_u32(at + i * kPane)), "r"(col), "r"(row), "r"(z)
+        : "memory");
+  }
+  // Loads panes 0 .. n - 1 (z, z + 1); the stores from them have to be read.
+  __device__ __forceinline__ void fetch(const CUtensorMap *map, int n, int col, int row, int z) {
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(bar, n * kPane);
+      for (int i = 0; i < n; ++i) ptx::tma_load_3d(at + i * kPane, map, col, row, z + i, bar);
+    }
+  }
+  __device__ __forceinline__ void fetched() {
+    ptx::mbar_wait(bar, parity, err, 304);
+    parity ^= 1;
+  }
+};
+
 // kSegment: stages to a segment, 0: all k in one.
-// Epi: constructed from its Args by every epilogue thread, then per tile
-// begin(tile, row, column), chunk(v, column) for each 32 columns of the
-// thread's row, end().
+// Epi: constructed from its Args and panes by every epilogue thread, then per tile
+// begin(tile, row, column, rows), chunk(v, column, j) for each 32 columns of the
+// thread's row, end().  kStaged: it uses the panes.
 template <class Epi, int kBN, int kSegment>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
@@ -216,13 +283,14 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
                const __grid_constant__ Product p0, const __grid_constant__ Product p1,
                const int count, const int bf16, const __grid_constant__ typename Epi::Args args,
                int *err) {
-  using S = Shape<kBN>;
+  using S = Shape<kBN, Epi::kStaged>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   // full: a stage landed in both blocks (the first block's is waited on);
   // empty: its products are done; accfull: a tile's are; accfree: both blocks'
   // epilogues have read them (the first block's)
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], accfull[2], accfree[2];
+  __shared__ __align__(8) uint64_t landed[kEpiWarps];  // panes of each epilogue warp
   __shared__ uint32_t tmem_slot;
   __shared__ Walk<kBN> walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -237,6 +305,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       ptx::mbar_init(&accfull[i], 1);
       ptx::mbar_init(&accfree[i], 2 * kEpiWarps);
     }
+    for (int i = 0; i < kEpiWarps; ++i) ptx::mbar_init(&landed[i], 1);
     ptx::fence_mbar_init();
     walk.plan(p0, p1, count);
   }
@@ -248,6 +317,9 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   const uint32_t tmem = tmem_slot;
   const int step = gridDim.x / 2, start = blockIdx.x / 2;
 
+  // The loops of warps 0 and 1 belong to one thread each and are latency bound
+  // (a stage is 512 clocks of products): what does not change within a tile
+  // is in registers.  Read from shared memory as they went, a stage took 740.
   if (warp == 0) {
     if (lane == 0) {
       ptx::prefetch_tmap(&a0);
@@ -256,38 +328,38 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
         ptx::prefetch_tmap(&a1);
         ptx::prefetch_tmap(&b1);
       }
-    }
-    int s = 0, round = 0;
-    for (int t = start; t < walk.total; t += step) {
-      const Tile o = walk.at(t, rank);
-      const Product &p = walk.p[o.which];
-      const CUtensorMap *ma = o.which ? &a1 : &a0, *mb = o.which ? &b1 : &b0;
-      for (int pair = 0; pair < p.pairs; ++pair) {
-        // with three: lo hi, hi lo, hi hi
-        const int za = o.batch * p.a_planes + (p.pairs == 3 && pair == 0);
-        const int zb = o.batch * p.b_planes + (p.pairs == 3 && pair == 1);
-        for (int k = 0; k < o.steps; ++k) {
-          if (round) ptx::mbar_wait(&empty[s], (round - 1) & 1, err, 300);
-          if (lane == 0) {
+      int s = 0, round = 0;
+      const uint32_t bars = in_first(full);
+      for (int t = start; t < walk.total; t += step) {
+        const Tile o = walk.at(t, rank);
+        const Product &p = walk.p[o.which];
+        const CUtensorMap *ma = o.which ? &a1 : &a0, *mb = o.which ? &b1 : &b0;
+        const int a_mn = p.a_mn, b_mn = p.b_mn, pairs = p.pairs, n = o.n + rank * (kBN / 2);
+        const int z = p.part ? 0 : o.batch, za = z * p.a_planes, zb = z * p.b_planes;
+        for (int pair = 0; pair < pairs; ++pair) {
+          // with three: lo hi, hi lo, hi hi
+          const int z0 = za + (pairs == 3 && pair == 0), z1 = zb + (pairs == 3 && pair == 1);
+          for (int k = o.k0; k < o.k0 + o.steps; ++k) {
+            if (round) ptx::mbar_wait(&empty[s], (round - 1) & 1, err, 300);
             if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
             uint8_t *at = smem + s * S::kStage;
-            const uint32_t bar = in_first(&full[s]);
-            load_operand(at, ma, p.a_mn, kRows, o.m, k * kTileK, za, bar);
-            load_operand(at + kBytesA, mb, p.b_mn, kBN / 2, o.n + rank * (kBN / 2), k * kTileK,
-                         zb, bar);
+            load_operand<kRows>(at, ma, a_mn, o.m, k * kTileK, z0, bars + 8 * s);
+            load_operand<kBN / 2>(at + kBytesA, mb, b_mn, n, k * kTileK, z1, bars + 8 * s);
+            if (++s == S::kStages) s = 0, ++round;
           }
-          __syncwarp();
-          if (++s == S::kStages) s = 0, ++round;
         }
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && lane == 0) {
       int s = 0, parity = 0, n = 0;
+      const uint32_t ring = ptx::smem_u32(smem) >> 4;
       for (int t = start; t < walk.total; t += step) {
         const Tile o = walk.at(t, rank);
         const Product &p = walk.p[o.which];
         const uint32_t id = idesc(kBN, bf16, p.a_mn, p.b_mn);
+        const uint64_t da = desc(p.a_mn), db = desc(p.b_mn);
+        const uint32_t ia = p.a_mn ? 128 : 2, ib = p.b_mn ? 128 : 2;  // to the next 16 k, by 16 bytes
         const int steps = o.steps * p.pairs, each = kSegment ? kSegment : steps;
         int k = 0;
         do {  // a segment (an empty one where there are no k)
@@ -298,19 +370,14 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
           for (; k < end; ++k) {
             ptx::mbar_wait(&full[s], parity, err, 302);
             ptx::tc_fence_after();
-            if (lane == 0) {
-              const uint32_t at = ptx::smem_u32(smem + s * S::kStage);
+            const uint32_t at = ring + s * (S::kStage / 16), bt = at + kBytesA / 16;
 #pragma unroll
-              for (int kk = 0; kk < kTileK / 16; ++kk)
-                mma(d, desc(at, p.a_mn, kk), desc(at + kBytesA, p.b_mn, kk), id,
-                    k > begin || kk > 0);
-              commit_both(&empty[s]);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kTileK / 16; ++kk)
+              mma(d, da + at + kk * ia, db + bt + kk * ib, id, k > begin || kk > 0);
+            commit_both(&empty[s]);
             if (++s == S::kStages) s = 0, parity ^= 1;
           }
-          if (lane == 0) commit_both(&accfull[n & 1]);
-          __syncwarp();
+          commit_both(&accfull[n & 1]);
           ++n;
         } while (k < steps);
       }
@@ -318,7 +385,8 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   } else {
     constexpr int kHalf = kBN / 2, kChunks = kHalf / kChunk;
     const int quad = warp & 3, c0 = warp >= 6 ? kHalf : 0;
-    Epi epi(args, err);
+    uint8_t *panes = smem + S::kStages * S::kStage + (warp - 2) * 2 * kPane;
+    Epi epi(args, Panes(panes, &landed[warp - 2], err), err);
     int n = 0;
     // 32 columns of the accumulator at `at`; the last ones hand it back
     auto read = [&](uint32_t at, int j, uint32_t (&r0)[16], uint32_t (&r1)[16]) {
@@ -351,7 +419,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
             v[i] = o.steps ? __uint_as_float(r0[i]) : 0.f;
             v[16 + i] = o.steps ? __uint_as_float(r1[i]) : 0.f;
           }
-          epi.chunk(v, o.n + c0 + j * kChunk);
+          epi.chunk(v, o.n + c0 + j * kChunk, j);
         }
         ++n;
       } else {
@@ -381,9 +449,12 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
           k += kSegment;
         } while (k < steps);
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) epi.chunk(v[j], o.n + c0 + j * kChunk);
+        for (int j = 0; j < kChunks; ++j) epi.chunk(v[j], o.n + c0 + j * kChunk, j);
       }
       epi.end();
+    }
+    if constexpr (Epi::kStaged) {
+      if (lane == 0) ptx::bulk_wait<0>();  // the panes are read and their values written
     }
   }
   ptx::tc_fence_before();
@@ -404,6 +475,16 @@ inline bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t r
   return make_tmap_sw128(map, base, true, 3, dims, strides, b);
 }
 
+// Map of an array [z][rows][cols] for panes.
+inline bool make_pane_map(CUtensorMap *map, const void *base, bool fp32, int64_t cols, int64_t rows,
+                          int64_t z, int64_t ld, int64_t zs) {
+  const uint64_t e = fp32 ? 4 : 2;
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)z};
+  const uint64_t strides[2] = {(uint64_t)ld * e, (uint64_t)zs * e};
+  const uint32_t b[3] = {(uint32_t)(128 / e), 32, 1};
+  return make_tmap_sw128(map, base, !fp32, 3, dims, strides, b);
+}
+
 // Elements to a row of an operand array: rows start on 32 bytes.
 inline int64_t padded(int64_t cols) { return (cols + 15) / 16 * 16; }
 
@@ -411,7 +492,7 @@ inline int64_t padded(int64_t cols) { return (cols + 15) / 16 * 16; }
 template <class Epi, int kBN, int kSegment = 0>
 cudaError_t launch(const CUtensorMap *maps, const Product *p, int count, bool bf16,
                    const typename Epi::Args &args, int *err, cudaStream_t st) {
-  using S = Shape<kBN>;
+  using S = Shape<kBN, Epi::kStaged>;
   auto *kernel = product_kernel<Epi, kBN, kSegment>;
   // set once a device (64 of them): every caller stores the same value
   static std::atomic<uint64_t> ready{0};

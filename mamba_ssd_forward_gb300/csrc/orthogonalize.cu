@@ -36,30 +36,55 @@ constexpr float kScale = 16384.f, kGramScale = 4096.f;  // of X; of A and B
 
 constexpr int kNormThreads = 512;
 
+// Eight consecutive elements from c on of a row of `cols`; those past its end are
+// zero.  `wide`: rows start on 16 bytes.
+template <typename IO>
+__device__ __forceinline__ void load8(const IO *p, int64_t c, int64_t cols, bool wide,
+                                      float (&v)[8]) {
+  if (wide && c + 8 <= cols) {
+    load_vec<8>(p + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? ld_io(p + c + e) : 0.f;
+  }
+}
+
+// The matrices in groups of eight elements, `per` groups to a row; a thread's
+// groups are gridDim.x kNormThreads apart.  Four loads at a time.
+template <typename IO, typename F>
+__device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
+                                      F f) {
+  const int64_t per = (cols + 7) / 8, all = rows * per, step = (int64_t)gridDim.x * kNormThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < all; i += 4 * step) {
+    float v[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * step < all) {
+        const int64_t r = (i + k * step) / per, c = (i + k * step - r * per) * 8;
+        load8(g.at(blockIdx.y, r), c, cols, wide, v[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * step < all) {
+        const int64_t r = (i + k * step) / per;
+        f(v[k], r, (i + k * step - r * per) * 8);
+      }
+  }
+}
+
+// Sums of squares, one a block.
 template <typename IO>
 __global__ void __launch_bounds__(kNormThreads)
-squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, float *__restrict__ part,
-               int *err) {
+squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
+               float *__restrict__ part, int *err) {
   __shared__ float sums[kNormThreads / 32];
-  const int64_t z = blockIdx.y;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t r = blockIdx.x * (kNormThreads / 32) + warp; r < rows;
-       r += gridDim.x * (kNormThreads / 32)) {
-    if (!SSD_IN_BOUNDS(z < gridDim.y, err, 80)) break;
-    const IO *p = g.at(z, r);
-    int64_t c = lane;
-    for (; c + 96 < cols; c += 128)
+  if (!SSD_IN_BOUNDS(rows > 0 && cols > 0, err, 80)) return;
+  each8(g, rows, cols, wide, [&](const float (&v)[8], int64_t, int64_t) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = ld_io(p + c + 32 * k);
-        s[k] = fmaf(v, v, s[k]);
-      }
-    for (; c < cols; c += 32) {
-      const float v = ld_io(p + c);
-      s[0] = fmaf(v, v, s[0]);
-    }
-  }
+    for (int e = 0; e < 8; ++e) s[e % 4] = fmaf(v[e], v[e], s[e % 4]);
+  });
   float t = (s[0] + s[1]) + (s[2] + s[3]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
@@ -68,24 +93,31 @@ squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, float *__restric
   if (threadIdx.x == 0) {
     t = sums[0];
     for (int w = 1; w < kNormThreads / 32; ++w) t += sums[w];
-    part[z * gridDim.x + blockIdx.x] = t;
+    part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
   }
 }
 
-__device__ __forceinline__ void split(float v, __half &hi, __half &lo) {
-  hi = __float2half_rn(v);
-  lo = __float2half_rn(v - __half2float(hi));
+// Eight values as fp16, and what that leaves of them.
+__device__ __forceinline__ uint4 pack8(float *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    v[2 * i] -= __low2float(h), v[2 * i + 1] -= __high2float(h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The first X: G times the power of two below kScale / (|G| + eps), in two
-// planes; rest[z]: what is left of that factor, in [1, 2).
+// The first X: G times the power of two below kScale / (|G| + eps), in one plane
+// or two; rest[z]: what is left of that factor, in [1, 2).
 template <typename IO>
 __global__ void __launch_bounds__(kNormThreads)
-start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, const float *__restrict__ part,
-             int parts, float eps, __half *__restrict__ x, int64_t ld,
-             float *__restrict__ rest, int *err) {
+start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
+             const float *__restrict__ part, int parts, float eps, __half *__restrict__ x,
+             int64_t ld, int planes, float *__restrict__ rest, int *err) {
   const int64_t z = blockIdx.y;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
   float s = 0.f;  // every warp adds the parts in the same order
   for (int i = lane; i < parts; i += 32) s += part[z * parts + i];
 #pragma unroll
@@ -96,121 +128,166 @@ start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, const float *__res
   const float pow2 = normal ? __uint_as_float(bits & 0x7f800000u) : 1.f;
   if (blockIdx.x == 0 && threadIdx.x == 0) rest[z] = whole / pow2;
   __half *hi = x + z * 2 * rows * ld, *lo = hi + rows * ld;
-  for (int64_t r = blockIdx.x * (kNormThreads / 32) + warp; r < rows;
-       r += gridDim.x * (kNormThreads / 32)) {
-    if (!SSD_IN_BOUNDS(z < gridDim.y && cols <= ld, err, 81)) break;
-    const IO *p = g.at(z, r);
-#pragma unroll 4
-    for (int64_t c = lane; c < cols; c += 32) {
-      __half h, l;
-      split(ld_io(p + c) * pow2, h, l);
-      hi[r * ld + c] = h;
-      lo[r * ld + c] = l;
-    }
-  }
+  if (!SSD_IN_BOUNDS(cols <= ld, err, 81)) return;
+  each8(g, rows, cols, wide, [&](float (&v)[8], int64_t r, int64_t c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= pow2;
+    *reinterpret_cast<uint4 *>(hi + r * ld + c) = pack8(v);
+    if (planes == 2) *reinterpret_cast<uint4 *>(lo + r * ld + c) = pack8(v);
+  });
 }
 
 // ------------------------------------------------------------------ epilogue
 
 // D = (alpha sum + beta C) rest^power, as fp16 planes or, the last X, as the
-// result.
+// result.  C comes through the panes that D leaves by.
 enum Kind { kPlanes, kBf16, kF32 };
 
 template <Kind kind>
 struct StepEpi {
   struct Args {
+    CUtensorMap c, d;  // planes of C; of D, or a bf16 result where TMA can write it
     float alpha, beta;
     const float *rest;  // of the first step, else NULL
     int power;
-    const __half *c;  // planes of C, NULL if there is none
-    int c_planes;     // read
-    int64_t c_ld, c_ps, c_zs;
-    __half *out;
-    int out_planes;
+    int c_planes, c_stored;  // planes of C to add (0: no C), and in its array
+    int planes, d_stored;    // of D
+    int half;                // columns of the tile that a warp takes
+    __half *out;             // D again, for its mirrored tiles
     int64_t ld, ps, zs;
     SeqView<__nv_bfloat16> bf16;
     SeqView<float> f32;
-    int N, wide;  // columns; rows of the result start on 16 bytes
+    int N, wide;  // columns; wide: rows of the result start on 16 bytes
   };
+  static constexpr bool kStaged = true;
   const Args &a;
+  gemm::Panes panes;
   int *err;
   float alpha, beta;
-  int row, M, mirror;
+  int row, col0, M, mirror;
   int64_t batch;
-  __device__ __forceinline__ StepEpi(const Args &args, int *e) : a(args), err(e) {}
-  __device__ __forceinline__ void begin(const Tile &o, int r, int, int rows) {
-    row = r, M = rows, mirror = o.mirror, batch = o.batch;
+  __device__ __forceinline__ StepEpi(const Args &args, gemm::Panes p, int *e)
+      : a(args), panes(p), err(e) {}
+  __device__ __forceinline__ void begin(const Tile &o, int r, int col, int rows) {
+    row = r, col0 = col, M = rows, mirror = o.mirror, batch = o.batch;
     float f = 1.f;
     if (a.rest) {
       f = a.rest[batch];
       if (a.power == 2) f *= f;
     }
     alpha = a.alpha * f, beta = a.beta * f;
+    if (some(col)) fetch(col);  // C of the first 64 columns, while the products run
   }
-  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
-    if (row >= M || col >= a.N) return;
+  // whether any of the warp's 32 rows x 64 columns from col on is there
+  __device__ __forceinline__ bool some(int col) const {
+    return row - panes.lane < M && col < a.N;
+  }
+  __device__ __forceinline__ void fetch(int col) {
+    if (!a.c_planes) return;
+    panes.reuse<0>();
+    panes.fetch(&a.c, a.c_planes, col, row - panes.lane, (int)batch * a.c_stored);
+  }
+  __device__ __forceinline__ void add_c(float (&v)[gemm::kChunk], int first) {
+    for (int p = 0; p < a.c_planes; ++p) {
 #pragma unroll
-    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
-    if (a.c) {
-      const __half *c = a.c + batch * a.c_zs + (int64_t)row * a.c_ld + col;
-      for (int p = 0; p < a.c_planes; ++p) {
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = panes.cell(p, first + i);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < gemm::kChunk; i += 8) {
-          if (col + i >= a.c_ld) break;  // rows of whole groups of 16
-          const uint4 q = *reinterpret_cast<const uint4 *>(c + p * a.c_ps + i);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
-            v[i + 2 * k] = fmaf(beta, f.x, v[i + 2 * k]);
-            v[i + 2 * k + 1] = fmaf(beta, f.y, v[i + 2 * k + 1]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
+          v[8 * i + 2 * k] = fmaf(beta, f.x, v[8 * i + 2 * k]);
+          v[8 * i + 2 * k + 1] = fmaf(beta, f.y, v[8 * i + 2 * k + 1]);
         }
       }
     }
-    if constexpr (kind == kPlanes) {
-      __half *base = a.out + batch * a.zs;
-      for (int p = 0; p < a.out_planes; ++p) {
+  }
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
+    const int first = (j & 1) * 4;  // pieces of the panes' rows: 64 columns in two chunks
+    const int from = col - (first ? gemm::kChunk : 0);
+    if (!some(from)) return;
+#pragma unroll
+    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
+    if (first == 0) {
+      if (a.c_planes) panes.fetched();
+      else panes.reuse<0>();
+    }
+    add_c(v, first);
+    if constexpr (kind == kF32) {
+      float *o = a.f32.at(batch, row) + col;
+      if (row < M && col < a.N) {
+        if (a.wide && col + gemm::kChunk <= a.N) {
+#pragma unroll
+          for (int i = 0; i < gemm::kChunk; i += 4) {
+            const float q[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+            store_vec<4>(o + i, q);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < gemm::kChunk; ++i)
+            if (col + i < a.N) o[i] = v[i];
+        }
+      }
+    } else {
+      for (int p = 0; p < a.planes; ++p) {
         uint32_t w[gemm::kChunk / 2];
 #pragma unroll
-        for (int i = 0; i < gemm::kChunk / 2; ++i) {
-          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t *>(&h);
-          v[2 * i] -= __low2float(h), v[2 * i + 1] -= __high2float(h);
+        for (int i = 0; i < 4; ++i) {
+          uint4 q;
+          if constexpr (kind == kBf16) q = pack_bf16(v + 8 * i);
+          else q = pack8(v + 8 * i);
+          panes.cell(p, first + i) = q;
+          w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
         }
-        __half *o = base + p * a.ps + (int64_t)row * a.ld + col;
-#pragma unroll
-        for (int i = 0; i < gemm::kChunk; i += 8)
-          if (col + i < a.ld && SSD_IN_BOUNDS(col + i + 8 <= a.ld, err, 82))
-            *reinterpret_cast<uint4 *>(o + i) =
-                make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
-        if (mirror) {  // row and column exchanged: the lanes' rows lie side by side
-          uint16_t *m = reinterpret_cast<uint16_t *>(base + p * a.ps) + (int64_t)col * a.ld + row;
+        if (kind == kPlanes && mirror && row < M && SSD_IN_BOUNDS(row < a.ld, err, 82)) {
+          // row and column exchanged: the lanes' rows lie side by side
+          uint16_t *m = reinterpret_cast<uint16_t *>(a.out + batch * a.zs + p * a.ps) +
+                        (int64_t)col * a.ld + row;
 #pragma unroll
           for (int i = 0; i < gemm::kChunk; ++i)
             if (col + i < a.N) m[i * a.ld] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
         }
       }
+    }
+    if (first == 0) return;
+    if constexpr (kind == kF32) {
+      panes.written();  // (C is read)
     } else {
-      using IO = std::conditional_t<kind == kBf16, __nv_bfloat16, float>;
-      IO *o;
-      if constexpr (kind == kBf16) o = a.bf16.at(batch, row) + col;
-      else o = a.f32.at(batch, row) + col;
-      constexpr int V = 16 / (int)sizeof(IO);
-      if (a.wide && col + gemm::kChunk <= a.N) {
-#pragma unroll
-        for (int i = 0; i < gemm::kChunk; i += V) {
-          float q[V];
-#pragma unroll
-          for (int k = 0; k < V; ++k) q[k] = v[i + k];
-          store_vec<V>(o + i, q);
+      panes.written();
+      if (kind == kPlanes || a.wide) {
+        if (panes.lane == 0) {
+          for (int p = 0; p < a.planes; ++p)
+            panes.store(p, &a.d, from, row, (int)batch * a.d_stored + p);
+          ptx::bulk_commit();
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < gemm::kChunk; ++i)
-          if (col + i < a.N) st_io(o + i, v[i]);
+        copy(from);
       }
     }
+    const int next = col + gemm::kChunk;
+    if (next < col0 + a.half && some(next)) fetch(next);
+  }
+  static __device__ __forceinline__ uint4 pack_bf16(const float *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The pane to rows that TMA cannot write: lanes along the columns.
+  __device__ __forceinline__ void copy(int col) {
+    const int row0 = row - panes.lane, rows = min(32, M - row0);
+    if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 83)) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t w = panes.word(0, r);
+      uint16_t *u = reinterpret_cast<uint16_t *>(a.bf16.at(batch, row0 + r) + col) + 2 * panes.lane;
+      if (col + 2 * panes.lane < a.N) u[0] = (uint16_t)w;
+      if (col + 2 * panes.lane + 1 < a.N) u[1] = (uint16_t)(w >> 16);
+    }
+    panes.written();  // (it is read)
   }
   __device__ __forceinline__ void end() {}
 };
@@ -231,9 +308,9 @@ Plan plan_of(const OrthArgs &a, ssd_dtype out, void *ws) {
   p.planes = out == SSD_F32 ? 2 : 1;
   p.side = a.rows < a.cols ? a.rows : a.cols;
   p.ld = gemm::padded(a.cols), p.gram_ld = gemm::padded(p.side);
-  // some 2 blocks an SM over all matrices, 16 rows at least to each
-  int64_t parts = (2 * sm_count() + a.count - 1) / a.count;
-  const int64_t most = (a.rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
+  // some 4 blocks an SM over all matrices, each thread with something to do
+  int64_t parts = (4 * sm_count() + a.count - 1) / a.count;
+  const int64_t most = (a.rows * ((a.cols + 7) / 8) + kNormThreads - 1) / kNormThreads;
   p.parts = (int)(parts < most ? parts : most);
   Carver c(ws);
   p.part = c.take<float>(a.count * p.parts);
@@ -260,11 +337,16 @@ cudaError_t multiply(const CUtensorMap *maps, const Product &q, int bn,
   return cudaErrorInvalidValue;
 }
 
-// Columns to a tile: 128 while tiles of 256 leave pairs of SMs without one.
+// Columns to a tile: 256, or 128 where the tiles then take less time in all.  A
+// stage of a tile of 256 takes 512 clocks of products, one of 128 half that, but
+// loads three quarters as much: 330 measured.
 int tile_columns(const Product &q) {
-  const int64_t tm = (q.M + 255) / 256, tn = (q.N + 255) / 256;
-  const int64_t tiles = q.batch * (q.symmetric ? tm * (tm + 1) / 2 : tm * tn);
-  return tiles < sm_count() / 2 ? 128 : 256;
+  auto rounds = [&](int64_t bn) {
+    const int64_t tm = (q.M + 255) / 256, tn = (q.N + bn - 1) / bn, r = 256 / bn;
+    const int64_t tiles = q.batch * (q.symmetric ? tm * tn - r * (tm * (tm - 1) / 2) : tm * tn);
+    return (tiles + sm_count() / 2 - 1) / (sm_count() / 2);
+  };
+  return rounds(128) * 330 < rounds(256) * 512 ? 128 : 256;
 }
 
 template <typename IN>
@@ -272,83 +354,98 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   const Plan p = plan_of(a, out, ws);
   const bool tall = a.rows > a.cols;
   const int64_t longer = tall ? a.rows : a.cols, xps = a.rows * p.ld;
+  // Planes that X of step k is added in (and held in: those of an fp32 result are
+  // operands too).  A bf16 G is exact in one.
+  auto carried = [&](int k) {
+    return p.planes == 2 || (k < a.steps - 2 && (k > 0 || sizeof(IN) == 4)) ? 2 : 1;
+  };
   const dim3 grid(p.parts, (unsigned)a.count);
   const auto g = view_of<const IN>(a.update);
-  squares_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, p.part, err);
-  start_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, p.part, p.parts, a.eps,
-                                                  p.x[0], p.ld, p.rest, err);
+  const bool wide = view_aligned(a.update, sizeof(IN), 16);
+  squares_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, wide, p.part, err);
+  start_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, wide, p.part, p.parts, a.eps,
+                                                  p.x[0], p.ld, carried(0), p.rest, err);
   cudaError_t e = cudaGetLastError();
 
   const int64_t gps = p.side * p.gram_ld;
   const int64_t xz = a.count * 2, gz = a.count * p.planes;
+  auto map_x = [&](CUtensorMap *m, const __half *x, bool mn, int box) {
+    return gemm::make_map(m, x, a.cols, a.rows, xz, p.ld, xps, mn, box);
+  };
+  auto map_gram = [&](CUtensorMap *m, const __half *x, int box) {
+    return gemm::make_map(m, x, p.side, p.side, gz, p.gram_ld, gps, false, box);
+  };
+  auto pane_x = [&](CUtensorMap *m, const __half *x) {
+    return gemm::make_pane_map(m, x, false, a.cols, a.rows, xz, p.ld, xps);
+  };
+  auto pane_gram = [&](CUtensorMap *m, const __half *x) {
+    return gemm::make_pane_map(m, x, false, p.side, p.side, gz, p.gram_ld, gps);
+  };
   for (int k = 0; k < a.steps && e == cudaSuccess; ++k) {
     const __half *x = p.x[k & 1];
     const bool last = k == a.steps - 1;
     Product q{};
     q.batch = (int)a.count, q.pairs = p.planes == 2 ? 3 : 1;
     CUtensorMap maps[2];
-    bool ok;
 
     // A = X X^T or X^T X
     q.M = q.N = (int)p.side, q.K = (int)longer;
     q.a_mn = q.b_mn = tall, q.a_planes = q.b_planes = 2, q.symmetric = 1;
     int bn = tile_columns(q);
-    ok = gemm::make_map(&maps[0], x, a.cols, a.rows, xz, p.ld, xps, tall, gemm::kRows) &&
-         gemm::make_map(&maps[1], x, a.cols, a.rows, xz, p.ld, xps, tall, bn / 2);
     StepEpi<kPlanes>::Args s{};
     s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
-    s.out = p.gram, s.out_planes = p.planes, s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps;
-    s.N = (int)p.side;
-    if (!ok) return cudaErrorInvalidValue;
+    s.out = p.gram, s.planes = s.d_stored = p.planes, s.half = bn / 2;
+    s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
+    if (!map_x(&maps[0], x, tall, gemm::kRows) || !map_x(&maps[1], x, tall, bn / 2) ||
+        !pane_gram(&s.d, p.gram))
+      return cudaErrorInvalidValue;
     e = multiply<kPlanes>(maps, q, bn, s, err, st);
     if (e != cudaSuccess) break;
 
     // B = b A + c A A
     q.K = (int)p.side, q.a_mn = q.b_mn = 0, q.a_planes = q.b_planes = p.planes;
-    ok = gemm::make_map(&maps[0], p.gram, p.side, p.side, gz, p.gram_ld, gps, false, gemm::kRows) &&
-         gemm::make_map(&maps[1], p.gram, p.side, p.side, gz, p.gram_ld, gps, false, bn / 2);
     s.alpha = a.c / kGramScale, s.beta = a.b, s.rest = nullptr;
-    s.c = p.gram, s.c_planes = p.planes, s.c_ld = p.gram_ld, s.c_ps = gps, s.c_zs = p.planes * gps;
-    s.out = p.poly;
-    if (!ok) return cudaErrorInvalidValue;
+    s.c_planes = s.c_stored = p.planes, s.out = p.poly;
+    if (!map_gram(&maps[0], p.gram, gemm::kRows) || !map_gram(&maps[1], p.gram, bn / 2) ||
+        !pane_gram(&s.c, p.gram) || !pane_gram(&s.d, p.poly))
+      return cudaErrorInvalidValue;
     e = multiply<kPlanes>(maps, q, bn, s, err, st);
     if (e != cudaSuccess) break;
 
     // X <- a X + B X or a X + X B
     q.M = (int)a.rows, q.N = (int)a.cols, q.symmetric = 0;
+    q.a_planes = tall ? 2 : p.planes, q.b_planes = tall ? p.planes : 2, q.b_mn = !tall;
     bn = tile_columns(q);
-    if (tall) {
-      q.a_planes = 2, q.b_planes = p.planes;
-      ok = gemm::make_map(&maps[0], x, a.cols, a.rows, xz, p.ld, xps, false, gemm::kRows) &&
-           gemm::make_map(&maps[1], p.poly, p.side, p.side, gz, p.gram_ld, gps, false, bn / 2);
-    } else {
-      q.a_planes = p.planes, q.b_planes = 2, q.b_mn = 1;
-      ok = gemm::make_map(&maps[0], p.poly, p.side, p.side, gz, p.gram_ld, gps, false,
-                          gemm::kRows) &&
-           gemm::make_map(&maps[1], x, a.cols, a.rows, xz, p.ld, xps, true, bn / 2);
-    }
-    if (!ok) return cudaErrorInvalidValue;
+    if (tall ? !map_x(&maps[0], x, false, gemm::kRows) || !map_gram(&maps[1], p.poly, bn / 2)
+             : !map_gram(&maps[0], p.poly, gemm::kRows) || !map_x(&maps[1], x, true, bn / 2))
+      return cudaErrorInvalidValue;
     auto fill = [&](auto &u) {
       u.alpha = 1.f / kGramScale, u.beta = a.a, u.rest = k ? nullptr : p.rest, u.power = 1;
       if (last) u.alpha /= kScale, u.beta /= kScale;
-      u.c = x, u.c_planes = p.planes == 2 || k < a.steps - 2 ? 2 : 1;
-      u.c_ld = p.ld, u.c_ps = xps, u.c_zs = 2 * xps, u.N = (int)a.cols;
+      u.c_planes = carried(k), u.c_stored = 2, u.planes = 1, u.d_stored = 1;
+      u.N = (int)a.cols, u.half = bn / 2;
+      return pane_x(&u.c, x);
     };
     if (!last) {
       StepEpi<kPlanes>::Args u{};
-      fill(u);
-      u.out = p.x[~k & 1], u.out_planes = p.planes == 2 || k + 1 < a.steps - 2 ? 2 : 1;
-      u.ld = p.ld, u.ps = xps, u.zs = 2 * xps;
+      u.out = p.x[~k & 1];
+      if (!fill(u) || !pane_x(&u.d, u.out)) return cudaErrorInvalidValue;
+      u.planes = carried(k + 1), u.d_stored = 2;
       e = multiply<kPlanes>(maps, q, bn, u, err, st);
     } else if (out == SSD_BF16) {
       StepEpi<kBf16>::Args u{};
-      fill(u);
-      u.bf16 = view_of<__nv_bfloat16>(a.out), u.wide = view_aligned(a.out, 2, 16);
+      u.bf16 = view_of<__nv_bfloat16>(a.out);
+      u.wide = view_aligned(a.out, 2, 16) && a.out->token_stride >= a.cols &&
+               (a.count == 1 || a.out->batch_stride > 0);
+      const int64_t zs = a.count == 1 ? a.rows * a.out->token_stride : a.out->batch_stride;
+      if (!fill(u) || (u.wide && !gemm::make_pane_map(&u.d, u.bf16.p, false, a.cols, a.rows,
+                                                      a.count, a.out->token_stride, zs)))
+        return cudaErrorInvalidValue;
       e = multiply<kBf16>(maps, q, bn, u, err, st);
     } else {
       StepEpi<kF32>::Args u{};
-      fill(u);
       u.f32 = view_of<float>(a.out), u.wide = view_aligned(a.out, 4, 16);
+      if (!fill(u)) return cudaErrorInvalidValue;
       e = multiply<kF32>(maps, q, bn, u, err, st);
     }
   }

@@ -124,7 +124,7 @@ struct Rows {
   float *lse, *g;  // [n] (backward)
 };
 
-constexpr int kPackTokens = 32, kPackThreads = 256;
+constexpr int kPackTokens = 8, kPackThreads = 256;  // a warp to a token
 
 // A block takes kPackTokens tokens.  It counts the targets in front of them
 // itself (they come from L2), so no launch of its own makes the list.
@@ -135,7 +135,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
             const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
             float *__restrict__ lse_out, Rows rows, uint16_t *__restrict__ xp, int64_t ld,
             int64_t ps, int planes, const uint32_t *__restrict__ top, int *err) {
-  __shared__ int sums[kPackThreads / 32], place[kPackTokens];
+  __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   int before = 0;
@@ -151,8 +151,9 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   if (warp == 0) {
     const bool mine = lane < here && counted(targets[first + (lane < here ? lane : 0)], ignore);
     const unsigned all = __ballot_sync(0xffffffffu, mine);
-    place[lane] = mine ? before + __popc(all & ((1u << lane) - 1)) : -1;
-    if (lane == 0) sums[0] = __popc(all);
+    if (lane < kPackTokens) place[lane] = mine ? before + __popc(all & ((1u << lane) - 1)) : -1;
+    if (lane == 0) mine_all = __popc(all);
+    __syncwarp();
     if (lane < here) {
       const int64_t t = first + lane;
       if (mine && SSD_IN_BOUNDS(place[lane] < n, err, 71)) {
@@ -173,20 +174,22 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   }
   __syncthreads();
   const float scale = top ? scale_of(top[kTopX]) : 1.f;
-  for (int i = warp; i < here; i += kPackThreads / 32) {
-    const int64_t t = first + i, b = t / L, at = t % L;
-    if (place[i] >= 0)
-      pack_row(x.at(b, at), xp + (int64_t)place[i] * ld, ps, d, scale, lane, 32);
+  if (warp < here) {
+    const int64_t t = first + warp, b = t / L, at = t % L;
+    if (place[warp] >= 0)
+      pack_row(x.at(b, at), xp + (int64_t)place[warp] * ld, ps, d, scale, lane, 32);
     else if (dx.p)
       for (int64_t c = lane; c < d; c += 32) st_io(dx.at(b, at) + c, 0.f);
   }
-  if (first + kPackTokens >= n) {
-    const int64_t live = before + sums[0], end = (live + gemm::kTileM - 1) / gemm::kTileM * gemm::kTileM;
-    if (tid == 0) *rows.live = (int)live;
-    // the last tile's other rows are operands too: zero
-    for (int p = 0; p < planes; ++p)
-      for (int64_t i = live * ld + tid; i < end * ld; i += kPackThreads) xp[p * ps + i] = 0;
-  }
+  if (first + kPackTokens < n) return;
+  const int64_t live = before + mine_all;
+  if (tid == 0) *rows.live = (int)live;
+  // backward the rows are k of a product, in stages of kTileK: the last one's other
+  // rows are zero (as are those of dz), whatever lay there
+  const int64_t end = rows.lse ? (live + gemm::kTileK - 1) / gemm::kTileK * gemm::kTileK : live;
+  for (int p = 0; p < planes; ++p)
+    for (int64_t i = (live * ld) / 8 + tid; i < end * ld / 8; i += kPackThreads)
+      reinterpret_cast<uint4 *>(xp + p * ps)[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Rows of W for the products, where TMA cannot take them as they are.
@@ -215,10 +218,11 @@ struct StatsEpi {
   };
   const Args &a;
   int *err;
+  static constexpr bool kStaged = false;
   float unit, scale, m, s;  // of the sums: a logit, and its log2e
   int row, run, target;
   bool live;
-  __device__ __forceinline__ StatsEpi(const Args &args, int *e) : a(args), err(e) {
+  __device__ __forceinline__ StatsEpi(const Args &args, gemm::Panes, int *e) : a(args), err(e) {
     unit = a.top ? inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW])) : 1.f;
     scale = unit * kLog2e;
   }
@@ -227,7 +231,7 @@ struct StatsEpi {
     m = -INFINITY, s = 0.f;
     target = live ? a.rows.target[r] - a.word0 : -1;
   }
-  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int) {
     if (col >= a.V) return;
     const int words = a.V - col;
     const int at = target - col;
@@ -258,23 +262,47 @@ struct StatsEpi {
   }
 };
 
+// Eight values as bf16, or as the planes of an fp32.
+__device__ __forceinline__ uint4 pack8(const float *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void split8(const float *v, uint4 &hi, uint4 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half h0, l0, h1, l1;
+    split(v[2 * i], 1.f, h0, l0);
+    split(v[2 * i + 1], 1.f, h1, l1);
+    h[i] = __half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
+    l[i] = __half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // dz of a piece of the vocabulary.
 template <typename IO>
 struct DlogitEpi {
   struct Args {
-    uint16_t *dz;  // [planes][.., ld]
-    int64_t ld, ps;
+    CUtensorMap dz;
     Rows rows;
     const uint32_t *top;
     int V, word0, uniform;
   };
-  static constexpr bool kSplit = sizeof(IO) == 4;
+  static constexpr bool kStaged = true, kSplit = sizeof(IO) == 4;
   const Args &a;
-  int *err;
+  gemm::Panes panes;
   float scale, up, lse, g;
   int row, target;
   bool live;
-  __device__ __forceinline__ DlogitEpi(const Args &args, int *e) : a(args), err(e) {
+  __device__ __forceinline__ DlogitEpi(const Args &args, gemm::Panes p, int *)
+      : a(args), panes(p) {
     scale = up = 1.f;
     if constexpr (kSplit) {
       scale = inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW]));
@@ -287,7 +315,7 @@ struct DlogitEpi {
     g = live ? a.rows.g[r] * up : 0.f;
     target = live ? a.rows.target[r] - a.word0 : -1;
   }
-  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
     const int words = a.V - col, at = target - col;
 #pragma unroll
     for (int i = 0; i < gemm::kChunk; ++i) {
@@ -295,117 +323,170 @@ struct DlogitEpi {
       if (i == at) p -= 1.f;
       v[i] = live && i < words ? p * g : 0.f;
     }
-    if (!SSD_IN_BOUNDS(col + gemm::kChunk <= a.ld, err, 75)) return;
-    uint16_t *o = a.dz + (int64_t)row * a.ld + col;
+    const int first = (j & 1) * 4;  // pieces of the pane's row: 64 columns in two chunks
     if constexpr (kSplit) {
-      uint32_t hi[gemm::kChunk / 2], lo[gemm::kChunk / 2];
+      if (first == 0) panes.reuse<0>();
 #pragma unroll
-      for (int i = 0; i < gemm::kChunk / 2; ++i) {
-        __half h0, l0, h1, l1;
-        split(v[2 * i], 1.f, h0, l0);
-        split(v[2 * i + 1], 1.f, h1, l1);
-        hi[i] = __half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
-        lo[i] = __half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
-      }
-#pragma unroll
-      for (int i = 0; i < gemm::kChunk / 8; ++i) {
-        reinterpret_cast<uint4 *>(o)[i] = *reinterpret_cast<const uint4 *>(hi + 4 * i);
-        reinterpret_cast<uint4 *>(o + a.ps)[i] = *reinterpret_cast<const uint4 *>(lo + 4 * i);
+      for (int i = 0; i < 4; ++i)
+        split8(v + 8 * i, panes.cell(0, first + i), panes.cell(1, first + i));
+      if (first == 0) return;
+      panes.written();
+      if (panes.lane == 0) {
+        panes.store(0, &a.dz, col - gemm::kChunk, row, 0);
+        panes.store(1, &a.dz, col - gemm::kChunk, row, 1);
+        ptx::bulk_commit();
       }
     } else {
+      const int pane = (j >> 1) & 1;
+      if (first == 0) panes.reuse<1>();
 #pragma unroll
-      for (int i = 0; i < gemm::kChunk / 8; ++i) {
-        float w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = v[8 * i + k];
-        store_vec<8>(reinterpret_cast<__nv_bfloat16 *>(o) + 8 * i, w);
+      for (int i = 0; i < 4; ++i) panes.cell(pane, first + i) = pack8(v + 8 * i);
+      if (first == 0) return;
+      panes.written();
+      if (panes.lane == 0) {
+        panes.store(pane, &a.dz, col - gemm::kChunk, row, 0);
+        ptx::bulk_commit();
       }
     }
   }
   __device__ __forceinline__ void end() {}
 };
 
-// The gradients: product 0 adds up dx over the pieces, product 1 is a piece of dW.
+// What the sums of the gradient products are short of: the scales of their
+// operands, and the factor that all tokens have in common.
+struct Factors {
+  Rows rows;
+  const uint32_t *top;
+  const float *gloss;  // one value for all tokens (uniform), or NULL
+  int uniform, mean;
+  __device__ __forceinline__ float of(Top other) const {
+    float f = uniform && gloss ? *gloss : 1.f;
+    if (mean) {
+      const int n = *rows.live;
+      f /= (float)(n > 1 ? n : 1);
+    }
+    if (top) {
+      f *= uniform ? 1.f / 16384.f : inverse_of(scale_of(top[kTopG]));
+      f *= inverse_of(scale_of(top[other]));
+    }
+    return f;
+  }
+};
+
+// The gradients: product 0 adds up dx over the pieces in fp32 (a slab for each
+// part of a piece), product 1 is a piece of dW.
 template <typename IO>
 struct GradEpi {
   struct Args {
-    float *sum;  // [.., ld] dx of the pieces so far; unused with a single one
-    int64_t ld;
-    SeqView<IO> dx;
-    IO *dw;
-    Rows rows;
-    const uint32_t *top;
-    const float *gloss;  // one value for all tokens (uniform), or NULL
-    int64_t L;
-    int d, uniform, mean, first, last, wide_x, wide_w;
+    CUtensorMap sum, dw;  // dw: where its rows allow TMA
+    IO *out;              // this piece's rows of dW
+    Factors f;
+    int d, words, first, direct;
   };
-  static constexpr int kVec = 16 / (int)sizeof(IO);
+  static constexpr bool kStaged = true, kWide = sizeof(IO) == 4;
   const Args &a;
+  gemm::Panes panes;
   int *err;
-  float factor, fx, fw;
-  int which, row;
-  bool live;
-  IO *out;
-  __device__ __forceinline__ GradEpi(const Args &args, int *e) : a(args), err(e) {
-    factor = a.uniform && a.gloss ? *a.gloss : 1.f;
-    if (a.mean) {
-      const int n = *a.rows.live;
-      factor /= (float)(n > 1 ? n : 1);
-    }
-    fx = fw = 1.f;
-    if (a.top) {
-      const float down = a.uniform ? 1.f / 16384.f : inverse_of(scale_of(a.top[kTopG]));
-      fx = down * inverse_of(scale_of(a.top[kTopW]));
-      fw = down * inverse_of(scale_of(a.top[kTopX]));
-    }
+  float factor;
+  int which, row0, slab, pane;  // pane: the one whose store is the older
+  __device__ __forceinline__ GradEpi(const Args &args, gemm::Panes p, int *e)
+      : a(args), panes(p), err(e), factor(args.f.of(kTopX)), pane(0) {}
+  __device__ __forceinline__ void begin(const Tile &o, int r, int, int) {
+    which = o.which, row0 = r - panes.lane, slab = o.batch;
   }
-  __device__ __forceinline__ void begin(const Tile &o, int r, int, int M) {
-    which = o.which, row = r, live = r < M;
-    out = nullptr;
-    if (!live) return;
-    if (which) {
-      out = a.dw + (int64_t)r * a.d;
-    } else if (a.last) {
-      const int64_t t = a.rows.token[r];
-      out = a.dx.at(t / a.L, t % a.L);
-    }
+  // 32 columns of fp32 into a pane
+  __device__ __forceinline__ void put(const float (&v)[gemm::kChunk]) {
+    panes.reuse<1>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      panes.cell(pane, i) =
+          make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    panes.written();
   }
-  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col) {
-    if (!live || col >= a.d) return;
-    const float f = which ? fw : fx;
-#pragma unroll
-    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= f;
-    if (!which && !(a.first && a.last)) {
-      float4 *p = reinterpret_cast<float4 *>(a.sum + (int64_t)row * a.ld + col);
-      if (!SSD_IN_BOUNDS(col + gemm::kChunk <= a.ld, err, 76)) return;
-#pragma unroll
-      for (int i = 0; i < gemm::kChunk / 4; ++i) {
-        float4 s = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : p[i];
-        s.x += v[4 * i], s.y += v[4 * i + 1], s.z += v[4 * i + 2], s.w += v[4 * i + 3];
-        if (!a.last) p[i] = s;
-        v[4 * i] = s.x, v[4 * i + 1] = s.y, v[4 * i + 2] = s.z, v[4 * i + 3] = s.w;
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
+    if (which == 0) {
+      if (col >= a.d) return;
+      put(v);
+      if (panes.lane == 0) {
+        if (a.first) panes.store(pane, &a.sum, col, row0, slab);
+        else panes.add(pane, &a.sum, col, row0, slab);
+        ptx::bulk_commit();
       }
-      if (!a.last) return;
+      pane ^= 1;
+      return;
     }
-    const bool wide = which ? a.wide_w : a.wide_x;
 #pragma unroll
     for (int i = 0; i < gemm::kChunk; ++i) v[i] *= factor;
-    if (wide && col + gemm::kChunk <= a.d) {
+    if constexpr (kWide) {
+      if (col >= a.d || row0 >= a.words) return;
+      put(v);
+    } else {
+      const int first = (j & 1) * 4;  // pieces of the pane's row: 64 columns in two chunks
+      if (first) col -= gemm::kChunk;
+      if (col >= a.d || row0 >= a.words) return;
+      if (first == 0) panes.reuse<1>();
 #pragma unroll
-      for (int i = 0; i < gemm::kChunk / kVec; ++i) {
-        float w[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) w[k] = v[kVec * i + k];
-        store_vec<kVec>(out + col + kVec * i, w);
+      for (int i = 0; i < 4; ++i) panes.cell(pane, first + i) = pack8(v + 8 * i);
+      if (first == 0) return;
+      panes.written();
+    }
+    if (a.direct) {
+      if (panes.lane == 0) {
+        panes.store(pane, &a.dw, col, row0, 0);
+        ptx::bulk_commit();
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < gemm::kChunk; ++i)
-        if (col + i < a.d) st_io(out + col + i, v[i]);
+      copy(col);
     }
+    pane ^= 1;
+  }
+  // A pane to rows that TMA cannot write: lanes along the columns.
+  __device__ __forceinline__ void copy(int col) {
+    const int rows = min(32, a.words - row0);
+    if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 76)) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t w = panes.word(pane, r);
+      IO *o = a.out + (int64_t)(row0 + r) * a.d + col;
+      if constexpr (kWide) {
+        if (col + panes.lane < a.d) o[panes.lane] = __uint_as_float(w);
+      } else {
+        uint16_t *u = reinterpret_cast<uint16_t *>(o) + 2 * panes.lane;
+        if (col + 2 * panes.lane < a.d) u[0] = (uint16_t)w;
+        if (col + 2 * panes.lane + 1 < a.d) u[1] = (uint16_t)(w >> 16);
+      }
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ void end() {}
 };
+
+// dx of the tokens with a target: its slabs added in their order, scaled, and
+// put back in the tokens' places.  A warp takes a row.
+template <typename IO>
+__global__ void __launch_bounds__(256)
+unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, Factors f,
+              SeqView<IO> dx, int64_t L, int64_t d, int *err) {
+  const float factor = f.of(kTopW);
+  const int live = *f.rows.live, lane = threadIdx.x % 32;
+  for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < live; r += gridDim.x * 8ll) {
+    const int64_t t = f.rows.token[r];
+    IO *o = dx.at(t / L, t % L);
+    const float *s = sum + r * ld;
+    if (!SSD_IN_BOUNDS(d <= ld, err, 79)) return;
+#pragma unroll 4
+    for (int64_t c = lane * 2; c < d; c += 64) {  // ld is even
+      float2 v = *reinterpret_cast<const float2 *>(s + c);
+      for (int z = 1; z < slabs; ++z) {
+        const float2 q = *reinterpret_cast<const float2 *>(s + z * zs + c);
+        v.x += q.x, v.y += q.y;
+      }
+      st_io(o + c, v.x * factor);
+      if (c + 1 < d) st_io(o + c + 1, v.y * factor);
+    }
+  }
+}
 
 // ------------------------------------------------------------ joining the runs
 
@@ -471,9 +552,10 @@ struct Plan {
   uint32_t *top;
   Rows r;
   uint16_t *xp, *wp, *dz;
-  float2 *part;
+  float2 *stat;
   float *loss, *sum;
   int64_t runs;
+  int slabs, part;  // parts of the k of dx (the piece's words), stages in each
   size_t bytes;
 };
 
@@ -506,11 +588,21 @@ Plan plan_of(const LossArgs &a, ssd_dtype io, bool back, void *ws) {
     p.r.lse = c.take<float>(a.n);
     p.r.g = c.take<float>(a.n);
     p.dz = c.take<uint16_t>(p.planes * p.rows * p.dz_ld);
-    p.sum = c.take<float>(p.piece < a.V ? p.rows * round_up(a.d, gemm::kChunk) : 0);
+    // dx has few tiles and many k where there are few tokens: as many parts as
+    // make two of its tiles no longer than a pair's share of all stages
+    const int64_t tn = round_up(a.d, kBN) / kBN, pairs = sm_count() / 2;
+    const int64_t steps = p.piece / gemm::kTileK, tall = p.rows / gemm::kTileM;
+    const int64_t all = tn * (tall * steps + p.piece / gemm::kTileM * (p.rows / gemm::kTileK));
+    const int64_t share = all / (2 * pairs) > 32 ? all / (2 * pairs) : 32;
+    int64_t slabs = (steps + share - 1) / share;
+    slabs = slabs > 8 ? 8 : slabs;
+    p.part = (int)((steps + slabs - 1) / slabs);
+    p.slabs = (int)((steps + p.part - 1) / p.part);
+    p.sum = c.take<float>(p.slabs * p.rows * gemm::padded(a.d));
   } else {
     p.r.zt = c.take<float>(a.n);
     p.loss = c.take<float>(a.n);
-    p.part = c.take<float2>(p.runs * p.rows);
+    p.stat = c.take<float2>(p.runs * p.rows);
   }
   p.bytes = c.used;
   return p;
@@ -590,13 +682,13 @@ struct Calls {
       CUtensorMap maps[2];
       Product q;
       if (!logits(a, p, w, maps, &q)) return cudaErrorInvalidValue;
-      const StatsEpi::Args s{p.part, p.rows, p.r, kPlanes == 2 ? p.top : nullptr, (int)w.n,
+      const StatsEpi::Args s{p.stat, p.rows, p.r, kPlanes == 2 ? p.top : nullptr, (int)w.n,
                              (int)word0, (int)(word0 / kRun)};
       e = gemm::launch<StatsEpi, kBN, kSegment>(maps, &q, 1, kBf16, s, err, st);
     }
     if (e != cudaSuccess) return e;
     join_kernel<<<(unsigned)((a.n + 31) / 32), 32 * kJoinWarps, 0, st>>>(
-        p.part, p.rows, (int)p.runs, p.r, loss, a.lse, err);
+        p.stat, p.rows, (int)p.runs, p.r, loss, a.lse, err);
     if (a.total)
       total_kernel<<<1, 1024, 0, st>>>(loss, a.n, p.r.live, a.reduction == SSD_REDUCE_MEAN,
                                        a.total, err);
@@ -608,6 +700,8 @@ struct Calls {
     const bool uniform = a.reduction != SSD_REDUCE_NONE || !a.gloss;
     const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
     const int64_t ps = p.rows * p.dz_ld;
+    const Factors f{p.r, top, uniform ? a.gloss : nullptr, uniform,
+                    a.reduction == SSD_REDUCE_MEAN};
     cudaError_t e = pack(a, p, true, nullptr, nullptr, err, st);
     for (int64_t word0 = 0; word0 < a.V && e == cudaSuccess; word0 += p.piece) {
       Words w;
@@ -616,51 +710,41 @@ struct Calls {
       CUtensorMap maps[4];
       Product q[2];
       if (!logits(a, p, w, maps, q)) return cudaErrorInvalidValue;
-      const typename DlogitEpi<IO>::Args z{p.dz, p.dz_ld, ps, p.r, top, (int)w.n, (int)word0,
-                                           uniform};
+      typename DlogitEpi<IO>::Args z{};
+      z.rows = p.r, z.top = top, z.V = (int)w.n, z.word0 = (int)word0, z.uniform = uniform;
+      if (!gemm::make_pane_map(&z.dz, p.dz, false, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps))
+        return cudaErrorInvalidValue;
       e = gemm::launch<DlogitEpi<IO>, kBN, kSegment>(maps, q, 1, kBf16, z, err, st);
       if (e != cudaSuccess) break;
       // dx [n, d] += dz [n, words] W [words, d];  dW [words, d] = dz^T x
-      int count = 0;
-      if (a.dx) {
-        q[0] = product(a.n, a.d, w.n);
-        q[0].live_m = p.r.live, q[0].b_mn = 1;
-        if (!gemm::make_map(&maps[0], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, false,
-                            gemm::kRows) ||
-            !gemm::make_map(&maps[1], w.at, a.d, w.n, kPlanes, w.ld, w.zs, true, kBN / 2))
-          return cudaErrorInvalidValue;
-        count = 1;
-      }
-      if (a.dweight) {
-        q[1] = product(w.n, a.d, a.n);
-        q[1].live_k = p.r.live, q[1].a_mn = q[1].b_mn = 1;
-        if (!gemm::make_map(&maps[2], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, true,
-                            gemm::kRows) ||
-            !gemm::make_map(&maps[3], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, true,
-                            kBN / 2))
-          return cudaErrorInvalidValue;
-        ++count;
-      }
-      if (count == 0) continue;
+      q[0] = product(a.dx ? a.n : 0, a.d, w.n);
+      q[0].b_mn = 1, q[0].batch = p.slabs, q[0].part = p.part;
+      if (a.dx) q[0].live_m = p.r.live;
+      q[1] = product(w.n, a.d, a.n);
+      q[1].live_k = p.r.live, q[1].a_mn = q[1].b_mn = 1;
       typename GradEpi<IO>::Args g{};
-      g.sum = p.sum, g.ld = round_up(a.d, gemm::kChunk), g.dx = view_of<IO>(a.dx);
-      g.dw = static_cast<IO *>(a.dweight) + word0 * a.d;
-      g.rows = p.r, g.top = top, g.gloss = uniform ? a.gloss : nullptr, g.L = a.L;
-      g.d = (int)a.d, g.uniform = uniform;
-      g.mean = a.reduction == SSD_REDUCE_MEAN;
-      g.first = word0 == 0, g.last = word0 + p.piece >= a.V;
-      g.wide_x = view_aligned(a.dx, sizeof(IO), 16);
-      g.wide_w = ptr_aligned(a.dweight, 16) && a.d * sizeof(IO) % 16 == 0;
-      // with dW alone it is still product 1 to the epilogue: product 0 has no rows
-      if (!a.dx) {
-        q[0] = q[1];
-        q[0].M = 0, q[0].live_m = nullptr;
-        maps[0] = maps[2], maps[1] = maps[3];
-        count = 2;
-      }
-      e = gemm::launch<GradEpi<IO>, kBN, kSegment>(maps, q, count, kBf16, g, err, st);
+      g.out = static_cast<IO *>(a.dweight) + word0 * a.d;
+      g.f = f, g.d = (int)a.d, g.words = (int)w.n, g.first = word0 == 0;
+      g.direct = ptr_aligned(a.dweight, 16) && a.d * sizeof(IO) % 16 == 0;
+      const int64_t sld = gemm::padded(a.d);
+      if (!gemm::make_map(&maps[0], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, false,
+                          gemm::kRows) ||
+          !gemm::make_map(&maps[1], w.at, a.d, w.n, kPlanes, w.ld, w.zs, true, kBN / 2) ||
+          !gemm::make_map(&maps[2], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, true,
+                          gemm::kRows) ||
+          !gemm::make_map(&maps[3], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, true,
+                          kBN / 2) ||
+          !gemm::make_pane_map(&g.sum, p.sum, true, sld, p.rows, p.slabs, sld, p.rows * sld) ||
+          (a.dweight && g.direct &&
+           !gemm::make_pane_map(&g.dw, g.out, !kBf16, a.d, w.n, 1, a.d, w.n * a.d)))
+        return cudaErrorInvalidValue;
+      e = gemm::launch<GradEpi<IO>, kBN, kSegment>(maps, q, a.dweight ? 2 : 1, kBf16, g, err, st);
     }
-    return e;
+    if (e != cudaSuccess || !a.dx) return e;
+    const int64_t sld = gemm::padded(a.d), blocks = (a.n + 7) / 8;
+    unpack_kernel<IO><<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(
+        p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx), a.L, a.d, err);
+    return cudaGetLastError();
   }
 };
 
