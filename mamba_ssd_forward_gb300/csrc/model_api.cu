@@ -55,7 +55,7 @@ ssd_status add_norm_args(const ssd_add_norm_dims *d, ssd_dtype t, ssd_dtype stre
     return SSD_ERR_INVALID_ARG;
   const ssd_status s = common_dims(d->batch, d->seqlen, d->channels, kMaxTokens);
   if (s != SSD_OK) return s;
-  if (d->channels > 32768 || (double)d->batch * d->seqlen > (double)kMaxTokens)
+  if (d->channels > 16384 || (double)d->batch * d->seqlen > (double)kMaxTokens)
     return SSD_ERR_UNSUPPORTED;
   *a = ssd::AddNormArgs{};
   a->b = d->batch, a->L = d->seqlen, a->D = d->channels, a->eps = d->eps;
