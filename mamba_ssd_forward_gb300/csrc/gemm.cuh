@@ -189,6 +189,18 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
                : "memory");
 }
 
+// One lane of a converged warp, the same each time.  (With it rather than a
+// comparison of the lane the compiler keeps what the instructions below take in
+// uniform registers.)
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
+}
+// A value that is the same in all lanes, said so.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Instruction descriptor of 256 x n products with fp32 sums: fp16 (0) or bf16
 // (1) operands.
 __device__ __forceinline__ uint32_t idesc(int n, int bf16, int a_mn, int b_mn) {
@@ -317,50 +329,55 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   const uint32_t tmem = tmem_slot;
   const int step = gridDim.x / 2, start = blockIdx.x / 2;
 
-  // The loops of warps 0 and 1 belong to one thread each and are latency bound
-  // (a stage is 512 clocks of products): what does not change within a tile
-  // is in registers.  Read from shared memory as they went, a stage took 740.
+  // The loops of warps 0 and 1 are latency bound (a stage is 512 clocks of
+  // products): what does not change within a tile is in registers, and one lane
+  // is elected where an instruction is a single thread's.
   if (warp == 0) {
-    if (lane == 0) {
+    if (elected()) {
       ptx::prefetch_tmap(&a0);
       ptx::prefetch_tmap(&b0);
       if (count > 1) {
         ptx::prefetch_tmap(&a1);
         ptx::prefetch_tmap(&b1);
       }
-      int s = 0, round = 0;
-      const uint32_t bars = in_first(full);
-      for (int t = start; t < walk.total; t += step) {
-        const Tile o = walk.at(t, rank);
-        const Product &p = walk.p[o.which];
-        const CUtensorMap *ma = o.which ? &a1 : &a0, *mb = o.which ? &b1 : &b0;
-        const int a_mn = p.a_mn, b_mn = p.b_mn, pairs = p.pairs, n = o.n + rank * (kBN / 2);
-        const int z = p.part ? 0 : o.batch, za = z * p.a_planes, zb = z * p.b_planes;
-        for (int pair = 0; pair < pairs; ++pair) {
-          // with three: lo hi, hi lo, hi hi
-          const int z0 = za + (pairs == 3 && pair == 0), z1 = zb + (pairs == 3 && pair == 1);
-          for (int k = o.k0; k < o.k0 + o.steps; ++k) {
-            if (round) ptx::mbar_wait(&empty[s], (round - 1) & 1, err, 300);
+    }
+    int s = 0, round = 0;
+    const uint32_t bars = in_first(full);
+    for (int t = start; t < walk.total; t += step) {
+      const Tile o = walk.at(t, rank);
+      const int which = uniform(o.which), k0 = uniform(o.k0), k1 = k0 + uniform(o.steps);
+      const Product &p = which ? p1 : p0;
+      const CUtensorMap *ma = which ? &a1 : &a0, *mb = which ? &b1 : &b0;
+      const int a_mn = p.a_mn, b_mn = p.b_mn, pairs = p.pairs;
+      const int m = uniform(o.m), n = uniform(o.n) + rank * (kBN / 2);
+      const int z = p.part ? 0 : uniform(o.batch), za = z * p.a_planes, zb = z * p.b_planes;
+      for (int pair = 0; pair < pairs; ++pair) {
+        // with three: lo hi, hi lo, hi hi
+        const int z0 = za + (pairs == 3 && pair == 0), z1 = zb + (pairs == 3 && pair == 1);
+        for (int k = k0; k < k1; ++k) {
+          if (round) ptx::mbar_wait(&empty[s], (round - 1) & 1, err, 300);
+          if (elected()) {
             if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
             uint8_t *at = smem + s * S::kStage;
-            load_operand<kRows>(at, ma, a_mn, o.m, k * kTileK, z0, bars + 8 * s);
+            load_operand<kRows>(at, ma, a_mn, m, k * kTileK, z0, bars + 8 * s);
             load_operand<kBN / 2>(at + kBytesA, mb, b_mn, n, k * kTileK, z1, bars + 8 * s);
-            if (++s == S::kStages) s = 0, ++round;
           }
+          __syncwarp();
+          if (++s == S::kStages) s = 0, ++round;
         }
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       int s = 0, parity = 0, n = 0;
       const uint32_t ring = ptx::smem_u32(smem) >> 4;
       for (int t = start; t < walk.total; t += step) {
         const Tile o = walk.at(t, rank);
-        const Product &p = walk.p[o.which];
+        const Product &p = uniform(o.which) ? p1 : p0;
         const uint32_t id = idesc(kBN, bf16, p.a_mn, p.b_mn);
         const uint64_t da = desc(p.a_mn), db = desc(p.b_mn);
         const uint32_t ia = p.a_mn ? 128 : 2, ib = p.b_mn ? 128 : 2;  // to the next 16 k, by 16 bytes
-        const int steps = o.steps * p.pairs, each = kSegment ? kSegment : steps;
+        const int steps = uniform(o.steps) * p.pairs, each = kSegment ? kSegment : steps;
         int k = 0;
         do {  // a segment (an empty one where there are no k)
           const uint32_t d = tmem + (n & 1) * kBN;
@@ -371,13 +388,17 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
             ptx::mbar_wait(&full[s], parity, err, 302);
             ptx::tc_fence_after();
             const uint32_t at = ring + s * (S::kStage / 16), bt = at + kBytesA / 16;
+            if (elected()) {
 #pragma unroll
-            for (int kk = 0; kk < kTileK / 16; ++kk)
-              mma(d, da + at + kk * ia, db + bt + kk * ib, id, k > begin || kk > 0);
-            commit_both(&empty[s]);
+              for (int kk = 0; kk < kTileK / 16; ++kk)
+                mma(d, da + at + kk * ia, db + bt + kk * ib, id, k > begin || kk > 0);
+              commit_both(&empty[s]);
+            }
+            __syncwarp();
             if (++s == S::kStages) s = 0, parity ^= 1;
           }
-          commit_both(&accfull[n & 1]);
+          if (elected()) commit_both(&accfull[n & 1]);
+          __syncwarp();
           ++n;
         } while (k < steps);
       }
