@@ -49,14 +49,15 @@ constexpr int kChunk = 32;  // columns an epilogue thread holds at a time
 constexpr int kExact = 4;   // stages to a segment where fp32's precision is asked for
 constexpr int kBytesA = kRows * 128;
 
-constexpr int kPane = 32 * 128;  // bytes of a pane: 32 rows of 128 bytes, swizzled
+constexpr int kPaneBytes = 8192;  // of an epilogue's warp
+constexpr int kPaneBars = 4;
 
-// kStaged: the epilogue's warps have two panes each.
+// kStaged: the epilogue's warps have panes.
 template <int kBN, bool kStaged>
 struct Shape {
   static constexpr int kBytesB = kBN / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kPanes = kStaged ? 2 * kEpiWarps * kPane : 0;
+  static constexpr int kPanes = kStaged ? kEpiWarps * kPaneBytes : 0;
   static constexpr int kStages = (229376 - kPanes) / kStage;
   static constexpr int kSmem = kStages * kStage + kPanes + 1024;
   static constexpr uint32_t kTmemCols = 2 * kBN;
@@ -227,26 +228,33 @@ __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *ma
   }
 }
 
-// A warp's two panes in shared memory.  A thread holds a row of the tile; through a
-// pane, 32 rows of 128 bytes go to memory and come from it by TMA, which clips
-// what lies outside the array.  (Row by row from registers every access would
-// touch 32 lines: measured 16000 clocks a tile against 6000 of products.)
+// A warp's panes in shared memory.  A thread holds a row of the tile; through a
+// pane, 32 rows, values go to memory and come from it by TMA, which clips what
+// lies outside the array.  (Row by row from registers every access would touch 32
+// lines: measured 16000 clocks a tile against 6000 of products.)  Two panes with
+// rows of 128 bytes, or four with rows of 64, swizzled.
+template <int kRowBytes>
 struct Panes {
+  static constexpr int kBytes = 32 * kRowBytes;
   uint8_t *at;
-  uint64_t *bar;
+  uint64_t *bars;  // kPaneBars
   int *err;
   int lane;
-  uint32_t parity;
+  uint32_t phases;  // a bit for each barrier
   __device__ __forceinline__ Panes(uint8_t *p, uint64_t *b, int *e)
-      : at(p), bar(b), err(e), lane(threadIdx.x & 31), parity(0) {}
-  // 16 bytes of this thread's row: piece 0 .. 7 of pane i
-  __device__ __forceinline__ uint4 &cell(int i, int piece) const {
-    return *reinterpret_cast<uint4 *>(at + i * kPane + lane * 128 + ((piece ^ (lane & 7)) << 4));
+      : at(p), bars(b), err(e), lane(threadIdx.x & 31), phases(0) {}
+  // byte offset of 16-byte piece `piece` of row r
+  __device__ __forceinline__ static int swizzled(int r, int piece) {
+    return r * kRowBytes + ((kRowBytes == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
   }
-  // 4 bytes of row r: word `lane` of pane i
-  __device__ __forceinline__ uint32_t word(int i, int r) const {
-    return *reinterpret_cast<const uint32_t *>(at + i * kPane + r * 128 +
-                                               (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+  // 16 bytes of this thread's row
+  __device__ __forceinline__ uint4 &cell(int pane, int piece) const {
+    return *reinterpret_cast<uint4 *>(at + pane * kBytes + swizzled(lane, piece));
+  }
+  // 4 bytes of row r
+  __device__ __forceinline__ uint32_t word(int pane, int r, int w) const {
+    return *reinterpret_cast<const uint32_t *>(at + pane * kBytes + swizzled(r, w >> 2) +
+                                               (w & 3) * 4);
   }
   // All but the newest kLeft groups of stores have read their panes.
   template <int kLeft>
@@ -254,40 +262,43 @@ struct Panes {
     if (lane == 0) ptx::bulk_wait_read<kLeft>();
     __syncwarp();
   }
-  // The warp has written its panes: lane 0 may store them.
+  // The warp has written (or read) its panes: lane 0 may store (or load) them.
   __device__ __forceinline__ void written() const {
     ptx::fence_async_smem();
     __syncwarp();
   }
-  __device__ __forceinline__ void store(int i, const CUtensorMap *map, int col, int row,
+  __device__ __forceinline__ void store(int pane, const CUtensorMap *map, int col, int row,
                                         int z) const {  // lane 0, then commit
-    ptx::tma_store_3d(map, at + i * kPane, col, row, z);
+    ptx::tma_store_3d(map, at + pane * kBytes, col, row, z);
   }
-  __device__ __forceinline__ void add(int i, const CUtensorMap *map, int col, int row,
+  __device__ __forceinline__ void add(int pane, const CUtensorMap *map, int col, int row,
                                       int z) const {  // fp32
     asm volatile(
         "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
         " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-        "r"(ptx::smem_u32(at + i * kPane)), "r"(col), "r"(row), "r"(z)
+        "r"(ptx::smem_u32(at + pane * kBytes)), "r"(col), "r"(row), "r"(z)
         : "memory");
   }
-  // Loads panes 0 .. n - 1 (z, z + 1); the stores from them have to be read.
-  __device__ __forceinline__ void fetch(const CUtensorMap *map, int n, int col, int row, int z) {
+  // Loads n panes from `pane` on (z, z + 1, ..); the stores from them have to be
+  // read.  fetched: they are there.
+  __device__ __forceinline__ void fetch(int bar, int pane, int n, const CUtensorMap *map, int col,
+                                        int row, int z) const {
     if (lane == 0) {
-      ptx::mbar_arrive_expect_tx(bar, n * kPane);
-      for (int i = 0; i < n; ++i) ptx::tma_load_3d(at + i * kPane, map, col, row, z + i, bar);
+      ptx::mbar_arrive_expect_tx(&bars[bar], n * kBytes);
+      for (int i = 0; i < n; ++i)
+        ptx::tma_load_3d(at + (pane + i) * kBytes, map, col, row, z + i, &bars[bar]);
     }
   }
-  __device__ __forceinline__ void fetched() {
-    ptx::mbar_wait(bar, parity, err, 304);
-    parity ^= 1;
+  __device__ __forceinline__ void fetched(int bar) {
+    ptx::mbar_wait(&bars[bar], (phases >> bar) & 1, err, 304);
+    phases ^= 1u << bar;
   }
 };
 
 // kSegment: stages to a segment, 0: all k in one.
 // Epi: constructed from its Args and panes by every epilogue thread, then per tile
 // begin(tile, row, column, rows), chunk(v, column, j) for each 32 columns of the
-// thread's row, end().  kStaged: it uses the panes.
+// thread's row, end().  kStaged: it uses the panes, of type Pane.
 template <class Epi, int kBN, int kSegment>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
@@ -302,7 +313,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   // empty: its products are done; accfull: a tile's are; accfree: both blocks'
   // epilogues have read them (the first block's)
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], accfull[2], accfree[2];
-  __shared__ __align__(8) uint64_t landed[kEpiWarps];  // panes of each epilogue warp
+  __shared__ __align__(8) uint64_t landed[kEpiWarps][kPaneBars];  // panes of each epilogue warp
   __shared__ uint32_t tmem_slot;
   __shared__ Walk<kBN> walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,8 +328,10 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       ptx::mbar_init(&accfull[i], 1);
       ptx::mbar_init(&accfree[i], 2 * kEpiWarps);
     }
-    for (int i = 0; i < kEpiWarps; ++i) ptx::mbar_init(&landed[i], 1);
+    for (int i = 0; i < kEpiWarps * kPaneBars; ++i) ptx::mbar_init(&landed[0][i], 1);
     ptx::fence_mbar_init();
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();  // (the numbers of rows are an earlier launch's)
     walk.plan(p0, p1, count);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, S::kTmemCols);
@@ -326,6 +339,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   __syncthreads();
   cluster_sync();
   ptx::tc_fence_after();
+  ptx::griddep_wait();
   const uint32_t tmem = tmem_slot;
   const int step = gridDim.x / 2, start = blockIdx.x / 2;
 
@@ -406,8 +420,8 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   } else {
     constexpr int kHalf = kBN / 2, kChunks = kHalf / kChunk;
     const int quad = warp & 3, c0 = warp >= 6 ? kHalf : 0;
-    uint8_t *panes = smem + S::kStages * S::kStage + (warp - 2) * 2 * kPane;
-    Epi epi(args, Panes(panes, &landed[warp - 2], err), err);
+    uint8_t *panes = smem + S::kStages * S::kStage + (warp - 2) * kPaneBytes;
+    Epi epi(args, typename Epi::Pane(panes, landed[warp - 2], err), err);
     int n = 0;
     // 32 columns of the accumulator at `at`; the last ones hand it back
     auto read = [&](uint32_t at, int j, uint32_t (&r0)[16], uint32_t (&r1)[16]) {
@@ -497,17 +511,33 @@ inline bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t r
 }
 
 // Map of an array [z][rows][cols] for panes.
-inline bool make_pane_map(CUtensorMap *map, const void *base, bool fp32, int64_t cols, int64_t rows,
-                          int64_t z, int64_t ld, int64_t zs) {
+template <int kRowBytes>
+bool make_pane_map(CUtensorMap *map, const void *base, bool fp32, int64_t cols, int64_t rows,
+                   int64_t z, int64_t ld, int64_t zs) {
   const uint64_t e = fp32 ? 4 : 2;
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)z};
   const uint64_t strides[2] = {(uint64_t)ld * e, (uint64_t)zs * e};
-  const uint32_t b[3] = {(uint32_t)(128 / e), 32, 1};
-  return make_tmap_sw128(map, base, !fp32, 3, dims, strides, b);
+  const uint32_t b[3] = {(uint32_t)(kRowBytes / e), 32, 1};
+  return (kRowBytes == 128 ? make_tmap_sw128 : make_tmap_sw64)(map, base, !fp32, 3, dims, strides,
+                                                               b);
 }
 
 // Elements to a row of an operand array: rows start on 32 bytes.
 inline int64_t padded(int64_t cols) { return (cols + 15) / 16 * 16; }
+
+// A launch that may start while the launch before it on the stream ends: the kernel
+// waits (griddep_wait) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         A... a) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(a)...);
+}
 
 // Launches `count` products (one or two) as one grid.
 template <class Epi, int kBN, int kSegment = 0>
@@ -533,9 +563,8 @@ cudaError_t launch(const CUtensorMap *maps, const Product *p, int count, bool bf
   const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
   if (!grid) return cudaSuccess;
   const int last = count - 1;
-  kernel<<<grid, kThreads, S::kSmem, st>>>(maps[0], maps[1], maps[2 * last], maps[2 * last + 1],
-                                           p[0], p[last], count, bf16, args, err);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(grid), kThreads, S::kSmem, st, maps[0], maps[1], maps[2 * last],
+                      maps[2 * last + 1], p[0], p[last], count, (int)bf16, args, err);
 }
 
 }  // namespace gemm

@@ -80,6 +80,7 @@ squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
   __shared__ float sums[kNormThreads / 32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
+  ptx::griddep_launch_dependents();
   if (!SSD_IN_BOUNDS(rows > 0 && cols > 0, err, 80)) return;
   each8(g, rows, cols, wide, [&](const float (&v)[8], int64_t, int64_t) {
 #pragma unroll
@@ -118,6 +119,8 @@ start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
              int64_t ld, int planes, float *__restrict__ rest, int *err) {
   const int64_t z = blockIdx.y;
   const int lane = threadIdx.x % 32;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   float s = 0.f;  // every warp adds the parts in the same order
   for (int i = lane; i < parts; i += 32) s += part[z * parts + i];
 #pragma unroll
@@ -160,14 +163,15 @@ struct StepEpi {
     int N, wide;  // columns; wide: rows of the result start on 16 bytes
   };
   static constexpr bool kStaged = true;
+  using Pane = gemm::Panes<64>;
   const Args &a;
-  gemm::Panes panes;
+  Pane panes;
   int *err;
   float alpha, beta;
-  int row, col0, M, mirror;
+  int row, col0, M, mirror, slots;  // slots: of one pane or two, for a chunk's planes
   int64_t batch;
-  __device__ __forceinline__ StepEpi(const Args &args, gemm::Panes p, int *e)
-      : a(args), panes(p), err(e) {}
+  __device__ __forceinline__ StepEpi(const Args &args, Pane p, int *e)
+      : a(args), panes(p), err(e), slots(args.c_planes == 2 || args.planes == 2 ? 2 : 4) {}
   __device__ __forceinline__ void begin(const Tile &o, int r, int col, int rows) {
     row = r, col0 = col, M = rows, mirror = o.mirror, batch = o.batch;
     float f = 1.f;
@@ -176,46 +180,46 @@ struct StepEpi {
       if (a.power == 2) f *= f;
     }
     alpha = a.alpha * f, beta = a.beta * f;
-    if (some(col)) fetch(col);  // C of the first 64 columns, while the products run
-  }
-  // whether any of the warp's 32 rows x 64 columns from col on is there
-  __device__ __forceinline__ bool some(int col) const {
-    return row - panes.lane < M && col < a.N;
-  }
-  __device__ __forceinline__ void fetch(int col) {
-    if (!a.c_planes) return;
     panes.reuse<0>();
-    panes.fetch(&a.c, a.c_planes, col, row - panes.lane, (int)batch * a.c_stored);
+    fetch(0, slots);  // C of the first chunks, while the products run
   }
-  __device__ __forceinline__ void add_c(float (&v)[gemm::kChunk], int first) {
-    for (int p = 0; p < a.c_planes; ++p) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 q = panes.cell(p, first + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
-          v[8 * i + 2 * k] = fmaf(beta, f.x, v[8 * i + 2 * k]);
-          v[8 * i + 2 * k + 1] = fmaf(beta, f.y, v[8 * i + 2 * k + 1]);
-        }
-      }
-    }
+  // whether any of the warp's 32 rows x 32 columns of chunk j is there
+  __device__ __forceinline__ bool some(int j) const {
+    return row - panes.lane < M && col0 + gemm::kChunk * j < a.N;
+  }
+  __device__ __forceinline__ void fetch(int from, int to) {
+    if (!a.c_planes) return;
+    for (int j = from; j < to && gemm::kChunk * j < a.half; ++j)
+      if (some(j))
+        panes.fetch(j % slots, j % slots * (4 / slots), a.c_planes, &a.c, col0 + gemm::kChunk * j,
+                    row - panes.lane, (int)batch * a.c_stored);
   }
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
-    const int first = (j & 1) * 4;  // pieces of the panes' rows: 64 columns in two chunks
-    const int from = col - (first ? gemm::kChunk : 0);
-    if (!some(from)) return;
+    if (!some(j)) return;
+    const int slot = j % slots, pane = slot * (4 / slots);
 #pragma unroll
     for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
-    if (first == 0) {
-      if (a.c_planes) panes.fetched();
-      else panes.reuse<0>();
+    if (a.c_planes) {
+      panes.fetched(slot);
+      for (int p = 0; p < a.c_planes; ++p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 q = panes.cell(pane + p, i);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
+            v[8 * i + 2 * k] = fmaf(beta, f.x, v[8 * i + 2 * k]);
+            v[8 * i + 2 * k + 1] = fmaf(beta, f.y, v[8 * i + 2 * k + 1]);
+          }
+        }
+      }
+    } else if (j >= slots) {
+      panes.reuse<1>();
     }
-    add_c(v, first);
     if constexpr (kind == kF32) {
-      float *o = a.f32.at(batch, row) + col;
-      if (row < M && col < a.N) {
+      if (row < M) {
+        float *o = a.f32.at(batch, row) + col;
         if (a.wide && col + gemm::kChunk <= a.N) {
 #pragma unroll
           for (int i = 0; i < gemm::kChunk; i += 4) {
@@ -228,6 +232,7 @@ struct StepEpi {
             if (col + i < a.N) o[i] = v[i];
         }
       }
+      panes.written();  // (C is read)
     } else {
       for (int p = 0; p < a.planes; ++p) {
         uint32_t w[gemm::kChunk / 2];
@@ -236,7 +241,7 @@ struct StepEpi {
           uint4 q;
           if constexpr (kind == kBf16) q = pack_bf16(v + 8 * i);
           else q = pack8(v + 8 * i);
-          panes.cell(p, first + i) = q;
+          panes.cell(pane + p, i) = q;
           w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
         }
         if (kind == kPlanes && mirror && row < M && SSD_IN_BOUNDS(row < a.ld, err, 82)) {
@@ -248,24 +253,21 @@ struct StepEpi {
             if (col + i < a.N) m[i * a.ld] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
         }
       }
-    }
-    if (first == 0) return;
-    if constexpr (kind == kF32) {
-      panes.written();  // (C is read)
-    } else {
       panes.written();
       if (kind == kPlanes || a.wide) {
         if (panes.lane == 0) {
           for (int p = 0; p < a.planes; ++p)
-            panes.store(p, &a.d, from, row, (int)batch * a.d_stored + p);
+            panes.store(pane + p, &a.d, col, row, (int)batch * a.d_stored + p);
           ptx::bulk_commit();
         }
       } else {
-        copy(from);
+        copy(pane, col);
       }
     }
-    const int next = col + gemm::kChunk;
-    if (next < col0 + a.half && some(next)) fetch(next);
+    if (j == 1 && slots == 2) {  // the other half of the tile's chunks
+      panes.reuse<0>();
+      fetch(2, 4);
+    }
   }
   static __device__ __forceinline__ uint4 pack_bf16(const float *v) {
     uint32_t w[4];
@@ -276,16 +278,16 @@ struct StepEpi {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // The pane to rows that TMA cannot write: lanes along the columns.
-  __device__ __forceinline__ void copy(int col) {
-    const int row0 = row - panes.lane, rows = min(32, M - row0);
+  // The pane to rows that TMA cannot write: 16 lanes along a row's columns.
+  __device__ __forceinline__ void copy(int pane, int col) {
+    const int row0 = row - panes.lane, rows = min(32, M - row0), w = panes.lane & 15;
     if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 83)) return;
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const uint32_t w = panes.word(0, r);
-      uint16_t *u = reinterpret_cast<uint16_t *>(a.bf16.at(batch, row0 + r) + col) + 2 * panes.lane;
-      if (col + 2 * panes.lane < a.N) u[0] = (uint16_t)w;
-      if (col + 2 * panes.lane + 1 < a.N) u[1] = (uint16_t)(w >> 16);
+    for (int r = panes.lane >> 4; r < rows; r += 2) {
+      const uint32_t q = panes.word(pane, r, w);
+      uint16_t *u = reinterpret_cast<uint16_t *>(a.bf16.at(batch, row0 + r) + col) + 2 * w;
+      if (col + 2 * w < a.N) u[0] = (uint16_t)q;
+      if (col + 2 * w + 1 < a.N) u[1] = (uint16_t)(q >> 16);
     }
     panes.written();  // (it is read)
   }
@@ -363,9 +365,10 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   const auto g = view_of<const IN>(a.update);
   const bool wide = view_aligned(a.update, sizeof(IN), 16);
   squares_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, wide, p.part, err);
-  start_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, wide, p.part, p.parts, a.eps,
-                                                  p.x[0], p.ld, carried(0), p.rest, err);
   cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = gemm::launch_after(start_kernel<IN>, grid, kNormThreads, 0, st, g, a.rows, a.cols, wide,
+                         p.part, p.parts, a.eps, p.x[0], p.ld, carried(0), p.rest, err);
 
   const int64_t gps = p.side * p.gram_ld;
   const int64_t xz = a.count * 2, gz = a.count * p.planes;
@@ -376,10 +379,10 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
     return gemm::make_map(m, x, p.side, p.side, gz, p.gram_ld, gps, false, box);
   };
   auto pane_x = [&](CUtensorMap *m, const __half *x) {
-    return gemm::make_pane_map(m, x, false, a.cols, a.rows, xz, p.ld, xps);
+    return gemm::make_pane_map<64>(m, x, false, a.cols, a.rows, xz, p.ld, xps);
   };
   auto pane_gram = [&](CUtensorMap *m, const __half *x) {
-    return gemm::make_pane_map(m, x, false, p.side, p.side, gz, p.gram_ld, gps);
+    return gemm::make_pane_map<64>(m, x, false, p.side, p.side, gz, p.gram_ld, gps);
   };
   for (int k = 0; k < a.steps && e == cudaSuccess; ++k) {
     const __half *x = p.x[k & 1];
@@ -438,7 +441,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
       u.wide = view_aligned(a.out, 2, 16) && a.out->token_stride >= a.cols &&
                (a.count == 1 || a.out->batch_stride > 0);
       const int64_t zs = a.count == 1 ? a.rows * a.out->token_stride : a.out->batch_stride;
-      if (!fill(u) || (u.wide && !gemm::make_pane_map(&u.d, u.bf16.p, false, a.cols, a.rows,
+      if (!fill(u) || (u.wide && !gemm::make_pane_map<64>(&u.d, u.bf16.p, false, a.cols, a.rows,
                                                       a.count, a.out->token_stride, zs)))
         return cudaErrorInvalidValue;
       e = multiply<kBf16>(maps, q, bn, u, err, st);

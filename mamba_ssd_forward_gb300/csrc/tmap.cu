@@ -29,10 +29,8 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-}  // namespace
-
-bool make_tmap_sw128(CUtensorMap *map, const void *base, bool bf16, int rank,
-                     const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+bool make_tmap(CUtensorMap *map, const void *base, bool bf16, int rank, const uint64_t *dims,
+               const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle) {
   EncodeTiled fn = encode_fn();
   if (!fn || rank < 1 || rank > 5) return false;
   cuuint64_t gd[5], gs[4];
@@ -46,9 +44,20 @@ bool make_tmap_sw128(CUtensorMap *map, const void *base, bool bf16, int rank,
   const CUresult r =
       fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
          (cuuint32_t)rank, const_cast<void *>(base), gd, gs, bx, es,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool make_tmap_sw128(CUtensorMap *map, const void *base, bool bf16, int rank,
+                     const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+  return make_tmap(map, base, bf16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool make_tmap_sw64(CUtensorMap *map, const void *base, bool bf16, int rank, const uint64_t *dims,
+                    const uint64_t *strides, const uint32_t *box) {
+  return make_tmap(map, base, bf16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // Device error word: kernels that give up a bounded wait record a code here

@@ -15,5 +15,8 @@ namespace ssd {
 // (box[0] * element size must be <= 128 bytes).  Returns false on failure.
 bool make_tmap_sw128(CUtensorMap *map, const void *base, bool bf16, int rank,
                      const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
+// The same with 64-byte swizzling (box[0] * element size <= 64 bytes).
+bool make_tmap_sw64(CUtensorMap *map, const void *base, bool bf16, int rank, const uint64_t *dims,
+                    const uint64_t *strides, const uint32_t *box);
 
 }  // namespace ssd

@@ -138,6 +138,8 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   int before = 0;
 #pragma unroll 4
   for (int64_t i = tid; i < first; i += kPackThreads) before += counted(targets[i], ignore);
@@ -199,6 +201,8 @@ pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d
                    uint16_t *__restrict__ wp, int64_t ld, int64_t ps,
                    const uint32_t *__restrict__ top, int *err) {
   const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   if (r >= rows || !SSD_IN_BOUNDS(ld >= d && ws >= 0, err, 72)) return;
   pack_row(w + r * ws, wp + r * ld, ps, d, top ? scale_of(top[kTopW]) : 1.f, threadIdx.x % 32, 32);
 }
@@ -219,10 +223,11 @@ struct StatsEpi {
   const Args &a;
   int *err;
   static constexpr bool kStaged = false;
+  using Pane = gemm::Panes<128>;
   float unit, scale, m, s;  // of the sums: a logit, and its log2e
   int row, run, target;
   bool live;
-  __device__ __forceinline__ StatsEpi(const Args &args, gemm::Panes, int *e) : a(args), err(e) {
+  __device__ __forceinline__ StatsEpi(const Args &args, Pane, int *e) : a(args), err(e) {
     unit = a.top ? inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW])) : 1.f;
     scale = unit * kLog2e;
   }
@@ -296,12 +301,13 @@ struct DlogitEpi {
     int V, word0, uniform;
   };
   static constexpr bool kStaged = true, kSplit = sizeof(IO) == 4;
+  using Pane = gemm::Panes<128>;
   const Args &a;
-  gemm::Panes panes;
+  Pane panes;
   float scale, up, lse, g;
   int row, target;
   bool live;
-  __device__ __forceinline__ DlogitEpi(const Args &args, gemm::Panes p, int *)
+  __device__ __forceinline__ DlogitEpi(const Args &args, Pane p, int *)
       : a(args), panes(p) {
     scale = up = 1.f;
     if constexpr (kSplit) {
@@ -384,12 +390,13 @@ struct GradEpi {
     int d, words, first, direct;
   };
   static constexpr bool kStaged = true, kWide = sizeof(IO) == 4;
+  using Pane = gemm::Panes<128>;
   const Args &a;
-  gemm::Panes panes;
+  Pane panes;
   int *err;
   float factor;
   int which, row0, slab, pane;  // pane: the one whose store is the older
-  __device__ __forceinline__ GradEpi(const Args &args, gemm::Panes p, int *e)
+  __device__ __forceinline__ GradEpi(const Args &args, Pane p, int *e)
       : a(args), panes(p), err(e), factor(args.f.of(kTopX)), pane(0) {}
   __device__ __forceinline__ void begin(const Tile &o, int r, int, int) {
     which = o.which, row0 = r - panes.lane, slab = o.batch;
@@ -447,7 +454,7 @@ struct GradEpi {
     if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 76)) return;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
-      const uint32_t w = panes.word(pane, r);
+      const uint32_t w = panes.word(pane, r, panes.lane);
       IO *o = a.out + (int64_t)(row0 + r) * a.d + col;
       if constexpr (kWide) {
         if (col + panes.lane < a.d) o[panes.lane] = __uint_as_float(w);
@@ -468,6 +475,8 @@ template <typename IO>
 __global__ void __launch_bounds__(256)
 unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, Factors f,
               SeqView<IO> dx, int64_t L, int64_t d, int *err) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const float factor = f.of(kTopW);
   const int live = *f.rows.live, lane = threadIdx.x % 32;
   for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < live; r += gridDim.x * 8ll) {
@@ -497,6 +506,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
             float *__restrict__ loss, float *__restrict__ lse, int *err) {
   __shared__ float2 each[kJoinWarps][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
   const bool live = row < *rows.live;
@@ -526,6 +537,8 @@ total_kernel(const float *__restrict__ loss, int64_t n, const int *__restrict__ 
              float *__restrict__ total, int *err) {
   __shared__ float sums[32];
   float s = 0.f;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   if (SSD_IN_BOUNDS(n > 0, err, 78))
 #pragma unroll 8
     for (int64_t i = threadIdx.x; i < n; i += 1024) s += loss[i];
@@ -627,7 +640,14 @@ struct Calls {
             static_cast<const float *>(a.weight->data), a.weight->token_stride, a.V, a.d, g, p.top,
             err);
     }
-    pack_kernel<IO><<<(unsigned)((a.n + kPackTokens - 1) / kPackTokens), kPackThreads, 0, st>>>(
+    // (the first launch of the call waits for what is on the stream the ordinary way)
+    const dim3 grid((unsigned)((a.n + kPackTokens - 1) / kPackTokens));
+    if (top)
+      return gemm::launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
+                                a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
+                                view_of<IO>(a.dx), loss, lse, p.r, p.xp, p.ld, p.rows * p.ld,
+                                kPlanes, top, err);
+    pack_kernel<IO><<<grid, kPackThreads, 0, st>>>(
         view_of<const IO>(a.x), a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
         view_of<IO>(a.dx), loss, lse, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, top, err);
     return cudaGetLastError();
@@ -647,10 +667,9 @@ struct Calls {
       return cudaSuccess;
     }
     w->at = p.wp, w->ld = p.ld, w->zs = p.piece * p.ld;
-    pack_weight_kernel<IO><<<(unsigned)((w->n + 7) / 8), 256, 0, st>>>(
-        src, a.weight->token_stride, w->n, a.d, p.wp, p.ld, w->zs,
-        kPlanes == 2 ? p.top : nullptr, err);
-    return cudaGetLastError();
+    const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
+    return gemm::launch_after(pack_weight_kernel<IO>, dim3((unsigned)((w->n + 7) / 8)), 256, 0, st,
+                              src, a.weight->token_stride, w->n, a.d, p.wp, p.ld, w->zs, top, err);
   }
 
   static Product product(int64_t M, int64_t N, int64_t K) {
@@ -687,12 +706,11 @@ struct Calls {
       e = gemm::launch<StatsEpi, kBN, kSegment>(maps, &q, 1, kBf16, s, err, st);
     }
     if (e != cudaSuccess) return e;
-    join_kernel<<<(unsigned)((a.n + 31) / 32), 32 * kJoinWarps, 0, st>>>(
-        p.stat, p.rows, (int)p.runs, p.r, loss, a.lse, err);
-    if (a.total)
-      total_kernel<<<1, 1024, 0, st>>>(loss, a.n, p.r.live, a.reduction == SSD_REDUCE_MEAN,
-                                       a.total, err);
-    return cudaGetLastError();
+    e = gemm::launch_after(join_kernel, dim3((unsigned)((a.n + 31) / 32)), 32 * kJoinWarps, 0, st,
+                           p.stat, p.rows, (int)p.runs, p.r, loss, a.lse, err);
+    if (e != cudaSuccess || !a.total) return e;
+    return gemm::launch_after(total_kernel, dim3(1), 1024, 0, st, loss, a.n, p.r.live,
+                              (int)(a.reduction == SSD_REDUCE_MEAN), a.total, err);
   }
 
   static cudaError_t backward(const LossArgs &a, void *ws, int *err, cudaStream_t st) {
@@ -712,7 +730,7 @@ struct Calls {
       if (!logits(a, p, w, maps, q)) return cudaErrorInvalidValue;
       typename DlogitEpi<IO>::Args z{};
       z.rows = p.r, z.top = top, z.V = (int)w.n, z.word0 = (int)word0, z.uniform = uniform;
-      if (!gemm::make_pane_map(&z.dz, p.dz, false, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps))
+      if (!gemm::make_pane_map<128>(&z.dz, p.dz, false, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps))
         return cudaErrorInvalidValue;
       e = gemm::launch<DlogitEpi<IO>, kBN, kSegment>(maps, q, 1, kBf16, z, err, st);
       if (e != cudaSuccess) break;
@@ -734,17 +752,17 @@ struct Calls {
                           gemm::kRows) ||
           !gemm::make_map(&maps[3], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, true,
                           kBN / 2) ||
-          !gemm::make_pane_map(&g.sum, p.sum, true, sld, p.rows, p.slabs, sld, p.rows * sld) ||
+          !gemm::make_pane_map<128>(&g.sum, p.sum, true, sld, p.rows, p.slabs, sld, p.rows * sld) ||
           (a.dweight && g.direct &&
-           !gemm::make_pane_map(&g.dw, g.out, !kBf16, a.d, w.n, 1, a.d, w.n * a.d)))
+           !gemm::make_pane_map<128>(&g.dw, g.out, !kBf16, a.d, w.n, 1, a.d, w.n * a.d)))
         return cudaErrorInvalidValue;
       e = gemm::launch<GradEpi<IO>, kBN, kSegment>(maps, q, a.dweight ? 2 : 1, kBf16, g, err, st);
     }
     if (e != cudaSuccess || !a.dx) return e;
     const int64_t sld = gemm::padded(a.d), blocks = (a.n + 7) / 8;
-    unpack_kernel<IO><<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(
-        p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx), a.L, a.d, err);
-    return cudaGetLastError();
+    return gemm::launch_after(unpack_kernel<IO>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                              256, 0, st, p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx),
+                              a.L, a.d, err);
   }
 };
 
