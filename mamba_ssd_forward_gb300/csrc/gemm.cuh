@@ -190,15 +190,6 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
                : "memory");
 }
 
-// One lane of a converged warp, the same each time.  (With it rather than a
-// comparison of the lane the compiler keeps what the instructions below take in
-// uniform registers.)
-__device__ __forceinline__ bool elected() {
-  uint32_t e;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
-  return e != 0;
-}
 // A value that is the same in all lanes, said so.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -228,6 +219,15 @@ __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *ma
   }
 }
 
+// One lane of a converged warp, the same each time.  (With it rather than a
+// comparison of the lane the compiler keeps what the instructions below take in
+// uniform registers.)
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
+}
 // A warp's panes in shared memory.  A thread holds a row of the tile; through a
 // pane, 32 rows, values go to memory and come from it by TMA, which clips what
 // lies outside the array.  (Row by row from registers every access would touch 32
@@ -259,16 +259,16 @@ struct Panes {
   // All but the newest kLeft groups of stores have read their panes.
   template <int kLeft>
   __device__ __forceinline__ void reuse() const {
-    if (lane == 0) ptx::bulk_wait_read<kLeft>();
+    if (elected()) ptx::bulk_wait_read<kLeft>();
     __syncwarp();
   }
-  // The warp has written (or read) its panes: lane 0 may store (or load) them.
+  // The warp has written (or read) its panes: the elected lane may store (or load) them.
   __device__ __forceinline__ void written() const {
     ptx::fence_async_smem();
     __syncwarp();
   }
   __device__ __forceinline__ void store(int pane, const CUtensorMap *map, int col, int row,
-                                        int z) const {  // lane 0, then commit
+                                        int z) const {  // the elected lane, then commit
     ptx::tma_store_3d(map, at + pane * kBytes, col, row, z);
   }
   __device__ __forceinline__ void add(int pane, const CUtensorMap *map, int col, int row,
@@ -283,7 +283,7 @@ struct Panes {
   // read.  fetched: they are there.
   __device__ __forceinline__ void fetch(int bar, int pane, int n, const CUtensorMap *map, int col,
                                         int row, int z) const {
-    if (lane == 0) {
+    if (elected()) {
       ptx::mbar_arrive_expect_tx(&bars[bar], n * kBytes);
       for (int i = 0; i < n; ++i)
         ptx::tma_load_3d(at + (pane + i) * kBytes, map, col, row, z + i, &bars[bar]);
@@ -433,7 +433,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       if (j == kChunks - 1) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at(in_first(&accfree[n & 1]));
+        if (elected()) arrive_at(in_first(&accfree[n & 1]));
       }
     };
     for (int t = start; t < walk.total; t += step) {
@@ -489,7 +489,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       epi.end();
     }
     if constexpr (Epi::kStaged) {
-      if (lane == 0) ptx::bulk_wait<0>();  // the panes are read and their values written
+      if (elected()) ptx::bulk_wait<0>();  // the panes are read and their values written
     }
   }
   ptx::tc_fence_before();

@@ -98,14 +98,14 @@ squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
   }
 }
 
-// Eight values as fp16, and what that leaves of them.
-__device__ __forceinline__ uint4 pack8(float *v) {
+// Eight values as fp16, and what that leaves of them if it is asked for.
+__device__ __forceinline__ uint4 pack8(float *v, bool more) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    v[2 * i] -= __low2float(h), v[2 * i + 1] -= __high2float(h);
+    if (more) v[2 * i] -= __low2float(h), v[2 * i + 1] -= __high2float(h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -135,8 +135,8 @@ start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
   each8(g, rows, cols, wide, [&](float (&v)[8], int64_t r, int64_t c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= pow2;
-    *reinterpret_cast<uint4 *>(hi + r * ld + c) = pack8(v);
-    if (planes == 2) *reinterpret_cast<uint4 *>(lo + r * ld + c) = pack8(v);
+    *reinterpret_cast<uint4 *>(hi + r * ld + c) = pack8(v, planes == 2);
+    if (planes == 2) *reinterpret_cast<uint4 *>(lo + r * ld + c) = pack8(v, false);
   });
 }
 
@@ -144,19 +144,22 @@ start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
 
 // D = (alpha sum + beta C) rest^power, as fp16 planes or, the last X, as the
 // result.  C comes through the panes that D leaves by.
-enum Kind { kPlanes, kBf16, kF32 };
+enum Kind { kOne, kTwo, kBf16, kF32 };  // one plane, two, the result
 
 template <Kind kind>
 struct StepEpi {
+  static constexpr bool kPlanes = kind == kOne || kind == kTwo;
+  static constexpr int kCount = kind == kTwo ? 2 : 1;  // planes of D
   struct Args {
     CUtensorMap c, d;  // planes of C; of D, or a bf16 result where TMA can write it
     float alpha, beta;
     const float *rest;  // of the first step, else NULL
     int power;
     int c_planes, c_stored;  // planes of C to add (0: no C), and in its array
-    int planes, d_stored;    // of D
+    int d_stored;            // of D
     int half;                // columns of the tile that a warp takes
-    __half *out;             // D again, for its mirrored tiles
+    int symmetric;           // there are mirrored tiles
+    __half *out;             // D again, for the mirrored tiles of two planes
     int64_t ld, ps, zs;
     SeqView<__nv_bfloat16> bf16;
     SeqView<float> f32;
@@ -168,39 +171,42 @@ struct StepEpi {
   Pane panes;
   int *err;
   float alpha, beta;
-  int row, col0, M, mirror, slots;  // slots: of one pane or two, for a chunk's planes
+  // A chunk's planes, or its plane and its mirror image, have two of the four
+  // panes; else one.
+  int row, row0, col0, M, mirror, pair;
   int64_t batch;
   __device__ __forceinline__ StepEpi(const Args &args, Pane p, int *e)
-      : a(args), panes(p), err(e), slots(args.c_planes == 2 || args.planes == 2 ? 2 : 4) {}
+      : a(args), panes(p), err(e),
+        pair(args.c_planes == 2 || kind == kTwo || args.symmetric) {}
   __device__ __forceinline__ void begin(const Tile &o, int r, int col, int rows) {
-    row = r, col0 = col, M = rows, mirror = o.mirror, batch = o.batch;
+    row = r, row0 = r - panes.lane, col0 = col, M = rows, mirror = o.mirror, batch = o.batch;
     float f = 1.f;
     if (a.rest) {
       f = a.rest[batch];
       if (a.power == 2) f *= f;
     }
     alpha = a.alpha * f, beta = a.beta * f;
-    panes.reuse<0>();
-    fetch(0, slots);  // C of the first chunks, while the products run
+    panes.template reuse<0>();
+    // C of the first chunks, while the products run
+    for (int j = 0; j < (pair ? 2 : 4); ++j) fetch(j);
   }
   // whether any of the warp's 32 rows x 32 columns of chunk j is there
   __device__ __forceinline__ bool some(int j) const {
-    return row - panes.lane < M && col0 + gemm::kChunk * j < a.N;
+    return row0 < M && col0 + gemm::kChunk * j < a.N && gemm::kChunk * j < a.half;
   }
-  __device__ __forceinline__ void fetch(int from, int to) {
-    if (!a.c_planes) return;
-    for (int j = from; j < to && gemm::kChunk * j < a.half; ++j)
-      if (some(j))
-        panes.fetch(j % slots, j % slots * (4 / slots), a.c_planes, &a.c, col0 + gemm::kChunk * j,
-                    row - panes.lane, (int)batch * a.c_stored);
+  __device__ __forceinline__ int slot(int j) const { return pair ? j & 1 : j & 3; }
+  __device__ __forceinline__ void fetch(int j) const {
+    if (a.c_planes && some(j))
+      panes.fetch(slot(j), slot(j) << pair, a.c_planes, &a.c, col0 + gemm::kChunk * j, row0,
+                  (int)batch * a.c_stored);
   }
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
     if (!some(j)) return;
-    const int slot = j % slots, pane = slot * (4 / slots);
+    const int pane = slot(j) << pair;
 #pragma unroll
     for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
     if (a.c_planes) {
-      panes.fetched(slot);
+      panes.fetched(slot(j));
       for (int p = 0; p < a.c_planes; ++p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -214,8 +220,10 @@ struct StepEpi {
           }
         }
       }
-    } else if (j >= slots) {
-      panes.reuse<1>();
+    }
+    if (pair && j > 0) {  // the other slot is free once its store has read it
+      panes.template reuse<0>();
+      fetch(j + 1);
     }
     if constexpr (kind == kF32) {
       if (row < M) {
@@ -233,41 +241,45 @@ struct StepEpi {
         }
       }
       panes.written();  // (C is read)
-    } else {
-      for (int p = 0; p < a.planes; ++p) {
-        uint32_t w[gemm::kChunk / 2];
+      return;
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 q;
-          if constexpr (kind == kBf16) q = pack_bf16(v + 8 * i);
-          else q = pack8(v + 8 * i);
-          panes.cell(pane + p, i) = q;
-          w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-        }
-        if (kind == kPlanes && mirror && row < M && SSD_IN_BOUNDS(row < a.ld, err, 82)) {
-          // row and column exchanged: the lanes' rows lie side by side
-          uint16_t *m = reinterpret_cast<uint16_t *>(a.out + batch * a.zs + p * a.ps) +
-                        (int64_t)col * a.ld + row;
+    for (int p = 0; p < kCount; ++p) {
+      uint32_t w[gemm::kChunk / 2];
 #pragma unroll
-          for (int i = 0; i < gemm::kChunk; ++i)
-            if (col + i < a.N) m[i * a.ld] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = kind == kBf16 ? pack_bf16(v + 8 * i) : pack8(v + 8 * i, p + 1 < kCount);
+        panes.cell(pane + p, i) = q;
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
       }
-      panes.written();
-      if (kind == kPlanes || a.wide) {
-        if (panes.lane == 0) {
-          for (int p = 0; p < a.planes; ++p)
-            panes.store(pane + p, &a.d, col, row, (int)batch * a.d_stored + p);
-          ptx::bulk_commit();
-        }
-      } else {
-        copy(pane, col);
+      if (kind == kOne && mirror) {
+        // the image, rows of the columns, into the pane beside
+        uint8_t *m = panes.at + (pane + 1) * Pane::kBytes + (panes.lane & 7) * 2;
+#pragma unroll
+        for (int i = 0; i < gemm::kChunk; ++i)
+          *reinterpret_cast<uint16_t *>(m + Pane::swizzled(i, panes.lane >> 3)) =
+              (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      }
+      if (kind == kTwo && mirror && row < M && SSD_IN_BOUNDS(row < a.ld, err, 82)) {
+        // (there is no pane left for it: the lanes' rows lie side by side)
+        uint16_t *m = reinterpret_cast<uint16_t *>(a.out + batch * a.zs + p * a.ps) +
+                      (int64_t)col * a.ld + row;
+#pragma unroll
+        for (int i = 0; i < gemm::kChunk; ++i)
+          if (col + i < a.N) m[i * a.ld] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
       }
     }
-    if (j == 1 && slots == 2) {  // the other half of the tile's chunks
-      panes.reuse<0>();
-      fetch(2, 4);
+    panes.written();
+    if (!kPlanes && !a.wide) {
+      copy(pane, col);
+    } else if (gemm::elected()) {
+#pragma unroll
+      for (int p = 0; p < kCount; ++p)
+        panes.store(pane + p, &a.d, col, row0, (int)batch * a.d_stored + p);
+      if (kind == kOne && mirror) panes.store(pane + 1, &a.d, row0, col, (int)batch * a.d_stored);
+      ptx::bulk_commit();
     }
+    __syncwarp();
   }
   static __device__ __forceinline__ uint4 pack_bf16(const float *v) {
     uint32_t w[4];
@@ -280,7 +292,7 @@ struct StepEpi {
   }
   // The pane to rows that TMA cannot write: 16 lanes along a row's columns.
   __device__ __forceinline__ void copy(int pane, int col) {
-    const int row0 = row - panes.lane, rows = min(32, M - row0), w = panes.lane & 15;
+    const int rows = min(32, M - row0), w = panes.lane & 15;
     if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 83)) return;
 #pragma unroll 4
     for (int r = panes.lane >> 4; r < rows; r += 2) {
@@ -332,11 +344,13 @@ cudaError_t multiply(const CUtensorMap *maps, const Product &q, int bn,
     return bn == 256 ? gemm::launch<StepEpi<kind>, 256, kSegment>(maps, &q, 1, false, e, err, st)
                      : gemm::launch<StepEpi<kind>, 128, kSegment>(maps, &q, 1, false, e, err, st);
   };
-  if constexpr (kind != kBf16)
-    if (q.pairs == 3) return with(std::integral_constant<int, gemm::kExact>());
-  if constexpr (kind != kF32)
-    if (q.pairs == 1) return with(std::integral_constant<int, 0>());
-  return cudaErrorInvalidValue;
+  if constexpr (kind == kBf16 || kind == kOne)
+    return q.pairs == 1 ? with(std::integral_constant<int, 0>()) : cudaErrorInvalidValue;
+  else if constexpr (kind == kF32)
+    return q.pairs == 3 ? with(std::integral_constant<int, gemm::kExact>()) : cudaErrorInvalidValue;
+  else
+    return q.pairs == 3 ? with(std::integral_constant<int, gemm::kExact>())
+                        : with(std::integral_constant<int, 0>());
 }
 
 // Columns to a tile: 256, or 128 where the tiles then take less time in all.  A
@@ -395,24 +409,33 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
     q.M = q.N = (int)p.side, q.K = (int)longer;
     q.a_mn = q.b_mn = tall, q.a_planes = q.b_planes = 2, q.symmetric = 1;
     int bn = tile_columns(q);
-    StepEpi<kPlanes>::Args s{};
-    s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
-    s.out = p.gram, s.planes = s.d_stored = p.planes, s.half = bn / 2;
-    s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
+    auto gram = [&](auto &s) {
+      s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
+      s.out = p.gram, s.d_stored = p.planes, s.half = bn / 2, s.symmetric = 1;
+      s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
+      return pane_gram(&s.d, p.gram);
+    };
+    auto poly = [&](auto &s) {
+      s.alpha = a.c / kGramScale, s.beta = a.b, s.rest = nullptr;
+      s.c_planes = s.c_stored = p.planes, s.out = p.poly;
+      return pane_gram(&s.c, p.gram) && pane_gram(&s.d, p.poly);
+    };
+    StepEpi<kOne>::Args s1{};
+    StepEpi<kTwo>::Args s2{};
     if (!map_x(&maps[0], x, tall, gemm::kRows) || !map_x(&maps[1], x, tall, bn / 2) ||
-        !pane_gram(&s.d, p.gram))
+        !gram(s1) || !gram(s2))
       return cudaErrorInvalidValue;
-    e = multiply<kPlanes>(maps, q, bn, s, err, st);
+    e = p.planes == 1 ? multiply<kOne>(maps, q, bn, s1, err, st)
+                      : multiply<kTwo>(maps, q, bn, s2, err, st);
     if (e != cudaSuccess) break;
 
     // B = b A + c A A
     q.K = (int)p.side, q.a_mn = q.b_mn = 0, q.a_planes = q.b_planes = p.planes;
-    s.alpha = a.c / kGramScale, s.beta = a.b, s.rest = nullptr;
-    s.c_planes = s.c_stored = p.planes, s.out = p.poly;
     if (!map_gram(&maps[0], p.gram, gemm::kRows) || !map_gram(&maps[1], p.gram, bn / 2) ||
-        !pane_gram(&s.c, p.gram) || !pane_gram(&s.d, p.poly))
+        !poly(s1) || !poly(s2))
       return cudaErrorInvalidValue;
-    e = multiply<kPlanes>(maps, q, bn, s, err, st);
+    e = p.planes == 1 ? multiply<kOne>(maps, q, bn, s1, err, st)
+                      : multiply<kTwo>(maps, q, bn, s2, err, st);
     if (e != cudaSuccess) break;
 
     // X <- a X + B X or a X + X B
@@ -425,16 +448,17 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
     auto fill = [&](auto &u) {
       u.alpha = 1.f / kGramScale, u.beta = a.a, u.rest = k ? nullptr : p.rest, u.power = 1;
       if (last) u.alpha /= kScale, u.beta /= kScale;
-      u.c_planes = carried(k), u.c_stored = 2, u.planes = 1, u.d_stored = 1;
+      u.c_planes = carried(k), u.c_stored = 2, u.d_stored = 1;
       u.N = (int)a.cols, u.half = bn / 2;
       return pane_x(&u.c, x);
     };
     if (!last) {
-      StepEpi<kPlanes>::Args u{};
-      u.out = p.x[~k & 1];
-      if (!fill(u) || !pane_x(&u.d, u.out)) return cudaErrorInvalidValue;
-      u.planes = carried(k + 1), u.d_stored = 2;
-      e = multiply<kPlanes>(maps, q, bn, u, err, st);
+      auto next = [&](auto &u) { return fill(u) && (u.d_stored = 2) && pane_x(&u.d, p.x[~k & 1]); };
+      StepEpi<kOne>::Args u1{};
+      StepEpi<kTwo>::Args u2{};
+      if (!next(u1) || !next(u2)) return cudaErrorInvalidValue;
+      e = carried(k + 1) == 1 ? multiply<kOne>(maps, q, bn, u1, err, st)
+                              : multiply<kTwo>(maps, q, bn, u2, err, st);
     } else if (out == SSD_BF16) {
       StepEpi<kBf16>::Args u{};
       u.bf16 = view_of<__nv_bfloat16>(a.out);

@@ -305,7 +305,7 @@ struct DlogitEpi {
   const Args &a;
   Pane panes;
   float scale, up, lse, g;
-  int row, target;
+  int row0, target;
   bool live;
   __device__ __forceinline__ DlogitEpi(const Args &args, Pane p, int *)
       : a(args), panes(p) {
@@ -316,7 +316,7 @@ struct DlogitEpi {
     }
   }
   __device__ __forceinline__ void begin(const Tile &, int r, int, int M) {
-    row = r, live = r < M;
+    row0 = r - panes.lane, live = r < M;
     lse = live ? a.rows.lse[r] : 0.f;
     g = live ? a.rows.g[r] * up : 0.f;
     target = live ? a.rows.target[r] - a.word0 : -1;
@@ -337,9 +337,9 @@ struct DlogitEpi {
         split8(v + 8 * i, panes.cell(0, first + i), panes.cell(1, first + i));
       if (first == 0) return;
       panes.written();
-      if (panes.lane == 0) {
-        panes.store(0, &a.dz, col - gemm::kChunk, row, 0);
-        panes.store(1, &a.dz, col - gemm::kChunk, row, 1);
+      if (gemm::elected()) {
+        panes.store(0, &a.dz, col - gemm::kChunk, row0, 0);
+        panes.store(1, &a.dz, col - gemm::kChunk, row0, 1);
         ptx::bulk_commit();
       }
     } else {
@@ -349,8 +349,8 @@ struct DlogitEpi {
       for (int i = 0; i < 4; ++i) panes.cell(pane, first + i) = pack8(v + 8 * i);
       if (first == 0) return;
       panes.written();
-      if (panes.lane == 0) {
-        panes.store(pane, &a.dz, col - gemm::kChunk, row, 0);
+      if (gemm::elected()) {
+        panes.store(pane, &a.dz, col - gemm::kChunk, row0, 0);
         ptx::bulk_commit();
       }
     }
@@ -415,7 +415,7 @@ struct GradEpi {
     if (which == 0) {
       if (col >= a.d) return;
       put(v);
-      if (panes.lane == 0) {
+      if (gemm::elected()) {
         if (a.first) panes.store(pane, &a.sum, col, row0, slab);
         else panes.add(pane, &a.sum, col, row0, slab);
         ptx::bulk_commit();
@@ -439,7 +439,7 @@ struct GradEpi {
       panes.written();
     }
     if (a.direct) {
-      if (panes.lane == 0) {
+      if (gemm::elected()) {
         panes.store(pane, &a.dw, col, row0, 0);
         ptx::bulk_commit();
       }
