@@ -31,7 +31,6 @@ namespace {
 using gemm::Product;
 using gemm::Tile;
 
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBN = 256;
 constexpr int kRun = kBN / 2;  // columns of one epilogue warp: a run of the statistics
 
@@ -39,16 +38,16 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // ------------------------------------------------- largest values, and scales
 
-// The power of two that takes values of the size of `top` (a float's bits) to
-// 2^14 .. 2^15; 1 for zero, infinity and NaN.  Held within 2^62 both ways.
-__device__ __forceinline__ float scale_of(uint32_t top) {
-  if (top == 0 || top >= 0x7f800000u) return 1.f;
-  int e = (int)(top >> 23) - 127;
-  e = e < -48 ? -48 : e > 76 ? 76 : e;
-  return __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+// The power of two (its exponent) that takes values of the size of `top` (a float's
+// bits) to 2^14 .. 2^15; 0 for zero, infinity and NaN.
+__device__ __forceinline__ int shift_of(uint32_t top) {
+  if (top == 0 || top >= 0x7f800000u) return 0;
+  const int e = (int)(top >> 23) - 127;
+  return 14 - (e < -110 ? -110 : e);
 }
-__device__ __forceinline__ float inverse_of(float pow2) {
-  return __uint_as_float((254u << 23) - __float_as_uint(pow2));
+// 2^e, zero where that is no normal number any more, at most 2^127.
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + (e > 127 ? 127 : e)) << 23);
 }
 
 enum Top { kTopX, kTopW, kTopG, kTops };
@@ -175,7 +174,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
     }
   }
   __syncthreads();
-  const float scale = top ? scale_of(top[kTopX]) : 1.f;
+  const float scale = top ? pow2(shift_of(top[kTopX])) : 1.f;
   if (warp < here) {
     const int64_t t = first + warp, b = t / L, at = t % L;
     if (place[warp] >= 0)
@@ -204,14 +203,15 @@ pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (r >= rows || !SSD_IN_BOUNDS(ld >= d && ws >= 0, err, 72)) return;
-  pack_row(w + r * ws, wp + r * ld, ps, d, top ? scale_of(top[kTopW]) : 1.f, threadIdx.x % 32, 32);
+  pack_row(w + r * ws, wp + r * ld, ps, d, top ? pow2(shift_of(top[kTopW])) : 1.f, threadIdx.x % 32, 32);
 }
 
 // ------------------------------------------------------------------ epilogues
 
-// The logits' statistics.  In units of log2 (the largest logit m and the sum of
-// 2^(z - m)), so that the exponential is one multiply-add and one ex2: its
-// error, 2^-22 relative, is the sum's.
+// The logits' statistics: the largest logit m and the sum of exp(z - m), each
+// exponential off by 2^-21 of itself.  (About m rather than in units of log2 from
+// the start, which would cost a multiplication less: logits near the end of the
+// number range would overflow.)
 struct StatsEpi {
   struct Args {
     float2 *part;  // [runs][ld]
@@ -224,12 +224,11 @@ struct StatsEpi {
   int *err;
   static constexpr bool kStaged = false;
   using Pane = gemm::Panes<128>;
-  float unit, scale, m, s;  // of the sums: a logit, and its log2e
+  float unit, m, s;  // unit: a logit to the tensor cores' sum
   int row, run, target;
   bool live;
   __device__ __forceinline__ StatsEpi(const Args &args, Pane, int *e) : a(args), err(e) {
-    unit = a.top ? inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW])) : 1.f;
-    scale = unit * kLog2e;
+    unit = a.top ? pow2(-shift_of(a.top[kTopX]) - shift_of(a.top[kTopW])) : 1.f;
   }
   __device__ __forceinline__ void begin(const Tile &, int r, int col, int M) {
     row = r, live = r < M, run = a.run0 + col / kRun;
@@ -253,12 +252,12 @@ struct StatsEpi {
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < gemm::kChunk; ++i) top = fmaxf(top, v[i]);
-    const float next = fmaxf(m, top * scale);
+    const float next = fmaxf(m, top * unit);
     const float about = next == -INFINITY ? 0.f : next;  // of nothing but -inf the sum is zero
     float q[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < gemm::kChunk; ++i) q[i % 4] += ex2(fmaf(v[i], scale, -about));
-    s = s * ex2(m - about) + ((q[0] + q[1]) + (q[2] + q[3]));
+    for (int i = 0; i < gemm::kChunk; ++i) q[i % 4] += ex2(fmaf(v[i], unit, -about) * kLog2e);
+    s = s * ex2((m - about) * kLog2e) + ((q[0] + q[1]) + (q[2] + q[3]));
     m = next;
   }
   __device__ __forceinline__ void end() {
@@ -311,8 +310,8 @@ struct DlogitEpi {
       : a(args), panes(p) {
     scale = up = 1.f;
     if constexpr (kSplit) {
-      scale = inverse_of(scale_of(a.top[kTopX])) * inverse_of(scale_of(a.top[kTopW]));
-      up = a.uniform ? 16384.f : scale_of(a.top[kTopG]);
+      scale = pow2(-shift_of(a.top[kTopX]) - shift_of(a.top[kTopW]));
+      up = pow2(a.uniform ? 14 : shift_of(a.top[kTopG]));
     }
   }
   __device__ __forceinline__ void begin(const Tile &, int r, int, int M) {
@@ -365,19 +364,22 @@ struct Factors {
   const uint32_t *top;
   const float *gloss;  // one value for all tokens (uniform), or NULL
   int uniform, mean;
-  __device__ __forceinline__ float of(Top other) const {
-    float f = uniform && gloss ? *gloss : 1.f;
+  // Three factors, to be applied in turn: the halves of the scales' exponent, so
+  // that nothing between leaves the number range, and the common factor.
+  __device__ __forceinline__ float3 of(Top other) const {
+    float3 f = make_float3(1.f, 1.f, uniform && gloss ? *gloss : 1.f);
     if (mean) {
       const int n = *rows.live;
-      f /= (float)(n > 1 ? n : 1);
+      f.z /= (float)(n > 1 ? n : 1);
     }
     if (top) {
-      f *= uniform ? 1.f / 16384.f : inverse_of(scale_of(top[kTopG]));
-      f *= inverse_of(scale_of(top[other]));
+      const int e = -(uniform ? 14 : shift_of(top[kTopG])) - shift_of(top[other]);
+      f.x = pow2(e / 2), f.y = pow2(e - e / 2);
     }
     return f;
   }
 };
+__device__ __forceinline__ float scaled(float v, const float3 &f) { return v * f.x * f.y * f.z; }
 
 // The gradients: product 0 adds up dx over the pieces in fp32 (a slab for each
 // part of a piece), product 1 is a piece of dW.
@@ -394,7 +396,7 @@ struct GradEpi {
   const Args &a;
   Pane panes;
   int *err;
-  float factor;
+  float3 factor;
   int which, row0, slab, pane;  // pane: the one whose store is the older
   __device__ __forceinline__ GradEpi(const Args &args, Pane p, int *e)
       : a(args), panes(p), err(e), factor(args.f.of(kTopX)), pane(0) {}
@@ -424,7 +426,7 @@ struct GradEpi {
       return;
     }
 #pragma unroll
-    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= factor;
+    for (int i = 0; i < gemm::kChunk; ++i) v[i] = scaled(v[i], factor);
     if constexpr (kWide) {
       if (col >= a.d || row0 >= a.words) return;
       put(v);
@@ -477,7 +479,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
               SeqView<IO> dx, int64_t L, int64_t d, int *err) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const float factor = f.of(kTopW);
+  const float3 factor = f.of(kTopW);
   const int live = *f.rows.live, lane = threadIdx.x % 32;
   for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < live; r += gridDim.x * 8ll) {
     const int64_t t = f.rows.token[r];
@@ -491,8 +493,8 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
         const float2 q = *reinterpret_cast<const float2 *>(s + z * zs + c);
         v.x += q.x, v.y += q.y;
       }
-      st_io(o + c, v.x * factor);
-      if (c + 1 < d) st_io(o + c + 1, v.y * factor);
+      st_io(o + c, scaled(v.x, factor));
+      if (c + 1 < d) st_io(o + c + 1, scaled(v.y, factor));
     }
   }
 }
@@ -514,7 +516,7 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
   float m = -INFINITY, s = 0.f;
   auto join = [&](float2 q) {
     const float next = fmaxf(m, q.x), about = next == -INFINITY ? 0.f : next;
-    s = s * ex2(m - about) + q.y * ex2(q.x - about);
+    s = s * ex2((m - about) * kLog2e) + q.y * ex2((q.x - about) * kLog2e);
     m = next;
   };
   if (live && SSD_IN_BOUNDS(row < ld, err, 77)) {
@@ -525,7 +527,7 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
   __syncthreads();
   if (warp || !live) return;
   for (int w = 1; w < kJoinWarps; ++w) join(each[w][lane]);
-  const float l = fmaf(m, kLn2, logf(s));
+  const float l = m + logf(s);
   const int t = rows.token[row];
   lse[t] = l;
   loss[t] = l - rows.zt[row];
