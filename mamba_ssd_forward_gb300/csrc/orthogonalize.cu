@@ -49,26 +49,30 @@ __device__ __forceinline__ void load8(const IO *p, int64_t c, int64_t cols, bool
   }
 }
 
-// The matrices in groups of eight elements, `per` groups to a row; a thread's
-// groups are gridDim.x kNormThreads apart.  Four loads at a time.
+// A matrix in groups of eight elements; a thread's groups are gridDim.x kNormThreads
+// apart, kAtOnce of them loaded together.  Row and column are walked along: a
+// division a group cost as much as its loads (10576 x 2560 bf16 20 us, now NN).
+constexpr int kAtOnce = 4;
 template <typename IO, typename F>
 __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
                                       F f) {
-  const int64_t per = (cols + 7) / 8, all = rows * per, step = (int64_t)gridDim.x * kNormThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < all; i += 4 * step) {
-    float v[4][8];
+  const uint32_t per = (uint32_t)((cols + 7) / 8), step = gridDim.x * kNormThreads;
+  const uint32_t rs = step / per, cs = step % per;  // to a thread's next group
+  const uint32_t i = blockIdx.x * kNormThreads + threadIdx.x;
+  uint32_t r = i / per, c = i % per;
+  while (r < rows) {
+    float v[kAtOnce][8];
+    uint32_t rr[kAtOnce], cc[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k * step < all) {
-        const int64_t r = (i + k * step) / per, c = (i + k * step - r * per) * 8;
-        load8(g.at(blockIdx.y, r), c, cols, wide, v[k]);
-      }
+    for (int k = 0; k < kAtOnce; ++k) {
+      rr[k] = r, cc[k] = c * 8;
+      if (r < rows) load8(g.at(blockIdx.y, r), cc[k], cols, wide, v[k]);
+      r += rs, c += cs;
+      if (c >= per) c -= per, ++r;
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k * step < all) {
-        const int64_t r = (i + k * step) / per;
-        f(v[k], r, (i + k * step - r * per) * 8);
-      }
+    for (int k = 0; k < kAtOnce; ++k)
+      if (rr[k] < rows) f(v[k], rr[k], cc[k]);
   }
 }
 
@@ -203,21 +207,25 @@ struct StepEpi {
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
     if (!some(j)) return;
     const int pane = slot(j) << pair;
+    if (!a.c_planes) {
 #pragma unroll
-    for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
-    if (a.c_planes) {
+      for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
+    } else {
       panes.fetched(slot(j));
-      for (int p = 0; p < a.c_planes; ++p) {
+      const bool two = a.c_planes == 2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 q = panes.cell(pane + p, i);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = panes.cell(pane, i), u = two ? panes.cell(pane + 1, i) : q;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w}, x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
-            v[8 * i + 2 * k] = fmaf(beta, f.x, v[8 * i + 2 * k]);
-            v[8 * i + 2 * k + 1] = fmaf(beta, f.y, v[8 * i + 2 * k + 1]);
+        for (int k = 0; k < 4; ++k) {
+          float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
+          if (two) {  // (exact: 22 bits)
+            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(x + k));
+            f.x += g.x, f.y += g.y;
           }
+          v[8 * i + 2 * k] = fmaf(beta, f.x, alpha * v[8 * i + 2 * k]);
+          v[8 * i + 2 * k + 1] = fmaf(beta, f.y, alpha * v[8 * i + 2 * k + 1]);
         }
       }
     }

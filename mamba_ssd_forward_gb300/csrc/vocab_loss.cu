@@ -68,8 +68,13 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
     const float *p = r < n ? x.at(r / L, r % L) : w + (r - n) * ws;
     uint32_t m = 0;
     if (!SSD_IN_BOUNDS(r < n + V, err, 70)) continue;
-#pragma unroll 4
-    for (int64_t c = lane; c < d; c += 32) m = max(m, __float_as_uint(p[c]) & 0x7fffffffu);
+    for (int64_t c = lane; c < d; c += 8 * 32) {
+      uint32_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < d ? __float_as_uint(p[c + 32 * k]) : 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, v[k] & 0x7fffffffu);
+    }
     if (r < n) {
       most[kTopX] = max(most[kTopX], m);
       if (g) most[kTopG] = max(most[kTopG], __float_as_uint(g[r]) & 0x7fffffffu);
@@ -105,12 +110,20 @@ __device__ __forceinline__ void pack_row(const __nv_bfloat16 *src, uint16_t *dst
 }
 __device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_t ps, int64_t d,
                                          float scale, int tid, int threads) {
-#pragma unroll 4
-  for (int64_t i = tid; i < d; i += threads) {
-    __half hi, lo;
-    split(src[i], scale, hi, lo);
-    dst[i] = __half_as_ushort(hi);
-    dst[ps + i] = __half_as_ushort(lo);
+  constexpr int kAtOnce = 8;
+  for (int64_t i = tid; i < d; i += kAtOnce * threads) {
+    float v[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) v[k] = i + k * threads < d ? src[i + k * threads] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      __half hi, lo;
+      split(v[k], scale, hi, lo);
+      if (i + k * threads < d) {
+        dst[i + k * threads] = __half_as_ushort(hi);
+        dst[ps + i + k * threads] = __half_as_ushort(lo);
+      }
+    }
   }
 }
 
@@ -472,7 +485,7 @@ struct GradEpi {
 };
 
 // dx of the tokens with a target: its slabs added in their order, scaled, and
-// put back in the tokens' places.  A warp takes a row.
+// put back in the tokens' places.  A warp takes 128 columns of a row.
 template <typename IO>
 __global__ void __launch_bounds__(256)
 unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, Factors f,
@@ -481,21 +494,20 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
   ptx::griddep_wait();
   const float3 factor = f.of(kTopW);
   const int live = *f.rows.live, lane = threadIdx.x % 32;
-  for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < live; r += gridDim.x * 8ll) {
-    const int64_t t = f.rows.token[r];
-    IO *o = dx.at(t / L, t % L);
-    const float *s = sum + r * ld;
-    if (!SSD_IN_BOUNDS(d <= ld, err, 79)) return;
-#pragma unroll 4
-    for (int64_t c = lane * 2; c < d; c += 64) {  // ld is even
-      float2 v = *reinterpret_cast<const float2 *>(s + c);
-      for (int z = 1; z < slabs; ++z) {
-        const float2 q = *reinterpret_cast<const float2 *>(s + z * zs + c);
-        v.x += q.x, v.y += q.y;
-      }
-      st_io(o + c, scaled(v.x, factor));
-      if (c + 1 < d) st_io(o + c + 1, scaled(v.y, factor));
+  const int64_t r = blockIdx.x;
+  if (r >= live || !SSD_IN_BOUNDS(d <= ld, err, 79)) return;
+  const int64_t t = f.rows.token[r];
+  IO *o = dx.at(t / L, t % L);
+  for (int64_t c = (threadIdx.x / 32) * 128 + lane * 4; c < d; c += blockDim.x * 4) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};  // (ld is a multiple of 16)
+#pragma unroll 8
+    for (int z = 0; z < slabs; ++z) {
+      const float4 q = *reinterpret_cast<const float4 *>(sum + z * zs + r * ld + c);
+      v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < d) st_io(o + c + e, scaled(v[e], factor));
   }
 }
 
@@ -503,7 +515,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
 
 // 32 rows (lanes) to a block; its warps take the runs in turn and their results
 // are joined in the warps' order.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
             float *__restrict__ loss, float *__restrict__ lse, int *err) {
@@ -520,8 +532,15 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
     m = next;
   };
   if (live && SSD_IN_BOUNDS(row < ld, err, 77)) {
-#pragma unroll 4
-    for (int r = warp; r < runs; r += kJoinWarps) join(part[(int64_t)r * ld + row]);
+    int r = warp;
+    for (; r + 3 * kJoinWarps < runs; r += 4 * kJoinWarps) {  // four loads at a time
+      float2 q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = part[(int64_t)(r + k * kJoinWarps) * ld + row];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) join(q[k]);
+    }
+    for (; r < runs; r += kJoinWarps) join(part[(int64_t)r * ld + row]);
   }
   each[warp][lane] = make_float2(m, s);
   __syncthreads();
@@ -761,9 +780,9 @@ struct Calls {
       e = gemm::launch<GradEpi<IO>, kBN, kSegment>(maps, q, a.dweight ? 2 : 1, kBf16, g, err, st);
     }
     if (e != cudaSuccess || !a.dx) return e;
-    const int64_t sld = gemm::padded(a.d), blocks = (a.n + 7) / 8;
-    return gemm::launch_after(unpack_kernel<IO>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
-                              256, 0, st, p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx),
+    const int64_t sld = gemm::padded(a.d), warps = (a.d + 127) / 128;
+    return gemm::launch_after(unpack_kernel<IO>, dim3((unsigned)a.n),
+                              (int)(32 * (warps < 8 ? warps : 8)), 0, st, p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx),
                               a.L, a.d, err);
   }
 };
