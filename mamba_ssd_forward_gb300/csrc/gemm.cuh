@@ -25,9 +25,9 @@
 // the epilogue's threads add up in registers (rounded to nearest): 64 x 4
 // k a segment measured 4e-6 -> 3e-7 off for sums of 3200 terms.
 //
-// Warps: 0 loads (TMA), 1 issues the products (the pair's first block only), 2 to
-// 9 run the epilogue: warp w reads lanes 32 (w mod 4) .. + 31 (a thread is a
-// row), the first four the left half of the tile's columns, the others the right.
+// Warps: 0 loads (TMA), 1 issues the products (the pair's first block only), the
+// others run the epilogue, eight or sixteen of them: warp w reads lanes 32 (w mod 4)
+// .. + 31 (a thread is a row), each four of them their share of the tile's columns.
 // Every wait is bounded.
 #pragma once
 
@@ -43,21 +43,19 @@ namespace ssd {
 namespace gemm {
 
 constexpr int kTileM = 256, kRows = 128, kTileK = 64;  // of a pair; of a block; per stage
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kChunk = 32;  // columns an epilogue thread holds at a time
 constexpr int kExact = 4;   // stages to a segment where fp32's precision is asked for
 constexpr int kBytesA = kRows * 128;
 
-constexpr int kPaneBytes = 8192;  // of an epilogue's warp
-constexpr int kPaneBars = 4;
+constexpr int kPaneBytes = 65536;  // of all epilogue warps
+constexpr int kPaneBars = 2;       // of a warp
 
 // kStaged: the epilogue's warps have panes.
 template <int kBN, bool kStaged>
 struct Shape {
   static constexpr int kBytesB = kBN / 2 * 128;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kPanes = kStaged ? kEpiWarps * kPaneBytes : 0;
+  static constexpr int kPanes = kStaged ? kPaneBytes : 0;
   static constexpr int kStages = (229376 - kPanes) / kStage;
   static constexpr int kSmem = kStages * kStage + kPanes + 1024;
   static constexpr uint32_t kTmemCols = 2 * kBN;
@@ -231,8 +229,8 @@ __device__ __forceinline__ bool elected() {
 // A warp's panes in shared memory.  A thread holds a row of the tile; through a
 // pane, 32 rows, values go to memory and come from it by TMA, which clips what
 // lies outside the array.  (Row by row from registers every access would touch 32
-// lines: measured 16000 clocks a tile against 6000 of products.)  Two panes with
-// rows of 128 bytes, or four with rows of 64, swizzled.
+// lines: measured 16000 clocks a tile against 6000 of products.)  Rows of 128 or 64
+// bytes, swizzled; a warp has 8 KB of panes, or 4 KB where there are sixteen warps.
 template <int kRowBytes>
 struct Panes {
   static constexpr int kBytes = 32 * kRowBytes;
@@ -298,9 +296,9 @@ struct Panes {
 // kSegment: stages to a segment, 0: all k in one.
 // Epi: constructed from its Args and panes by every epilogue thread, then per tile
 // begin(tile, row, column, rows), chunk(v, column, j) for each 32 columns of the
-// thread's row, end().  kStaged: it uses the panes, of type Pane.
+// thread's row, end().  kWarps: epilogue warps; kStaged: they use panes, of type Pane.
 template <class Epi, int kBN, int kSegment>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (2 + Epi::kWarps), 1)
 product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
                const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
                const __grid_constant__ Product p0, const __grid_constant__ Product p1,
@@ -313,7 +311,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   // empty: its products are done; accfull: a tile's are; accfree: both blocks'
   // epilogues have read them (the first block's)
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], accfull[2], accfree[2];
-  __shared__ __align__(8) uint64_t landed[kEpiWarps][kPaneBars];  // panes of each epilogue warp
+  __shared__ __align__(8) uint64_t landed[Epi::kWarps][kPaneBars];  // panes of each epilogue warp
   __shared__ uint32_t tmem_slot;
   __shared__ Walk<kBN> walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,9 +324,9 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&accfull[i], 1);
-      ptx::mbar_init(&accfree[i], 2 * kEpiWarps);
+      ptx::mbar_init(&accfree[i], 2 * Epi::kWarps);
     }
-    for (int i = 0; i < kEpiWarps * kPaneBars; ++i) ptx::mbar_init(&landed[0][i], 1);
+    for (int i = 0; i < Epi::kWarps * kPaneBars; ++i) ptx::mbar_init(&landed[0][i], 1);
     ptx::fence_mbar_init();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();  // (the numbers of rows are an earlier launch's)
@@ -418,9 +416,10 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       }
     }
   } else {
-    constexpr int kHalf = kBN / 2, kChunks = kHalf / kChunk;
-    const int quad = warp & 3, c0 = warp >= 6 ? kHalf : 0;
-    uint8_t *panes = smem + S::kStages * S::kStage + (warp - 2) * kPaneBytes;
+    constexpr int kShare = kBN / (Epi::kWarps / 4), kChunks = kShare / kChunk;
+    static_assert(kChunks * kChunk == kShare, "");
+    const int quad = warp & 3, c0 = (warp - 2) / 4 * kShare;
+    uint8_t *panes = smem + S::kStages * S::kStage + (warp - 2) * (kPaneBytes / Epi::kWarps);
     Epi epi(args, typename Epi::Pane(panes, landed[warp - 2], err), err);
     int n = 0;
     // 32 columns of the accumulator at `at`; the last ones hand it back
@@ -563,7 +562,7 @@ cudaError_t launch(const CUtensorMap *maps, const Product *p, int count, bool bf
   const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
   if (!grid) return cudaSuccess;
   const int last = count - 1;
-  return launch_after(kernel, dim3(grid), kThreads, S::kSmem, st, maps[0], maps[1], maps[2 * last],
+  return launch_after(kernel, dim3(grid), 32 * (2 + Epi::kWarps), S::kSmem, st, maps[0], maps[1], maps[2 * last],
                       maps[2 * last + 1], p[0], p[last], count, (int)bf16, args, err);
 }
 

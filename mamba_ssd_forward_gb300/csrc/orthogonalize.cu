@@ -161,7 +161,7 @@ struct StepEpi {
     int power;
     int c_planes, c_stored;  // planes of C to add (0: no C), and in its array
     int d_stored;            // of D
-    int half;                // columns of the tile that a warp takes
+    int share;               // columns of the tile that a warp takes
     int symmetric;           // there are mirrored tiles
     __half *out;             // D again, for the mirrored tiles of two planes
     int64_t ld, ps, zs;
@@ -169,14 +169,17 @@ struct StepEpi {
     SeqView<float> f32;
     int N, wide;  // columns; wide: rows of the result start on 16 bytes
   };
+  // Sixteen warps: with few k to a tile the epilogue is what a tile takes longest
+  // for, and the last tile's is not covered by anything.
+  static constexpr int kWarps = 16;
   static constexpr bool kStaged = true;
   using Pane = gemm::Panes<64>;
   const Args &a;
   Pane panes;
   int *err;
   float alpha, beta;
-  // A chunk's planes, or its plane and its mirror image, have two of the four
-  // panes; else one.
+  // A chunk's planes, or its plane and its mirror image, have both panes; else each
+  // chunk has its own.
   int row, row0, col0, M, mirror, pair;
   int64_t batch;
   __device__ __forceinline__ StepEpi(const Args &args, Pane p, int *e)
@@ -192,21 +195,22 @@ struct StepEpi {
     alpha = a.alpha * f, beta = a.beta * f;
     panes.template reuse<0>();
     // C of the first chunks, while the products run
-    for (int j = 0; j < (pair ? 2 : 4); ++j) fetch(j);
+    fetch(0);
+    if (!pair) fetch(1);
   }
   // whether any of the warp's 32 rows x 32 columns of chunk j is there
   __device__ __forceinline__ bool some(int j) const {
-    return row0 < M && col0 + gemm::kChunk * j < a.N && gemm::kChunk * j < a.half;
+    return row0 < M && col0 + gemm::kChunk * j < a.N && gemm::kChunk * j < a.share;
   }
-  __device__ __forceinline__ int slot(int j) const { return pair ? j & 1 : j & 3; }
+  __device__ __forceinline__ int slot(int j) const { return pair ? 0 : j & 1; }
   __device__ __forceinline__ void fetch(int j) const {
     if (a.c_planes && some(j))
-      panes.fetch(slot(j), slot(j) << pair, a.c_planes, &a.c, col0 + gemm::kChunk * j, row0,
+      panes.fetch(slot(j), slot(j), a.c_planes, &a.c, col0 + gemm::kChunk * j, row0,
                   (int)batch * a.c_stored);
   }
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
     if (!some(j)) return;
-    const int pane = slot(j) << pair;
+    const int pane = slot(j);
     if (!a.c_planes) {
 #pragma unroll
       for (int i = 0; i < gemm::kChunk; ++i) v[i] *= alpha;
@@ -229,10 +233,6 @@ struct StepEpi {
         }
       }
     }
-    if (pair && j > 0) {  // the other slot is free once its store has read it
-      panes.template reuse<0>();
-      fetch(j + 1);
-    }
     if constexpr (kind == kF32) {
       if (row < M) {
         float *o = a.f32.at(batch, row) + col;
@@ -249,6 +249,7 @@ struct StepEpi {
         }
       }
       panes.written();  // (C is read)
+      if (pair) fetch(j + 1);
       return;
     }
 #pragma unroll
@@ -288,6 +289,10 @@ struct StepEpi {
       ptx::bulk_commit();
     }
     __syncwarp();
+    if (pair && some(j + 1)) {  // the panes are free once the store has read them
+      panes.template reuse<0>();
+      fetch(j + 1);
+    }
   }
   static __device__ __forceinline__ uint4 pack_bf16(const float *v) {
     uint32_t w[4];
@@ -419,7 +424,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
     int bn = tile_columns(q);
     auto gram = [&](auto &s) {
       s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
-      s.out = p.gram, s.d_stored = p.planes, s.half = bn / 2, s.symmetric = 1;
+      s.out = p.gram, s.d_stored = p.planes, s.share = bn / 4, s.symmetric = 1;
       s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
       return pane_gram(&s.d, p.gram);
     };
@@ -457,7 +462,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
       u.alpha = 1.f / kGramScale, u.beta = a.a, u.rest = k ? nullptr : p.rest, u.power = 1;
       if (last) u.alpha /= kScale, u.beta /= kScale;
       u.c_planes = carried(k), u.c_stored = 2, u.d_stored = 1;
-      u.N = (int)a.cols, u.half = bn / 2;
+      u.N = (int)a.cols, u.share = bn / 4;
       return pane_x(&u.c, x);
     };
     if (!last) {

@@ -236,6 +236,7 @@ struct StatsEpi {
   const Args &a;
   int *err;
   static constexpr bool kStaged = false;
+  static constexpr int kWarps = 8;
   using Pane = gemm::Panes<128>;
   float unit, m, s;  // unit: a logit to the tensor cores' sum
   int row, run, target;
@@ -313,6 +314,7 @@ struct DlogitEpi {
     int V, word0, uniform;
   };
   static constexpr bool kStaged = true, kSplit = sizeof(IO) == 4;
+  static constexpr int kWarps = 8;
   using Pane = gemm::Panes<128>;
   const Args &a;
   Pane panes;
@@ -405,6 +407,7 @@ struct GradEpi {
     int d, words, first, direct;
   };
   static constexpr bool kStaged = true, kWide = sizeof(IO) == 4;
+  static constexpr int kWarps = 8;
   using Pane = gemm::Panes<128>;
   const Args &a;
   Pane panes;
