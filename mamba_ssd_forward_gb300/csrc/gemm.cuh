@@ -332,6 +332,14 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
     ptx::griddep_wait();  // (the numbers of rows are an earlier launch's)
     walk.plan(p0, p1, count);
   }
+  if (warp == 2 && elected()) {  // (parameters: no earlier launch's)
+    ptx::prefetch_tmap(&a0);
+    ptx::prefetch_tmap(&b0);
+    if (count > 1) {
+      ptx::prefetch_tmap(&a1);
+      ptx::prefetch_tmap(&b1);
+    }
+  }
   if (warp == 1) tmem_alloc(&tmem_slot, S::kTmemCols);
   ptx::tc_fence_before();
   __syncthreads();
@@ -345,14 +353,6 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
   // products): what does not change within a tile is in registers, and one lane
   // is elected where an instruction is a single thread's.
   if (warp == 0) {
-    if (elected()) {
-      ptx::prefetch_tmap(&a0);
-      ptx::prefetch_tmap(&b0);
-      if (count > 1) {
-        ptx::prefetch_tmap(&a1);
-        ptx::prefetch_tmap(&b1);
-      }
-    }
     int s = 0, round = 0;
     const uint32_t bars = in_first(full);
     for (int t = start; t < walk.total; t += step) {
