@@ -13,7 +13,8 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from .layer import (_IO, _dense, _first_order, _io, _needed, _out, _seq, _separate,
+from ._abi import SsdAddNormDims, SsdSeq
+from .layer import (_IO, _dense, _first_order, _io, _needed, _out, _refuse, _seq, _separate,
                     _stream, _token, _wanted, _workspace)
 
 _REDUCTIONS = {"none": _abi.SSD_REDUCE_NONE, "sum": _abi.SSD_REDUCE_SUM,
@@ -24,8 +25,8 @@ def _lead(x, name):
     """Sequences and tokens of [tokens, D] (one sequence) or [b, L, D]."""
     if x.dim() not in (2, 3):
         raise ValueError(f"{name} must be [tokens, D] or [b, L, D]")
-    b, L = (1, x.shape[0]) if x.dim() == 2 else x.shape[:2]
-    if not b * L or not x.shape[-1]:
+    b, L, D = x.shape if x.dim() == 3 else (1, *x.shape)
+    if not b * L * D:
         raise ValueError(f"{name} must not be empty")
     return b, L
 
@@ -43,30 +44,47 @@ def _view(t, name, shape, dtype, like):
 
 # -------------------------------------------------- residual addition and norm
 
+# A call for a few tokens takes 5 us on the device, so these two keep to as few
+# Python calls as their checks allow (23 us -> NN).
+
 def _stream_type(x, stream):
     """The residual stream's type: that of x, or float32."""
-    if stream not in (x.dtype, torch.float32):
+    if stream is not x.dtype and stream is not torch.float32:
         raise TypeError(f"the residual must be {x.dtype} or torch.float32, got {stream}")
     return stream
 
 
 def _add_norm_dims(x, eps):
     b, L = _lead(x, "x")
-    return _abi.SsdAddNormDims(b, L, x.shape[-1], eps)
+    return SsdAddNormDims(b, L, x.shape[-1], eps)
+
+
+def _rows(t, name, shape, dtype, dev, like):
+    """View of [tokens, D] or [b, L, D]; what else it may be is refused."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(t, name, shape, dtype, like)
+    *lead, last = t.stride()
+    if last != 1 and shape[-1] != 1:
+        _refuse(t, name, shape, dtype, like)
+    if len(lead) == 1:
+        return SsdSeq(t.data_ptr(), 0, lead[0] if shape[0] > 1 else 0)
+    return SsdSeq(t.data_ptr(), lead[0] if shape[0] > 1 else 0, lead[1] if shape[1] > 1 else 0)
 
 
 def _add_norm_inputs(x, residual, weight, total, eps):
-    """The leading arguments of the forward calls, checked, and total."""
-    d, io = _add_norm_dims(x, eps), _io(x, "x")
-    if residual is not None:
-        stream = _stream_type(x, residual.dtype)
-    else:
-        stream = x.dtype if total is None else _stream_type(x, total.dtype)
-    if residual is not None or total is not None:
-        total = _out(total, "total", x.shape, stream, x)
-    return [d, io, _IO[stream]], [
-        _view(x, "x", x.shape, x.dtype, x), _view(residual, "residual", x.shape, stream, x),
-        _dense(weight, "weight", (x.shape[-1],), torch.float32, x)], total, stream
+    """What both forward calls check and pass, and total."""
+    d, io, shape, dev = _add_norm_dims(x, eps), _io(x, "x"), x.shape, x.get_device()
+    like = residual if residual is not None else total
+    stream = x.dtype if like is None else _stream_type(x, like.dtype)
+    if total is not None:
+        _out(total, "total", shape, stream, x)
+        _separate(total, "total", x, "x")
+    elif residual is not None:
+        total = torch.empty(shape, dtype=stream, device=x.device)
+    return (d, io, _IO[stream], _rows(x, "x", shape, x.dtype, dev, x),
+            None if residual is None else _rows(residual, "residual", shape, stream, dev, x),
+            _dense(weight, "weight", shape[-1:], torch.float32, x),
+            None if total is None else _rows(total, "total", shape, stream, dev, x), total)
 
 
 def add_norm_forward(x, residual, weight, eps: float = 1e-5, y=None, total=None):
@@ -77,13 +95,13 @@ def add_norm_forward(x, residual, weight, eps: float = 1e-5, y=None, total=None)
     shape, in the I/O type or float32; weight [D] float32.  The norm is that of the
     sum before total's rounding.  Without a residual (None) total is None
     unless it is given.  y may be x, total may be residual."""
-    head, inputs, total, stream = _add_norm_inputs(x, residual, weight, total, eps)
+    d, io, st, xv, rv, w, tv, total = _add_norm_inputs(x, residual, weight, total, eps)
     y = _out(y, "y", x.shape, x.dtype, x)
     _separate(y, "y", residual, "residual")
-    _separate(total, "total", x, "x")
-    _abi.check("ssd_add_norm", _abi.load().ssd_add_norm(
-        *head, *inputs, _view(y, "y", x.shape, x.dtype, x),
-        _view(total, "total", x.shape, stream, x), _stream(x)))
+    yv = _rows(y, "y", x.shape, x.dtype, x.get_device(), x)
+    code = _abi.load().ssd_add_norm(d, io, st, xv, rv, w, yv, tv, _stream(x))
+    if code:
+        _abi.check("ssd_add_norm", code)
     return y, total
 
 
@@ -95,17 +113,19 @@ def add_norm_quantized(x, residual, weight, block: int = 128, eps: float = 1e-5,
     channels (32, 64 or 128) or, with block = 0, over the token."""
     if block not in (0, 32, 64, 128):
         raise ValueError(f"block must be 0, 32, 64 or 128, got {block!r}")
-    head, inputs, total, stream = _add_norm_inputs(x, residual, weight, total, eps)
-    parts = -(-x.shape[-1] // block) if block else 1
-    shape = (*x.shape[:-1], parts)
-    q = _out(q, "q", x.shape, torch.float8_e4m3fn, x)
+    d, io, st, xv, rv, w, tv, total = _add_norm_inputs(x, residual, weight, total, eps)
+    shape = x.shape
+    parts = (*shape[:-1], -(-shape[-1] // block) if block else 1)
+    q = _out(q, "q", shape, torch.float8_e4m3fn, x)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-    _separate(total, "total", x, "x")
-    _abi.check("ssd_add_norm_quantized", _abi.load().ssd_add_norm_quantized(
-        *head, block, *inputs, _view(q, "q", x.shape, torch.float8_e4m3fn, x),
-        _dense(scales, "scales", shape, torch.float32, x),
-        _view(total, "total", x.shape, stream, x), _stream(x)))
+        scales = torch.empty(parts, dtype=torch.float32, device=x.device)
+        at = scales.data_ptr()
+    else:
+        at = _dense(scales, "scales", parts, torch.float32, x)
+    qv = _rows(q, "q", shape, torch.float8_e4m3fn, x.get_device(), x)
+    code = _abi.load().ssd_add_norm_quantized(d, io, st, block, xv, rv, w, qv, at, tv, _stream(x))
+    if code:
+        _abi.check("ssd_add_norm_quantized", code)
     return q, scales, total
 
 
