@@ -504,7 +504,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
 inline bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t z,
                      int64_t ld, int64_t zs, bool mn, int box) {
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)z};
-  const uint64_t strides[2] = {(uint64_t)ld * 2, (uint64_t)zs * 2};
+  const uint64_t strides[2] = {(uint64_t)ld * 2, (uint64_t)(z > 1 ? zs : ld) * 2};
   const uint32_t b[3] = {64, (uint32_t)(mn ? 64 : box), 1};
   return make_tmap_sw128(map, base, true, 3, dims, strides, b);
 }
@@ -515,7 +515,7 @@ bool make_pane_map(CUtensorMap *map, const void *base, bool fp32, int64_t cols, 
                    int64_t z, int64_t ld, int64_t zs) {
   const uint64_t e = fp32 ? 4 : 2;
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)z};
-  const uint64_t strides[2] = {(uint64_t)ld * e, (uint64_t)zs * e};
+  const uint64_t strides[2] = {(uint64_t)ld * e, (uint64_t)(z > 1 ? zs : ld) * e};
   const uint32_t b[3] = {(uint32_t)(kRowBytes / e), 32, 1};
   return (kRowBytes == 128 ? make_tmap_sw128 : make_tmap_sw64)(map, base, !fp32, 3, dims, strides,
                                                                b);

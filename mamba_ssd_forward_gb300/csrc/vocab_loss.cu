@@ -39,9 +39,9 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // ------------------------------------------------- largest values, and scales
 
 // The power of two (its exponent) that takes values of the size of `top` (a float's
-// bits) to 2^14 .. 2^15; 0 for zero, infinity and NaN.
+// bits) to 2^14 .. 2^15; 0 for zero.
 __device__ __forceinline__ int shift_of(uint32_t top) {
-  if (top == 0 || top >= 0x7f800000u) return 0;
+  if (top == 0) return 0;
   const int e = (int)(top >> 23) - 127;
   return 14 - (e < -110 ? -110 : e);
 }
@@ -54,8 +54,13 @@ enum Top { kTopX, kTopW, kTopG, kTops };
 
 __device__ __forceinline__ bool counted(int64_t target, int64_t ignore) { return target != ignore; }
 
-// Bits of the largest |value| (of a NaN: above infinity's) of x's rows with a
-// target, of W, and of the tokens' factors.  The order of the maxima has no say.
+// Bits of the largest finite |value| of x's rows with a target, of W, and of the
+// tokens' factors.  (A row's infinity or NaN must not cost the other rows their
+// scale.)  The order of the maxima has no say.
+__device__ __forceinline__ uint32_t size_of(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
 __global__ void __launch_bounds__(256)
 top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t ignore, int64_t L,
            int64_t n, const float *__restrict__ w, int64_t ws, int64_t V, int64_t d,
@@ -71,13 +76,13 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
     for (int64_t c = lane; c < d; c += 8 * 32) {
       uint32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < d ? __float_as_uint(p[c + 32 * k]) : 0u;
+      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < d ? size_of(p[c + 32 * k]) : 0u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, v[k] & 0x7fffffffu);
+      for (int k = 0; k < 8; ++k) m = max(m, v[k]);
     }
     if (r < n) {
       most[kTopX] = max(most[kTopX], m);
-      if (g) most[kTopG] = max(most[kTopG], __float_as_uint(g[r]) & 0x7fffffffu);
+      if (g) most[kTopG] = max(most[kTopG], size_of(g[r]));
     } else {
       most[kTopW] = max(most[kTopW], m);
     }
@@ -137,15 +142,37 @@ struct Rows {
 };
 
 constexpr int kPackTokens = 8, kPackThreads = 256;  // a warp to a token
+constexpr int kGroup = 2048;                        // tokens counted together
+
+// Targets of each group of tokens.
+__global__ void __launch_bounds__(kPackThreads)
+count_kernel(const int64_t *__restrict__ targets, int64_t ignore, int64_t n,
+             int *__restrict__ counts, int *err) {
+  __shared__ int sums[kPackThreads / 32];
+  const int64_t first = (int64_t)blockIdx.x * kGroup;
+  int c = 0;
+#pragma unroll
+  for (int k = 0; k < kGroup / kPackThreads; ++k) {
+    const int64_t i = first + k * kPackThreads + threadIdx.x;
+    if (i < n && SSD_IN_BOUNDS(i >= 0, err, 69)) c += counted(targets[i], ignore);
+  }
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = c;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < kPackThreads / 32; ++w) c += sums[w];
+  counts[blockIdx.x] = c;
+}
 
 // A block takes kPackTokens tokens.  It counts the targets in front of them
-// itself (they come from L2), so no launch of its own makes the list.
+// itself (they come from L2), so no launch of its own makes the list; of many
+// tokens (counts not NULL) those of whole groups are counted before.
 template <typename IO>
 __global__ void __launch_bounds__(kPackThreads)
 pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
             int64_t L, int64_t n, int64_t d, const float *__restrict__ lse,
             const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
-            float *__restrict__ lse_out, Rows rows, uint16_t *__restrict__ xp, int64_t ld,
+            float *__restrict__ lse_out, const int *__restrict__ counts, Rows rows, uint16_t *__restrict__ xp, int64_t ld,
             int64_t ps, int planes, const uint32_t *__restrict__ top, int *err) {
   __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
@@ -153,8 +180,11 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   int before = 0;
+  const int64_t groups = counts ? first / kGroup : 0;
+  for (int64_t i = tid; i < groups; i += kPackThreads) before += counts[i];
 #pragma unroll 4
-  for (int64_t i = tid; i < first; i += kPackThreads) before += counted(targets[i], ignore);
+  for (int64_t i = groups * kGroup + tid; i < first; i += kPackThreads)
+    before += counted(targets[i], ignore);
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) sums[warp] = before;
   __syncthreads();
@@ -587,6 +617,7 @@ struct Plan {
   int64_t rows, ld, piece, dz_ld;  // padded rows; elements to a packed row; words; dz's row
   bool direct;                     // W as it is
   uint32_t *top;
+  int *counts;  // NULL for few tokens
   Rows r;
   uint16_t *xp, *wp, *dz;
   float2 *stat;
@@ -616,6 +647,8 @@ Plan plan_of(const LossArgs &a, ssd_dtype io, bool back, void *ws) {
   p.runs = all / kRun;
   Carver c(ws);
   p.top = c.take<uint32_t>(kTops);
+  // (a block would count 8192 targets in a few microseconds, 10^6 in 100)
+  p.counts = a.n > 4 * kGroup ? c.take<int>((a.n + kGroup - 1) / kGroup) : nullptr;
   p.r.live = c.take<int>(1);
   p.r.token = c.take<int>(a.n);
   p.r.target = c.take<int>(a.n);
@@ -664,16 +697,20 @@ struct Calls {
             static_cast<const float *>(a.weight->data), a.weight->token_stride, a.V, a.d, g, p.top,
             err);
     }
+    if (p.counts)
+      count_kernel<<<(unsigned)((a.n + kGroup - 1) / kGroup), kPackThreads, 0, st>>>(
+          a.targets, a.ignore, a.n, p.counts, err);
     // (the first launch of the call waits for what is on the stream the ordinary way)
     const dim3 grid((unsigned)((a.n + kPackTokens - 1) / kPackTokens));
-    if (top)
+    if (top || p.counts)
       return gemm::launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
                                 a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
-                                view_of<IO>(a.dx), loss, lse, p.r, p.xp, p.ld, p.rows * p.ld,
-                                kPlanes, top, err);
+                                view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld,
+                                p.rows * p.ld, kPlanes, top, err);
     pack_kernel<IO><<<grid, kPackThreads, 0, st>>>(
         view_of<const IO>(a.x), a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
-        view_of<IO>(a.dx), loss, lse, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, top, err);
+        view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, top,
+        err);
     return cudaGetLastError();
   }
 

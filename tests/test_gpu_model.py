@@ -310,6 +310,31 @@ def test_logits_at_the_ends(ssd):
     assert dx["dweight"] is None and torch.isfinite(dx["dx"][[0, 3, 4]]).all()
 
 
+def test_an_infinite_fp32_row_costs_the_others_nothing(ssd):
+    x, w, t, n = loss_case((70, 64, 300), "fp32", "none")
+    x *= 2.0 ** 20
+    w *= 2.0 ** -20
+    lse = ssd.linear_cross_entropy_forward(x, w, t)[1]
+    y, keep = x.clone(), torch.arange(70, device="cuda") != 9
+    y[9, 3] = math.inf
+    loss, got = ssd.linear_cross_entropy_forward(y, w, t)
+    assert not torch.isfinite(loss[9]) and torch.equal(got[keep], lse[keep])
+    dx = ssd.linear_cross_entropy_backward(y, w, t, got, want=("dx",))["dx"]
+    ref = ssd.linear_cross_entropy_backward(x, w, t, lse, want=("dx",))["dx"]
+    assert torch.equal(dx[keep], ref[keep])
+
+
+@pytest.mark.parametrize("tokens", [8192, 8193, 20000])
+def test_many_tokens_with_few_targets(ssd, tokens):
+    """Targets counted by the packing blocks themselves, and in groups."""
+    n = gen(tokens)
+    x, w = n(tokens, 24, dtype=B16), n(90, 24, scale=0.4, dtype=B16)
+    t = torch.full((tokens,), -100, device="cuda")
+    t[::97] = torch.arange(len(t[::97]), device="cuda") % 90
+    t[-1] = 5
+    check_loss(ssd, x, w, t, n(tokens), "bf16", 24, 90)
+
+
 @pytest.mark.parametrize("size", [1e-25, 1e-6, 1e6, 1e15])
 def test_fp32_operands_of_any_size(ssd, size):
     """x and W scaled against one another: the same logits."""
