@@ -161,7 +161,7 @@ struct Quant {
 __device__ __forceinline__ float quantiser(float top, float *scale) {
   const float m = fmaxf(top, kTop8 * kLeastScale);
   if (scale) *scale = top == 0.f ? 0.f : m * (1.f / kTop8);
-  return __fdividef(kTop8, m);
+  return __fdividef(0.25f * kTop8, 0.25f * m);  // (it takes no divisor beyond 2^126)
 }
 // V values of a warp's 256 channels in e4m3, a scale to each qu.block of them.
 template <bool kWide>

@@ -562,8 +562,9 @@ cudaError_t launch(const CUtensorMap *maps, const Product *p, int count, bool bf
   const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
   if (!grid) return cudaSuccess;
   const int last = count - 1;
-  return launch_after(kernel, dim3(grid), 32 * (2 + Epi::kWarps), S::kSmem, st, maps[0], maps[1], maps[2 * last],
-                      maps[2 * last + 1], p[0], p[last], count, (int)bf16, args, err);
+  return launch_after(kernel, dim3(grid), 32 * (2 + Epi::kWarps), S::kSmem, st, maps[0], maps[1],
+                      maps[2 * last], maps[2 * last + 1], p[0], p[last], count, (int)bf16, args,
+                      err);
 }
 
 }  // namespace gemm

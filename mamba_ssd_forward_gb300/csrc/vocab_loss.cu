@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(kPackThreads)
 pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ignore, int64_t V,
             int64_t L, int64_t n, int64_t d, const float *__restrict__ lse,
             const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
-            float *__restrict__ lse_out, const int *__restrict__ counts, Rows rows, uint16_t *__restrict__ xp, int64_t ld,
-            int64_t ps, int planes, const uint32_t *__restrict__ top, int *err) {
+            float *__restrict__ lse_out, const int *__restrict__ counts, Rows rows,
+            uint16_t *__restrict__ xp, int64_t ld, int64_t ps, int planes,
+            const uint32_t *__restrict__ top, int *err) {
   __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -246,7 +247,8 @@ pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (r >= rows || !SSD_IN_BOUNDS(ld >= d && ws >= 0, err, 72)) return;
-  pack_row(w + r * ws, wp + r * ld, ps, d, top ? pow2(shift_of(top[kTopW])) : 1.f, threadIdx.x % 32, 32);
+  pack_row(w + r * ws, wp + r * ld, ps, d, top ? pow2(shift_of(top[kTopW])) : 1.f,
+           threadIdx.x % 32, 32);
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -585,7 +587,8 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
   loss[t] = l - rows.zt[row];
 }
 
-// The sum of every token's loss (or the mean over those with a target, 0 without one), in a fixed order.
+// The sum of every token's loss (or the mean over those with a target, 0 without
+// one), in a fixed order.
 __global__ void __launch_bounds__(1024)
 total_kernel(const float *__restrict__ loss, int64_t n, const int *__restrict__ live, int mean,
              float *__restrict__ total, int *err) {
@@ -696,10 +699,15 @@ struct Calls {
             view_of<const float>(a.x), a.targets, a.ignore, a.L, a.n,
             static_cast<const float *>(a.weight->data), a.weight->token_stride, a.V, a.d, g, p.top,
             err);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
     }
-    if (p.counts)
+    if (p.counts) {
       count_kernel<<<(unsigned)((a.n + kGroup - 1) / kGroup), kPackThreads, 0, st>>>(
           a.targets, a.ignore, a.n, p.counts, err);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
     // (the first launch of the call waits for what is on the stream the ordinary way)
     const dim3 grid((unsigned)((a.n + kPackTokens - 1) / kPackTokens));
     if (top || p.counts)
@@ -822,8 +830,8 @@ struct Calls {
     if (e != cudaSuccess || !a.dx) return e;
     const int64_t sld = gemm::padded(a.d), warps = (a.d + 127) / 128;
     return gemm::launch_after(unpack_kernel<IO>, dim3((unsigned)a.n),
-                              (int)(32 * (warps < 8 ? warps : 8)), 0, st, p.sum, sld, p.rows * sld, p.slabs, f, view_of<IO>(a.dx),
-                              a.L, a.d, err);
+                              (int)(32 * (warps < 8 ? warps : 8)), 0, st, p.sum, sld, p.rows * sld,
+                              p.slabs, f, view_of<IO>(a.dx), a.L, a.d, err);
   }
 };
 

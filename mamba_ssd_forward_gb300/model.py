@@ -44,8 +44,8 @@ def _view(t, name, shape, dtype, like):
 
 # -------------------------------------------------- residual addition and norm
 
-# A call for a few tokens takes 5 us on the device, so these two keep to as few
-# Python calls as their checks allow (23 us -> NN).
+# A call for a few tokens takes 5 us on the device, so these keep to as few Python
+# steps as their checks allow.
 
 def _stream_type(x, stream):
     """The residual stream's type: that of x, or float32."""
@@ -63,28 +63,40 @@ def _rows(t, name, shape, dtype, dev, like):
     """View of [tokens, D] or [b, L, D]; what else it may be is refused."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
         _refuse(t, name, shape, dtype, like)
-    *lead, last = t.stride()
-    if last != 1 and shape[-1] != 1:
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
         _refuse(t, name, shape, dtype, like)
-    if len(lead) == 1:
-        return SsdSeq(t.data_ptr(), 0, lead[0] if shape[0] > 1 else 0)
-    return SsdSeq(t.data_ptr(), lead[0] if shape[0] > 1 else 0, lead[1] if shape[1] > 1 else 0)
+    if len(st) == 2:
+        return SsdSeq(t.data_ptr(), 0, st[0] if shape[0] > 1 else 0)
+    return SsdSeq(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+
+
+def _new_rows(shape, dtype, like):
+    """A new dense tensor of that shape, and its view."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    D = shape[-1]
+    return t, SsdSeq(t.data_ptr(), shape[1] * D if len(shape) == 3 else 0, D)
 
 
 def _add_norm_inputs(x, residual, weight, total, eps):
-    """What both forward calls check and pass, and total."""
-    d, io, shape, dev = _add_norm_dims(x, eps), _io(x, "x"), x.shape, x.get_device()
+    """What both forward calls check and pass, total, and what they share."""
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    d, io = _add_norm_dims(x, eps), _io(x, "x")
     like = residual if residual is not None else total
-    stream = x.dtype if like is None else _stream_type(x, like.dtype)
+    stream = dtype if like is None else _stream_type(x, like.dtype)
+    xv = _rows(x, "x", shape, dtype, dev, x)
+    rv = None if residual is None else _rows(residual, "residual", shape, stream, dev, x)
+    if (weight.dtype is not torch.float32 or weight.dim() != 1 or len(weight) != shape[-1]
+            or weight.stride(0) != 1 or weight.get_device() != dev):
+        _dense(weight, "weight", shape[-1:], torch.float32, x)
+    tv = None
     if total is not None:
         _out(total, "total", shape, stream, x)
         _separate(total, "total", x, "x")
+        tv = _rows(total, "total", shape, stream, dev, x)
     elif residual is not None:
-        total = torch.empty(shape, dtype=stream, device=x.device)
-    return (d, io, _IO[stream], _rows(x, "x", shape, x.dtype, dev, x),
-            None if residual is None else _rows(residual, "residual", shape, stream, dev, x),
-            _dense(weight, "weight", shape[-1:], torch.float32, x),
-            None if total is None else _rows(total, "total", shape, stream, dev, x), total)
+        total, tv = _new_rows(shape, stream, x)
+    return (d, io, _IO[stream]), (xv, rv, weight.data_ptr()), total, tv, shape, dev
 
 
 def add_norm_forward(x, residual, weight, eps: float = 1e-5, y=None, total=None):
@@ -95,11 +107,15 @@ def add_norm_forward(x, residual, weight, eps: float = 1e-5, y=None, total=None)
     shape, in the I/O type or float32; weight [D] float32.  The norm is that of the
     sum before total's rounding.  Without a residual (None) total is None
     unless it is given.  y may be x, total may be residual."""
-    d, io, st, xv, rv, w, tv, total = _add_norm_inputs(x, residual, weight, total, eps)
-    y = _out(y, "y", x.shape, x.dtype, x)
-    _separate(y, "y", residual, "residual")
-    yv = _rows(y, "y", x.shape, x.dtype, x.get_device(), x)
-    code = _abi.load().ssd_add_norm(d, io, st, xv, rv, w, yv, tv, _stream(x))
+    head, ins, total, tv, shape, dev = _add_norm_inputs(x, residual, weight, total, eps)
+    if y is None:
+        y, yv = _new_rows(shape, x.dtype, x)
+    else:
+        _out(y, "y", shape, x.dtype, x)
+        _separate(y, "y", residual, "residual")
+        _separate(y, "y", total, "total")
+        yv = _rows(y, "y", shape, x.dtype, dev, x)
+    code = _abi.load().ssd_add_norm(*head, *ins, yv, tv, _stream(x))
     if code:
         _abi.check("ssd_add_norm", code)
     return y, total
@@ -113,17 +129,20 @@ def add_norm_quantized(x, residual, weight, block: int = 128, eps: float = 1e-5,
     channels (32, 64 or 128) or, with block = 0, over the token."""
     if block not in (0, 32, 64, 128):
         raise ValueError(f"block must be 0, 32, 64 or 128, got {block!r}")
-    d, io, st, xv, rv, w, tv, total = _add_norm_inputs(x, residual, weight, total, eps)
-    shape = x.shape
-    parts = (*shape[:-1], -(-shape[-1] // block) if block else 1)
-    q = _out(q, "q", shape, torch.float8_e4m3fn, x)
+    head, ins, total, tv, shape, dev = _add_norm_inputs(x, residual, weight, total, eps)
+    *lead, D = shape
+    lead.append(-(-D // block) if block else 1)
     if scales is None:
-        scales = torch.empty(parts, dtype=torch.float32, device=x.device)
+        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
         at = scales.data_ptr()
     else:
-        at = _dense(scales, "scales", parts, torch.float32, x)
-    qv = _rows(q, "q", shape, torch.float8_e4m3fn, x.get_device(), x)
-    code = _abi.load().ssd_add_norm_quantized(d, io, st, block, xv, rv, w, qv, at, tv, _stream(x))
+        at = _dense(scales, "scales", tuple(lead), torch.float32, x)
+    if q is None:
+        q, qv = _new_rows(shape, torch.float8_e4m3fn, x)
+    else:
+        _out(q, "q", shape, torch.float8_e4m3fn, x)
+        qv = _rows(q, "q", shape, torch.float8_e4m3fn, dev, x)
+    code = _abi.load().ssd_add_norm_quantized(*head, block, *ins, qv, at, tv, _stream(x))
     if code:
         _abi.check("ssd_add_norm_quantized", code)
     return q, scales, total
@@ -147,24 +166,26 @@ def add_norm_backward(total, weight, gy, gtotal=None, eps: float = 1e-5, workspa
     (float32).  `want` names those to compute (None = all)."""
     has = _wanted(want, _ADD_NORM_GRADS, "add_norm_backward")
     d, io, lib = _add_norm_dims(gy, eps), _io(gy, "gy"), _abi.load()
-    stream, shape = _stream_type(gy, total.dtype), gy.shape
-    one = stream == gy.dtype
-
-    def out(there, sizes, dtype):
-        return torch.empty(sizes, dtype=dtype, device=gy.device) if there else None
-
-    dx = out(has("dx") or (one and has("dresidual")), shape, gy.dtype)
-    dr = out(has("dresidual") and not one, shape, stream)
-    dw = out(has("dweight"), (shape[-1],), torch.float32)
-    ws, wp, wn = (None, None, 0) if dw is None else _workspace(
-        lib.ssd_add_norm_backward_workspace_size(d, io, _IO[stream]), workspace, gy,
-        "add_norm_backward")
-    _abi.check("ssd_add_norm_backward", lib.ssd_add_norm_backward(
-        d, io, _IO[stream], _view(total, "total", shape, stream, gy),
-        _dense(weight, "weight", (shape[-1],), torch.float32, gy),
-        _view(gy, "gy", shape, gy.dtype, gy), _view(gtotal, "gtotal", shape, stream, gy),
-        _view(dx, "dx", shape, gy.dtype, gy), _view(dr, "dresidual", shape, stream, gy),
-        None if dw is None else dw.data_ptr(), wp, wn, _stream(gy)))
+    stream, shape, dtype, dev = _stream_type(gy, total.dtype), gy.shape, gy.dtype, gy.get_device()
+    st, one = _IO[stream], stream is dtype
+    ins = (_rows(total, "total", shape, stream, dev, gy),
+           _dense(weight, "weight", shape[-1:], torch.float32, gy),
+           _rows(gy, "gy", shape, dtype, dev, gy),
+           None if gtotal is None else _rows(gtotal, "gtotal", shape, stream, dev, gy))
+    dx = xv = dr = rv = dw = ws = None
+    wp, wn = None, 0
+    if has("dx") or (one and has("dresidual")):
+        dx, xv = _new_rows(shape, dtype, gy)
+    if has("dresidual") and not one:
+        dr, rv = _new_rows(shape, stream, gy)
+    if has("dweight"):
+        dw = torch.empty(shape[-1:], dtype=torch.float32, device=gy.device)
+        ws, wp, wn = _workspace(lib.ssd_add_norm_backward_workspace_size(d, io, st), workspace,
+                                gy, "add_norm_backward")
+    code = lib.ssd_add_norm_backward(d, io, st, *ins, xv, rv,
+                                     None if dw is None else dw.data_ptr(), wp, wn, _stream(gy))
+    if code:
+        _abi.check("ssd_add_norm_backward", code)
     dr = dx if one else dr
     return {"dx": dx if has("dx") else None, "dresidual": dr if has("dresidual") else None,
             "dweight": dw}
@@ -175,14 +196,17 @@ class _AddNorm(torch.autograd.Function):
     def forward(ctx, x, residual, weight, eps):
         y, total = add_norm_forward(x, residual, weight, eps)
         ctx.save_for_backward(total, weight)
-        ctx.eps = eps
+        ctx.eps, ctx.io = eps, x.dtype
+        ctx.set_materialize_grads(False)  # (behind the last block nothing uses total)
         return y, total
 
     @staticmethod
     @_first_order
     def backward(ctx, gy, gtotal):
         total, weight = ctx.saved_tensors
-        g = add_norm_backward(total, weight, gy.contiguous(), gtotal.contiguous(), ctx.eps,
+        gy = torch.zeros_like(total, dtype=ctx.io) if gy is None else gy.contiguous()
+        gtotal = None if gtotal is None else gtotal.contiguous()
+        g = add_norm_backward(total, weight, gy, gtotal, ctx.eps,
                               want=_needed(ctx, _ADD_NORM_GRADS))
         return (*(g[k] for k in _ADD_NORM_GRADS), None)
 

@@ -170,6 +170,49 @@ def test_add_norm_values_at_the_ends(ssd):
     assert float(s[4]) == 2.0 ** -126
     within(q[4].double() * s[4].double(), torch.full((256,), 1e-39, dtype=torch.float64,
                                                       device="cuda"), 1e-39 / 16 + 2.0 ** -136)
+    huge = torch.full((256,), 1e38, device="cuda")  # a scale whose block is near the range's end
+    for block in (0, 64):
+        q, s, _ = ssd.add_norm_quantized(x, r, huge, block=block)
+        ref, _ = R.add_norm(x[5:], r[5:], huge)
+        near = R.norm_bound(256, F32) + 2.0 ** -21
+        step = s[5:].double().repeat_interleave(256 // s.shape[1], 1)
+        within(q[5:].double() * step, ref,
+               ref.abs() * (R.HALF[q.dtype] * (1 + near) + near) + step * 2.0 ** -10, "huge")
+
+
+def test_offsets_beyond_32_bits(ssd):
+    """Rows so far apart that their places pass 2^32 elements: the bits of dense ones."""
+    base, n = torch.empty(2 ** 32 + 2 ** 20, dtype=B16, device="cuda"), gen(31)
+
+    def far(t, at):
+        """t's rows spread over `base`, from element `at` on."""
+        v = base.as_strided(t.shape, (2 ** 32 // (t.shape[0] - 1) // 8 * 8, *t.stride()[1:]), at)
+        return v.copy_(t)
+
+    x, r, w = n(2, 5, 640, dtype=B16), n(2, 5, 640, dtype=B16), 1.0 + n(640, scale=0.2)
+    y, total = ssd.add_norm_forward(x, r, w)
+    yv, tv = far(y, 0).zero_(), far(y, 65536).zero_()
+    ssd.add_norm_forward(far(x, 131072), far(r, 262144), w, y=yv, total=tv)
+    assert torch.equal(yv, y) and torch.equal(tv, total)
+    g = ssd.add_norm_backward(total, w, x, r)
+    v = ssd.add_norm_backward(tv, w, far(x, 131072), far(r, 262144))
+    assert all(torch.equal(g[k], v[k]) for k in g)
+
+    W, t = n(9, 640, dtype=B16), torch.tensor([[0, 8, 3, 1, -100], [8, 7, 2, 5, 6]], device="cuda")
+    ref = ssd.linear_cross_entropy_forward(x, W, t)
+    for at in (0, 1):  # taken where they lie, and packed
+        words = far(W, at)
+        got = ssd.linear_cross_entropy_forward(far(x, 524288), words, t)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+        g = ssd.linear_cross_entropy_backward(x, W, t, ref[1])
+        v = ssd.linear_cross_entropy_backward(far(x, 524288), words, t, ref[1])
+        assert all(torch.equal(g[k], v[k]) for k in g)
+
+    G = n(2, 64, 128, dtype=B16)
+    X = ssd.orthogonalize(G)
+    out = far(X, 0).zero_()
+    ssd.orthogonalize(far(G, 65536), out=out)
+    assert torch.equal(out, X)
 
 
 # ---------------------------------------------------------- cross entropy

@@ -173,6 +173,20 @@ def test_autograd_gives_the_backward_calls(ssd, reduction):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("used", ["y", "total"])
+def test_autograd_of_one_output(ssd, used):
+    """What nothing uses has no gradient: that of zeros."""
+    a = inputs(12)
+    leaf = {k: a[k].clone().requires_grad_() for k in ("x", "r", "w")}
+    y, total = ssd.add_norm(*leaf.values())
+    zero = torch.zeros_like
+    out, gy, gt = (y, a["gy"], zero(total)) if used == "y" else (total, zero(y), a["r"])
+    got = torch.autograd.grad(out, list(leaf.values()), gy if used == "y" else gt)
+    ref = ssd.add_norm_backward(total.detach(), a["w"], gy, gt)
+    for p, k in zip(got, ("dx", "dresidual", "dweight")):
+        assert torch.equal(p, ref[k]), k
+
+
 def test_no_second_derivatives(ssd):
     a = inputs(7, io=F32)
     x = a["x"].requires_grad_()

@@ -192,6 +192,8 @@ def refusals():
         "transposed": (lambda: f(far(8, 4, dtype=B16).t(), r, w), ValueError, "dense along"),
         "host": (lambda: f(torch.zeros(4, 8, dtype=B16), r, w), ValueError, "CUDA tensor"),
         "y is residual": (lambda: f(far(4, 8), r, w, y=r), ValueError, "must not be the memory"),
+        "y is total": (lambda z=far(4, 8): f(far(4, 8), r, w, y=z, total=z), ValueError,
+                       "must not be the memory"),
         "y rows": (lambda: f(x, r, w, y=far(1, 8, dtype=B16).expand(4, 8)), ValueError,
                    "must not share"),
         "block": (lambda: q(x, r, w, block=16), ValueError, "block must be"),
