@@ -363,6 +363,7 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
   const int64_t first = (int64_t)blockIdx.x * per + (per > 1 ? threadIdx.x / 32 : 0);
   const int64_t step = (int64_t)gridDim.x * per;
   const int tid = per > 1 ? threadIdx.x % 32 : threadIdx.x;
+  ptx::griddep_launch_dependents();  // (the sum over the blocks waits for them)
   if (!SSD_IN_BOUNDS((int64_t)team * K * V >= D, err, 91)) return;
   const Weights<K, kWide> weights(weight, tid, team, D);
   // (two vectors of three tensors twice would not fit the registers)

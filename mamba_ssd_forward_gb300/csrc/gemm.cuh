@@ -35,6 +35,7 @@
 
 #include <atomic>
 
+#include "layer.cuh"
 #include "ptx.cuh"
 #include "ssd_internal.cuh"
 #include "tmap.cuh"
@@ -523,20 +524,6 @@ bool make_pane_map(CUtensorMap *map, const void *base, bool fp32, int64_t cols, 
 
 // Elements to a row of an operand array: rows start on 32 bytes.
 inline int64_t padded(int64_t cols) { return (cols + 15) / 16 * 16; }
-
-// A launch that may start while the launch before it on the stream ends: the kernel
-// waits (griddep_wait) before it touches memory.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                         A... a) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = attr, c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(a)...);
-}
 
 // Launches `count` products (one or two) as one grid.
 template <class Epi, int kBN, int kSegment = 0>

@@ -142,6 +142,20 @@ __device__ __forceinline__ int64_t tokens_of(const int32_t *lengths, int64_t b, 
   return n < 0 ? 0 : n > L ? L : n;
 }
 
+// A launch that may start while the launch before it on the stream ends: the kernel
+// waits (griddep_wait) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         A... a) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(a)...);
+}
+
 // Column sums of up to four partial arrays in one launch, rows added in a
 // fixed order: dst[i] = sum_{r < rows} src[r * n + i].
 struct ColSum {

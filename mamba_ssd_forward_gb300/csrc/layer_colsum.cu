@@ -3,6 +3,7 @@
 // order.  The order depends on the sizes only, so results repeat bit for bit.
 // Bandwidth-bound on arrays that are small next to what produced them.
 #include "layer.cuh"
+#include "ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -20,6 +21,7 @@ __global__ void __launch_bounds__(kCols *kSlices) colsum_kernel(ColSum a, int *e
   }
   const ColSum::Seg g = a.seg[s];
   const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+  ptx::griddep_wait();
   const int64_t i = blk * kCols + col;
   float acc = 0.f;
   if (i < g.n && SSD_IN_BOUNDS(g.rows >= 0, err, 60)) {
@@ -48,8 +50,7 @@ cudaError_t launch_colsum(const ColSum &in, int *err, cudaStream_t st) {
       blocks += (in.seg[s].n + kCols - 1) / kCols;
     }
   if (!blocks) return cudaSuccess;
-  colsum_kernel<<<(unsigned)blocks, kCols * kSlices, 0, st>>>(a, err);
-  return cudaGetLastError();
+  return launch_after(colsum_kernel, dim3((unsigned)blocks), kCols * kSlices, 0, st, a, err);
 }
 
 }  // namespace ssd

@@ -394,7 +394,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   squares_kernel<IN><<<grid, kNormThreads, 0, st>>>(g, a.rows, a.cols, wide, p.part, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = gemm::launch_after(start_kernel<IN>, grid, kNormThreads, 0, st, g, a.rows, a.cols, wide,
+  e = launch_after(start_kernel<IN>, grid, kNormThreads, 0, st, g, a.rows, a.cols, wide,
                          p.part, p.parts, a.eps, p.x[0], p.ld, carried(0), p.rest, err);
 
   const int64_t gps = p.side * p.gram_ld;

@@ -711,7 +711,7 @@ struct Calls {
     // (the first launch of the call waits for what is on the stream the ordinary way)
     const dim3 grid((unsigned)((a.n + kPackTokens - 1) / kPackTokens));
     if (top || p.counts)
-      return gemm::launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
+      return launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
                                 a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
                                 view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld,
                                 p.rows * p.ld, kPlanes, top, err);
@@ -737,7 +737,7 @@ struct Calls {
     }
     w->at = p.wp, w->ld = p.ld, w->zs = p.piece * p.ld;
     const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
-    return gemm::launch_after(pack_weight_kernel<IO>, dim3((unsigned)((w->n + 7) / 8)), 256, 0, st,
+    return launch_after(pack_weight_kernel<IO>, dim3((unsigned)((w->n + 7) / 8)), 256, 0, st,
                               src, a.weight->token_stride, w->n, a.d, p.wp, p.ld, w->zs, top, err);
   }
 
@@ -775,10 +775,10 @@ struct Calls {
       e = gemm::launch<StatsEpi, kBN, kSegment>(maps, &q, 1, kBf16, s, err, st);
     }
     if (e != cudaSuccess) return e;
-    e = gemm::launch_after(join_kernel, dim3((unsigned)((a.n + 31) / 32)), 32 * kJoinWarps, 0, st,
+    e = launch_after(join_kernel, dim3((unsigned)((a.n + 31) / 32)), 32 * kJoinWarps, 0, st,
                            p.stat, p.rows, (int)p.runs, p.r, loss, a.lse, err);
     if (e != cudaSuccess || !a.total) return e;
-    return gemm::launch_after(total_kernel, dim3(1), 1024, 0, st, loss, a.n, p.r.live,
+    return launch_after(total_kernel, dim3(1), 1024, 0, st, loss, a.n, p.r.live,
                               (int)(a.reduction == SSD_REDUCE_MEAN), a.total, err);
   }
 
@@ -829,7 +829,7 @@ struct Calls {
     }
     if (e != cudaSuccess || !a.dx) return e;
     const int64_t sld = gemm::padded(a.d), warps = (a.d + 127) / 128;
-    return gemm::launch_after(unpack_kernel<IO>, dim3((unsigned)a.n),
+    return launch_after(unpack_kernel<IO>, dim3((unsigned)a.n),
                               (int)(32 * (warps < 8 ? warps : 8)), 0, st, p.sum, sld, p.rows * sld,
                               p.slabs, f, view_of<IO>(a.dx), a.L, a.d, err);
   }
