@@ -349,9 +349,12 @@ Plan plan_of(const OrthArgs &a, ssd_dtype out, void *ws) {
   return p;
 }
 
-template <Kind kind>
-cudaError_t multiply(const CUtensorMap *maps, const Product &q, int bn,
-                     const typename StepEpi<kind>::Args &e, int *err, cudaStream_t st) {
+// A product whose epilogue's arguments `fill` writes.
+template <Kind kind, typename Fill>
+cudaError_t multiply(const CUtensorMap *maps, const Product &q, int bn, Fill fill, int *err,
+                     cudaStream_t st) {
+  typename StepEpi<kind>::Args e{};
+  fill(e);
   auto with = [&](auto segment) {
     constexpr int kSegment = decltype(segment)::value;
     return bn == 256 ? gemm::launch<StepEpi<kind>, 256, kSegment>(maps, &q, 1, false, e, err, st)
@@ -397,99 +400,94 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   e = launch_after(start_kernel<IN>, grid, kNormThreads, 0, st, g, a.rows, a.cols, wide,
                          p.part, p.parts, a.eps, p.x[0], p.ld, carried(0), p.rest, err);
 
-  const int64_t gps = p.side * p.gram_ld;
-  const int64_t xz = a.count * 2, gz = a.count * p.planes;
-  auto map_x = [&](CUtensorMap *m, const __half *x, bool mn, int box) {
-    return gemm::make_map(m, x, a.cols, a.rows, xz, p.ld, xps, mn, box);
+  if (e != cudaSuccess) return e;
+
+  // A = X X^T or X^T X;  B = b A + c A A;  X <- a X + B X or a X + X B
+  Product gram{}, poly{}, next{};
+  gram.batch = poly.batch = next.batch = (int)a.count;
+  gram.pairs = poly.pairs = next.pairs = p.planes == 2 ? 3 : 1;
+  gram.symmetric = poly.symmetric = 1;
+  gram.M = gram.N = poly.M = poly.N = poly.K = next.K = (int)p.side, gram.K = (int)longer;
+  gram.a_mn = gram.b_mn = tall, gram.a_planes = gram.b_planes = 2;
+  poly.a_planes = poly.b_planes = p.planes;
+  next.M = (int)a.rows, next.N = (int)a.cols, next.b_mn = !tall;
+  next.a_planes = tall ? 2 : p.planes, next.b_planes = tall ? p.planes : 2;
+  const int bn = tile_columns(gram), next_bn = tile_columns(next);
+
+  // Every array as an operand and through panes, described once: X is one of two
+  // arrays in turn.
+  const int64_t gps = p.side * p.gram_ld, xz = a.count * 2, gz = a.count * p.planes;
+  CUtensorMap of_gram[2][2], of_poly[2], of_next[2][2];  // [X][operand]; [operand]
+  CUtensorMap pane_x[2], pane_gram, pane_poly, pane_out;
+  auto x_map = [&](CUtensorMap *m, int i, bool mn, int box) {
+    return gemm::make_map(m, p.x[i], a.cols, a.rows, xz, p.ld, xps, mn, box);
   };
-  auto map_gram = [&](CUtensorMap *m, const __half *x, int box) {
+  auto side_map = [&](CUtensorMap *m, const __half *x, int box) {
     return gemm::make_map(m, x, p.side, p.side, gz, p.gram_ld, gps, false, box);
   };
-  auto pane_x = [&](CUtensorMap *m, const __half *x) {
-    return gemm::make_pane_map<64>(m, x, false, a.cols, a.rows, xz, p.ld, xps);
-  };
-  auto pane_gram = [&](CUtensorMap *m, const __half *x) {
+  auto side_pane = [&](CUtensorMap *m, const __half *x) {
     return gemm::make_pane_map<64>(m, x, false, p.side, p.side, gz, p.gram_ld, gps);
   };
-  for (int k = 0; k < a.steps && e == cudaSuccess; ++k) {
-    const __half *x = p.x[k & 1];
-    const bool last = k == a.steps - 1;
-    Product q{};
-    q.batch = (int)a.count, q.pairs = p.planes == 2 ? 3 : 1;
-    CUtensorMap maps[2];
-
-    // A = X X^T or X^T X
-    q.M = q.N = (int)p.side, q.K = (int)longer;
-    q.a_mn = q.b_mn = tall, q.a_planes = q.b_planes = 2, q.symmetric = 1;
-    int bn = tile_columns(q);
-    auto gram = [&](auto &s) {
-      s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
-      s.out = p.gram, s.d_stored = p.planes, s.share = bn / 4, s.symmetric = 1;
-      s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
-      return pane_gram(&s.d, p.gram);
-    };
-    auto poly = [&](auto &s) {
-      s.alpha = a.c / kGramScale, s.beta = a.b, s.rest = nullptr;
-      s.c_planes = s.c_stored = p.planes, s.out = p.poly;
-      return pane_gram(&s.c, p.gram) && pane_gram(&s.d, p.poly);
-    };
-    StepEpi<kOne>::Args s1{};
-    StepEpi<kTwo>::Args s2{};
-    if (!map_x(&maps[0], x, tall, gemm::kRows) || !map_x(&maps[1], x, tall, bn / 2) ||
-        !gram(s1) || !gram(s2))
-      return cudaErrorInvalidValue;
-    e = p.planes == 1 ? multiply<kOne>(maps, q, bn, s1, err, st)
-                      : multiply<kTwo>(maps, q, bn, s2, err, st);
-    if (e != cudaSuccess) break;
-
-    // B = b A + c A A
-    q.K = (int)p.side, q.a_mn = q.b_mn = 0, q.a_planes = q.b_planes = p.planes;
-    if (!map_gram(&maps[0], p.gram, gemm::kRows) || !map_gram(&maps[1], p.gram, bn / 2) ||
-        !poly(s1) || !poly(s2))
-      return cudaErrorInvalidValue;
-    e = p.planes == 1 ? multiply<kOne>(maps, q, bn, s1, err, st)
-                      : multiply<kTwo>(maps, q, bn, s2, err, st);
-    if (e != cudaSuccess) break;
-
-    // X <- a X + B X or a X + X B
-    q.M = (int)a.rows, q.N = (int)a.cols, q.symmetric = 0;
-    q.a_planes = tall ? 2 : p.planes, q.b_planes = tall ? p.planes : 2, q.b_mn = !tall;
-    bn = tile_columns(q);
-    if (tall ? !map_x(&maps[0], x, false, gemm::kRows) || !map_gram(&maps[1], p.poly, bn / 2)
-             : !map_gram(&maps[0], p.poly, gemm::kRows) || !map_x(&maps[1], x, true, bn / 2))
-      return cudaErrorInvalidValue;
-    auto fill = [&](auto &u) {
-      u.alpha = 1.f / kGramScale, u.beta = a.a, u.rest = k ? nullptr : p.rest, u.power = 1;
-      if (last) u.alpha /= kScale, u.beta /= kScale;
-      u.c_planes = carried(k), u.c_stored = 2, u.d_stored = 1;
-      u.N = (int)a.cols, u.share = bn / 4;
-      return pane_x(&u.c, x);
-    };
-    if (!last) {
-      auto next = [&](auto &u) { return fill(u) && (u.d_stored = 2) && pane_x(&u.d, p.x[~k & 1]); };
-      StepEpi<kOne>::Args u1{};
-      StepEpi<kTwo>::Args u2{};
-      if (!next(u1) || !next(u2)) return cudaErrorInvalidValue;
-      e = carried(k + 1) == 1 ? multiply<kOne>(maps, q, bn, u1, err, st)
-                              : multiply<kTwo>(maps, q, bn, u2, err, st);
-    } else if (out == SSD_BF16) {
-      StepEpi<kBf16>::Args u{};
-      u.bf16 = view_of<__nv_bfloat16>(a.out);
-      u.wide = view_aligned(a.out, 2, 16) && a.out->token_stride >= a.cols &&
+  bool ok = side_map(&of_poly[0], p.gram, gemm::kRows) && side_map(&of_poly[1], p.gram, bn / 2) &&
+            side_pane(&pane_gram, p.gram) && side_pane(&pane_poly, p.poly);
+  for (int i = 0; i < 2 && ok; ++i)
+    ok = x_map(&of_gram[i][0], i, tall, gemm::kRows) && x_map(&of_gram[i][1], i, tall, bn / 2) &&
+         gemm::make_pane_map<64>(&pane_x[i], p.x[i], false, a.cols, a.rows, xz, p.ld, xps) &&
+         (tall ? x_map(&of_next[i][0], i, false, gemm::kRows) &&
+                     side_map(&of_next[i][1], p.poly, next_bn / 2)
+               : side_map(&of_next[i][0], p.poly, gemm::kRows) &&
+                     x_map(&of_next[i][1], i, true, next_bn / 2));
+  bool wide_out = false;
+  if (out == SSD_BF16 && ok) {
+    wide_out = view_aligned(a.out, 2, 16) && a.out->token_stride >= a.cols &&
                (a.count == 1 || a.out->batch_stride > 0);
-      const int64_t zs = a.count == 1 ? a.rows * a.out->token_stride : a.out->batch_stride;
-      if (!fill(u) || (u.wide && !gemm::make_pane_map<64>(&u.d, u.bf16.p, false, a.cols, a.rows,
-                                                      a.count, a.out->token_stride, zs)))
-        return cudaErrorInvalidValue;
-      e = multiply<kBf16>(maps, q, bn, u, err, st);
-    } else {
-      StepEpi<kF32>::Args u{};
-      u.f32 = view_of<float>(a.out), u.wide = view_aligned(a.out, 4, 16);
-      if (!fill(u)) return cudaErrorInvalidValue;
-      e = multiply<kF32>(maps, q, bn, u, err, st);
-    }
+    ok = !wide_out || gemm::make_pane_map<64>(&pane_out, a.out->data, false, a.cols, a.rows,
+                                              a.count, a.out->token_stride, a.out->batch_stride);
   }
-  return e;
+  if (!ok) return cudaErrorInvalidValue;
+
+  for (int k = 0; k < a.steps; ++k) {
+    const int i = k & 1;
+    const bool last = k == a.steps - 1;
+    auto gram_args = [&](auto &s) {
+      s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
+      s.d = pane_gram, s.out = p.gram, s.d_stored = p.planes, s.share = bn / 4, s.symmetric = 1;
+      s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
+    };
+    auto poly_args = [&](auto &s) {
+      gram_args(s);
+      s.alpha = a.c / kGramScale, s.beta = a.b, s.rest = nullptr;
+      s.c = pane_gram, s.c_planes = s.c_stored = p.planes, s.d = pane_poly, s.out = p.poly;
+    };
+    auto next_args = [&](auto &s) {
+      s.alpha = 1.f / kGramScale, s.beta = a.a, s.rest = k ? nullptr : p.rest, s.power = 1;
+      if (last) s.alpha /= kScale, s.beta /= kScale;
+      s.c = pane_x[i], s.c_planes = carried(k), s.c_stored = 2, s.d = pane_x[!i], s.d_stored = 2;
+      s.N = (int)a.cols, s.share = next_bn / 4;
+    };
+    auto bf16_args = [&](auto &s) {
+      next_args(s);
+      s.d_stored = 1, s.bf16 = view_of<__nv_bfloat16>(a.out), s.wide = wide_out;
+      if (wide_out) s.d = pane_out;
+    };
+    auto f32_args = [&](auto &s) {
+      next_args(s);
+      s.f32 = view_of<float>(a.out), s.wide = view_aligned(a.out, 4, 16);
+    };
+    e = p.planes == 1 ? multiply<kOne>(of_gram[i], gram, bn, gram_args, err, st)
+                      : multiply<kTwo>(of_gram[i], gram, bn, gram_args, err, st);
+    if (e != cudaSuccess) return e;
+    e = p.planes == 1 ? multiply<kOne>(of_poly, poly, bn, poly_args, err, st)
+                      : multiply<kTwo>(of_poly, poly, bn, poly_args, err, st);
+    if (e != cudaSuccess) return e;
+    e = last                  ? (out == SSD_BF16
+                                     ? multiply<kBf16>(of_next[i], next, next_bn, bf16_args, err, st)
+                                     : multiply<kF32>(of_next[i], next, next_bn, f32_args, err, st))
+        : carried(k + 1) == 1 ? multiply<kOne>(of_next[i], next, next_bn, next_args, err, st)
+                              : multiply<kTwo>(of_next[i], next, next_bn, next_args, err, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
