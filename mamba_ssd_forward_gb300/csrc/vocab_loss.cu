@@ -66,9 +66,31 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
            int64_t n, const float *__restrict__ w, int64_t ws, int64_t V, int64_t d,
            const float *__restrict__ g, uint32_t *__restrict__ top, int *err) {
   uint32_t most[kTops] = {0, 0, 0};
-  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
-  const int64_t warps = (int64_t)gridDim.x * blockDim.x / 32;
-  for (int64_t r = warp; r < n + V; r += warps) {
+  const int64_t thread = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, lane = threadIdx.x % 32;
+  const int64_t threads = (int64_t)gridDim.x * blockDim.x, warp = thread / 32, warps = threads / 32;
+  // W's rows one after the other are one run (row by row, 4 bytes a lane, 32003 x 771
+  // took 29 us, so 23)
+  const bool run = ws == d && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  if (run) {
+    constexpr int kAtOnce = 8;
+    const int64_t all = V * d, vecs = all / 4;
+    uint32_t m = 0;
+    for (int64_t i = thread; i < vecs; i += kAtOnce * threads) {
+      float4 v[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int64_t at = i + k * threads;
+        v[k] = at < vecs ? reinterpret_cast<const float4 *>(w)[at] : make_float4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        m = max(max(m, max(size_of(v[k].x), size_of(v[k].y))),
+                max(size_of(v[k].z), size_of(v[k].w)));
+    }
+    if (4 * vecs + thread < all) m = max(m, size_of(w[4 * vecs + thread]));
+    most[kTopW] = m;
+  }
+  for (int64_t r = warp; r < (run ? n : n + V); r += warps) {
     if (r < n && !counted(targets[r], ignore)) continue;
     const float *p = r < n ? x.at(r / L, r % L) : w + (r - n) * ws;
     uint32_t m = 0;
