@@ -51,8 +51,8 @@ __device__ __forceinline__ void load8(const IO *p, int64_t c, int64_t cols, bool
 
 // A matrix in groups of eight elements; a thread's groups are gridDim.x kNormThreads
 // apart, kAtOnce of them loaded together (10576 x 2560 bf16: the squares 18 us, 3.0
-// TB/s with cold caches, the first X 24).  Row and column are walked along: a division
-// a group, and one load at a time, took 20 and 28.
+// TB/s with cold caches, the first X 24).  Row and column are walked along: with a
+// division a group, and one load at a time, the squares took 20.
 constexpr int kAtOnce = 4;
 template <typename IO, typename F>
 __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
