@@ -70,7 +70,7 @@ struct Product {
   int pairs;               // 1, or 3 with operands of two planes
   int a_planes, b_planes;  // planes that each operand's array holds
   int symmetric;           // D is: only tiles on and above the diagonal
-  int part;                // > 0: batch i sums k from i part kTileK on, part stages of them
+  int part, parts;         // part > 0: every `parts` batches are one, each sums `part` stages of k
 };
 
 // What a block does of a tile: rows m .. m + 127, columns n .. n + kBN - 1.
@@ -124,7 +124,7 @@ struct Walk {  // the tiles of up to two products, in order; in shared memory
     }
     o.m = mi * kTileM + rank * kRows;
     o.n = ni * kBN;
-    o.k0 = o.batch * p[i].part;
+    o.k0 = p[i].part ? o.batch % p[i].parts * p[i].part : 0;
     o.steps = (K[i] + kTileK - 1) / kTileK - o.k0;
     if (p[i].part) o.steps = max(0, min(o.steps, p[i].part));
     o.mirror = p[i].symmetric && o.n >= (mi + 1) * kTileM;
@@ -363,7 +363,7 @@ product_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ C
       const CUtensorMap *ma = which ? &a1 : &a0, *mb = which ? &b1 : &b0;
       const int a_mn = p.a_mn, b_mn = p.b_mn, pairs = p.pairs;
       const int m = uniform(o.m), n = uniform(o.n) + rank * (kBN / 2);
-      const int z = p.part ? 0 : uniform(o.batch), za = z * p.a_planes, zb = z * p.b_planes;
+      const int z = uniform(p.part ? o.batch / p.parts : o.batch), za = z * p.a_planes, zb = z * p.b_planes;
       for (int pair = 0; pair < pairs; ++pair) {
         // with three: lo hi, hi lo, hi hi
         const int z0 = za + (pairs == 3 && pair == 0), z1 = zb + (pairs == 3 && pair == 1);

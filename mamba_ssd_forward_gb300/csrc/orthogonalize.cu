@@ -6,6 +6,8 @@
 // Three products a step (gemm.cuh).  A and B are symmetric: their tiles below the
 // diagonal are written as the transposes of those above it.  Bound by the tensor
 // cores: s^2 l + s^3 + 2 s^2 l operations a step for s = min, l = max of the sides.
+// Measured, five steps in bf16: 10576 x 2560 900 to 920 us, 1.25 PFLOP/s; 24 of
+// 768 x 1536 485 us, 0.78 PFLOP/s; small ones 5.4 us a launch.
 //
 // Precision.  A step takes small singular values times a = 3.4, five steps 485:
 // it enlarges the rounding of X with them.  bf16 operands would leave the result
@@ -320,13 +322,84 @@ struct StepEpi {
   __device__ __forceinline__ void end() {}
 };
 
+// ------------------------------------------------------ A in parts of its sums
+
+// A = X X^T of long, narrow X is few tiles of many stages, which would be summed one
+// after the other by few pairs: its k is cut into parts, which as many pairs sum into
+// fp32 slabs, and a launch adds these in their order.
+struct SlabEpi {
+  struct Args {
+    CUtensorMap d;  // [matrix, part][side][side]
+    int N;
+  };
+  static constexpr int kWarps = 16;
+  static constexpr bool kStaged = true;
+  using Pane = gemm::Panes<128>;
+  const Args &a;
+  Pane panes;
+  int row0, M, batch;
+  __device__ __forceinline__ SlabEpi(const Args &args, Pane p, int *) : a(args), panes(p) {}
+  __device__ __forceinline__ void begin(const Tile &o, int r, int, int rows) {
+    row0 = r - panes.lane, M = rows, batch = o.batch;
+  }
+  __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int) {
+    if (row0 >= M || col >= a.N) return;
+    panes.reuse<0>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      panes.cell(0, i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                    __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    panes.written();
+    if (gemm::elected()) {
+      panes.store(0, &a.d, col, row0, batch);
+      ptx::bulk_commit();
+    }
+  }
+  __device__ __forceinline__ void end() {}
+};
+
+// The sum of a matrix's slabs, times alpha rest^2, in fp16 planes; a thread takes eight
+// columns.  (Columns from `side` on are nobody's.)
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
+join_parts_kernel(const float *__restrict__ slabs, int parts, int64_t side, int64_t ld, float alpha,
+                  const float *__restrict__ rest, __half *__restrict__ gram, int planes, int *err) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t z = blockIdx.y, i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  const int64_t r = i / (ld / 8), c = i % (ld / 8) * 8;
+  if (r >= side || !SSD_IN_BOUNDS(side <= ld, err, 84)) return;
+  const float *p = slabs + z * parts * side * ld + r * ld + c;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int q = 0; q < parts; ++q, p += side * ld) {
+    const float4 *s = reinterpret_cast<const float4 *>(p);
+    const float4 a = s[0], b = s[1];
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  const float f = rest ? alpha * rest[z] * rest[z] : alpha;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= f;
+  __half *o = gram + z * planes * side * ld + r * ld + c;
+  *reinterpret_cast<uint4 *>(o) = pack8(v, planes == 2);
+  if (planes == 2) *reinterpret_cast<uint4 *>(o + side * ld) = pack8(v, false);
+}
+
 // ----------------------------------------------------------------- the host
+
+constexpr int kSplitBN = 128;  // columns to a tile of A in parts
+// A goes in parts where that saves more stages than this.  Five steps, us: saving 8 of 16
+// stages 1000 x 100 into bf16 takes 119 -> 127, 16 of 24 1500 x 100 131 -> 129, 24 of 32
+// 2000 x 100 140 -> 130; 5034 x 30 into bf16 175 -> 113, into fp32 (237 stages) 392 -> 140.
+constexpr int kSplitSaves = 12;
 
 struct Plan {
   int planes;  // of A, B and of the products
   int64_t side, ld, gram_ld;
-  int parts;
-  float *part, *rest;
+  int parts;           // of the norm's sums
+  int split, stages;   // parts of A's k (1: A in one go), stages of k in each
+  float *part, *rest, *slabs;
   __half *x[2], *gram, *poly;
   size_t bytes;
 };
@@ -340,8 +413,22 @@ Plan plan_of(const OrthArgs &a, ssd_dtype out, void *ws) {
   int64_t parts = (4 * sm_count() + a.count - 1) / a.count;
   const int64_t most = (a.rows * ((a.cols + 7) / 8) + kNormThreads - 1) / kNormThreads;
   p.parts = (int)(parts < most ? parts : most);
+  // A's parts: as many as there are pairs for, of some eight stages at least (counting
+  // those of all planes; with five or twelve no case is faster by more than 2 %)
+  const int64_t tiles = a.count * ((p.side + 255) / 256) * ((p.side + kSplitBN - 1) / kSplitBN);
+  const int64_t stages = ((a.rows > a.cols ? a.rows : a.cols) + gemm::kTileK - 1) / gemm::kTileK;
+  const int64_t each = p.planes == 2 ? 3 : 1, most_parts = sm_count() / 2 / tiles;
+  int64_t split = stages * each / 8;
+  split = split < most_parts ? split : most_parts;
+  if (split > 1 && (stages - (stages + split - 1) / split) * each > kSplitSaves) {
+    p.stages = (int)((stages + split - 1) / split);
+    p.split = (int)((stages + p.stages - 1) / p.stages);
+  } else {
+    p.split = 1, p.stages = 0;
+  }
   Carver c(ws);
   p.part = c.take<float>(a.count * p.parts);
+  p.slabs = c.take<float>(p.split > 1 ? a.count * p.split * p.side * p.gram_ld : 0);
   p.rest = c.take<float>(a.count);
   for (int i = 0; i < 2; ++i) p.x[i] = c.take<__half>(a.count * 2 * a.rows * p.ld);
   p.gram = c.take<__half>(a.count * p.planes * p.side * p.gram_ld);
@@ -414,6 +501,9 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   next.M = (int)a.rows, next.N = (int)a.cols, next.b_mn = !tall;
   next.a_planes = tall ? 2 : p.planes, next.b_planes = tall ? p.planes : 2;
   const int bn = tile_columns(gram), next_bn = tile_columns(next);
+  Product part = gram;  // A in parts: all its tiles
+  part.symmetric = 0, part.part = p.stages, part.parts = p.split, part.batch *= p.split;
+  const int gram_bn = p.split > 1 ? kSplitBN : bn;
 
   // Every array as an operand and through panes, described once: X is one of two
   // arrays in turn.
@@ -432,12 +522,17 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
   bool ok = side_map(&of_poly[0], p.gram, gemm::kRows) && side_map(&of_poly[1], p.gram, bn / 2) &&
             side_pane(&pane_gram, p.gram) && side_pane(&pane_poly, p.poly);
   for (int i = 0; i < 2 && ok; ++i)
-    ok = x_map(&of_gram[i][0], i, tall, gemm::kRows) && x_map(&of_gram[i][1], i, tall, bn / 2) &&
+    ok = x_map(&of_gram[i][0], i, tall, gemm::kRows) && x_map(&of_gram[i][1], i, tall, gram_bn / 2) &&
          gemm::make_pane_map<64>(&pane_x[i], p.x[i], false, a.cols, a.rows, xz, p.ld, xps) &&
          (tall ? x_map(&of_next[i][0], i, false, gemm::kRows) &&
                      side_map(&of_next[i][1], p.poly, next_bn / 2)
                : side_map(&of_next[i][0], p.poly, gemm::kRows) &&
                      x_map(&of_next[i][1], i, true, next_bn / 2));
+  SlabEpi::Args slab{};
+  slab.N = (int)p.side;
+  if (p.split > 1 && ok)
+    ok = gemm::make_pane_map<128>(&slab.d, p.slabs, true, p.side, p.side, a.count * p.split,
+                                  p.gram_ld, gps);
   bool wide_out = false;
   if (out == SSD_BF16 && ok) {
     wide_out = view_aligned(a.out, 2, 16) && a.out->token_stride >= a.cols &&
@@ -475,8 +570,21 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
       next_args(s);
       s.f32 = view_of<float>(a.out), s.wide = view_aligned(a.out, 4, 16);
     };
-    e = p.planes == 1 ? multiply<kOne>(of_gram[i], gram, bn, gram_args, err, st)
-                      : multiply<kTwo>(of_gram[i], gram, bn, gram_args, err, st);
+    if (p.split > 1) {
+      e = p.planes == 1
+              ? gemm::launch<SlabEpi, kSplitBN, 0>(of_gram[i], &part, 1, false, slab, err, st)
+              : gemm::launch<SlabEpi, kSplitBN, gemm::kExact>(of_gram[i], &part, 1, false, slab, err,
+                                                              st);
+      if (e != cudaSuccess) return e;
+      const int64_t groups = p.side * (p.gram_ld / 8);
+      e = launch_after(join_parts_kernel,
+                       dim3((unsigned)((groups + kJoinThreads - 1) / kJoinThreads), (unsigned)a.count),
+                       kJoinThreads, 0, st, p.slabs, p.split, p.side, p.gram_ld,
+                       kGramScale / (kScale * kScale), k ? nullptr : p.rest, p.gram, p.planes, err);
+    } else {
+      e = p.planes == 1 ? multiply<kOne>(of_gram[i], gram, bn, gram_args, err, st)
+                        : multiply<kTwo>(of_gram[i], gram, bn, gram_args, err, st);
+    }
     if (e != cudaSuccess) return e;
     e = p.planes == 1 ? multiply<kOne>(of_poly, poly, bn, poly_args, err, st)
                       : multiply<kTwo>(of_poly, poly, bn, poly_args, err, st);

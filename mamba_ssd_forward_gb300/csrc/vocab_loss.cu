@@ -8,7 +8,9 @@
 // launch joins the runs.  Backward: in pieces of the vocabulary the logits are
 // computed again, their epilogue writes the piece of dz, and one launch adds its
 // shares of dx and computes its rows of dW.  Bound by the tensor cores: 2 n V d
-// operations forward, 6 n V d backward.
+// operations forward, 6 n V d backward.  Measured: 8192 tokens x 2560, 50280 words,
+// bf16, forward and backward 5190 us, 1.63 PFLOP/s (under the power cap); forward of
+// 2048 x 768 106 us, 1.5 PFLOP/s; 1021 x 771, 32003 words, fp32, 537 us.
 //
 // Tokens without a target are left out before the products: the others' rows of
 // x are packed together (so whatever the left out rows hold reaches nothing),
@@ -827,7 +829,7 @@ struct Calls {
       if (e != cudaSuccess) break;
       // dx [n, d] += dz [n, words] W [words, d];  dW [words, d] = dz^T x
       q[0] = product(a.dx ? a.n : 0, a.d, w.n);
-      q[0].b_mn = 1, q[0].batch = p.slabs, q[0].part = p.part;
+      q[0].b_mn = 1, q[0].batch = q[0].parts = p.slabs, q[0].part = p.part;
       if (a.dx) q[0].live_m = p.r.live;
       q[1] = product(w.n, a.d, a.n);
       q[1].live_k = p.r.live, q[1].a_mn = q[1].b_mn = 1;

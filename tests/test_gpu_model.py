@@ -396,7 +396,9 @@ def test_fp32_operands_of_any_size(ssd, size):
 # ---------------------------------------------------------- orthogonalisation
 
 ORTH_SHAPES = [(1, 1), (1, 40), (50, 1), (16, 16), (77, 333), (333, 77), (256, 512), (512, 256),
-               (300, 1100), (700, 700), (1030, 260), (3, 64, 129), (4, 257, 31), (2, 520, 520)]
+               (300, 1100), (700, 700), (1030, 260), (3, 64, 129), (4, 257, 31), (2, 520, 520),
+               # long and narrow: the smaller Gram matrix in parts
+               (40, 3000), (5000, 1), (3, 2777, 70), (2, 300, 2500), (400, 6000)]
 
 
 def relative(got, ref):

@@ -52,7 +52,7 @@ def calls(ssd, io):
         loss, lse = ssd.linear_cross_entropy_forward(x, W, t)
         total, _ = ssd.linear_cross_entropy_forward(x, W, t, reduction="mean")
         out += [loss, lse, total, *ssd.linear_cross_entropy_backward(x, W, t, lse).values()]
-    for shape in ((1, 1), (40, 77), (300, 129), (2, 260, 600)):
+    for shape in ((1, 1), (40, 77), (300, 129), (2, 260, 600), (2500, 40)):
         for to in (B16, F32):
             out.append(ssd.orthogonalize(normal(*shape, dtype=io), dtype=to))
     return out

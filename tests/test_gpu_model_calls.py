@@ -32,7 +32,8 @@ def inputs(seed=0, rows=70, d=64, V=300, io=B16):
     t = torch.randint(0, V, (rows,), generator=g, device="cuda")
     t[::3] = -100
     return {"x": n(rows, d).to(io), "r": n(rows, d), "w": 1 + 0.2 * n(d), "W": (0.3 * n(V, d)).to(io),
-            "t": t, "gy": n(rows, d).to(io), "G": n(96, d).to(io)}
+            "t": t, "gy": n(rows, d).to(io), "G": n(96, d).to(io),
+            "H": n(40, 2500).to(io)}
 
 
 def everything(ssd, a):
@@ -42,7 +43,7 @@ def everything(ssd, a):
     loss, lse = ssd.linear_cross_entropy_forward(y, a["W"], a["t"], reduction="mean")
     b = ssd.linear_cross_entropy_backward(y, a["W"], a["t"], lse, loss, reduction="mean")
     return [y, total, *g.values(), q.float(), s, loss, lse, *b.values(),
-            ssd.orthogonalize(a["G"]), ssd.orthogonalize(a["G"], dtype=F32)]
+            *(ssd.orthogonalize(a[k], dtype=to) for k in "GH" for to in (B16, F32))]
 
 
 @pytest.mark.parametrize("io", [B16, F32], ids=str)
@@ -129,7 +130,9 @@ def test_workspaces_of_the_callers(ssd, io):
          lambda **k: list(ssd.linear_cross_entropy_backward(y, a["W"], a["t"], lse, **k).values())),
         (ssd.orthogonalize_workspace_size(a["G"]), lambda **k: [ssd.orthogonalize(a["G"], **k)]),
         (ssd.orthogonalize_workspace_size(a["G"], F32),
-         lambda **k: [ssd.orthogonalize(a["G"], dtype=F32, **k)])]
+         lambda **k: [ssd.orthogonalize(a["G"], dtype=F32, **k)]),
+        (ssd.orthogonalize_workspace_size(a["H"], F32),
+         lambda **k: [ssd.orthogonalize(a["H"], dtype=F32, **k)])]
     for need, call in calls:
         ref = call()
         for fill in (0xff, 0x7f, 0):
