@@ -135,7 +135,15 @@ __device__ __forceinline__ void pack_row(const __nv_bfloat16 *src, uint16_t *dst
 #pragma unroll 4
   for (int64_t i = tid; i < wide; i += threads)
     reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(s)[i];
-  for (int64_t i = 8 * wide + tid; i < d; i += threads) dst[i] = s[i];
+  constexpr int kAtOnce = 8;
+  for (int64_t i = 8 * wide + tid; i < d; i += kAtOnce * threads) {
+    uint16_t v[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) v[k] = i + k * threads < d ? s[i + k * threads] : 0;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (i + k * threads < d) dst[i + k * threads] = v[k];
+  }
 }
 __device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_t ps, int64_t d,
                                          float scale, int tid, int threads) {
@@ -166,6 +174,7 @@ struct Rows {
 };
 
 constexpr int kPackTokens = 8, kPackThreads = 256;  // a warp to a token
+constexpr int kPackCols = 256;                      // columns to a block at least
 constexpr int kGroup = 2048;                        // tokens counted together
 
 // Targets of each group of tokens.
@@ -188,7 +197,8 @@ count_kernel(const int64_t *__restrict__ targets, int64_t ignore, int64_t n,
   counts[blockIdx.x] = c;
 }
 
-// A block takes kPackTokens tokens.  It counts the targets in front of them
+// A block takes kPackTokens tokens, and of few tokens `cols` columns (a warp takes its
+// row load by load: 4 x 2370 bf16 30 us from cold caches as one block, 5 so).  It counts the targets in front of them
 // itself (they come from L2), so no launch of its own makes the list; of many
 // tokens (counts not NULL) those of whole groups are counted before.
 template <typename IO>
@@ -197,7 +207,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
             int64_t L, int64_t n, int64_t d, const float *__restrict__ lse,
             const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
             float *__restrict__ lse_out, const int *__restrict__ counts, Rows rows,
-            uint16_t *__restrict__ xp, int64_t ld, int64_t ps, int planes,
+            uint16_t *__restrict__ xp, int64_t ld, int64_t ps, int planes, int64_t cols,
             const uint32_t *__restrict__ top, int *err) {
   __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
@@ -223,7 +233,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
     if (lane < kPackTokens) place[lane] = mine ? before + __popc(all & ((1u << lane) - 1)) : -1;
     if (lane == 0) mine_all = __popc(all);
     __syncwarp();
-    if (lane < here) {
+    if (lane < here && blockIdx.y == 0) {
       const int64_t t = first + lane;
       if (mine && SSD_IN_BOUNDS(place[lane] < n, err, 71)) {
         const int64_t word = targets[t];
@@ -245,12 +255,13 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   const float scale = top ? pow2(shift_of(top[kTopX])) : 1.f;
   if (warp < here) {
     const int64_t t = first + warp, b = t / L, at = t % L;
+    const int64_t c0 = blockIdx.y * cols, n_cols = d - c0 < cols ? d - c0 : cols;
     if (place[warp] >= 0)
-      pack_row(x.at(b, at), xp + (int64_t)place[warp] * ld, ps, d, scale, lane, 32);
+      pack_row(x.at(b, at) + c0, xp + (int64_t)place[warp] * ld + c0, ps, n_cols, scale, lane, 32);
     else if (dx.p)
-      for (int64_t c = lane; c < d; c += 32) st_io(dx.at(b, at) + c, 0.f);
+      for (int64_t c = lane; c < n_cols; c += 32) st_io(dx.at(b, at) + c0 + c, 0.f);
   }
-  if (first + kPackTokens < n) return;
+  if (first + kPackTokens < n || blockIdx.y) return;
   const int64_t live = before + mine_all;
   if (tid == 0) *rows.live = (int)live;
   // backward the rows are k of a product, in stages of kTileK: the last one's other
@@ -733,16 +744,20 @@ struct Calls {
       if (e != cudaSuccess) return e;
     }
     // (the first launch of the call waits for what is on the stream the ordinary way)
-    const dim3 grid((unsigned)((a.n + kPackTokens - 1) / kPackTokens));
+    const int64_t blocks = (a.n + kPackTokens - 1) / kPackTokens;
+    const int64_t slices = blocks < 2 * sm_count() ? 2 * sm_count() / blocks : 1;
+    int64_t cols = round_up((a.d + slices - 1) / slices, 64);
+    cols = cols < kPackCols ? kPackCols : cols;
+    const dim3 grid((unsigned)blocks, (unsigned)((a.d + cols - 1) / cols));
     if (top || p.counts)
       return launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
                                 a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
                                 view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld,
-                                p.rows * p.ld, kPlanes, top, err);
+                                p.rows * p.ld, kPlanes, cols, top, err);
     pack_kernel<IO><<<grid, kPackThreads, 0, st>>>(
         view_of<const IO>(a.x), a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
-        view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, top,
-        err);
+        view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, cols,
+        top, err);
     return cudaGetLastError();
   }
 
