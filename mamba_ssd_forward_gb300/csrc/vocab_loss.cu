@@ -524,13 +524,13 @@ struct GradEpi {
       if (first == 0) return;
       panes.written();
     }
-    if (a.direct) {
-      if (gemm::elected()) {
-        panes.store(pane, &a.dw, col, row0, 0);
-        ptx::bulk_commit();
-      }
-    } else {
-      copy(col);
+    if (!a.direct) copy(col);
+    if (gemm::elected()) {
+      if (a.direct) panes.store(pane, &a.dw, col, row0, 0);
+      // A group for each use of a pane, an empty one where its values are copied: with
+      // all but the newest group read, the other pane's store is, also that of the last
+      // tile of dx.
+      ptx::bulk_commit();
     }
     pane ^= 1;
   }
