@@ -48,9 +48,12 @@ __device__ __forceinline__ int shift_of(uint32_t top) {
   const int e = (int)(top >> 23) - 127;
   return 14 - (e < -110 ? -110 : e);
 }
-// 2^e, zero where that is no normal number any more, at most 2^127.
+// 2^e, held within 2^-126 .. 2^127.  (Not zero below: logits are multiplied by it, and
+// the words that fill up a row's last tile are -inf.  A sum of 65536 products of scaled
+// operands is at most 2^46, so a logit that is held is 2^-80 at most.)
 __device__ __forceinline__ float pow2(int e) {
-  return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + (e > 127 ? 127 : e)) << 23);
+  e = e < -126 ? -126 : e > 127 ? 127 : e;
+  return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 enum Top { kTopX, kTopW, kTopG, kTops };

@@ -17,3 +17,12 @@ def test_dweight_off_the_grid_behind_dx_tiles(ssd, io, shape):  # noqa: F811
     add to dx."""
     x, w, t, n = loss_case(shape, io, "some")
     check_loss(ssd, x, w, t, n(shape[0]), io, shape[1], shape[2])
+
+
+@pytest.mark.parametrize("ex,ew", [(-60, -60), (-30, -75), (-110, 5)])
+@pytest.mark.parametrize("V", [300, 320])
+def test_fp32_logits_that_vanish(ssd, V, ex, ew):  # noqa: F811
+    """x and W so small that no fp32 holds the power of two that takes the products of
+    their planes to logits: a loss of log V, with and without words that fill up a tile."""
+    x, w, t, n = loss_case((70, 64, V), "fp32", "some")
+    check_loss(ssd, x * 2.0 ** ex, w * 2.0 ** ew, t, n(70), "fp32", 64, V)
