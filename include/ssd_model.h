@@ -89,7 +89,9 @@ typedef struct {
  * [0, vocab) gives a NaN.
  *
  * The logits are never stored.  fp32 operands are taken in two planes of 11
- * bits after a scaling by powers of two: products as exact as fp32 ones.
+ * bits after a scaling by powers of two: products as exact as fp32 ones of
+ * values down to 2^-28 of the largest finite one of x's rows with a target, or
+ * of W; smaller ones are off by 2^-39 of that.
  */
 SSD_API size_t ssd_linear_cross_entropy_workspace_size(const ssd_loss_dims *dims, ssd_dtype dtype,
                                                const ssd_seq *weight);
@@ -103,6 +105,10 @@ SSD_API ssd_status ssd_linear_cross_entropy(const ssd_loss_dims *dims, ssd_dtype
  * [batch, seqlen] without a reduction, else dL/dtotal, one fp32 value on the
  * device; NULL = 1.  dx: a view of dtype (rows of tokens without a target are
  * zero); dweight: dense [vocab, channels] of dtype.  Either may be NULL.
+ *
+ * fp32: softmax terms below 2^-28 are off by 2^-39.  A token's factor is applied
+ * to its dx after the product, whatever the others' are; for dweight the products
+ * gloss x have the limits of x.
  */
 SSD_API size_t ssd_linear_cross_entropy_backward_workspace_size(const ssd_loss_dims *dims,
                                                         ssd_dtype dtype, const ssd_seq *weight);

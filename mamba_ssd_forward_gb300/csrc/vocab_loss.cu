@@ -22,7 +22,9 @@
 // as the gradients' own rounding); a factor common to all tokens is applied to
 // the fp32 sums instead.  fp32: x, W and dz are split into two fp16 planes after
 // scaling by powers of two that take the largest value to 2^14..2^15 (values
-// below 2^-28 of the largest keep 2^-39 of it), three products each.
+// below 2^-28 of the largest keep 2^-39 of it), three products each.  Tokens' factors
+// of their own may be of very different sizes, so they are no part of dz there: dx takes a
+// token's factor after the product, dW from g x in the place of x.
 #include <cmath>
 
 #include "gemm.cuh"
@@ -56,12 +58,19 @@ __device__ __forceinline__ float pow2(int e) {
   return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
+// kTopG: of g x, for factors that each token has of its own; the sum of the largest two's
+// exponents plus kTopBias (0: nothing but zeros).
 enum Top { kTopX, kTopW, kTopG, kTops };
+constexpr int kTopBias = 512;
+// The exponent that takes the products g x below 2^15.
+__device__ __forceinline__ int product_shift(uint32_t top) {
+  return top == 0 ? 0 : 13 - ((int)top - kTopBias);
+}
 
 __device__ __forceinline__ bool counted(int64_t target, int64_t ignore) { return target != ignore; }
 
-// Bits of the largest finite |value| of x's rows with a target, of W, and of the
-// tokens' factors.  (A row's infinity or NaN must not cost the other rows their
+// Bits of the largest finite |value| of x's rows with a target and of W, and the size of
+// the largest g x.  (A row's infinity or NaN must not cost the other rows their
 // scale.)  The order of the maxima has no say.
 __device__ __forceinline__ uint32_t size_of(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
@@ -110,7 +119,8 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
     }
     if (r < n) {
       most[kTopX] = max(most[kTopX], m);
-      if (g) most[kTopG] = max(most[kTopG], size_of(g[r]));
+      if (const uint32_t f = g ? size_of(g[r]) : 0u; f && m)
+        most[kTopG] = max(most[kTopG], (m >> 23) + (f >> 23) - 2 * 127 + kTopBias);
     } else {
       most[kTopW] = max(most[kTopW], m);
     }
@@ -149,8 +159,9 @@ __device__ __forceinline__ void pack_row(const __nv_bfloat16 *src, uint16_t *dst
       if (i + k * threads < d) dst[i + k * threads] = v[k];
   }
 }
-__device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_t ps, int64_t d,
-                                         float scale, int tid, int threads) {
+template <typename F>
+__device__ __forceinline__ void pack_planes(const float *src, uint16_t *dst, int64_t ps, int64_t d,
+                                            F scaled, int tid, int threads) {
   constexpr int kAtOnce = 8;
   for (int64_t i = tid; i < d; i += kAtOnce * threads) {
     float v[kAtOnce];
@@ -159,13 +170,27 @@ __device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       __half hi, lo;
-      split(v[k], scale, hi, lo);
+      split(scaled(v[k]), 1.f, hi, lo);
       if (i + k * threads < d) {
         dst[i + k * threads] = __half_as_ushort(hi);
         dst[ps + i + k * threads] = __half_as_ushort(lo);
       }
     }
   }
+}
+__device__ __forceinline__ void pack_row(const float *src, uint16_t *dst, int64_t ps, int64_t d,
+                                         float scale, int tid, int threads) {
+  pack_planes(src, dst, ps, d, [=](float v) { return v * scale; }, tid, threads);
+}
+// The same of a row times its token's factor and 2^shift: x 2^k m with g 2^shift = m 2^k,
+// 2^k in halves, so that nothing between leaves the number range.
+__device__ __forceinline__ void pack_product(const float *src, uint16_t *dst, int64_t ps,
+                                             int64_t d, float g, int shift, int tid, int threads) {
+  int k = 0;
+  float m = g;
+  if (g != 0.f && isfinite(g)) m = frexpf(g, &k), k += shift;
+  const float a = pow2(k / 2), b = pow2(k - k / 2);
+  pack_planes(src, dst, ps, d, [=](float v) { return v * a * b * m; }, tid, threads);
 }
 
 // What the later launches know of the rows with a target.
@@ -211,8 +236,8 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
             int64_t L, int64_t n, int64_t d, const float *__restrict__ lse,
             const float *__restrict__ gloss, SeqView<IO> dx, float *__restrict__ loss,
             float *__restrict__ lse_out, const int *__restrict__ counts, Rows rows,
-            uint16_t *__restrict__ xp, int64_t ld, int64_t ps, int planes, int64_t cols,
-            const uint32_t *__restrict__ top, int *err) {
+            uint16_t *__restrict__ xp, uint16_t *__restrict__ xg, int64_t ld, int64_t ps,
+            int planes, int64_t cols, const uint32_t *__restrict__ top, int *err) {
   __shared__ int sums[kPackThreads / 32], place[kPackTokens], mine_all;
   const int64_t first = (int64_t)blockIdx.x * kPackTokens;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -260,9 +285,17 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   if (warp < here) {
     const int64_t t = first + warp, b = t / L, at = t % L;
     const int64_t c0 = blockIdx.y * cols, n_cols = d - c0 < cols ? d - c0 : cols;
-    if (place[warp] >= 0)
-      pack_row(x.at(b, at) + c0, xp + (int64_t)place[warp] * ld + c0, ps, n_cols, scale, lane, 32);
-    else if (dx.p)
+    if (place[warp] >= 0) {
+      const int64_t to = (int64_t)place[warp] * ld + c0;
+      pack_row(x.at(b, at) + c0, xp + to, ps, n_cols, scale, lane, 32);
+      if constexpr (sizeof(IO) == 4) {
+        const int64_t word = targets[t];
+        if (xg)
+          pack_product(x.at(b, at) + c0, xg + to, ps, n_cols,
+                       word >= 0 && word < V ? gloss[t] : __int_as_float(0x7fc00000),
+                       product_shift(top[kTopG]), lane, 32);
+      }
+    } else if (dx.p)
       for (int64_t c = lane; c < n_cols; c += 32) st_io(dx.at(b, at) + c0 + c, 0.f);
   }
   if (first + kPackTokens < n || blockIdx.y) return;
@@ -272,8 +305,10 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   // rows are zero (as are those of dz), whatever lay there
   const int64_t end = rows.lse ? (live + gemm::kTileK - 1) / gemm::kTileK * gemm::kTileK : live;
   for (int p = 0; p < planes; ++p)
-    for (int64_t i = (live * ld) / 8 + tid; i < end * ld / 8; i += kPackThreads)
+    for (int64_t i = (live * ld) / 8 + tid; i < end * ld / 8; i += kPackThreads) {
       reinterpret_cast<uint4 *>(xp + p * ps)[i] = make_uint4(0, 0, 0, 0);
+      if (xg) reinterpret_cast<uint4 *>(xg + p * ps)[i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // Rows of W for the products, where TMA cannot take them as they are.
@@ -382,7 +417,7 @@ struct DlogitEpi {
     CUtensorMap dz;
     Rows rows;
     const uint32_t *top;
-    int V, word0, uniform;
+    int V, word0, own;  // own: each token has a factor, which is no part of dz
   };
   static constexpr bool kStaged = true, kSplit = sizeof(IO) == 4;
   static constexpr int kWarps = 8;
@@ -397,13 +432,13 @@ struct DlogitEpi {
     scale = up = 1.f;
     if constexpr (kSplit) {
       scale = pow2(-shift_of(a.top[kTopX]) - shift_of(a.top[kTopW]));
-      up = pow2(a.uniform ? 14 : shift_of(a.top[kTopG]));
+      up = pow2(14);
     }
   }
   __device__ __forceinline__ void begin(const Tile &, int r, int, int M) {
     row0 = r - panes.lane, live = r < M;
     lse = live ? a.rows.lse[r] : 0.f;
-    g = live ? a.rows.g[r] * up : 0.f;
+    g = live ? (a.own ? up : a.rows.g[r] * up) : 0.f;
     target = live ? a.rows.target[r] - a.word0 : -1;
   }
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int j) {
@@ -448,18 +483,19 @@ struct DlogitEpi {
 struct Factors {
   Rows rows;
   const uint32_t *top;
-  const float *gloss;  // one value for all tokens (uniform), or NULL
-  int uniform, mean;
+  const float *gloss;  // one value for all tokens, or NULL
+  int own, mean;       // own: each token has a factor, which dz is short of too
   // Three factors, to be applied in turn: the halves of the scales' exponent, so
   // that nothing between leaves the number range, and the common factor.
   __device__ __forceinline__ float3 of(Top other) const {
-    float3 f = make_float3(1.f, 1.f, uniform && gloss ? *gloss : 1.f);
+    float3 f = make_float3(1.f, 1.f, gloss ? *gloss : 1.f);
     if (mean) {
       const int n = *rows.live;
       f.z /= (float)(n > 1 ? n : 1);
     }
     if (top) {
-      const int e = -(uniform ? 14 : shift_of(top[kTopG])) - shift_of(top[other]);
+      const int e = -14 - (own && other == kTopX ? product_shift(top[kTopG])
+                                                 : shift_of(top[other]));
       f.x = pow2(e / 2), f.y = pow2(e - e / 2);
     }
     return f;
@@ -571,6 +607,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
   const int64_t r = blockIdx.x;
   if (r >= live || !SSD_IN_BOUNDS(d <= ld, err, 79)) return;
   const int64_t t = f.rows.token[r];
+  const float g = f.own ? f.rows.g[r] : 1.f;
   IO *o = dx.at(t / L, t % L);
   for (int64_t c = (threadIdx.x / 32) * 128 + lane * 4; c < d; c += blockDim.x * 4) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};  // (ld is a multiple of 16)
@@ -581,7 +618,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < d) st_io(o + c + e, scaled(v[e], factor));
+      if (c + e < d) st_io(o + c + e, v[e] * factor.x * g * factor.y * factor.z);
   }
 }
 
@@ -661,7 +698,7 @@ struct Plan {
   uint32_t *top;
   int *counts;  // NULL for few tokens
   Rows r;
-  uint16_t *xp, *wp, *dz;
+  uint16_t *xp, *xg, *wp, *dz;     // xg: x times the tokens' own factors, NULL if there are none
   float2 *stat;
   float *loss, *sum;
   int64_t runs;
@@ -699,6 +736,9 @@ Plan plan_of(const LossArgs &a, ssd_dtype io, bool back, void *ws) {
   if (back) {
     p.r.lse = c.take<float>(a.n);
     p.r.g = c.take<float>(a.n);
+    if (p.planes == 2 && a.reduction == SSD_REDUCE_NONE)
+      p.xg = c.take<uint16_t>(p.planes * p.rows * p.ld);
+    if (!a.gloss || !a.dweight) p.xg = nullptr;
     p.dz = c.take<uint16_t>(p.planes * p.rows * p.dz_ld);
     // dx has few tiles and many k where there are few tokens: as many parts as
     // make two of its tiles no longer than a pair's share of all stages
@@ -756,12 +796,12 @@ struct Calls {
     if (top || p.counts)
       return launch_after(pack_kernel<IO>, grid, kPackThreads, 0, st, view_of<const IO>(a.x),
                                 a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
-                                view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld,
+                                view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.xg, p.ld,
                                 p.rows * p.ld, kPlanes, cols, top, err);
     pack_kernel<IO><<<grid, kPackThreads, 0, st>>>(
         view_of<const IO>(a.x), a.targets, a.ignore, a.V, a.L, a.n, a.d, a.lse_in, g,
-        view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.ld, p.rows * p.ld, kPlanes, cols,
-        top, err);
+        view_of<IO>(a.dx), loss, lse, p.counts, p.r, p.xp, p.xg, p.ld, p.rows * p.ld, kPlanes,
+        cols, top, err);
     return cudaGetLastError();
   }
 
@@ -827,11 +867,11 @@ struct Calls {
 
   static cudaError_t backward(const LossArgs &a, void *ws, int *err, cudaStream_t st) {
     const Plan p = plan_of(a, kBf16 ? SSD_BF16 : SSD_F32, true, ws);
-    const bool uniform = a.reduction != SSD_REDUCE_NONE || !a.gloss;
+    const bool each = a.reduction == SSD_REDUCE_NONE && a.gloss;  // a factor for each token
+    const bool own = each && kPlanes == 2;
     const uint32_t *top = kPlanes == 2 ? p.top : nullptr;
     const int64_t ps = p.rows * p.dz_ld;
-    const Factors f{p.r, top, uniform ? a.gloss : nullptr, uniform,
-                    a.reduction == SSD_REDUCE_MEAN};
+    const Factors f{p.r, top, each ? nullptr : a.gloss, own, a.reduction == SSD_REDUCE_MEAN};
     cudaError_t e = pack(a, p, true, nullptr, nullptr, err, st);
     for (int64_t word0 = 0; word0 < a.V && e == cudaSuccess; word0 += p.piece) {
       Words w;
@@ -841,7 +881,7 @@ struct Calls {
       Product q[2];
       if (!logits(a, p, w, maps, q)) return cudaErrorInvalidValue;
       typename DlogitEpi<IO>::Args z{};
-      z.rows = p.r, z.top = top, z.V = (int)w.n, z.word0 = (int)word0, z.uniform = uniform;
+      z.rows = p.r, z.top = top, z.V = (int)w.n, z.word0 = (int)word0, z.own = own;
       if (!gemm::make_pane_map<128>(&z.dz, p.dz, false, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps))
         return cudaErrorInvalidValue;
       e = gemm::launch<DlogitEpi<IO>, kBN, kSegment>(maps, q, 1, kBf16, z, err, st);
@@ -862,8 +902,8 @@ struct Calls {
           !gemm::make_map(&maps[1], w.at, a.d, w.n, kPlanes, w.ld, w.zs, true, kBN / 2) ||
           !gemm::make_map(&maps[2], p.dz, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps, true,
                           gemm::kRows) ||
-          !gemm::make_map(&maps[3], p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld, true,
-                          kBN / 2) ||
+          !gemm::make_map(&maps[3], p.xg ? p.xg : p.xp, a.d, p.rows, kPlanes, p.ld, p.rows * p.ld,
+                          true, kBN / 2) ||
           !gemm::make_pane_map<128>(&g.sum, p.sum, true, sld, p.rows, p.slabs, sld, p.rows * sld) ||
           (a.dweight && g.direct &&
            !gemm::make_pane_map<128>(&g.dw, g.out, !kBf16, a.d, w.n, 1, a.d, w.n * a.d)))
