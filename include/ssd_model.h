@@ -136,9 +136,10 @@ typedef struct {
  *
  * Precision goes by out_dtype.  SSD_BF16: products of operands rounded to fp16
  * (11 bits), X carried in 22 bits until the last two steps.  SSD_F32: everything
- * in 22 bits.  The norm's squares are summed in fp32, so entries beyond about 1e18
- * give NaN; steps that take X beyond 4 or b A + c A A beyond 16 (the usual
- * coefficients stay below 1.3 and 3) overflow.
+ * in 22 bits.  Entries and eps may lie anywhere in their types' range; entries below
+ * 2^-28 of |G| keep 2^-39 of it.  A matrix that holds an infinity or a NaN gives NaN, the
+ * others of a stack are not touched by it.  Steps that take X beyond 4 or b A + c A A
+ * beyond 16 (the usual coefficients stay below 1.3 and 3) overflow.
  */
 SSD_API size_t ssd_orthogonalize_workspace_size(const ssd_orth_dims *dims, ssd_dtype in_dtype,
                                         ssd_dtype out_dtype);

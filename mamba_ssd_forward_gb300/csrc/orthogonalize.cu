@@ -79,29 +79,58 @@ __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t
   }
 }
 
-// Sums of squares, one a block.
+// Sums of squares, one a block, in units of 2^(2 e).  e is 0 where the block's largest
+// |value| is within kLeastPlain .. kMostPlain: its squares stay within fp32 and what falls out
+// below is 2^-46 of its square.  Else the block walks its values again, times 2^-e, which
+// takes the largest to 1 .. 2.
+struct BlockSum {
+  float s;
+  int e;
+};
+constexpr float kLeastPlain = 0x1p-40f, kMostPlain = 0x1p40f;
 template <typename IO>
 __global__ void __launch_bounds__(kNormThreads)
 squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
-               float *__restrict__ part, int *err) {
-  __shared__ float sums[kNormThreads / 32];
+               BlockSum *__restrict__ part, int *err) {
+  constexpr int kWarps = kNormThreads / 32;
+  __shared__ float sums[kWarps], tops[kWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
   ptx::griddep_launch_dependents();
   if (!SSD_IN_BOUNDS(rows > 0 && cols > 0, err, 80)) return;
-  each8(g, rows, cols, wide, [&](const float (&v)[8], int64_t, int64_t) {
+  float top = 0.f;
+  auto walk = [&](auto scaled) {  // this warp's sum into sums
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    each8(g, rows, cols, wide, [&](const float (&v)[8], int64_t, int64_t) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e % 4] = fmaf(v[e], v[e], s[e % 4]);
-  });
-  float t = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int e = 0; e < 8; ++e) {
+        const float x = scaled(v[e]);
+        s[e % 4] = fmaf(x, x, s[e % 4]);
+        top = fmaxf(top, fabsf(x));
+      }
+    });
+    float t = (s[0] + s[1]) + (s[2] + s[3]);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  if (lane == 0) sums[warp] = t;
+    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (lane == 0) sums[warp] = t;
+  };
+  walk([](float v) { return v; });
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) tops[warp] = top;
   __syncthreads();
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+  int e = 0;
+  if (top > 0.f && (top < kLeastPlain || top > kMostPlain) && isfinite(top)) {
+    e = ilogbf(top);
+    const float a = ldexpf(1.f, -e / 2), b = ldexpf(1.f, -e - -e / 2);
+    __syncthreads();
+    walk([=](float v) { return v * a * b; });
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
-    t = sums[0];
-    for (int w = 1; w < kNormThreads / 32; ++w) t += sums[w];
-    part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
+    float t = sums[0];
+    for (int w = 1; w < kWarps; ++w) t += sums[w];
+    part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = {t, e};
   }
 }
 
@@ -117,31 +146,53 @@ __device__ __forceinline__ uint4 pack8(float *v, bool more) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// kScale / (|G| + eps) as rest 2^q with rest in [1, 2), from the blocks' sums; for a |G| that
+// is no number rest is NaN, and with it the result.  (|G| may leave fp32's range.)
+__device__ __forceinline__ float scale_of(const BlockSum *__restrict__ part, int parts, float eps,
+                                          int *q) {
+  const int lane = threadIdx.x % 32;
+  int unit = -1000;  // the largest sum's
+  for (int i = lane; i < parts; i += 32)
+    if (part[i].s != 0.f) unit = max(unit, part[i].e);
+  unit = __reduce_max_sync(0xffffffffu, unit);
+  float s = 0.f;  // every warp adds the parts in the same order
+  for (int i = lane; i < parts; i += 32)
+    if (part[i].s != 0.f) s += ldexpf(part[i].s, 2 * (part[i].e - unit));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  *q = 0;
+  if (!isfinite(s)) return __int_as_float(0x7fc00000);
+  const float norm = sqrtf(s);
+  int en, ee, ew;
+  frexpf(norm, &en);
+  frexpf(eps, &ee);
+  const int top = norm > 0.f ? max(en + unit, ee) : ee;  // norm + eps is 2^(top - 1) at least
+  const float whole = kScale / ((norm > 0.f ? ldexpf(norm, unit - top) : 0.f) + ldexpf(eps, -top));
+  const float rest = 2.f * frexpf(whole, &ew);
+  *q = ew - 1 - top;
+  return rest;
+}
+
 // The first X: G times the power of two below kScale / (|G| + eps), in one plane
 // or two; rest[z]: what is left of that factor, in [1, 2).
 template <typename IO>
 __global__ void __launch_bounds__(kNormThreads)
 start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
-             const float *__restrict__ part, int parts, float eps, __half *__restrict__ x,
+             const BlockSum *__restrict__ part, int parts, float eps, __half *__restrict__ x,
              int64_t ld, int planes, float *__restrict__ rest, int *err) {
   const int64_t z = blockIdx.y;
-  const int lane = threadIdx.x % 32;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  float s = 0.f;  // every warp adds the parts in the same order
-  for (int i = lane; i < parts; i += 32) s += part[z * parts + i];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  const float whole = kScale / (sqrtf(s) + eps);
-  const uint32_t bits = __float_as_uint(whole);
-  const bool normal = bits >= 0x00800000u && bits < 0x7f800000u;
-  const float pow2 = normal ? __uint_as_float(bits & 0x7f800000u) : 1.f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) rest[z] = whole / pow2;
+  int q;
+  const float left = scale_of(part + z * parts, parts, eps, &q);
+  if (blockIdx.x == 0 && threadIdx.x == 0) rest[z] = left;
+  // (in halves: 2^q may leave fp32's range where G times it does not)
+  const float up = ldexpf(1.f, q / 2), more = ldexpf(1.f, q - q / 2);
   __half *hi = x + z * 2 * rows * ld, *lo = hi + rows * ld;
   if (!SSD_IN_BOUNDS(cols <= ld, err, 81)) return;
   each8(g, rows, cols, wide, [&](float (&v)[8], int64_t r, int64_t c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= pow2;
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * up * more;
     *reinterpret_cast<uint4 *>(hi + r * ld + c) = pack8(v, planes == 2);
     if (planes == 2) *reinterpret_cast<uint4 *>(lo + r * ld + c) = pack8(v, false);
   });
@@ -399,7 +450,8 @@ struct Plan {
   int64_t side, ld, gram_ld;
   int parts;           // of the norm's sums
   int split, stages;   // parts of A's k (1: A in one go), stages of k in each
-  float *part, *rest, *slabs;
+  BlockSum *part;
+  float *rest, *slabs;
   __half *x[2], *gram, *poly;
   size_t bytes;
 };
@@ -427,7 +479,7 @@ Plan plan_of(const OrthArgs &a, ssd_dtype out, void *ws) {
     p.split = 1, p.stages = 0;
   }
   Carver c(ws);
-  p.part = c.take<float>(a.count * p.parts);
+  p.part = c.take<BlockSum>(a.count * p.parts);
   p.slabs = c.take<float>(p.split > 1 ? a.count * p.split * p.side * p.gram_ld : 0);
   p.rest = c.take<float>(a.count);
   for (int i = 0; i < 2; ++i) p.x[i] = c.take<__half>(a.count * 2 * a.rows * p.ld);

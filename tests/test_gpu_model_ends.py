@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import model_ref64 as R
-from test_gpu_model import F32, check_loss, loss_case, ssd, within  # noqa: F401
+from test_gpu_model import F32, IO, check_loss, gen, loss_case, relative, ssd, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,46 @@ def test_fp32_factors_at_the_ends_of_the_range(ssd):  # noqa: F811
     keep = torch.arange(70, device="cuda") > 4
     assert torch.equal(dx[keep], ref["dx"][keep]) and torch.equal(dx[:3], ref["dx"][:3])
     assert not torch.isfinite(dx[3]).any() and torch.isnan(dx[4]).all()
+
+
+# ----------------------------------------------------- orthogonalised updates
+
+@pytest.mark.parametrize("to", ["bf16", "fp32"])
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("size,eps", [(1e-13, 1e-20), (1e-25, 1e-32), (1e-38, 1e-45), (1e12, 1e-7),
+                                      (1e20, 1e-7), (1e37, 1e-7)])
+def test_updates_of_every_size(ssd, size, eps, io, to):  # noqa: F811
+    """Entries whose squares leave fp32 at either end, down to denormals, and a norm beyond
+    its range; in stacks beside matrices of usual size, whose bits do not change."""
+    for shape in ((70, 130), (3, 200, 90)):
+        G = gen(shape[-1])(*shape, scale=size, dtype=IO[io])
+        X = ssd.orthogonalize(G, dtype=IO[to], eps=eps)
+        assert relative(X, R.orthogonalize(G, eps=eps)) <= R.orth_bound(IO[to], G)
+    H = gen(2)(3, 200, 90, dtype=IO[io])
+    ref = ssd.orthogonalize(H, dtype=IO[to], eps=eps)
+    H[1] = G[1]
+    Y = ssd.orthogonalize(H, dtype=IO[to], eps=eps)
+    assert torch.equal(Y[::2], ref[::2]) and torch.equal(Y[1], X[1])
+
+
+@pytest.mark.parametrize("to", ["bf16", "fp32"])
+def test_an_update_of_mixed_sizes(ssd, to):  # noqa: F811
+    """Rows of 1e-30, 1 and 1e30 in one matrix: its large rows orthogonalised, the others
+    what is left of them next to those (their share of the norm is 1e-30)."""
+    G = gen(3)(300, 600)
+    G[::3] *= 1e-30
+    G[1::3] *= 1e30
+    X = ssd.orthogonalize(G, dtype=IO[to])
+    assert relative(X, R.orthogonalize(G)) <= R.orth_bound(IO[to], G)
+
+
+@pytest.mark.parametrize("to", ["bf16", "fp32"])
+@pytest.mark.parametrize("eps", [1e-7, 1e-30, 1e-37, 1e-45])
+def test_updates_of_zeros_and_of_no_numbers(ssd, eps, to):  # noqa: F811
+    """Zeros stay zeros whatever eps is; an infinity or a NaN gives NaN, in its matrix."""
+    G = torch.zeros(5, 40, 70, device="cuda")
+    G[1, 3, 5] = 1e-30
+    G[2, 3, 5], G[3, 7, 7], G[4] = float("inf"), float("nan"), 1e38
+    G[4, 0, 0] = float("-inf")
+    X = ssd.orthogonalize(G, dtype=IO[to], eps=eps)
+    assert (X[0] == 0).all() and torch.isfinite(X[1]).all() and torch.isnan(X[2:]).all()
