@@ -34,7 +34,7 @@ typedef struct {
  * x, y [batch, seqlen, channels] of dtype; residual, total of stream_dtype,
  * which is dtype or SSD_F32; weight [channels] fp32.  residual NULL: t = x, and
  * total (if given) is x in stream_dtype.  total NULL: not written.  y may be x,
- * total may be residual; other overlaps are not allowed.
+ * total may be residual (the same view each); other overlaps are not allowed.
  */
 SSD_API ssd_status ssd_add_norm(const ssd_add_norm_dims *dims, ssd_dtype dtype, ssd_dtype stream_dtype,
                         const ssd_seq *x, const ssd_seq *residual, const float *weight,
@@ -46,7 +46,7 @@ SSD_API ssd_status ssd_add_norm(const ssd_add_norm_dims *dims, ssd_dtype dtype, 
  * to e4m3 (4 exponent bits, 3 mantissa bits, largest value 448); a block of zeros has scale 0.
  *
  * block: 32, 64, 128, or 0 (a scale for each token).  q: a view of bytes;
- * scales: dense fp32 [batch, seqlen, ceil(channels / block)].
+ * scales: dense fp32 [batch, seqlen, ceil(channels / block)].  Both overlap nothing.
  */
 SSD_API ssd_status ssd_add_norm_quantized(const ssd_add_norm_dims *dims, ssd_dtype dtype,
                                   ssd_dtype stream_dtype, int64_t block, const ssd_seq *x,

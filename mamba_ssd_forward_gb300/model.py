@@ -71,6 +71,14 @@ def _rows(t, name, shape, dtype, dev, like):
     return SsdSeq(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
 
 
+def _in_place(out, name, source, source_name):
+    """Refuses an output at the address of an input that it may be, unless it is
+    that view: rows elsewhere are other threads' to read."""
+    if (source is not None and out.data_ptr() == source.data_ptr()
+            and any(a != b for a, b, n in zip(out.stride(), source.stride(), out.shape) if n > 1)):
+        raise ValueError(f"{name} must be {source_name} itself or other memory")
+
+
 def _new_rows(shape, dtype, like):
     """A new dense tensor of that shape, and its view."""
     t = torch.empty(shape, dtype=dtype, device=like.device)
@@ -93,6 +101,7 @@ def _add_norm_inputs(x, residual, weight, total, eps):
     if total is not None:
         _out(total, "total", shape, stream, x)
         _separate(total, "total", x, "x")
+        _in_place(total, "total", residual, "residual")
         tv = _rows(total, "total", shape, stream, dev, x)
     elif residual is not None:
         total, tv = _new_rows(shape, stream, x)
@@ -114,6 +123,7 @@ def add_norm_forward(x, residual, weight, eps: float = 1e-5, y=None, total=None)
         _out(y, "y", shape, x.dtype, x)
         _separate(y, "y", residual, "residual")
         _separate(y, "y", total, "total")
+        _in_place(y, "y", x, "x")
         yv = _rows(y, "y", shape, x.dtype, dev, x)
     code = _abi.load().ssd_add_norm(*head, *ins, yv, tv, _stream(x))
     if code:
@@ -126,7 +136,8 @@ def add_norm_quantized(x, residual, weight, block: int = 128, eps: float = 1e-5,
     """add_norm_forward with y in 8 bits (ssd_add_norm_quantized): q
     (float8_e4m3fn, the shape of x), scales (float32 [.., ceil(D / block)]) and
     total.  y is q times its block's scale, which is max|y| / 448 over `block`
-    channels (32, 64 or 128) or, with block = 0, over the token."""
+    channels (32, 64 or 128) or, with block = 0, over the token.  q and scales
+    have memory of their own."""
     if block not in (0, 32, 64, 128):
         raise ValueError(f"block must be 0, 32, 64 or 128, got {block!r}")
     head, ins, total, tv, shape, dev = _add_norm_inputs(x, residual, weight, total, eps)
@@ -137,10 +148,14 @@ def add_norm_quantized(x, residual, weight, block: int = 128, eps: float = 1e-5,
         at = scales.data_ptr()
     else:
         at = _dense(scales, "scales", tuple(lead), torch.float32, x)
+        for t, name in ((x, "x"), (residual, "residual"), (total, "total")):
+            _separate(scales, "scales", t, name)
     if q is None:
         q, qv = _new_rows(shape, torch.float8_e4m3fn, x)
     else:
         _out(q, "q", shape, torch.float8_e4m3fn, x)
+        for t, name in ((x, "x"), (residual, "residual"), (total, "total"), (scales, "scales")):
+            _separate(q, "q", t, name)
         qv = _rows(q, "q", shape, torch.float8_e4m3fn, dev, x)
     code = _abi.load().ssd_add_norm_quantized(*head, block, *ins, qv, at, tv, _stream(x))
     if code:
