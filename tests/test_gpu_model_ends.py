@@ -117,3 +117,14 @@ def test_updates_of_zeros_and_of_no_numbers(ssd, eps, to):  # noqa: F811
     G[4, 0, 0] = float("-inf")
     X = ssd.orthogonalize(G, dtype=IO[to], eps=eps)
     assert (X[0] == 0).all() and torch.isfinite(X[1]).all() and torch.isnan(X[2:]).all()
+
+
+def test_smoke_decomposes_nothing_on_the_gpu(ssd, monkeypatch):  # noqa: F811
+    """The GPU's decompositions come from a library that need not be there."""
+    import __graft_entry__ as entry
+    for name in ("svd", "svdvals", "qr", "eigh"):
+        def on_host(a, *args, real=getattr(torch.linalg, name), **kw):
+            assert not a.is_cuda
+            return real(a, *args, **kw)
+        monkeypatch.setattr(torch.linalg, name, on_host)
+    entry._smoke_model(ssd)
