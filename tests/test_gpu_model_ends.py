@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import model_ref64 as R
-from test_gpu_model import F32, IO, check_loss, gen, loss_case, relative, ssd, within  # noqa: F401
+from test_gpu_model import (B16, F32, IO, check_loss, gen, loss_case, relative, ssd,  # noqa: F401
+                            within)
 
 pytestmark = pytest.mark.gpu
 
@@ -76,6 +77,27 @@ def test_fp32_factors_at_the_ends_of_the_range(ssd):  # noqa: F811
     assert not torch.isfinite(dx[3]).any() and torch.isnan(dx[4]).all()
 
 
+def test_losses_of_sure_rows(ssd):  # noqa: F811
+    """Logits near 1e4 with the target the largest, the next one tens below: a loss of 0 up to
+    the rounding of numbers near 1e4 (loss_bound's 2^-22 of lse, 2.4e-3, and the logits'
+    own), each row by its own size.  Losing the target, or counting it twice, shows."""
+    x = torch.zeros(5, 16, dtype=B16, device="cuda")
+    w = torch.zeros(300, 16, dtype=B16, device="cuda")
+    w[:, 0] = torch.linspace(-1, 1, 300, device="cuda")
+    w[299, 0] = 1
+    x[0, 0], x[1, 0] = 1e4, -1e4
+    t = torch.full((5,), 299, device="cuda")
+    t[1], t[2] = 0, 7
+    ref, ref_lse, live = R.cross_entropy(x, w, t)
+    loss, lse = ssd.linear_cross_entropy_forward(x, w, t)
+    for i in range(5):
+        z = R.logit_bound(x[i:i + 1], w, B16, live[i:i + 1])
+        off = R.loss_bound(z, 300, ref_lse[i])
+        assert float(off) < 0.05
+        within(loss[i], ref[i], off, "loss")
+        within(lse[i], ref_lse[i], off, "lse")
+
+
 # ----------------------------------------------------- orthogonalised updates
 
 @pytest.mark.parametrize("to", ["bf16", "fp32"])
@@ -117,6 +139,17 @@ def test_updates_of_zeros_and_of_no_numbers(ssd, eps, to):  # noqa: F811
     G[4, 0, 0] = float("-inf")
     X = ssd.orthogonalize(G, dtype=IO[to], eps=eps)
     assert (X[0] == 0).all() and torch.isfinite(X[1]).all() and torch.isnan(X[2:]).all()
+
+
+def test_a_stack_between_the_rows_of_another_axis(ssd):  # noqa: F811
+    """Matrices whose rows alternate in memory, read and written so."""
+    G = gen(1)(3, 40, 72, dtype=B16)
+    X = ssd.orthogonalize(G)
+    out = torch.zeros(40, 3, 72, dtype=B16, device="cuda").permute(1, 0, 2)
+    ssd.orthogonalize(G, out=out)
+    assert torch.equal(out, X)
+    H = torch.empty(40, 3, 72, dtype=B16, device="cuda").permute(1, 0, 2).copy_(G)
+    assert torch.equal(ssd.orthogonalize(H), X)
 
 
 def test_smoke_decomposes_nothing_on_the_gpu(ssd, monkeypatch):  # noqa: F811
