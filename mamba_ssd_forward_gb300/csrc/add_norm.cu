@@ -37,11 +37,14 @@ constexpr int V = 8;  // channels to a vector
 template <bool kWide>
 struct Channels {
   static constexpr int kStep = kWide ? 1 : 32;
-  int c, D;
-  __device__ __forceinline__ Channels(int vector, int d)
-      : c(kWide ? vector * V : vector / 32 * 32 * V + vector % 32), D(d) {}
+  int c, D, *err;
+  __device__ __forceinline__ Channels(int vector, int d, int *e)
+      : c(kWide ? vector * V : vector / 32 * 32 * V + vector % 32), D(d), err(e) {}
   __device__ __forceinline__ int at(int e) const { return c + e * kStep; }
-  __device__ __forceinline__ bool any() const { return c < D; }
+  // (every access of eight channels at once is behind this)
+  __device__ __forceinline__ bool any() const {
+    return c < D && SSD_IN_BOUNDS(!kWide || c + V <= D, err, 500);
+  }
 };
 // V channels of a row as the memory holds them (elements of 16 bits by
 // themselves where they come so: packing them would wait for the loads), so that
@@ -94,10 +97,11 @@ struct Weights {
   static constexpr bool kKept = K * V <= 16;
   const float *p;
   Raw<float, kWide> kept[kKept ? K : 1];
-  __device__ __forceinline__ Weights(const float *weight, int tid, int team, int D) : p(weight) {
+  __device__ __forceinline__ Weights(const float *weight, int tid, int team, int D, int *err)
+      : p(weight) {
     if constexpr (kKept)
 #pragma unroll
-      for (int k = 0; k < K; ++k) kept[k].load(p, Channels<kWide>(tid + k * team, D));
+      for (int k = 0; k < K; ++k) kept[k].load(p, Channels<kWide>(tid + k * team, D, err));
   }
   __device__ __forceinline__ Raw<float, kWide> of(int k, const Channels<kWide> &c) const {
     if constexpr (kKept) return kept[k];
@@ -179,7 +183,8 @@ __device__ __forceinline__ void quantise(float (&t)[V], const Channels<kWide> &c
 #pragma unroll
     for (int e = 0; e < V; ++e) m = fmaxf(m, fabsf(t[e]));
     m = spread(m, qu.block / V);
-    const bool leads = c.any() && c.c % qu.block == 0;
+    const bool leads = c.any() && c.c % qu.block == 0 &&
+                       SSD_IN_BOUNDS(c.c / qu.block < qu.parts, c.err, 501);
     const float up = quantiser(m, leads ? scales + c.c / qu.block : nullptr);
 #pragma unroll
     for (int e = 0; e < V; ++e) t[e] *= up;
@@ -197,7 +202,8 @@ __device__ __forceinline__ void quantise(float (&t)[V], const Channels<kWide> &c
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (e % group == 0) {
-        const bool leads = threadIdx.x % 32 == 0 && c.at(e) < c.D;
+        const bool leads = threadIdx.x % 32 == 0 && c.at(e) < c.D &&
+                           SSD_IN_BOUNDS(c.at(e) / qu.block < qu.parts, c.err, 501);
         m[e] = quantiser(spread(m[e], 32), leads ? scales + c.at(e) / qu.block : nullptr);
       } else {
         m[e] = m[e - 1];
@@ -261,19 +267,19 @@ add_norm_kernel(SeqView<const IO> x, SeqView<const ST> residual, const float *__
   const int64_t step = (int64_t)gridDim.x * per;
   if (first >= rows) return;
   const int tid = per > 1 ? threadIdx.x % 32 : threadIdx.x;
-  if (!SSD_IN_BOUNDS((int64_t)team * K * V >= D, err, 90)) return;
-  const Weights<K, kWide> weights(weight, tid, team, D);
+  const Weights<K, kWide> weights(weight, tid, team, D, err);
   Raw<IO, kWide> xn[K];
   Raw<ST, kWide> rn[K];
   auto load = [&](const IO *xr, const ST *rr) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Channels<kWide> c(tid + k * team, D);
+      const Channels<kWide> c(tid + k * team, D, err);
       xn[k].load(xr, c);
       if (residual.p) rn[k].load(rr, c);
     }
   };
   auto fetch = [&](int64_t row) {
+    if (!SSD_IN_BOUNDS(row < rows, err, 502)) return;
     const uint32_t b = (uint32_t)row / (uint32_t)L, at = (uint32_t)row - b * (uint32_t)L;
     load(x.at(b, at), residual.at(b, at));
   };
@@ -317,7 +323,7 @@ add_norm_kernel(SeqView<const IO> x, SeqView<const ST> residual, const float *__
     float top[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Channels<kWide> c(tid + k * team, D);
+      const Channels<kWide> c(tid + k * team, D, err);
       if (c.any()) {
         if (total.p) store_row(total.at(b, at), c, t[k]);
         const Raw<float, kWide> w = weights.of(k, c);
@@ -340,7 +346,7 @@ add_norm_kernel(SeqView<const IO> x, SeqView<const ST> residual, const float *__
         const float up = quantiser(top[0], tid == 0 ? qu.scales + row : nullptr);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const Channels<kWide> c(tid + k * team, D);
+          const Channels<kWide> c(tid + k * team, D, err);
           if (!c.any()) continue;
 #pragma unroll
           for (int e = 0; e < V; ++e) t[k][e] *= up;
@@ -366,8 +372,7 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
   const int64_t step = (int64_t)gridDim.x * per;
   const int tid = per > 1 ? threadIdx.x % 32 : threadIdx.x;
   ptx::griddep_launch_dependents();  // (the sum over the blocks waits for them)
-  if (!SSD_IN_BOUNDS((int64_t)team * K * V >= D, err, 91)) return;
-  const Weights<K, kWide> weights(weight, tid, team, D);
+  const Weights<K, kWide> weights(weight, tid, team, D, err);
   // (two vectors of three tensors twice would not fit the registers)
   constexpr bool kNext = !kRing && K == 1;
   Raw<ST, kWide> t[K], gt[K], tn[kNext ? K : 1], gtn[kNext ? K : 1];
@@ -375,13 +380,14 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
   auto load = [&](const ST *tr, const IO *gr, const ST *ur, auto &t, auto &g, auto &gt) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Channels<kWide> c(tid + k * team, D);
+      const Channels<kWide> c(tid + k * team, D, err);
       t[k].load(tr, c);
       g[k].load(gr, c);
       if (gtotal.p) gt[k].load(ur, c);
     }
   };
   auto fetch = [&](int64_t row, auto &t, auto &g, auto &gt) {
+    if (!SSD_IN_BOUNDS(row < rows, err, 503)) return;
     const uint32_t b = (uint32_t)row / (uint32_t)L, at = (uint32_t)row - b * (uint32_t)L;
     load(total.at(b, at), gy.at(b, at), gtotal.at(b, at), t, g, gt);
   };
@@ -422,7 +428,7 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Raw<float, kWide> w = weights.of(k, Channels<kWide>(tid + k * team, D));
+      const Raw<float, kWide> w = weights.of(k, Channels<kWide>(tid + k * team, D, err));
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         s[0] = fmaf(t[k].at(e), t[k].at(e), s[0]);
@@ -438,7 +444,7 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
     const float rstd = rsqrtf(s[0] / (float)D + eps), mean = s[1] * rstd / (float)D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Channels<kWide> c(tid + k * team, D);
+      const Channels<kWide> c(tid + k * team, D, err);
       if (!c.any()) continue;
       const Raw<float, kWide> w = weights.of(k, c);
       float o[V];
@@ -467,7 +473,7 @@ add_norm_grad_kernel(SeqView<const ST> total, const float *__restrict__ weight,
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Channels<kWide> c(tid + k * team, D);
+    const Channels<kWide> c(tid + k * team, D, err);
 #pragma unroll
     for (int e = 0; e < V; ++e)
       if (c.at(e) < D) part[(int64_t)blockIdx.x * D + c.at(e)] = dw[k][e];

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kCols *kSlices) colsum_kernel(ColSum a, int *e
   ptx::griddep_wait();
   const int64_t i = blk * kCols + col;
   float acc = 0.f;
-  if (i < g.n && SSD_IN_BOUNDS(g.rows >= 0, err, 60)) {
+  if (i < g.n && SSD_IN_BOUNDS(blk < (g.n + kCols - 1) / kCols, err, 60)) {
     const float *p = g.src + i;
 #pragma unroll 8
     for (int64_t r = slice; r < g.rows; r += kSlices) acc += p[r * g.n];

@@ -58,7 +58,7 @@ __device__ __forceinline__ void load8(const IO *p, int64_t c, int64_t cols, bool
 constexpr int kAtOnce = 4;
 template <typename IO, typename F>
 __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
-                                      F f) {
+                                      int *err, F f) {
   const uint32_t per = (uint32_t)((cols + 7) / 8), step = gridDim.x * kNormThreads;
   const uint32_t rs = step / per, cs = step % per;  // to a thread's next group
   const uint32_t i = blockIdx.x * kNormThreads + threadIdx.x;
@@ -69,7 +69,8 @@ __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       rr[k] = r, cc[k] = c * 8;
-      if (r < rows) load8(g.at(blockIdx.y, r), cc[k], cols, wide, v[k]);
+      if (r < rows && SSD_IN_BOUNDS(cc[k] < cols, err, 530))
+        load8(g.at(blockIdx.y, r), cc[k], cols, wide, v[k]);
       r += rs, c += cs;
       if (c >= per) c -= per, ++r;
     }
@@ -96,11 +97,10 @@ squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
   __shared__ float sums[kWarps], tops[kWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ptx::griddep_launch_dependents();
-  if (!SSD_IN_BOUNDS(rows > 0 && cols > 0, err, 80)) return;
   float top = 0.f;
   auto walk = [&](auto scaled) {  // this warp's sum into sums
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    each8(g, rows, cols, wide, [&](const float (&v)[8], int64_t, int64_t) {
+    each8(g, rows, cols, wide, err, [&](const float (&v)[8], int64_t, int64_t) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x = scaled(v[e]);
@@ -189,8 +189,8 @@ start_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
   // (in halves: 2^q may leave fp32's range where G times it does not)
   const float up = ldexpf(1.f, q / 2), more = ldexpf(1.f, q - q / 2);
   __half *hi = x + z * 2 * rows * ld, *lo = hi + rows * ld;
-  if (!SSD_IN_BOUNDS(cols <= ld, err, 81)) return;
-  each8(g, rows, cols, wide, [&](float (&v)[8], int64_t r, int64_t c) {
+  each8(g, rows, cols, wide, err, [&](float (&v)[8], int64_t r, int64_t c) {
+    if (!SSD_IN_BOUNDS(r < rows && c + 8 <= ld, err, 531)) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * up * more;
     *reinterpret_cast<uint4 *>(hi + r * ld + c) = pack8(v, planes == 2);
@@ -215,6 +215,7 @@ struct StepEpi {
     int power;
     int c_planes, c_stored;  // planes of C to add (0: no C), and in its array
     int d_stored;            // of D
+    int count;               // matrices
     int share;               // columns of the tile that a warp takes
     int symmetric;           // there are mirrored tiles
     __half *out;             // D again, for the mirrored tiles of two planes
@@ -242,7 +243,7 @@ struct StepEpi {
   __device__ __forceinline__ void begin(const Tile &o, int r, int col, int rows) {
     row = r, row0 = r - panes.lane, col0 = col, M = rows, mirror = o.mirror, batch = o.batch;
     float f = 1.f;
-    if (a.rest) {
+    if (a.rest && SSD_IN_BOUNDS(batch < a.count, err, 532)) {
       f = a.rest[batch];
       if (a.power == 2) f *= f;
     }
@@ -288,7 +289,7 @@ struct StepEpi {
       }
     }
     if constexpr (kind == kF32) {
-      if (row < M) {
+      if (row < M && SSD_IN_BOUNDS(batch < a.count && col < a.N, err, 533)) {
         float *o = a.f32.at(batch, row) + col;
         if (a.wide && col + gemm::kChunk <= a.N) {
 #pragma unroll
@@ -323,7 +324,7 @@ struct StepEpi {
           *reinterpret_cast<uint16_t *>(m + Pane::swizzled(i, panes.lane >> 3)) =
               (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
       }
-      if (kind == kTwo && mirror && row < M && SSD_IN_BOUNDS(row < a.ld, err, 82)) {
+      if (kind == kTwo && mirror && row < M && SSD_IN_BOUNDS(batch < a.count && row < a.N, err, 534)) {
         // (there is no pane left for it: the lanes' rows lie side by side)
         uint16_t *m = reinterpret_cast<uint16_t *>(a.out + batch * a.zs + p * a.ps) +
                       (int64_t)col * a.ld + row;
@@ -360,7 +361,7 @@ struct StepEpi {
   // The pane to rows that TMA cannot write: 16 lanes along a row's columns.
   __device__ __forceinline__ void copy(int pane, int col) {
     const int rows = min(32, M - row0), w = panes.lane & 15;
-    if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 83)) return;
+    if (!SSD_IN_BOUNDS(batch < a.count && row0 < M && col < a.N, err, 535)) return;
 #pragma unroll 4
     for (int r = panes.lane >> 4; r < rows; r += 2) {
       const uint32_t q = panes.word(pane, r, w);
@@ -419,7 +420,7 @@ join_parts_kernel(const float *__restrict__ slabs, int parts, int64_t side, int6
   ptx::griddep_wait();
   const int64_t z = blockIdx.y, i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   const int64_t r = i / (ld / 8), c = i % (ld / 8) * 8;
-  if (r >= side || !SSD_IN_BOUNDS(side <= ld, err, 84)) return;
+  if (r >= side || !SSD_IN_BOUNDS(c + 8 <= ld, err, 536)) return;
   const float *p = slabs + z * parts * side * ld + r * ld + c;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -600,6 +601,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
     auto gram_args = [&](auto &s) {
       s.alpha = kGramScale / (kScale * kScale), s.rest = k ? nullptr : p.rest, s.power = 2;
       s.d = pane_gram, s.out = p.gram, s.d_stored = p.planes, s.share = bn / 4, s.symmetric = 1;
+      s.count = (int)a.count;
       s.ld = p.gram_ld, s.ps = gps, s.zs = p.planes * gps, s.N = (int)p.side;
     };
     auto poly_args = [&](auto &s) {
@@ -611,7 +613,7 @@ cudaError_t run(const OrthArgs &a, ssd_dtype out, void *ws, int *err, cudaStream
       s.alpha = 1.f / kGramScale, s.beta = a.a, s.rest = k ? nullptr : p.rest, s.power = 1;
       if (last) s.alpha /= kScale, s.beta /= kScale;
       s.c = pane_x[i], s.c_planes = carried(k), s.c_stored = 2, s.d = pane_x[!i], s.d_stored = 2;
-      s.N = (int)a.cols, s.share = next_bn / 4;
+      s.N = (int)a.cols, s.share = next_bn / 4, s.count = (int)a.count;
     };
     auto bf16_args = [&](auto &s) {
       next_args(s);

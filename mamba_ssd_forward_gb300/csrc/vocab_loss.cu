@@ -95,7 +95,9 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
         const int64_t at = i + k * threads;
-        v[k] = at < vecs ? reinterpret_cast<const float4 *>(w)[at] : make_float4(0, 0, 0, 0);
+        v[k] = at < vecs && SSD_IN_BOUNDS(4 * at + 4 <= V * d, err, 510)
+                   ? reinterpret_cast<const float4 *>(w)[at]
+                   : make_float4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
@@ -109,7 +111,7 @@ top_kernel(SeqView<const float> x, const int64_t *__restrict__ targets, int64_t 
     if (r < n && !counted(targets[r], ignore)) continue;
     const float *p = r < n ? x.at(r / L, r % L) : w + (r - n) * ws;
     uint32_t m = 0;
-    if (!SSD_IN_BOUNDS(r < n + V, err, 70)) continue;
+    if (!SSD_IN_BOUNDS(r < n + V, err, 511)) continue;
     for (int64_t c = lane; c < d; c += 8 * 32) {
       uint32_t v[8];
 #pragma unroll
@@ -216,12 +218,12 @@ count_kernel(const int64_t *__restrict__ targets, int64_t ignore, int64_t n,
 #pragma unroll
   for (int k = 0; k < kGroup / kPackThreads; ++k) {
     const int64_t i = first + k * kPackThreads + threadIdx.x;
-    if (i < n && SSD_IN_BOUNDS(i >= 0, err, 69)) c += counted(targets[i], ignore);
+    if (i < n) c += counted(targets[i], ignore);
   }
   c = __reduce_add_sync(0xffffffffu, c);
   if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = c;
   __syncthreads();
-  if (threadIdx.x) return;
+  if (threadIdx.x || !SSD_IN_BOUNDS(first < n, err, 512)) return;
   for (int w = 1; w < kPackThreads / 32; ++w) c += sums[w];
   counts[blockIdx.x] = c;
 }
@@ -243,6 +245,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if (!SSD_IN_BOUNDS(first < n, err, 513)) return;
   int before = 0;
   const int64_t groups = counts ? first / kGroup : 0;
   for (int64_t i = tid; i < groups; i += kPackThreads) before += counts[i];
@@ -264,7 +267,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
     __syncwarp();
     if (lane < here && blockIdx.y == 0) {
       const int64_t t = first + lane;
-      if (mine && SSD_IN_BOUNDS(place[lane] < n, err, 71)) {
+      if (mine && SSD_IN_BOUNDS(place[lane] < n, err, 514)) {
         const int64_t word = targets[t];
         const bool real = word >= 0 && word < V;
         rows.token[place[lane]] = (int)t;
@@ -285,7 +288,9 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   if (warp < here) {
     const int64_t t = first + warp, b = t / L, at = t % L;
     const int64_t c0 = blockIdx.y * cols, n_cols = d - c0 < cols ? d - c0 : cols;
-    if (place[warp] >= 0) {
+    const bool fits = SSD_IN_BOUNDS(place[warp] < n && c0 + n_cols <= ld &&
+                                        ((int64_t)place[warp] + 1) * ld <= ps, err, 515);
+    if (fits && place[warp] >= 0) {
       const int64_t to = (int64_t)place[warp] * ld + c0;
       pack_row(x.at(b, at) + c0, xp + to, ps, n_cols, scale, lane, 32);
       if constexpr (sizeof(IO) == 4) {
@@ -295,7 +300,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
                        word >= 0 && word < V ? gloss[t] : __int_as_float(0x7fc00000),
                        product_shift(top[kTopG]), lane, 32);
       }
-    } else if (dx.p)
+    } else if (fits && dx.p)
       for (int64_t c = lane; c < n_cols; c += 32) st_io(dx.at(b, at) + c0 + c, 0.f);
   }
   if (first + kPackTokens < n || blockIdx.y) return;
@@ -306,6 +311,7 @@ pack_kernel(SeqView<const IO> x, const int64_t *__restrict__ targets, int64_t ig
   const int64_t end = rows.lse ? (live + gemm::kTileK - 1) / gemm::kTileK * gemm::kTileK : live;
   for (int p = 0; p < planes; ++p)
     for (int64_t i = (live * ld) / 8 + tid; i < end * ld / 8; i += kPackThreads) {
+      if (!SSD_IN_BOUNDS(8 * i + 8 <= ps, err, 516)) break;
       reinterpret_cast<uint4 *>(xp + p * ps)[i] = make_uint4(0, 0, 0, 0);
       if (xg) reinterpret_cast<uint4 *>(xg + p * ps)[i] = make_uint4(0, 0, 0, 0);
     }
@@ -320,7 +326,7 @@ pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d
   const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  if (r >= rows || !SSD_IN_BOUNDS(ld >= d && ws >= 0, err, 72)) return;
+  if (r >= rows || !SSD_IN_BOUNDS(r * ld + d <= ps, err, 517)) return;
   pack_row(w + r * ws, wp + r * ld, ps, d, top ? pow2(shift_of(top[kTopW])) : 1.f,
            threadIdx.x % 32, 32);
 }
@@ -334,10 +340,10 @@ pack_weight_kernel(const IO *__restrict__ w, int64_t ws, int64_t rows, int64_t d
 struct StatsEpi {
   struct Args {
     float2 *part;  // [runs][ld]
-    int64_t ld;
+    int64_t ld, n;  // rows of `part`; tokens
     Rows rows;
     const uint32_t *top;
-    int V, word0, run0;  // words of this piece; its first word and run
+    int V, word0, run0, runs;  // words of this piece; its first word and run; all runs
   };
   const Args &a;
   int *err;
@@ -353,7 +359,7 @@ struct StatsEpi {
   __device__ __forceinline__ void begin(const Tile &, int r, int col, int M) {
     row = r, live = r < M, run = a.run0 + col / kRun;
     m = -INFINITY, s = 0.f;
-    target = live ? a.rows.target[r] - a.word0 : -1;
+    target = live && SSD_IN_BOUNDS(r < a.n, err, 518) ? a.rows.target[r] - a.word0 : -1;
   }
   __device__ __forceinline__ void chunk(float (&v)[gemm::kChunk], int col, int) {
     if (col >= a.V) return;
@@ -363,7 +369,7 @@ struct StatsEpi {
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < gemm::kChunk; ++i) z = i == at ? v[i] : z;
-      if (SSD_IN_BOUNDS(row < a.ld, err, 73)) a.rows.zt[row] = z * unit;
+      if (SSD_IN_BOUNDS(row < a.n, err, 519)) a.rows.zt[row] = z * unit;
     }
     if (words < gemm::kChunk) {
 #pragma unroll
@@ -381,7 +387,7 @@ struct StatsEpi {
     m = next;
   }
   __device__ __forceinline__ void end() {
-    if (live && SSD_IN_BOUNDS(row < a.ld, err, 74))
+    if (live && SSD_IN_BOUNDS(row < a.ld && run < a.runs, err, 520))
       a.part[(int64_t)run * a.ld + row] = make_float2(m, s);
   }
 };
@@ -417,6 +423,7 @@ struct DlogitEpi {
     CUtensorMap dz;
     Rows rows;
     const uint32_t *top;
+    int64_t n;  // tokens
     int V, word0, own;  // own: each token has a factor, which is no part of dz
   };
   static constexpr bool kStaged = true, kSplit = sizeof(IO) == 4;
@@ -424,11 +431,12 @@ struct DlogitEpi {
   using Pane = gemm::Panes<128>;
   const Args &a;
   Pane panes;
+  int *err;
   float scale, up, lse, g;
   int row0, target;
   bool live;
-  __device__ __forceinline__ DlogitEpi(const Args &args, Pane p, int *)
-      : a(args), panes(p) {
+  __device__ __forceinline__ DlogitEpi(const Args &args, Pane p, int *e)
+      : a(args), panes(p), err(e) {
     scale = up = 1.f;
     if constexpr (kSplit) {
       scale = pow2(-shift_of(a.top[kTopX]) - shift_of(a.top[kTopW]));
@@ -436,7 +444,7 @@ struct DlogitEpi {
     }
   }
   __device__ __forceinline__ void begin(const Tile &, int r, int, int M) {
-    row0 = r - panes.lane, live = r < M;
+    row0 = r - panes.lane, live = r < M && SSD_IN_BOUNDS(r < a.n, err, 521);
     lse = live ? a.rows.lse[r] : 0.f;
     g = live ? (a.own ? up : a.rows.g[r] * up) : 0.f;
     target = live ? a.rows.target[r] - a.word0 : -1;
@@ -576,10 +584,10 @@ struct GradEpi {
   // A pane to rows that TMA cannot write: lanes along the columns.
   __device__ __forceinline__ void copy(int col) {
     const int rows = min(32, a.words - row0);
-    if (!SSD_IN_BOUNDS(row0 >= 0 && col >= 0, err, 76)) return;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
       const uint32_t w = panes.word(pane, r, panes.lane);
+      if (!SSD_IN_BOUNDS(row0 + r < a.words && col < a.d, err, 522)) break;
       IO *o = a.out + (int64_t)(row0 + r) * a.d + col;
       if constexpr (kWide) {
         if (col + panes.lane < a.d) o[panes.lane] = __uint_as_float(w);
@@ -605,14 +613,16 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
   const float3 factor = f.of(kTopW);
   const int live = *f.rows.live, lane = threadIdx.x % 32;
   const int64_t r = blockIdx.x;
-  if (r >= live || !SSD_IN_BOUNDS(d <= ld, err, 79)) return;
+  if (r >= live) return;
   const int64_t t = f.rows.token[r];
+  if (!SSD_IN_BOUNDS(t < gridDim.x && (r + 1) * ld <= zs, err, 523)) return;
   const float g = f.own ? f.rows.g[r] : 1.f;
   IO *o = dx.at(t / L, t % L);
   for (int64_t c = (threadIdx.x / 32) * 128 + lane * 4; c < d; c += blockDim.x * 4) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};  // (ld is a multiple of 16)
 #pragma unroll 8
     for (int z = 0; z < slabs; ++z) {
+      if (!SSD_IN_BOUNDS(c + 4 <= ld, err, 524)) break;
       const float4 q = *reinterpret_cast<const float4 *>(sum + z * zs + r * ld + c);
       v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
     }
@@ -628,7 +638,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
 // are joined in the warps' order.
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
-join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
+join_kernel(const float2 *__restrict__ part, int64_t ld, int64_t n, int runs, Rows rows,
             float *__restrict__ loss, float *__restrict__ lse, int *err) {
   __shared__ float2 each[kJoinWarps][32];
   ptx::griddep_launch_dependents();
@@ -642,7 +652,7 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
     s = s * ex2((m - about) * kLog2e) + q.y * ex2((q.x - about) * kLog2e);
     m = next;
   };
-  if (live && SSD_IN_BOUNDS(row < ld, err, 77)) {
+  if (live && SSD_IN_BOUNDS(row < n && row < ld, err, 525)) {
     int r = warp;
     for (; r + 3 * kJoinWarps < runs; r += 4 * kJoinWarps) {  // four loads at a time
       float2 q[4];
@@ -659,6 +669,7 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
   for (int w = 1; w < kJoinWarps; ++w) join(each[w][lane]);
   const float l = m + logf(s);
   const int t = rows.token[row];
+  if (!SSD_IN_BOUNDS(t < n, err, 526)) return;
   lse[t] = l;
   loss[t] = l - rows.zt[row];
 }
@@ -667,14 +678,13 @@ join_kernel(const float2 *__restrict__ part, int64_t ld, int runs, Rows rows,
 // one), in a fixed order.
 __global__ void __launch_bounds__(1024)
 total_kernel(const float *__restrict__ loss, int64_t n, const int *__restrict__ live, int mean,
-             float *__restrict__ total, int *err) {
+             float *__restrict__ total) {
   __shared__ float sums[32];
   float s = 0.f;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  if (SSD_IN_BOUNDS(n > 0, err, 78))
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += loss[i];
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += loss[i];
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
@@ -853,16 +863,16 @@ struct Calls {
       CUtensorMap maps[2];
       Product q;
       if (!logits(a, p, w, maps, &q)) return cudaErrorInvalidValue;
-      const StatsEpi::Args s{p.stat, p.rows, p.r, kPlanes == 2 ? p.top : nullptr, (int)w.n,
-                             (int)word0, (int)(word0 / kRun)};
+      const StatsEpi::Args s{p.stat, p.rows, a.n, p.r, kPlanes == 2 ? p.top : nullptr, (int)w.n,
+                             (int)word0, (int)(word0 / kRun), (int)p.runs};
       e = gemm::launch<StatsEpi, kBN, kSegment>(maps, &q, 1, kBf16, s, err, st);
     }
     if (e != cudaSuccess) return e;
     e = launch_after(join_kernel, dim3((unsigned)((a.n + 31) / 32)), 32 * kJoinWarps, 0, st,
-                           p.stat, p.rows, (int)p.runs, p.r, loss, a.lse, err);
+                           p.stat, p.rows, a.n, (int)p.runs, p.r, loss, a.lse, err);
     if (e != cudaSuccess || !a.total) return e;
     return launch_after(total_kernel, dim3(1), 1024, 0, st, loss, a.n, p.r.live,
-                              (int)(a.reduction == SSD_REDUCE_MEAN), a.total, err);
+                              (int)(a.reduction == SSD_REDUCE_MEAN), a.total);
   }
 
   static cudaError_t backward(const LossArgs &a, void *ws, int *err, cudaStream_t st) {
@@ -881,7 +891,7 @@ struct Calls {
       Product q[2];
       if (!logits(a, p, w, maps, q)) return cudaErrorInvalidValue;
       typename DlogitEpi<IO>::Args z{};
-      z.rows = p.r, z.top = top, z.V = (int)w.n, z.word0 = (int)word0, z.own = own;
+      z.rows = p.r, z.top = top, z.n = a.n, z.V = (int)w.n, z.word0 = (int)word0, z.own = own;
       if (!gemm::make_pane_map<128>(&z.dz, p.dz, false, p.dz_ld, p.rows, kPlanes, p.dz_ld, ps))
         return cudaErrorInvalidValue;
       e = gemm::launch<DlogitEpi<IO>, kBN, kSegment>(maps, q, 1, kBf16, z, err, st);
