@@ -80,58 +80,60 @@ __device__ __forceinline__ void each8(SeqView<const IO> g, int64_t rows, int64_t
   }
 }
 
-// Sums of squares, one a block, in units of 2^(2 e).  e is 0 where the block's largest
-// |value| is within kLeastPlain .. kMostPlain: its squares stay within fp32 and what falls out
-// below is 2^-46 of its square.  Else the block walks its values again, times 2^-e, which
-// takes the largest to 1 .. 2.
-struct BlockSum {
+// Sums of squares, one a block, in units of 2^(2 e).  e is 0 where the plain sum is within
+// kLeastPlain .. kMostPlain: no square has left fp32, and what fell out below is 2^-46 of
+// the sum a value.  Else the block walks its values again, for the largest and then times
+// 2^-e, which takes that to 1 .. 2.
+struct __align__(8) BlockSum {
   float s;
   int e;
 };
-constexpr float kLeastPlain = 0x1p-40f, kMostPlain = 0x1p40f;
+constexpr float kLeastPlain = 0x1p-80f, kMostPlain = 0x1p120f;
+constexpr int kNoNumber = 1000;  // of an infinite or NaN sum, next to which no other counts
 template <typename IO>
 __global__ void __launch_bounds__(kNormThreads)
 squares_kernel(SeqView<const IO> g, int64_t rows, int64_t cols, bool wide,
                BlockSum *__restrict__ part, int *err) {
   constexpr int kWarps = kNormThreads / 32;
-  __shared__ float sums[kWarps], tops[kWarps];
+  __shared__ float warps[kWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ptx::griddep_launch_dependents();
-  float top = 0.f;
-  auto walk = [&](auto scaled) {  // this warp's sum into sums
+  // the warps' values, in their order, in every thread
+  auto all = [&](float t, auto join) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t = join(t, __shfl_xor_sync(0xffffffffu, t, off));
+    __syncthreads();
+    if (lane == 0) warps[warp] = t;
+    __syncthreads();
+    t = warps[0];
+    for (int w = 1; w < kWarps; ++w) t = join(t, warps[w]);
+    return t;
+  };
+  auto sum = [&](auto scaled) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     each8(g, rows, cols, wide, err, [&](const float (&v)[8], int64_t, int64_t) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = scaled(v[e]);
-        s[e % 4] = fmaf(x, x, s[e % 4]);
-        top = fmaxf(top, fabsf(x));
-      }
+      for (int e = 0; e < 8; ++e) s[e % 4] = fmaf(scaled(v[e]), scaled(v[e]), s[e % 4]);
     });
-    float t = (s[0] + s[1]) + (s[2] + s[3]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    if (lane == 0) sums[warp] = t;
+    return all((s[0] + s[1]) + (s[2] + s[3]), [](float a, float b) { return a + b; });
   };
-  walk([](float v) { return v; });
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+  float t = sum([](float v) { return v; });
   int e = 0;
-  if (top > 0.f && (top < kLeastPlain || top > kMostPlain) && isfinite(top)) {
-    e = ilogbf(top);
-    const float a = ldexpf(1.f, -e / 2), b = ldexpf(1.f, -e - -e / 2);
-    __syncthreads();
-    walk([=](float v) { return v * a * b; });
-    __syncthreads();
+  if (t < kLeastPlain || t > kMostPlain) {
+    float top = 0.f;
+    each8(g, rows, cols, wide, err, [&](const float (&v)[8], int64_t, int64_t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+    });
+    top = all(top, [](float a, float b) { return fmaxf(a, b); });
+    if (top > 0.f && isfinite(top)) {  // (of a NaN as well: it is in t)
+      e = ilogbf(top);
+      const float a = ldexpf(1.f, -e / 2), b = ldexpf(1.f, -e - -e / 2);
+      t = sum([=](float v) { return v * a * b; });
+    }
   }
-  if (threadIdx.x == 0) {
-    float t = sums[0];
-    for (int w = 1; w < kWarps; ++w) t += sums[w];
-    part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = {t, e};
-  }
+  if (!isfinite(t)) e = kNoNumber;
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = {t, e};
 }
 
 // Eight values as fp16, and what that leaves of them if it is asked for.
@@ -151,13 +153,20 @@ __device__ __forceinline__ uint4 pack8(float *v, bool more) {
 __device__ __forceinline__ float scale_of(const BlockSum *__restrict__ part, int parts, float eps,
                                           int *q) {
   const int lane = threadIdx.x % 32;
-  int unit = -1000;  // the largest sum's
-  for (int i = lane; i < parts; i += 32)
-    if (part[i].s != 0.f) unit = max(unit, part[i].e);
+  int unit = -1000;  // the largest of the sums'
+#pragma unroll 4
+  for (int i = lane; i < parts; i += 32) {
+    const BlockSum b = part[i];
+    if (b.s != 0.f) unit = max(unit, b.e);
+  }
   unit = __reduce_max_sync(0xffffffffu, unit);
   float s = 0.f;  // every warp adds the parts in the same order
-  for (int i = lane; i < parts; i += 32)
-    if (part[i].s != 0.f) s += ldexpf(part[i].s, 2 * (part[i].e - unit));
+#pragma unroll 4
+  for (int i = lane; i < parts; i += 32) {
+    const BlockSum b = part[i];
+    const int e = 2 * (b.e - unit);
+    if (b.s != 0.f && e > -127) s += b.s * __uint_as_float((uint32_t)(127 + e) << 23);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   *q = 0;

@@ -141,6 +141,16 @@ def test_updates_of_zeros_and_of_no_numbers(ssd, eps, to):  # noqa: F811
     assert (X[0] == 0).all() and torch.isfinite(X[1]).all() and torch.isnan(X[2:]).all()
 
 
+@pytest.mark.parametrize("to", ["bf16", "fp32"])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_no_number_among_large_values(ssd, what, to):  # noqa: F811
+    """The one block of a large matrix that holds it has the smallest values otherwise."""
+    G = gen(4)(300, 600)
+    G[:250] *= 1e37
+    G[299, 599] = float(what)
+    assert torch.isnan(ssd.orthogonalize(G, dtype=IO[to])).all()
+
+
 def test_a_stack_between_the_rows_of_another_axis(ssd):  # noqa: F811
     """Matrices whose rows alternate in memory, read and written so."""
     G = gen(1)(3, 40, 72, dtype=B16)
