@@ -98,6 +98,24 @@ def test_losses_of_sure_rows(ssd):  # noqa: F811
         within(lse[i], ref_lse[i], off, "lse")
 
 
+def test_words_without_a_share(ssd):  # noqa: F811
+    """A channel that is 1 in every token makes W's column a bias: -inf there leaves the
+    word out, in bf16.  In fp32, in planes, it is a NaN for every token."""
+    n = gen(8)
+    x, W = n(70, 40, dtype=B16), n(500, 40, scale=0.3, dtype=B16)
+    x[:, 0] = 1
+    W[::3, 0] = float("-inf")
+    t = torch.arange(70, device="cuda") * 6 + 1
+    loss, lse = ssd.linear_cross_entropy_forward(x, W, t)
+    z = x.double() @ W.double().t()
+    ref = torch.logsumexp(z, 1)
+    keep = W[:, 0].isfinite()
+    off = R.loss_bound(R.logit_bound(x, W[keep], B16, t >= 0), 500, ref)
+    within(lse, ref, off, "lse")
+    within(loss, ref - z.gather(1, t[:, None])[:, 0], off, "loss")
+    assert torch.isnan(ssd.linear_cross_entropy_forward(x.float(), W.float(), t)[0]).all()
+
+
 # ----------------------------------------------------- orthogonalised updates
 
 @pytest.mark.parametrize("to", ["bf16", "fp32"])
