@@ -236,7 +236,7 @@ def add_norm(x, residual, weight, eps: float = 1e-5):
 
 # ------------------------------------------------ cross entropy over a vocabulary
 
-def _loss_dims(x, weight, targets, ignore_index, reduction):
+def _loss_dims(x, weight, ignore_index, reduction):
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be 'none', 'sum' or 'mean', got {reduction!r}")
     b, L = _lead(x, "x")
@@ -254,7 +254,7 @@ def _words(weight, x):
 def linear_cross_entropy_workspace_size(x, weight) -> int:
     """Bytes of workspace that linear_cross_entropy_forward needs."""
     return int(_abi.load().ssd_linear_cross_entropy_workspace_size(
-        _loss_dims(x, weight, None, -100, "none"), _io(x, "x"), _words(weight, x)))
+        _loss_dims(x, weight, -100, "none"), _io(x, "x"), _words(weight, x)))
 
 
 def linear_cross_entropy_forward(x, weight, targets, ignore_index: int = -100,
@@ -268,7 +268,7 @@ def linear_cross_entropy_forward(x, weight, targets, ignore_index: int = -100,
     without any).  lse: the logarithm of the sum of exponentials, float32, for
     the backward pass.  Tokens whose target is ignore_index have a loss and an
     lse of zero; another target outside [0, V) gives a NaN."""
-    d, io, lib = _loss_dims(x, weight, targets, ignore_index, reduction), _io(x, "x"), _abi.load()
+    d, io, lib = _loss_dims(x, weight, ignore_index, reduction), _io(x, "x"), _abi.load()
     lead, w = x.shape[:-1], _words(weight, x)
     lse = torch.empty(lead, dtype=torch.float32, device=x.device)
     loss = torch.empty(lead if reduction == "none" else (), dtype=torch.float32, device=x.device)
@@ -289,7 +289,7 @@ _LOSS_GRADS = ("dx", "dweight")
 def linear_cross_entropy_backward_workspace_size(x, weight) -> int:
     """Bytes of workspace that linear_cross_entropy_backward needs."""
     return int(_abi.load().ssd_linear_cross_entropy_backward_workspace_size(
-        _loss_dims(x, weight, None, -100, "none"), _io(x, "x"), _words(weight, x)))
+        _loss_dims(x, weight, -100, "none"), _io(x, "x"), _words(weight, x)))
 
 
 def linear_cross_entropy_backward(x, weight, targets, lse, gloss=None, ignore_index: int = -100,
@@ -300,7 +300,7 @@ def linear_cross_entropy_backward(x, weight, targets, lse, gloss=None, ignore_in
     target) and dweight [V, D], both in the I/O type.  `want` names those to
     compute (None = both)."""
     has = _wanted(want, _LOSS_GRADS, "linear_cross_entropy_backward")
-    d, io, lib = _loss_dims(x, weight, targets, ignore_index, reduction), _io(x, "x"), _abi.load()
+    d, io, lib = _loss_dims(x, weight, ignore_index, reduction), _io(x, "x"), _abi.load()
     lead, w = x.shape[:-1], _words(weight, x)
     ws, wp, wn = _workspace(lib.ssd_linear_cross_entropy_backward_workspace_size(d, io, w),
                             workspace, x, "linear_cross_entropy_backward")
