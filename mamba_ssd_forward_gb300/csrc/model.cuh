@@ -54,7 +54,7 @@ struct AddNormArgs {
   const float *weight;
   float *scales, *dweight;
 };
-// y in the I/O type, or with `block` > 0 in e4m3
+// y in the I/O type, or where `scales` is given in e4m3 (block 0: a scale a token)
 cudaError_t launch_add_norm(const AddNormArgs &a, ssd_dtype io, ssd_dtype stream, int *err,
                             cudaStream_t st);
 size_t add_norm_backward_workspace(const AddNormArgs &a, ssd_dtype io, ssd_dtype stream);

@@ -6,8 +6,8 @@
 // Three products a step (gemm.cuh).  A and B are symmetric: their tiles below the
 // diagonal are written as the transposes of those above it.  Bound by the tensor
 // cores: s^2 l + s^3 + 2 s^2 l operations a step for s = min, l = max of the sides.
-// Measured, five steps in bf16: 10576 x 2560 900 to 920 us, 1.25 PFLOP/s; 24 of
-// 768 x 1536 485 us, 0.78 PFLOP/s; small ones 5.4 us a launch.
+// Measured, five steps in bf16: 10576 x 2560 905 to 920 us, 1.23 PFLOP/s; 24 of
+// 768 x 1536 490 us, 0.78 PFLOP/s; small ones 5.4 us a launch.
 //
 // Precision.  A step takes small singular values times a = 3.4, five steps 485:
 // it enlarges the rounding of X with them.  bf16 operands would leave the result
@@ -53,7 +53,7 @@ __device__ __forceinline__ void load8(const IO *p, int64_t c, int64_t cols, bool
 
 // A matrix in groups of eight elements; a thread's groups are gridDim.x kNormThreads
 // apart, kAtOnce of them loaded together (10576 x 2560 bf16: the squares 18 us, 3.0
-// TB/s with cold caches, the first X 24).  Row and column are walked along: with a
+// TB/s with cold caches, the first X 26).  Row and column are walked along: with a
 // division a group, and one load at a time, the squares took 20.
 constexpr int kAtOnce = 4;
 template <typename IO, typename F>

@@ -9,16 +9,19 @@
 // computed again, their epilogue writes the piece of dz, and one launch adds its
 // shares of dx and computes its rows of dW.  Bound by the tensor cores: 2 n V d
 // operations forward, 6 n V d backward.  Measured: 8192 tokens x 2560, 50280 words,
-// bf16, forward and backward 5190 us, 1.63 PFLOP/s (under the power cap); forward of
-// 2048 x 768 106 us, 1.5 PFLOP/s; 1021 x 771, 32003 words, fp32, 534 us; forward of
+// bf16, forward and backward 5170 to 5250 us, 1.61 to 1.63 PFLOP/s (under the power cap);
+// forward of 2048 x 768 107 us, 1.5 PFLOP/s; 1021 x 771, 32003 words, fp32, 537 us; forward of
 // 5 x 2560, 50280 words, bf16, 58 us, 4.4 TB/s of W.
 //
 // Tokens without a target are left out before the products: the others' rows of
 // x are packed together (so whatever the left out rows hold reaches nothing),
 // their number stays on the device.
 //
-// bf16: the logits are exact products with fp32 sums.  dz is rounded once to
-// bf16, as the operand of both gradient products (2^-9 of each term, as far off
+// bf16: the products of the logits are exact, their fp32 sums those of the tensor cores,
+// which cut towards zero at 24 bits with each 16 channels (all d in one go: losses measured
+// 4e-7 off, 6e-8 where the same products are added with rounding; the fp32 path's segments
+// would keep the epilogue from running under the next tile's products).  dz is rounded once
+// to bf16, as the operand of both gradient products (up to 2^-8 of each term, as far off
 // as the gradients' own rounding); a factor common to all tokens is applied to
 // the fp32 sums instead.  fp32: x, W and dz are split into two fp16 planes after
 // scaling by powers of two that take the largest value to 2^14..2^15 (values
@@ -700,7 +703,8 @@ total_kernel(const float *__restrict__ loss, int64_t n, const int *__restrict__ 
 
 // What a call keeps where.  Pieces: words to a piece (forward: all where W can be
 // taken as it is, else as many as keep the packed rows near 256 MB; backward: as
-// many as keep dz near that, where a piece of 2048 already fills the tiles).
+// many as keep dz near that, but 2048 at least, which fill the tiles: more than 65536
+// tokens, 32768 in fp32, take more).
 struct Plan {
   int planes;
   int64_t rows, ld, piece, dz_ld;  // padded rows; elements to a packed row; words; dz's row
