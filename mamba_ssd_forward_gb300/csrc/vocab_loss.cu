@@ -620,6 +620,10 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
   const int64_t t = f.rows.token[r];
   if (!SSD_IN_BOUNDS(t < gridDim.x && (r + 1) * ld <= zs, err, 523)) return;
   const float g = f.own ? f.rows.g[r] : 1.f;
+  // a large factor last, a small one between the halves: nothing on the way is larger
+  // than the result or the sum
+  const bool last = fabsf(g) >= 1.f;
+  const float g0 = last ? 1.f : g, g1 = last ? g : 1.f;
   IO *o = dx.at(t / L, t % L);
   for (int64_t c = (threadIdx.x / 32) * 128 + lane * 4; c < d; c += blockDim.x * 4) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};  // (ld is a multiple of 16)
@@ -631,7 +635,7 @@ unpack_kernel(const float *__restrict__ sum, int64_t ld, int64_t zs, int slabs, 
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < d) st_io(o + c + e, v[e] * factor.x * g * factor.y * factor.z);
+      if (c + e < d) st_io(o + c + e, v[e] * factor.x * g0 * factor.y * factor.z * g1);
   }
 }
 

@@ -70,6 +70,9 @@ def test_fp32_factors_at_the_ends_of_the_range(ssd):  # noqa: F811
         r = ssd.linear_cross_entropy_backward(x, w, t, lse, g * 2.0 ** k)
         for name in ref:
             within(r[name], ref[name].double() * 2.0 ** k, 2.0 ** -149, name)  # (denormals)
+    dx = ssd.linear_cross_entropy_backward(x, w, t, lse, g * 2.0 ** 124, want=("dx",))["dx"]
+    assert float(ref["dx"].abs().max()) < 16 and float(g.abs().max()) < 16
+    within(dx, ref["dx"].double() * 2.0 ** 124, 0.0, "dx near the range's end")
     g[3], t[4] = float("inf"), 300  # a token's infinity, and a target that is no word
     dx = ssd.linear_cross_entropy_backward(x, w, t, lse, g, want=("dx",))["dx"]
     keep = torch.arange(70, device="cuda") > 4
